@@ -521,6 +521,170 @@ MOE_API int moe_layer_fwd(const moe_shape_t* shape, const moe_fwd_args_t* args, 
 MOE_API int moe_layer_bwd(const moe_shape_t* shape, const moe_bwd_args_t* args, const moe_saved_t* saved,
                   void* ws, void* stream);
 
+/* ------------------------------------------------------------ around the layer
+ * The operators that stand next to the layer in a transformer block: the
+ * residual addition with the norm before it (and the dropout of its output),
+ * and the experts on 4-bit weights for serving.  The pages have no counterpart
+ * to these calls; their arithmetic is written out with each.
+ *
+ * Matrices here have a row stride `ld` (elements, >= the row's length); their
+ * pointers need only the alignment of their element type.  Rows whose groups
+ * of eight columns lie on 16-byte boundaries (base 16-byte aligned, row stride
+ * a multiple of 16 bytes, the width a multiple of 8) take vector loads.
+ * A call with no rows (rows, T or M = 0) is valid and writes nothing. */
+typedef enum { MOE_DT_BF16 = 0, MOE_DT_F16 = 1, MOE_DT_F32 = 2 } moe_dtype_t;
+
+/* Residual addition with root-mean-square norm, one pass over the data:
+ *   u = dropout(x) (below; p = 0: u = x)
+ *   h = residual + u, rounded to res_dtype (residual NULL: h = u)
+ *   rstd = (mean over d of h^2 + eps)^(-1/2), of the rounded h
+ *   y = h * rstd * weight
+ * y is written in `dtype`, or (y_q set, y NULL, dtype bf16, d a multiple of
+ * 128) as MXFP8: E4M3 codes and E8M0 scales of the unrounded 32-bit y, rounding
+ * and MOE_SF layout as moe_quantize_mxfp8 (block_axis 1).  These buffers hold
+ * roundup(rows, 128) rows, the ones past `rows` are written as zero codes with
+ * scale 2^0: they can be given to moe_grouped_gemm and moe_dequantize_mxfp8.
+ * y_dq (nullable): also the values that the codes stand for, bf16.
+ *   x, y       dtype [rows, d]            residual, h  res_dtype [rows, d]
+ *   weight     w_dtype [d]                rstd         fp32 [rows] or NULL
+ *   res_dtype and w_dtype: dtype, or fp32.
+ *   h may be NULL only without residual and dropout (then h = x in its own
+ *   type).  h may be the residual's buffer, and y that of x, with equal strides.
+ * Envelope: 1 <= d <= 32768, rows < 2^31, eps >= 0, 0 <= p <= 1. */
+typedef struct {
+  int64_t rows;
+  int32_t d;
+  int32_t dtype;
+  int32_t res_dtype;
+  int32_t w_dtype;
+  const void* x;
+  int64_t ld_x;
+  const void* residual;
+  int64_t ld_residual;
+  const void* weight;
+  void* h;
+  int64_t ld_h;
+  void* y;
+  int64_t ld_y;
+  float* rstd;
+  uint8_t* y_q;
+  uint8_t* y_scales;
+  void* y_dq;
+  uint64_t seed;
+  uint64_t offset;
+  float eps;
+  float p;
+} moe_add_norm_args_t;
+MOE_API int moe_add_norm(const moe_add_norm_args_t* args, void* stream);
+
+/* Backward of moe_add_norm from the h and rstd that it wrote (without residual
+ * and dropout: h is x, res_dtype = dtype).  With g = weight * dy:
+ *   dh = dres + rstd * (g - h * rstd^2 * mean(g * h))   res_dtype: the gradient
+ *        of h and of residual (dres: gradient that h gets from its other uses,
+ *        NULL: none)
+ *   dx = dropout of dh with the forward's p, seed and offset (of the 32-bit
+ *        dh)                                             dtype
+ *   dw = sum over rows of dy * h * rstd                  fp32 [d]
+ * Through an 8-bit output the gradient passes as if it were not rounded.
+ * dh, dx and dw may each be NULL (not all three).  dh may be dres' or h's
+ * buffer and dx that of dy, with equal strides.  dw needs `ws`, of
+ * moe_add_norm_bwd_workspace_size bytes.  Deterministic (fixed-order sums). */
+typedef struct {
+  int64_t rows;
+  int32_t d;
+  int32_t dtype;
+  int32_t res_dtype;
+  int32_t w_dtype;
+  const void* dy;
+  int64_t ld_dy;
+  const void* h;
+  int64_t ld_h;
+  const void* dres;
+  int64_t ld_dres;
+  const float* rstd;
+  const void* weight;
+  void* dh;
+  int64_t ld_dh;
+  void* dx;
+  int64_t ld_dx;
+  float* dw;
+  uint64_t seed;
+  uint64_t offset;
+  float p;
+} moe_add_norm_bwd_args_t;
+MOE_API int moe_add_norm_bwd_workspace_size(int64_t rows, int32_t d, size_t* ws_bytes);
+MOE_API int moe_add_norm_bwd(const moe_add_norm_bwd_args_t* args, void* ws, void* stream);
+
+/* Dropout of a [rows, cols] matrix with a mask that is computed, not stored:
+ *   thr = round(p * 2^16);  y = x * 2^16 / (2^16 - thr) where the element's
+ *   16-bit number is at least thr, else 0 (whatever x holds there).
+ * The number of (row, col) is half-word col % 8 (low half-words first) of
+ * Philox4x32-10 (Salmon et al., SC 2011) with key = seed and counter
+ * (col / 8, row, offset low 32 bits, offset high 32 bits): a function of the
+ * element's place alone, not of types, strides or the launch.  A step that
+ * drops several matrices gives each its own offset.  The backward is the same
+ * call on dy.  y may be x (same stride).  cols <= 2^30, rows < 2^31. */
+MOE_API int moe_dropout(int64_t rows, int32_t cols, int32_t dtype, const void* x, int64_t ld_x,
+                        void* y, int64_t ld_y, float p, uint64_t seed, uint64_t offset,
+                        void* stream);
+
+/* 4-bit weights with group scales along K (G = group = 32, 64 or 128, K a
+ * multiple of it): W[n, k] = (code[n, k] - 8) * scale[n, k / G], codes 0..15.
+ *   q       uint8 [rows, K/2]; byte j holds column 2j (low nibble) and 2j + 1
+ *   scales  dtype [rows, K/G] (bf16 or fp16, the activations' type)
+ * moe_quantize_w4: scale = max |w| / 7 of the group, rounded to dtype; code =
+ * w / scale rounded to nearest even, clamped to [-8, 7], plus 8 (an all-zero
+ * group: scale 0, codes 8).  Batches of matrices are more rows.
+ * moe_dequantize_w4 writes fp32 [rows, K] (exact). */
+MOE_API int moe_quantize_w4(int64_t rows, int32_t K, int32_t group, int32_t dtype, const void* src,
+                            uint8_t* q, void* scales, void* stream);
+MOE_API int moe_dequantize_w4(int64_t rows, int32_t K, int32_t group, int32_t dtype,
+                              const uint8_t* q, const void* scales, float* out, void* stream);
+
+/* y[m, n] = sum_k x[m, k] W[n, k], fp32 sums, for a few vectors: x dtype
+ * [M, K] (16-byte aligned rows), W as above with N rows, y dtype [M, N].
+ * N <= 1048560. */
+MOE_API int moe_matvec_w4(int32_t M, int32_t N, int32_t K, int32_t group, int32_t dtype,
+                          const void* x, int64_t ld_x, const uint8_t* q, const void* scales,
+                          void* y, int64_t ld_y, void* stream);
+
+/* The layer's SwiGLU experts on 4-bit weights for a few tokens (decoding):
+ *   out[t] = sum_j gates[t, j] * W_down[e] (silu(W_gate[e] x[t]) * (W_up[e] x[t])),
+ *   e = topk_idx[t, j]
+ * fp32 sums; the activations between the products keep 16 bits (two bf16
+ * parts), out is rounded once.  An index of -1 stands for no expert and adds
+ * nothing (a token without any gets zeros: unused places of a batch); any
+ * other index outside [0, E) adds nothing and sets MOE_DEVERR_BOUNDS in the
+ * workspace's error word.  Only the weights of experts with routes are read.
+ *   x, out  dtype [T, d] (bf16 or fp16)   topk_idx int32 [T, k], gates fp32 [T, k]
+ *   *_q, *_s  4-bit weights as above: W_gate, W_up [E, f, d], W_down [E, d, f]
+ *   ws  moe_experts_w4_workspace_size bytes; its first word is the error word
+ * Envelope: d and f multiples of 128, E <= 256, k <= 32, T * k <=
+ * MOE_W4_MAX_ROUTES (larger batches: the layer's grouped GEMMs). */
+#define MOE_W4_MAX_ROUTES 4096
+typedef struct {
+  int32_t T;
+  int32_t d_model;
+  int32_t n_experts;
+  int32_t top_k;
+  int32_t d_ff;
+  int32_t group;
+  int32_t dtype;
+  const void* x;
+  const int32_t* topk_idx;
+  const float* gates;
+  const uint8_t* gate_q;
+  const void* gate_s;
+  const uint8_t* up_q;
+  const void* up_s;
+  const uint8_t* down_q;
+  const void* down_s;
+  void* out;
+} moe_experts_w4_args_t;
+MOE_API int moe_experts_w4_workspace_size(int32_t T, int32_t d, int32_t E, int32_t k, int32_t f,
+                                          size_t* ws_bytes);
+MOE_API int moe_experts_w4(const moe_experts_w4_args_t* args, void* ws, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from dataclasses import dataclass
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -49,6 +50,9 @@ EXPORTS = (
     "moe_route_noalloc", "moe_dequantize_mxfp8", "moe_build_mx_weights",
     "moe_debug_inject_stall", "moe_profile_start", "moe_profile_stop", "moe_load_balance",
     "moe_checks_read",
+    "moe_add_norm", "moe_add_norm_bwd_workspace_size", "moe_add_norm_bwd", "moe_dropout",
+    "moe_quantize_w4", "moe_dequantize_w4", "moe_matvec_w4", "moe_experts_w4_workspace_size",
+    "moe_experts_w4",
 )
 
 
@@ -120,7 +124,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                            "(the MoE layer has no CPU or eager fallback)")
     lib = ctypes.CDLL(path)
     P = ctypes.POINTER
-    i32 = ctypes.c_int32
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
     sig = {
         "moe_init": [ctypes.c_int],
         "moe_rows_max": [P(Shape), P(ctypes.c_int64)],
@@ -145,6 +149,16 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_layer_fwd": [P(Shape), P(FwdArgs), P(Saved), _vp, _vp],
         "moe_layer_bwd": [P(Shape), P(BwdArgs), P(Saved), _vp, _vp],
         "moe_checks_read": [P(i32), i32],
+        "moe_add_norm": [_vp, _vp],
+        "moe_add_norm_bwd_workspace_size": [i64, i32, P(ctypes.c_size_t)],
+        "moe_add_norm_bwd": [_vp, _vp, _vp],
+        "moe_dropout": [i64, i32, i32, _vp, i64, _vp, i64, ctypes.c_float, ctypes.c_uint64,
+                        ctypes.c_uint64, _vp],
+        "moe_quantize_w4": [i64, i32, i32, i32, _vp, _vp, _vp, _vp],
+        "moe_dequantize_w4": [i64, i32, i32, i32, _vp, _vp, _vp, _vp],
+        "moe_matvec_w4": [i32] * 5 + [_vp, i64, _vp, _vp, _vp, i64, _vp],
+        "moe_experts_w4_workspace_size": [i32] * 5 + [P(ctypes.c_size_t)],
+        "moe_experts_w4": [_vp, _vp, _vp],
     }
     for name, args in sig.items():
         fn = getattr(lib, name)
@@ -373,6 +387,206 @@ def layer_fwd(s, fwd: FwdArgs, saved: Saved, ws, stream=None):
 def layer_bwd(s, bwd: BwdArgs, saved: Saved, ws, stream=None):
     _check("moe_layer_bwd", load().moe_layer_bwd(ctypes.byref(s), ctypes.byref(bwd),
                                                  ctypes.byref(saved), _ptr(ws), _stream(stream)))
+
+
+# ------------------------------------------------------------------ around the layer
+# The operators before and after the layer in a block (include/moe.h, "around the
+# layer").  These wrappers check what the C entry points cannot see: types, shapes,
+# devices and strides of the tensors.
+DT_BF16, DT_F16, DT_F32 = 0, 1, 2
+W4_MAX_ROUTES = 4096
+_ADD_NORM = struct.Struct("@qiiii" + "Pq" * 2 + "P" + "Pq" * 2 + "PPPP" + "QQff")
+_ADD_NORM_BWD = struct.Struct("@qiiii" + "Pq" * 3 + "PP" + "Pq" * 2 + "P" + "QQf0q")
+_EXPERTS_W4 = struct.Struct("@7i" + "P" * 10)
+_dtypes = None
+
+
+def _dtype(t, what):
+    global _dtypes
+    if _dtypes is None:
+        import torch
+        _dtypes = {torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32}
+    dt = _dtypes.get(t.dtype)
+    if dt is None:
+        raise TypeError(f"{what}: {t.dtype} is not bf16, fp16 or fp32")
+    return dt
+
+
+def _matrix(t, what, rows=None, cols=None, dtype=None):
+    """(address, row stride) of a matrix on the device, its last axis contiguous;
+    axes before the last one are rows (more than one of them: contiguous)."""
+    if t is None:
+        return 0, 0
+    if not t.is_cuda:
+        raise ValueError(f"{what}: not a CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what}: {t.dtype}, expected {dtype}")
+    shape = t.shape
+    n = len(shape)
+    if n == 2 and t.stride(1) == 1:
+        r, c, ld = shape[0], shape[1], t.stride(0)
+    elif n and t.is_contiguous():
+        c = shape[-1]
+        r, ld = t.numel() // c if c else 0, c
+    else:
+        raise ValueError(f"{what}: the last axis has to be contiguous (and more than two axes all of it)")
+    if r <= 1:
+        ld = c
+    if (rows is not None and r != rows) or (cols is not None and c != cols):
+        raise ValueError(f"{what}: {r} x {c}, expected {rows} x {cols}")
+    return t.data_ptr(), ld
+
+
+def _flat(t, what, numel, dtype, at_least=False):
+    """Address of a contiguous tensor of `numel` elements (or more)."""
+    if t is None:
+        return 0
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what}: not a contiguous CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{what}: {t.dtype}, expected {dtype}")
+    if t.numel() != numel and not (at_least and t.numel() > numel):
+        raise ValueError(f"{what}: {t.numel()} elements, expected {numel}")
+    return t.data_ptr()
+
+
+def add_norm(x, weight, y, residual=None, h=None, rstd=None, eps=1e-5, p=0.0, seed=0, offset=0,
+             y_q=None, y_scales=None, y_dq=None, stream=None):
+    """moe_add_norm: h = residual + dropout(x), y = h * rstd * weight.  y=None with
+    y_q, y_scales (and y_dq): the MXFP8 output, buffers of roundup(rows, 128) rows."""
+    import torch
+    dt = _dtype(x, "x")
+    d = x.shape[-1]
+    rows = x.numel() // d if d else 0
+    px, ld_x = _matrix(x, "x")
+    stream_t = residual if residual is not None else h
+    rt = dt if stream_t is None else _dtype(stream_t, "residual")
+    pr, ld_r = _matrix(residual, "residual", rows, d)
+    ph, ld_h = _matrix(h, "h", rows, d, None if stream_t is None else stream_t.dtype)
+    py, ld_y = _matrix(y, "y", rows, d, x.dtype)
+    pad = (rows + 127) // 128 * 128
+    args = _ADD_NORM.pack(
+        rows, d, dt, rt, _dtype(weight, "weight"), px, ld_x, pr, ld_r,
+        _flat(weight, "weight", d, weight.dtype), ph, ld_h, py, ld_y,
+        _flat(rstd, "rstd", rows, torch.float32), _flat(y_q, "y_q", pad * d, torch.uint8, True),
+        _flat(y_scales, "y_scales", pad * d // 32, torch.uint8, True),
+        _flat(y_dq, "y_dq", pad * d, torch.bfloat16, True), seed, offset, eps, p)
+    _check("moe_add_norm", load().moe_add_norm(args, _stream(stream)))
+
+
+def add_norm_bwd_workspace(rows, d) -> int:
+    """Bytes of workspace that add_norm_bwd needs for dw."""
+    v = ctypes.c_size_t()
+    _check("moe_add_norm_bwd_workspace_size",
+           load().moe_add_norm_bwd_workspace_size(int(rows), int(d), ctypes.byref(v)))
+    return v.value
+
+
+def add_norm_bwd(dy, h, rstd, weight, dres=None, dh=None, dx=None, dw=None, ws=None, p=0.0, seed=0,
+                 offset=0, stream=None):
+    """moe_add_norm_bwd: dh (gradient of the stream), dx (of the dropped input), dw."""
+    import torch
+    dt = _dtype(dy, "dy")
+    d = dy.shape[-1]
+    rows = dy.numel() // d if d else 0
+    pdy, ld_dy = _matrix(dy, "dy")
+    ph, ld_h = _matrix(h, "h", rows, d)
+    pdr, ld_dr = _matrix(dres, "dres", rows, d, h.dtype)
+    pdh, ld_dh = _matrix(dh, "dh", rows, d, h.dtype)
+    pdx, ld_dx = _matrix(dx, "dx", rows, d, dy.dtype)
+    pws = 0
+    if dw is not None:
+        pws = _flat(ws, "ws", add_norm_bwd_workspace(rows, d), torch.uint8, True)
+    args = _ADD_NORM_BWD.pack(
+        rows, d, dt, _dtype(h, "h"), _dtype(weight, "weight"), pdy, ld_dy, ph, ld_h, pdr, ld_dr,
+        _flat(rstd, "rstd", rows, torch.float32), _flat(weight, "weight", d, weight.dtype),
+        pdh, ld_dh, pdx, ld_dx, _flat(dw, "dw", d, torch.float32), seed, offset, p)
+    _check("moe_add_norm_bwd", load().moe_add_norm_bwd(args, pws or None, _stream(stream)))
+
+
+def dropout(x, y, p, seed, offset=0, stream=None):
+    """moe_dropout: y = dropout(x), the mask a function of (seed, offset, row,
+    column); the backward is the same call on the gradient."""
+    dt = _dtype(x, "x")
+    d = x.shape[-1]
+    rows = x.numel() // d if d else 0
+    px, ld_x = _matrix(x, "x")
+    py, ld_y = _matrix(y, "y", rows, d, x.dtype)
+    _check("moe_dropout", load().moe_dropout(rows, d, dt, px, ld_x, py, ld_y, p, seed, offset,
+                                             _stream(stream)))
+
+
+def _w4(q, scales, what):
+    """(rows, K, group) of 4-bit weights, from the shapes of codes and scales."""
+    import torch
+    if q.dtype != torch.uint8:
+        raise TypeError(f"{what}: codes are {q.dtype}, expected uint8")
+    K, ng = 2 * q.shape[-1], scales.shape[-1]
+    if q.shape[:-1] != scales.shape[:-1] or ng == 0 or K % ng:
+        raise ValueError(f"{what}: codes {tuple(q.shape)} and scales {tuple(scales.shape)} do not belong together")
+    if not (q.is_cuda and scales.is_cuda and q.is_contiguous() and scales.is_contiguous()):
+        raise ValueError(f"{what}: not contiguous CUDA tensors")
+    return q.numel() // q.shape[-1], K, K // ng
+
+
+def quantize_w4(src, q, scales, stream=None):
+    """moe_quantize_w4: bf16 or fp16 weights [..., K] to codes [..., K/2] and scales
+    [..., K/G] of the same type."""
+    rows, K, g = _w4(q, scales, "quantize_w4")
+    ps = _flat(src, "src", rows * K, scales.dtype)
+    _check("moe_quantize_w4", load().moe_quantize_w4(rows, K, g, _dtype(src, "src"), ps, q.data_ptr(),
+                                                     scales.data_ptr(), _stream(stream)))
+
+
+def dequantize_w4(q, scales, out, stream=None):
+    """moe_dequantize_w4: the weights that codes and scales stand for, fp32."""
+    import torch
+    rows, K, g = _w4(q, scales, "dequantize_w4")
+    po = _flat(out, "out", rows * K, torch.float32)
+    _check("moe_dequantize_w4", load().moe_dequantize_w4(
+        rows, K, g, _dtype(scales, "scales"), q.data_ptr(), scales.data_ptr(), po, _stream(stream)))
+
+
+def matvec_w4(x, q, scales, y, stream=None):
+    """moe_matvec_w4: y [M, N] = x [M, K] times the 4-bit weights [N, K] transposed."""
+    N, K, g = _w4(q, scales, "matvec_w4")
+    M = x.numel() // K
+    px, ld_x = _matrix(x, "x", M, K, scales.dtype)
+    py, ld_y = _matrix(y, "y", M, N, scales.dtype)
+    _check("moe_matvec_w4", load().moe_matvec_w4(M, N, K, g, _dtype(x, "x"), px, ld_x, q.data_ptr(),
+                                                 scales.data_ptr(), py, ld_y, _stream(stream)))
+
+
+def experts_w4_workspace(T, d, E, k, f) -> int:
+    """Bytes of workspace that experts_w4 needs (its first word is the error word)."""
+    v = ctypes.c_size_t()
+    _check("moe_experts_w4_workspace_size", load().moe_experts_w4_workspace_size(
+        int(T), int(d), int(E), int(k), int(f), ctypes.byref(v)))
+    return v.value
+
+
+def experts_w4(x, topk_idx, gates, w: dict, out, ws, stream=None):
+    """moe_experts_w4: the SwiGLU experts on 4-bit weights for a few tokens.  `w`
+    holds gate_q, gate_s, up_q, up_s [E, f, ...] and down_q, down_s [E, d, ...];
+    an index of -1 in topk_idx stands for no expert."""
+    import torch
+    T, k = topk_idx.shape
+    E, f = w["gate_q"].shape[:2]
+    d = x.shape[-1]
+    shapes = [_w4(w[n + "_q"], w[n + "_s"], n) for n in ("gate", "up", "down")]
+    g = shapes[0][2]
+    if shapes != [(E * f, d, g), (E * f, d, g), (E * d, f, g)]:
+        raise ValueError(f"experts_w4: weights {shapes} do not fit E={E}, d={d}, f={f}")
+    dt = x.dtype
+    if any(w[n + "_s"].dtype != dt for n in ("gate", "up", "down")):
+        raise TypeError("experts_w4: scales of another type than x")
+    args = _EXPERTS_W4.pack(
+        T, d, E, k, f, g, _dtype(x, "x"), _flat(x, "x", T * d, dt),
+        _flat(topk_idx, "topk_idx", T * k, torch.int32), _flat(gates, "gates", T * k, torch.float32),
+        *(w[n].data_ptr() for n in ("gate_q", "gate_s", "up_q", "up_s", "down_q", "down_s")),
+        _flat(out, "out", T * d, dt))
+    pws = _flat(ws, "ws", experts_w4_workspace(T, d, E, k, f), torch.uint8, True)
+    _check("moe_experts_w4", load().moe_experts_w4(args, pws, _stream(stream)))
 
 
 # ------------------------------------------------------------------ buffers
