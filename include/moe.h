@@ -643,7 +643,7 @@ MOE_API int moe_dequantize_w4(int64_t rows, int32_t K, int32_t group, int32_t dt
 
 /* y[m, n] = sum_k x[m, k] W[n, k], fp32 sums, for a few vectors: x dtype
  * [M, K] (16-byte aligned rows), W as above with N rows, y dtype [M, N].
- * N <= 1048560. */
+ * N <= 1048560, K <= 2^18. */
 MOE_API int moe_matvec_w4(int32_t M, int32_t N, int32_t K, int32_t group, int32_t dtype,
                           const void* x, int64_t ld_x, const uint8_t* q, const void* scales,
                           void* y, int64_t ld_y, void* stream);
@@ -659,7 +659,7 @@ MOE_API int moe_matvec_w4(int32_t M, int32_t N, int32_t K, int32_t group, int32_
  *   x, out  dtype [T, d] (bf16 or fp16)   topk_idx int32 [T, k], gates fp32 [T, k]
  *   *_q, *_s  4-bit weights as above: W_gate, W_up [E, f, d], W_down [E, d, f]
  *   ws  moe_experts_w4_workspace_size bytes; its first word is the error word
- * Envelope: d and f multiples of 128, E <= 256, k <= 32, T * k <=
+ * Envelope: d and f multiples of 128 (<= 2^18), E <= 256, k <= 32, T * k <=
  * MOE_W4_MAX_ROUTES (larger batches: the layer's grouped GEMMs). */
 #define MOE_W4_MAX_ROUTES 4096
 typedef struct {

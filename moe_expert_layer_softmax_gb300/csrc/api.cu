@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "moe.h"
+#include "block.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -308,6 +309,8 @@ int moe_init(int device) {
   int sms = 0;
   MOE_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device));
   MOE_CUDA(gemm_init_attributes());
+  MOE_CUDA(matvec_w4_init());
+  MOE_CUDA(experts_w4_init());
   noalloc_forget_device(device);
   g_dev[device].sm_count = sms;
   g_dev[device].ready = true;

@@ -58,7 +58,7 @@ int check_norm_types(int64_t rows, int32_t d, int dtype, int res_dtype, int w_dt
 int check_w4(int64_t rows, int32_t K, int32_t group, int dtype) {
   if (rows < 0 || K < 1 || (dtype != MOE_DT_BF16 && dtype != MOE_DT_F16)) return MOE_ERR_INVALID;
   if (group != 32 && group != 64 && group != 128) return MOE_ERR_UNSUPPORTED;
-  if (K % group != 0) return MOE_ERR_UNSUPPORTED;
+  if (K % group != 0 || K > kW4MaxColumns) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
@@ -80,6 +80,7 @@ size_t round256(size_t v) { return (v + 255) & ~size_t(255); }
 int check_experts(int32_t T, int32_t d, int32_t E, int32_t k, int32_t f, int32_t group) {
   if (T < 0 || d < 1 || E < 1 || k < 1 || f < 1) return MOE_ERR_INVALID;
   if (d % 128 != 0 || f % 128 != 0 || E > 256 || k > 32) return MOE_ERR_UNSUPPORTED;
+  if (d > kW4MaxColumns || f > kW4MaxColumns) return MOE_ERR_UNSUPPORTED;
   if (group != 32 && group != 64 && group != 128) return MOE_ERR_UNSUPPORTED;
   if ((int64_t)T * k > MOE_W4_MAX_ROUTES) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;

@@ -72,6 +72,8 @@ cudaError_t launch_add_norm_bwd(AddNormBwdParams p, int dtype, int res_dtype, bo
 cudaError_t launch_dropout(const DropoutParams& p, int dtype, bool vec, cudaStream_t s);
 
 // ---------------------------------------------------------------- 4-bit weights
+constexpr int kW4MaxColumns = 1 << 18;   // K, d and f: stages of a block's share count in 32 bits
+
 struct ExpertsW4Params {
   int32_t T, d, E, k, f, group;
   const void* x;
@@ -82,11 +84,13 @@ struct ExpertsW4Params {
   const void *gate_s, *up_s, *down_s;
   void* out;
   int64_t ld_out;
-  void* act;       // workspace: activations of each route, two bf16 parts [2][T*k, f]
-  float* y;        // workspace: gated expert outputs of each route [T*k, d]
+  void* act;       // workspace: gated activations of each route: fp32 [T*k, f], or two bf16 parts [2][T*k, f]
+  float* y;        // workspace (more than one token): product of each route [T*k, d]
   int32_t* err;
 };
 
+cudaError_t matvec_w4_init();    // dynamic shared memory limits (moe_init)
+cudaError_t experts_w4_init();
 cudaError_t launch_quantize_w4(int64_t rows, int K, int group, int dtype, const void* src,
                                uint8_t* q, void* scales, cudaStream_t s);
 cudaError_t launch_dequantize_w4(int64_t rows, int K, int group, int dtype, const uint8_t* q,

@@ -1,0 +1,159 @@
+// Products of a few vectors with 4-bit weights (sm_103a): y[m, n] = sum_k x[m, k]
+// W[n, k].  How the weights are streamed: w4.cuh.
+#include "w4.cuh"
+
+namespace moe {
+
+namespace {
+
+struct MatvecArgs {
+  int M, N, K;
+  const void* x;
+  int64_t ld_x;
+  const uint8_t* q;
+  const void* sc;
+  void* y;
+  int64_t ld_y;
+  int seg_tiles;   // most tiles of a segment (shared memory of the parts)
+};
+
+// Rows past N repeat row N - 1 and are not written.
+template <typename S, int W> struct MatvecRows {
+  const uint8_t* q;
+  const S* sc;
+  int64_t n0;
+  int N, K, groups;
+  MOE_DEV RowPtr operator()(int tile, int stage) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int64_t base = n0 + tile * 16, last = N - 1;
+    const int64_t at = (int64_t)stage * 64 + t * 16;
+    return {q + min(base + g, last) * (K / 2) + at, q + min(base + g + 8, last) * (K / 2) + at,
+            reinterpret_cast<const uint8_t*>(sc + min(base + (lane & 15), last) * groups + stage * (4 / W))};
+  }
+  MOE_DEV void scales(int tile, const S** a, const S** b) const {
+    const int g = (threadIdx.x & 31) >> 2;
+    const int64_t base = n0 + tile * 16, last = N - 1;
+    *a = sc + min(base + g, last) * groups;
+    *b = sc + min(base + g + 8, last) * groups;
+  }
+};
+
+template <typename T, int W, int NT, XSource XS, bool FULL>
+__global__ void __launch_bounds__(kW4Threads, 1) matvec_w4_kernel(MatvecArgs a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  pdl_begin();
+  const uint32_t rings = smem_u32(smem);
+  float* parts = reinterpret_cast<float*>(smem + kRingsBytes);
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int all = (a.N + 15) / 16, stages = (a.K + 127) / 128;
+  StagedAt at;
+  at.x = rings + kRingsBytes + (a.seg_tiles + kW4Warps) * NT * 512;
+  at.low = 0;
+  at.stride = staged_stride(a.K);
+  at.table = at.x + min(a.M, 8) * at.stride;
+  const int first = (int)((int64_t)blockIdx.x * all / gridDim.x);
+  const int last = (int)((int64_t)(blockIdx.x + 1) * all / gridDim.x);
+  const T* x = static_cast<const T*>(a.x);
+  const T* sc = static_cast<const T*>(a.sc);
+  T* y = static_cast<T*>(a.y);
+  for (int t0 = first; t0 < last; t0 += a.seg_tiles) {
+    const int tiles = min(last - t0, a.seg_tiles);
+    const MatvecRows<T, W> rows = {a.q, sc, (int64_t)t0 * 16, a.N, a.K, a.K / (32 * W)};
+    for (int m0 = 0; m0 < a.M; m0 += 8 * NT) {
+      Segment<T, T, W, NT, false, XS, FULL, false, 8, MatvecRows<T, W>> seg(
+          rings, rows, tiles, stages, stages, a.K, sc + (int64_t)a.N * rows.groups);
+      seg.start();
+      const int here = min(a.M - m0, 8 * NT);   // vectors past it repeat the last one, unused
+      if constexpr (XS == kStaged) {   // M <= 8: once
+        if (t0 == first)
+          stage_vectors<T, W, false, 8>(at, here, a.K, [&](int m) { return x + m * a.ld_x; });
+        __syncthreads();
+      }
+      Vectors<T, NT> v;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) v.x[j] = x + (m0 + min(j * 8 + g, here - 1)) * a.ld_x;
+      v.low = 0;
+      v.s = at.x + min(g, here - 1) * at.stride;
+      v.s_low = 0;
+      v.table = at.table + t * 16;
+      seg.finish(v, (here + 7) / 8, parts);
+      __syncthreads();
+      for (int i = threadIdx.x; i < tiles * here * 16; i += kW4Threads) {
+        const int row = i & 15, tile = (i >> 4) / here, col = (i >> 4) - tile * here;
+        const int64_t n = (int64_t)(t0 + tile) * 16 + row;
+        if (n < a.N) {
+          const PartRange w(tile, tiles, stages);
+          y[(m0 + col) * a.ld_y + n] = Elem<T>::from_f(
+              sum_parts(parts, NT * 128, tile, w, (col >> 3) * 128 + row * 8 + (col & 7)));
+        }
+      }
+      __syncthreads();
+    }
+  }
+}
+
+int staged_bytes(int M, int K, int W) { return M * staged_stride(K) + K / (32 * W) * 64; }
+
+// a = NULL: raise the kernel's shared memory limit.
+template <typename T, int W, int NT, XSource XS, bool FULL>
+cudaError_t matvec_launch(const MatvecArgs* a, cudaStream_t s) {
+  auto* kernel = &matvec_w4_kernel<T, W, NT, XS, FULL>;
+  if (a == nullptr) return allow_smem(kernel);
+  const int all = (a->N + 15) / 16;
+  const int sms = device_info()->sm_count;
+  const int blocks = all < sms ? all : sms;
+  const int x_bytes = XS == kStaged ? staged_bytes(a->M, a->K, W) : 0;
+  const int room = (kSmemMost - kRingsBytes - x_bytes) / (NT * 512) - kW4Warps;
+  const int share = (all + blocks - 1) / blocks;
+  MatvecArgs args = *a;
+  args.seg_tiles = share < room ? share : room;
+  const size_t smem = kRingsBytes + (size_t)(args.seg_tiles + kW4Warps) * NT * 512 + x_bytes;
+  return launch_pdl(kernel, dim3(blocks), dim3(kW4Threads), smem, s, args);
+}
+
+// Up to eight vectors are staged while they leave room for the parts of eight
+// tiles; more of them are read where they are.
+template <typename T, int W, bool FULL>
+cudaError_t matvec_nt(const MatvecArgs* a, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if constexpr (FULL) {
+    const bool fits = a != nullptr && a->M <= 8 && a->K <= 65536 &&
+                      staged_bytes(a->M, a->K, W) <= kSmemMost - kRingsBytes - (8 + kW4Warps) * 512;
+    if (a == nullptr || fits) e = matvec_launch<T, W, 1, kStaged, FULL>(a, s);
+    if (fits || e != cudaSuccess) return e;
+  }
+  if (a == nullptr || a->M <= 16) e = matvec_launch<T, W, 2, kNatural, FULL>(a, s);
+  if (e == cudaSuccess && (a == nullptr || a->M > 16)) e = matvec_launch<T, W, 4, kNatural, FULL>(a, s);
+  return e;
+}
+
+template <typename T> cudaError_t matvec_group(int group, const MatvecArgs* a, cudaStream_t s) {
+  const bool full = a == nullptr || a->K % 128 == 0, cut = a == nullptr || !full;
+  cudaError_t e = cudaSuccess;
+  if (group == 32 && full) e = matvec_nt<T, 1, true>(a, s);
+  if (e == cudaSuccess && group == 32 && cut) e = matvec_nt<T, 1, false>(a, s);
+  if (e == cudaSuccess && group == 64 && full) e = matvec_nt<T, 2, true>(a, s);
+  if (e == cudaSuccess && group == 64 && cut) e = matvec_nt<T, 2, false>(a, s);
+  if (e == cudaSuccess && group == 128) e = matvec_nt<T, 4, true>(a, s);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t matvec_w4_init() {
+  cudaError_t e = cudaSuccess;
+  for (int g = 32; g <= 128 && e == cudaSuccess; g *= 2) {
+    e = matvec_group<__nv_bfloat16>(g, nullptr, nullptr);
+    if (e == cudaSuccess) e = matvec_group<__half>(g, nullptr, nullptr);
+  }
+  return e;
+}
+
+cudaError_t launch_matvec_w4(int M, int N, int K, int group, int dtype, const void* x, int64_t ld_x,
+                             const uint8_t* q, const void* scales, void* y, int64_t ld_y,
+                             cudaStream_t s) {
+  const MatvecArgs a = {M, N, K, x, ld_x, q, scales, y, ld_y, 0};
+  return dtype == MOE_DT_BF16 ? matvec_group<__nv_bfloat16>(group, &a, s) : matvec_group<__half>(group, &a, s);
+}
+
+}  // namespace moe
