@@ -176,10 +176,22 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None   # (function, device function) giving the current stream's handle
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            c = torch._C
+            if hasattr(c, "_cuda_getCurrentRawStream") and hasattr(c, "_cuda_getDevice"):
+                # the handle without a Stream object around it (3 us less a call)
+                _raw_stream = (c._cuda_getCurrentRawStream, c._cuda_getDevice)
+            else:
+                _raw_stream = (lambda dev: torch.cuda.current_stream(dev).cuda_stream,
+                               torch.cuda.current_device)
+        return _raw_stream[0](_raw_stream[1]())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -398,43 +410,45 @@ W4_MAX_ROUTES = 4096
 _ADD_NORM = struct.Struct("@qiiii" + "Pq" * 2 + "P" + "Pq" * 2 + "PPPP" + "QQff")
 _ADD_NORM_BWD = struct.Struct("@qiiii" + "Pq" * 3 + "PP" + "Pq" * 2 + "P" + "QQf0q")
 _EXPERTS_W4 = struct.Struct("@7i" + "P" * 10)
-_dtypes = None
+_torch = None
+_dtypes = {}
 
 
 def _dtype(t, what):
-    global _dtypes
-    if _dtypes is None:
-        import torch
-        _dtypes = {torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32}
     dt = _dtypes.get(t.dtype)
-    if dt is None:
-        raise TypeError(f"{what}: {t.dtype} is not bf16, fp16 or fp32")
-    return dt
+    if dt is not None:
+        return dt
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+        _dtypes.update({torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32})
+        return _dtype(t, what)
+    raise TypeError(f"{what}: {t.dtype} is not bf16, fp16 or fp32")
 
 
-def _matrix(t, what, rows=None, cols=None, dtype=None):
+def _shape(x):
+    """(rows, columns) of a tensor whose axes before the last are rows."""
+    d = x.size(-1)
+    return (x.numel() // d if d else 0), d
+
+
+def _matrix(t, what, rows, cols, dtype):
     """(address, row stride) of a matrix on the device, its last axis contiguous;
     axes before the last one are rows (more than one of them: contiguous)."""
     if t is None:
         return 0, 0
     if not t.is_cuda:
         raise ValueError(f"{what}: not a CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what}: {t.dtype}, expected {dtype}")
-    shape = t.shape
-    n = len(shape)
-    if n == 2 and t.stride(1) == 1:
-        r, c, ld = shape[0], shape[1], t.stride(0)
-    elif n and t.is_contiguous():
-        c = shape[-1]
-        r, ld = t.numel() // c if c else 0, c
-    else:
-        raise ValueError(f"{what}: the last axis has to be contiguous (and more than two axes all of it)")
-    if r <= 1:
-        ld = c
-    if (rows is not None and r != rows) or (cols is not None and c != cols):
-        raise ValueError(f"{what}: {r} x {c}, expected {rows} x {cols}")
-    return t.data_ptr(), ld
+    if t.numel() != rows * cols or t.size(-1) != cols:
+        raise ValueError(f"{what}: shape {tuple(t.shape)}, expected {rows} rows of {cols}")
+    if t.is_contiguous():
+        return t.data_ptr(), cols
+    if t.dim() == 2 and t.stride(1) == 1:
+        return t.data_ptr(), t.stride(0)
+    raise ValueError(f"{what}: the last axis has to be contiguous (and more than two axes all of it)")
 
 
 def _flat(t, what, numel, dtype, at_least=False):
@@ -443,7 +457,7 @@ def _flat(t, what, numel, dtype, at_least=False):
         return 0
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}: not a contiguous CUDA tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{what}: {t.dtype}, expected {dtype}")
     if t.numel() != numel and not (at_least and t.numel() > numel):
         raise ValueError(f"{what}: {t.numel()} elements, expected {numel}")
@@ -454,24 +468,28 @@ def add_norm(x, weight, y, residual=None, h=None, rstd=None, eps=1e-5, p=0.0, se
              y_q=None, y_scales=None, y_dq=None, stream=None):
     """moe_add_norm: h = residual + dropout(x), y = h * rstd * weight.  y=None with
     y_q, y_scales (and y_dq): the MXFP8 output, buffers of roundup(rows, 128) rows."""
-    import torch
+    xt = x.dtype
     dt = _dtype(x, "x")
-    d = x.shape[-1]
-    rows = x.numel() // d if d else 0
-    px, ld_x = _matrix(x, "x")
-    stream_t = residual if residual is not None else h
-    rt = dt if stream_t is None else _dtype(stream_t, "residual")
-    pr, ld_r = _matrix(residual, "residual", rows, d)
-    ph, ld_h = _matrix(h, "h", rows, d, None if stream_t is None else stream_t.dtype)
-    py, ld_y = _matrix(y, "y", rows, d, x.dtype)
-    pad = (rows + 127) // 128 * 128
+    rows, d = _shape(x)
+    px, ld_x = _matrix(x, "x", rows, d, xt)
+    like = residual if residual is not None else h   # the stream's type
+    st = xt if like is None else like.dtype
+    pr, ld_r = _matrix(residual, "residual", rows, d, st)
+    ph, ld_h = _matrix(h, "h", rows, d, st)
+    py, ld_y = _matrix(y, "y", rows, d, xt)
+    pq = ps = pd = 0
+    if y_q is not None or y_scales is not None or y_dq is not None:
+        pad = (rows + 127) // 128 * 128
+        pq = _flat(y_q, "y_q", pad * d, _torch.uint8, True)
+        ps = _flat(y_scales, "y_scales", pad * d // 32, _torch.uint8, True)
+        pd = _flat(y_dq, "y_dq", pad * d, _torch.bfloat16, True)
     args = _ADD_NORM.pack(
-        rows, d, dt, rt, _dtype(weight, "weight"), px, ld_x, pr, ld_r,
-        _flat(weight, "weight", d, weight.dtype), ph, ld_h, py, ld_y,
-        _flat(rstd, "rstd", rows, torch.float32), _flat(y_q, "y_q", pad * d, torch.uint8, True),
-        _flat(y_scales, "y_scales", pad * d // 32, torch.uint8, True),
-        _flat(y_dq, "y_dq", pad * d, torch.bfloat16, True), seed, offset, eps, p)
-    _check("moe_add_norm", load().moe_add_norm(args, _stream(stream)))
+        rows, d, dt, dt if like is None else _dtype(like, "residual"), _dtype(weight, "weight"),
+        px, ld_x, pr, ld_r, _flat(weight, "weight", d, weight.dtype), ph, ld_h, py, ld_y,
+        _flat(rstd, "rstd", rows, _torch.float32), pq, ps, pd, seed, offset, eps, p)
+    rc = load().moe_add_norm(args, _stream(stream))
+    if rc:
+        raise MoEError("moe_add_norm", rc)
 
 
 def add_norm_bwd_workspace(rows, d) -> int:
@@ -485,48 +503,50 @@ def add_norm_bwd_workspace(rows, d) -> int:
 def add_norm_bwd(dy, h, rstd, weight, dres=None, dh=None, dx=None, dw=None, ws=None, p=0.0, seed=0,
                  offset=0, stream=None):
     """moe_add_norm_bwd: dh (gradient of the stream), dx (of the dropped input), dw."""
-    import torch
+    xt, ht = dy.dtype, h.dtype
     dt = _dtype(dy, "dy")
-    d = dy.shape[-1]
-    rows = dy.numel() // d if d else 0
-    pdy, ld_dy = _matrix(dy, "dy")
-    ph, ld_h = _matrix(h, "h", rows, d)
-    pdr, ld_dr = _matrix(dres, "dres", rows, d, h.dtype)
-    pdh, ld_dh = _matrix(dh, "dh", rows, d, h.dtype)
-    pdx, ld_dx = _matrix(dx, "dx", rows, d, dy.dtype)
-    pws = 0
+    rows, d = _shape(dy)
+    pdy, ld_dy = _matrix(dy, "dy", rows, d, xt)
+    ph, ld_h = _matrix(h, "h", rows, d, ht)
+    pdr, ld_dr = _matrix(dres, "dres", rows, d, ht)
+    pdh, ld_dh = _matrix(dh, "dh", rows, d, ht)
+    pdx, ld_dx = _matrix(dx, "dx", rows, d, xt)
+    pws = None
     if dw is not None:
-        pws = _flat(ws, "ws", add_norm_bwd_workspace(rows, d), torch.uint8, True)
+        pws = _flat(ws, "ws", add_norm_bwd_workspace(rows, d), _torch.uint8, True) or None
     args = _ADD_NORM_BWD.pack(
         rows, d, dt, _dtype(h, "h"), _dtype(weight, "weight"), pdy, ld_dy, ph, ld_h, pdr, ld_dr,
-        _flat(rstd, "rstd", rows, torch.float32), _flat(weight, "weight", d, weight.dtype),
-        pdh, ld_dh, pdx, ld_dx, _flat(dw, "dw", d, torch.float32), seed, offset, p)
-    _check("moe_add_norm_bwd", load().moe_add_norm_bwd(args, pws or None, _stream(stream)))
+        _flat(rstd, "rstd", rows, _torch.float32), _flat(weight, "weight", d, weight.dtype),
+        pdh, ld_dh, pdx, ld_dx, _flat(dw, "dw", d, _torch.float32), seed, offset, p)
+    rc = load().moe_add_norm_bwd(args, pws, _stream(stream))
+    if rc:
+        raise MoEError("moe_add_norm_bwd", rc)
 
 
 def dropout(x, y, p, seed, offset=0, stream=None):
     """moe_dropout: y = dropout(x), the mask a function of (seed, offset, row,
     column); the backward is the same call on the gradient."""
     dt = _dtype(x, "x")
-    d = x.shape[-1]
-    rows = x.numel() // d if d else 0
-    px, ld_x = _matrix(x, "x")
+    rows, d = _shape(x)
+    px, ld_x = _matrix(x, "x", rows, d, x.dtype)
     py, ld_y = _matrix(y, "y", rows, d, x.dtype)
-    _check("moe_dropout", load().moe_dropout(rows, d, dt, px, ld_x, py, ld_y, p, seed, offset,
-                                             _stream(stream)))
+    rc = load().moe_dropout(rows, d, dt, px, ld_x, py, ld_y, p, seed, offset, _stream(stream))
+    if rc:
+        raise MoEError("moe_dropout", rc)
 
 
 def _w4(q, scales, what):
     """(rows, K, group) of 4-bit weights, from the shapes of codes and scales."""
-    import torch
-    if q.dtype != torch.uint8:
+    _dtype(scales, what)
+    if q.dtype is not _torch.uint8:
         raise TypeError(f"{what}: codes are {q.dtype}, expected uint8")
-    K, ng = 2 * q.shape[-1], scales.shape[-1]
-    if q.shape[:-1] != scales.shape[:-1] or ng == 0 or K % ng:
+    half, ng = q.size(-1), scales.size(-1)
+    K, rows = 2 * half, (q.numel() // half if half else 0)
+    if ng == 0 or K % ng or q.shape[:-1] != scales.shape[:-1]:
         raise ValueError(f"{what}: codes {tuple(q.shape)} and scales {tuple(scales.shape)} do not belong together")
     if not (q.is_cuda and scales.is_cuda and q.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{what}: not contiguous CUDA tensors")
-    return q.numel() // q.shape[-1], K, K // ng
+    return rows, K, K // ng
 
 
 def quantize_w4(src, q, scales, stream=None):
@@ -540,9 +560,8 @@ def quantize_w4(src, q, scales, stream=None):
 
 def dequantize_w4(q, scales, out, stream=None):
     """moe_dequantize_w4: the weights that codes and scales stand for, fp32."""
-    import torch
     rows, K, g = _w4(q, scales, "dequantize_w4")
-    po = _flat(out, "out", rows * K, torch.float32)
+    po = _flat(out, "out", rows * K, _torch.float32)
     _check("moe_dequantize_w4", load().moe_dequantize_w4(
         rows, K, g, _dtype(scales, "scales"), q.data_ptr(), scales.data_ptr(), po, _stream(stream)))
 
@@ -550,11 +569,14 @@ def dequantize_w4(q, scales, out, stream=None):
 def matvec_w4(x, q, scales, y, stream=None):
     """moe_matvec_w4: y [M, N] = x [M, K] times the 4-bit weights [N, K] transposed."""
     N, K, g = _w4(q, scales, "matvec_w4")
-    M = x.numel() // K
-    px, ld_x = _matrix(x, "x", M, K, scales.dtype)
-    py, ld_y = _matrix(y, "y", M, N, scales.dtype)
-    _check("moe_matvec_w4", load().moe_matvec_w4(M, N, K, g, _dtype(x, "x"), px, ld_x, q.data_ptr(),
-                                                 scales.data_ptr(), py, ld_y, _stream(stream)))
+    dt = scales.dtype
+    M = x.numel() // K if K else 0
+    px, ld_x = _matrix(x, "x", M, K, dt)
+    py, ld_y = _matrix(y, "y", M, N, dt)
+    rc = load().moe_matvec_w4(M, N, K, g, _dtypes[dt], px, ld_x, q.data_ptr(), scales.data_ptr(),
+                              py, ld_y, _stream(stream))
+    if rc:
+        raise MoEError("moe_matvec_w4", rc)
 
 
 def experts_w4_workspace(T, d, E, k, f) -> int:
@@ -569,24 +591,27 @@ def experts_w4(x, topk_idx, gates, w: dict, out, ws, stream=None):
     """moe_experts_w4: the SwiGLU experts on 4-bit weights for a few tokens.  `w`
     holds gate_q, gate_s, up_q, up_s [E, f, ...] and down_q, down_s [E, d, ...];
     an index of -1 in topk_idx stands for no expert."""
-    import torch
     T, k = topk_idx.shape
-    E, f = w["gate_q"].shape[:2]
-    d = x.shape[-1]
-    shapes = [_w4(w[n + "_q"], w[n + "_s"], n) for n in ("gate", "up", "down")]
+    gq, uq, dq = w["gate_q"], w["up_q"], w["down_q"]
+    gs, us, ds = w["gate_s"], w["up_s"], w["down_s"]
+    E, f = gq.size(0), gq.size(1)
+    d = x.size(-1)
+    shapes = (_w4(gq, gs, "gate"), _w4(uq, us, "up"), _w4(dq, ds, "down"))
     g = shapes[0][2]
-    if shapes != [(E * f, d, g), (E * f, d, g), (E * d, f, g)]:
+    if shapes != ((E * f, d, g), (E * f, d, g), (E * d, f, g)):
         raise ValueError(f"experts_w4: weights {shapes} do not fit E={E}, d={d}, f={f}")
     dt = x.dtype
-    if any(w[n + "_s"].dtype != dt for n in ("gate", "up", "down")):
+    if gs.dtype is not dt or us.dtype is not dt or ds.dtype is not dt:
         raise TypeError("experts_w4: scales of another type than x")
     args = _EXPERTS_W4.pack(
         T, d, E, k, f, g, _dtype(x, "x"), _flat(x, "x", T * d, dt),
-        _flat(topk_idx, "topk_idx", T * k, torch.int32), _flat(gates, "gates", T * k, torch.float32),
-        *(w[n].data_ptr() for n in ("gate_q", "gate_s", "up_q", "up_s", "down_q", "down_s")),
+        _flat(topk_idx, "topk_idx", T * k, _torch.int32), _flat(gates, "gates", T * k, _torch.float32),
+        gq.data_ptr(), gs.data_ptr(), uq.data_ptr(), us.data_ptr(), dq.data_ptr(), ds.data_ptr(),
         _flat(out, "out", T * d, dt))
-    pws = _flat(ws, "ws", experts_w4_workspace(T, d, E, k, f), torch.uint8, True)
-    _check("moe_experts_w4", load().moe_experts_w4(args, pws, _stream(stream)))
+    pws = _flat(ws, "ws", experts_w4_workspace(T, d, E, k, f), _torch.uint8, True)
+    rc = load().moe_experts_w4(args, pws, _stream(stream))
+    if rc:
+        raise MoEError("moe_experts_w4", rc)
 
 
 # ------------------------------------------------------------------ buffers

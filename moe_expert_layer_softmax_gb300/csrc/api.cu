@@ -309,8 +309,10 @@ int moe_init(int device) {
   int sms = 0;
   MOE_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device));
   MOE_CUDA(gemm_init_attributes());
+  MOE_CUDA(norm_init());
   MOE_CUDA(matvec_w4_init());
-  MOE_CUDA(experts_w4_init());
+  MOE_CUDA(experts_w4_init_bf16());
+  MOE_CUDA(experts_w4_init_f16());
   noalloc_forget_device(device);
   g_dev[device].sm_count = sms;
   g_dev[device].ready = true;

@@ -149,7 +149,7 @@ int moe_add_norm(const moe_add_norm_args_t* a, void* stream) {
 int moe_add_norm_bwd_workspace_size(int64_t rows, int32_t d, size_t* ws_bytes) {
   if (rows < 0 || d < 1 || ws_bytes == nullptr) return MOE_ERR_INVALID;
   if (d > kNormMaxWidth || rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
-  *ws_bytes = round256((size_t)norm_partial_rows(rows, d) * d * 4);
+  *ws_bytes = round256((size_t)(rows < kNormPartialRows ? rows : kNormPartialRows) * d * 4);
   return MOE_OK;
 }
 
@@ -289,9 +289,9 @@ int moe_experts_w4(const moe_experts_w4_args_t* a, void* ws, void* stream) {
   p.err = reinterpret_cast<int32_t*>(w);
   p.act = w + 256;
   p.y = reinterpret_cast<float*>(w + 256 + round256(R * a->d_ff * 4));
-  return launch_experts_w4(p, a->dtype, static_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  const cudaError_t e = a->dtype == MOE_DT_BF16 ? launch_experts_w4_bf16(p, st) : launch_experts_w4_f16(p, st);
+  return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
 }
 
 }  // extern "C"

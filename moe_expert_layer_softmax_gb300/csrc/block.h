@@ -63,9 +63,9 @@ struct DropoutParams {
 };
 
 constexpr int kNormMaxWidth = 32768;     // 1024 threads, four groups of eight columns each
-constexpr int kNormPartialRows = 1216;   // most rows of partial weight gradients
+constexpr int kNormPartialRows = 1024;   // rows of partial weight gradients: blocks of the backward
 
-int64_t norm_partial_rows(int64_t rows, int d);
+cudaError_t norm_init();   // dynamic shared memory limits (moe_init)
 cudaError_t launch_add_norm(AddNormParams p, int dtype, int res_dtype, bool vec, cudaStream_t s);
 cudaError_t launch_add_norm_bwd(AddNormBwdParams p, int dtype, int res_dtype, bool vec, float* dw,
                                 cudaStream_t s);
@@ -90,7 +90,8 @@ struct ExpertsW4Params {
 };
 
 cudaError_t matvec_w4_init();    // dynamic shared memory limits (moe_init)
-cudaError_t experts_w4_init();
+cudaError_t experts_w4_init_bf16();
+cudaError_t experts_w4_init_f16();
 cudaError_t launch_quantize_w4(int64_t rows, int K, int group, int dtype, const void* src,
                                uint8_t* q, void* scales, cudaStream_t s);
 cudaError_t launch_dequantize_w4(int64_t rows, int K, int group, int dtype, const uint8_t* q,
@@ -98,6 +99,7 @@ cudaError_t launch_dequantize_w4(int64_t rows, int K, int group, int dtype, cons
 cudaError_t launch_matvec_w4(int M, int N, int K, int group, int dtype, const void* x, int64_t ld_x,
                              const uint8_t* q, const void* scales, void* y, int64_t ld_y,
                              cudaStream_t s);
-cudaError_t launch_experts_w4(const ExpertsW4Params& p, int dtype, cudaStream_t s);
+cudaError_t launch_experts_w4_bf16(const ExpertsW4Params& p, cudaStream_t s);
+cudaError_t launch_experts_w4_f16(const ExpertsW4Params& p, cudaStream_t s);
 
 }  // namespace moe

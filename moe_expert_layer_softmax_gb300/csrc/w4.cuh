@@ -99,32 +99,30 @@ MOE_DEV void codes_fp16(uint32_t w, uint32_t* a) {
   a[3] = u & 0x00F000F0u;
 }
 
+// The warp's number, known to be the same in all its lanes: what follows from it
+// (shares, counters, slots) then stays in uniform registers.
+MOE_DEV int warp_id() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+
 // ------------------------------------------------------------------ weight stream
 // A warp works on tiles of 16 weight rows.  A stage is 128 columns of a tile (1
-// KB of codes and the scales); the lanes copy it in 16-byte pieces with cp.async
-// into the warp's own ring, kRing - 1 stages ahead, past L1.  Only the warp
-// itself waits for its ring, so no barrier of the block lies in the loop, and
-// five stages a warp stay in flight without registers.
-constexpr int kRing = 6;
-constexpr int kStageBytes = 1024 + 128;   // codes, scales (16 rows x 8 bytes)
-constexpr int kRingBytes = kRing * kStageBytes;
+// KB of codes and the scales), a step two stages; the lanes copy a step in
+// 16-byte pieces with cp.async into the warp's own ring, kRing - 1 steps ahead,
+// past L1.  Only the warp itself waits for its ring, so no barrier of the block
+// lies in the loop, and six stages a warp stay in flight without registers.  The
+// two stages of a step are independent chains of matrix instructions.
+constexpr int kRing = 3;
+constexpr int kStepBytes = 2048 + 256;   // 16 rows of 128 bytes of codes, 16 of 16 bytes for scales
+constexpr int kRingBytes = kRing * kStepBytes;
 constexpr int kRingsBytes = kW4Warps * kRingBytes;
 constexpr int kSmemMost = 227 * 1024;
 
-MOE_DEV void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 template <int N> MOE_DEV void cp_async_small(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(bytes) : "memory");
 }
-MOE_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> MOE_DEV void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
-// 16-byte pieces of a row's 64 bytes are permuted by the row, so that lanes
-// reading one, two or four words of eight rows touch every bank once.
-MOE_DEV int piece_swizzle(int g) { return ((g >> 1) & 1) << 1 | ((g >> 2) & 1); }
+// The eight 16-byte pieces of a row's 128 bytes are permuted by the row, so that
+// lanes reading one, two or four words of eight rows touch every bank once.
+MOE_DEV int piece_swizzle(int g) { return (g & 1) << 2 | ((g >> 1) & 1) << 1 | ((g >> 2) & 1); }
 
 // Where a lane finds its vectors.
 //   kStaged   in shared memory, as fp16 with a power of two per 128 columns
@@ -166,113 +164,148 @@ template <int W> MOE_DEV Words<W> load_words(uint32_t at) {
   return r;
 }
 
-// What a tile's rows are, for this lane: codes of rows g and g + 8 (its piece t
-// of a stage) and scales of row lane % 16, at some stage.
+// A tile's rows as this lane copies them, from some stage on: its piece (lane %
+// 8) of rows lane / 8 + 0, 4, 8 and 12, and the scales of row lane % 16.
 struct RowPtr {
-  const uint8_t* a;
-  const uint8_t* b;
+  const uint8_t* row[4];
   const uint8_t* s;
 };
 
-// One warp's share of a segment: `tiles` tiles of `stages` stages each.  The
-// rows of a tile are contiguous for `run` stages (RUNS: run < stages, each run of
-// the same K); rows(tile, stage) gives the pointers where a run starts or the
-// share does.  Parts of tiles go to parts[tile + warp] (NT x 16 rows x 8 vectors
-// each): the slot is the warp's own, since a warp starts no earlier than in the
-// tile where the one before it ends.
+// One warp's share of a segment: `tiles` tiles of `runs` runs of `run` stages
+// each; a run's rows are contiguous (RUNS: more than one run a tile).  The share
+// is counted in steps; a run's last step is half a step where `run` is odd.
+// rows(tile, r, stage) gives the pointers to a stage of run r.  Parts of tiles go
+// to parts[tile + warp] (NT x 16 rows x 8 vectors each): the slot is the warp's
+// own, since a warp starts no earlier than in the tile where the one before it
+// ends.
 //   FULL   K is a multiple of 128, scales come through the ring; otherwise (K
 //          32 or 64 more than that) the last stage is cut and the scales are
 //          read directly
 //   T      type of the vectors, S of the scales;  LOW: a vector has two parts
-//   VC     vectors that the table of kStaged is for: 8, or 1 (all columns the same)
+//   VC     vectors that the table of kStaged is for: 8 or 1
 template <typename T, typename S, int W, int NT, bool LOW, XSource XS, bool FULL, bool RUNS, int VC, typename Rows>
 struct Segment {
   static constexpr int kScales = 4 / W;   // of a row in a stage
   using Mma = MmaT<T>;
-  const Rows& rows;
-  uint32_t put, get, swz, scl, ring;
-  int stages, run, groups, v0, n;
-  int copy_tile, copy_stage, copy_left, copy_run;   // next stage to copy
-  int row_bytes;
-  RowPtr r;
+  Rows rows;
+  uint32_t put, put4, get, swz, scl, sget;
+  int run, runs, steps, groups, n;   // steps of a run, of the share
+  int tile0, run0, step0;            // where the share begins: tile, run, step of the run
+  int copy_tile, copy_run, copy_step;   // the next step to copy
+  RowPtr r;                          // of the next step to copy
+  uint32_t copy_slot;                // bytes
+  int copy_left;                     // steps to copy
   const uint8_t* scales_end;
 
-  MOE_DEV Segment(uint32_t rings, const Rows& rows_, int tiles, int stages_, int run_, int K,
+  MOE_DEV Segment(uint32_t rings, const Rows& rows_, int tiles, int runs_, int run_, int K,
                   const void* scales_end_)
-      : rows(rows_), stages(stages_), run(run_), groups(K / (32 * W)), row_bytes(K / 2),
+      : rows(rows_), run(run_), runs(RUNS ? runs_ : 1), steps((run_ + 1) / 2), groups(K / (32 * W)),
         scales_end(static_cast<const uint8_t*>(scales_end_)) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    ring = rings + warp * kRingBytes;
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    const uint32_t ring = rings + warp_id() * kRingBytes;
     swz = piece_swizzle(g) << 4;
-    put = ring + g * 64 + ((t << 4) ^ swz);
-    get = ring + g * 64;
-    scl = ring + 1024 + (lane & 15) * 8;
-    const int V = tiles * stages;
-    v0 = warp * V / kW4Warps;
-    n = (warp + 1) * V / kW4Warps - v0;
-    copy_tile = v0 / stages;
-    copy_stage = v0 - copy_tile * stages;
-    copy_run = RUNS ? run - copy_stage % run : 0;
-    copy_left = n;
-    if (n > 0) r = rows(copy_tile, copy_stage);
+    get = ring + g * 128;
+    // rows lane / 8 and 4 more have swizzles that differ in the lowest bit alone
+    put = ring + (lane >> 3) * 128 + (((lane & 7) ^ piece_swizzle(lane >> 3)) << 4);
+    put4 = ring + ((lane >> 3) + 4) * 128 + (((lane & 7) ^ piece_swizzle((lane >> 3) + 4)) << 4);
+    scl = ring + 2048 + (lane & 15) * 16;
+    sget = ring + 2048 + g * 16;
+    reset(tiles);
   }
 
-  MOE_DEV void copy(int slot) {
-    const int lane = threadIdx.x & 31;
+  // A segment of as many tiles of the same kind (rows may have changed).
+  MOE_DEV void reset(int tiles) {
+    const int warp = warp_id();
+    tiles = __shfl_sync(0xffffffffu, tiles, 0);
+    const int per = steps * runs, V = tiles * per, v0 = warp * V / kW4Warps;
+    n = (warp + 1) * V / kW4Warps - v0;
+    tile0 = v0 / per;
+    const int in = v0 - tile0 * per;
+    run0 = RUNS ? in / steps : 0;
+    step0 = in - run0 * steps;
+    copy_tile = tile0;
+    copy_run = run0;
+    copy_step = step0;
+    copy_left = n;
+    if (n > 0) r = rows(copy_tile, copy_run, copy_step * 2);
+  }
+
+  MOE_DEV static uint32_t next_slot(uint32_t slot) {
+    return slot == (kRing - 1) * kStepBytes ? 0 : slot + kStepBytes;
+  }
+
+  MOE_DEV void copy() {
     if (copy_left > 0) {
-      const bool there = FULL || (copy_stage * 64 + (lane & 3) * 16) < row_bytes;
-      if (there) {
-        cp_async16(put + slot * kStageBytes, r.a);
-        cp_async16(put + slot * kStageBytes + 512, r.b);
+      const int lane = threadIdx.x & 31;
+      // the second half of a run's last step may lie past its end
+      const bool two = copy_step * 2 + 1 < run;
+      if (FULL ? (lane & 4) == 0 || two : copy_step * 128 + (lane & 7) * 16 < groups * (16 * W)) {
+        cp_async16(put + copy_slot, r.row[0]);
+        cp_async16(put4 + copy_slot, r.row[1]);
+        cp_async16(put + copy_slot + 1024, r.row[2]);
+        cp_async16(put4 + copy_slot + 1024, r.row[3]);
       }
       if (FULL && lane < 16) {
-        if constexpr (W == 4) {   // one scale: the aligned word that holds it
-          const uint8_t* w = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(r.s) & ~uintptr_t(3));
-          cp_async_small<4>(scl + slot * kStageBytes, w, w + 4 > scales_end ? 2 : 4);
+        const uint32_t to = scl + copy_slot;
+        if constexpr (W == 4) {   // two scales: the aligned words that hold them
+          const uint8_t* p = reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(r.s) & ~uintptr_t(3));
+          cp_async_small<4>(to, p, p + 4 > scales_end ? 2 : 4);
+          if (groups & 1) {   // every other row starts in the middle of a word
+            const int there = two ? (p + 8 > scales_end ? (p + 4 >= scales_end ? 0 : 2) : 4) : 0;
+            cp_async_small<4>(to + 4, there ? p + 4 : p, there);
+          }
         } else {
-          cp_async_small<2 * kScales>(scl + slot * kStageBytes, r.s, 2 * kScales);
+          cp_async_small<2 * kScales>(to, r.s, 2 * kScales);
+          if (two) cp_async_small<2 * kScales>(to + 2 * kScales, r.s + 2 * kScales, 2 * kScales);
         }
       }
-      r.a += 64;
-      r.b += 64;
-      r.s += 2 * kScales;
-      ++copy_stage;
+      copy_slot = next_slot(copy_slot);
       --copy_left;
-      bool turn = copy_stage == stages;
-      if (turn) {
-        copy_stage = 0;
-        ++copy_tile;
+      if (++copy_step == steps) {
+        if (copy_left > 0) {
+          copy_step = 0;
+          if (!RUNS || ++copy_run == runs) {
+            copy_run = 0;
+            ++copy_tile;
+          }
+          r = rows(copy_tile, copy_run, 0);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.row[i] += 128;
+        r.s += 4 * kScales;
       }
-      if (RUNS && --copy_run == 0) {
-        turn = true;
-        copy_run = run;
-      }
-      if (turn && copy_left > 0) r = rows(copy_tile, copy_stage);
     }
     cp_async_commit();
   }
 
+  // Fill the ring (empty before).
   MOE_DEV void start() {
-#pragma unroll
-    for (int i = 0; i < kRing - 1; ++i) copy(i);
+    copy_slot = 0;
+#pragma unroll 1
+    for (int i = 0; i < kRing - 1; ++i) copy();
   }
 
-  // The scales of a stage's groups for this lane's rows g and g + 8; `q` is the
-  // stage within its run.
-  MOE_DEV void load_scales(int slot, int tile, int stage, int q, float* fa, float* fb) const {
-    const int lane = threadIdx.x & 31, g = lane >> 2;
+  // Where the consumer stands.
+  struct At {
+    int tile, stage;        // stage: within its run
+    uint32_t slot;
+    uint32_t half;          // W = 4: byte of a step's first scale in its word
+    uint32_t x, low, table;
+  };
+
+  // The scales of a stage's groups for this lane's rows g and g + 8.
+  MOE_DEV void load_scales(int h, const At& at, float* fa, float* fb) const {
     if constexpr (FULL) {
-      const uint32_t at = ring + slot * kStageBytes + 1024 + g * 8;
+      const uint32_t from = sget + at.slot + h * (2 * kScales);
       if constexpr (W == 4) {
-        // rows are numbered from an even one: the half-word is known from g
-        const uint32_t half = at + (((g * groups + q) & 1) << 1);
         uint16_t a, b;
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(a) : "r"(half));
-        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(half + 64));
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(a) : "r"(from + at.half));
+        asm volatile("ld.shared.u16 %0, [%1];" : "=h"(b) : "r"(from + at.half + 128));
         fa[0] = Elem<S>::to_f(*reinterpret_cast<S*>(&a));
         fb[0] = Elem<S>::to_f(*reinterpret_cast<S*>(&b));
       } else {
-        const Words<kScales / 2> a = load_words<kScales / 2>(at), b = load_words<kScales / 2>(at + 64);
+        const Words<kScales / 2> a = load_words<kScales / 2>(from), b = load_words<kScales / 2>(from + 128);
         const S* pa = reinterpret_cast<const S*>(&a);
         const S* pb = reinterpret_cast<const S*>(&b);
 #pragma unroll
@@ -280,28 +313,28 @@ struct Segment {
       }
     } else {
       const S *pa, *pb;
-      rows.scales(tile, &pa, &pb);
+      rows.scales(at.tile, &pa, &pb);
 #pragma unroll
       for (int j = 0; j < kScales; ++j) {
-        const int i = stage * kScales + j;
+        const int i = (at.stage + h) * kScales + j;
         fa[j] = i < groups ? Elem<S>::to_f(pa[i]) : 0.0f;
         fb[j] = i < groups ? Elem<S>::to_f(pb[i]) : 0.0f;
       }
     }
   }
 
-  MOE_DEV void product(int slot, int tile, int stage, int q, const Vectors<T, NT>& v, int nt,
-                       float (*acc)[4]) const {
+  // Stage h of the present step.
+  MOE_DEV void product(int h, const At& at, const Vectors<T, NT>& v, int nt, float (*acc)[4]) const {
     const int t = threadIdx.x & 3;
     float fa[kScales], fb[kScales];
-    load_scales(slot, tile, stage, q, fa, fb);
+    load_scales(h, at, fa, fb);
     const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < kScales; ++j) {
-      if (!FULL && stage * kScales + j >= groups) break;
-      const int at = (j * 4 * W + t * W) * 4;   // byte of the row's 64
-      const uint32_t p = get + ((at & 48) ^ swz) + (at & 15) + slot * kStageBytes;
-      const Words<W> wa = load_words<W>(p), wb = load_words<W>(p + 512);
+      if (!FULL && (at.stage + h) * kScales + j >= groups) break;
+      const int byte = h * 64 + (j * 4 * W + t * W) * 4;   // of the row's 128
+      const uint32_t p = get + ((byte & 112) ^ swz) + (byte & 15) + at.slot;
+      const Words<W> wa = load_words<W>(p), wb = load_words<W>(p + 1024);
       if constexpr (XS == kStaged) {
         float c[4], cl[4];
 #pragma unroll
@@ -309,18 +342,18 @@ struct Segment {
           uint32_t a[4], b[4];
           codes_fp16(wa.w[i], a);
           codes_fp16(wb.w[i], b);
-          const uint32_t to = stage * 256 + t * 16 + (j * W + i) * 64;
-          const Words<4> x = load_words<4>(v.s + to);
+          const int to = h * 256 + (j * W + i) * 64;
+          const Words<4> x = load_words<4>(at.x + to);
           MmaT<__half>::mma(c, i == 0 ? zero : c, a[0], b[0], a[1], b[1], x.w[0], x.w[1]);
           MmaT<__half>::mma(c, c, a[2], b[2], a[3], b[3], x.w[2], x.w[3]);
           if constexpr (LOW) {
-            const Words<4> y = load_words<4>(v.s_low + to);
+            const Words<4> y = load_words<4>(at.low + to);
             MmaT<__half>::mma(cl, i == 0 ? zero : cl, a[0], b[0], a[1], b[1], y.w[0], y.w[1]);
             MmaT<__half>::mma(cl, cl, a[2], b[2], a[3], b[3], y.w[2], y.w[3]);
           }
         }
         float f0, s0, f1, s1;   // factor and 8 times the group's sum, of two columns
-        const uint32_t entry = v.table + (stage * kScales + j) * (VC * 8);
+        const uint32_t entry = at.table + (h * kScales + j) * (VC * 8);
         if constexpr (VC == 8) {
           asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f0), "=f"(s0), "=f"(f1), "=f"(s1) : "r"(entry));
         } else {
@@ -350,9 +383,9 @@ struct Segment {
               for (int part = 0; part < (LOW ? 2 : 1); ++part) {
                 uint4 x;
                 if constexpr (XS == kOrdered)
-                  x = *reinterpret_cast<const uint4*>(v.x[m] + part * v.low + stage * 128 + ((j * W + i) * 4 + t) * 8);
+                  x = *reinterpret_cast<const uint4*>(v.x[m] + part * v.low + (at.stage + h) * 128 + ((j * W + i) * 4 + t) * 8);
                 else
-                  x = order_piece(*reinterpret_cast<const uint4*>(v.x[m] + stage * 128 + j * 32 * W + t * 8 * W + i * 8));
+                  x = order_piece(*reinterpret_cast<const uint4*>(v.x[m] + (at.stage + h) * 128 + j * 32 * W + t * 8 * W + i * 8));
                 Mma::mma(c[m], i == 0 && part == 0 ? zero : c[m], a[0], b[0], a[1], b[1], x.x, x.y);
                 Mma::mma(c[m], c[m], a[2], b[2], a[3], b[3], x.z, x.w);
               }
@@ -385,43 +418,69 @@ struct Segment {
   }
 
   MOE_DEV void finish(const Vectors<T, NT>& v, int nt, float* parts) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float acc[NT][4];
 #pragma unroll
     for (int m = 0; m < NT; ++m)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[m][i] = 0.0f;
-    int tile = v0 / stages, stage = v0 - tile * stages;
-    int q = RUNS ? stage % run : stage;
-    for (int i0 = 0; i0 < n; i0 += kRing) {
-#pragma unroll
-      for (int u = 0; u < kRing; ++u) {
-        if (i0 + u >= n) break;
-        copy((u + kRing - 1) % kRing);
-        cp_async_wait<kRing - 1>();
-        __syncwarp();
-        product(u, tile, stage, RUNS ? q : stage, v, nt, acc);
-        __syncwarp();   // the slot is free for every lane's next copy
-        if (RUNS && ++q == run) q = 0;
-        if (++stage == stages) {
-          store_part(parts, tile, acc);
-          stage = 0;
-          ++tile;
+    At at;
+    // rows are numbered from an even one: a scale's half-word is known from g
+    // (a step starts at an even stage)
+    at.half = W == 4 ? (uint32_t)((g * groups) & 1) << 1 : 0;
+    at.tile = tile0;
+    at.stage = step0 * 2;
+    int in_run = run0, turn = steps - step0, left = n;
+    at.slot = 0;
+    auto enter = [&](int step) {   // at a step of run in_run
+      const int stage = (RUNS ? in_run * run : 0) + step * 2;
+      at.x = v.s + t * 16 + stage * 256;
+      at.low = v.s_low + t * 16 + stage * 256;
+      at.table = v.table + stage * kScales * VC * 8;
+    };
+    enter(step0);
+#pragma unroll 1
+    for (; left > 0; --left) {
+      copy();   // into the slot of the step before
+      cp_async_wait<kRing - 1>();
+      __syncwarp();
+      if (at.stage + 1 < run) {
+        product(0, at, v, nt, acc);
+        product(1, at, v, nt, acc);
+      } else {
+        product(0, at, v, nt, acc);
+      }
+      __syncwarp();   // the slot is free for every lane's next copy
+      at.slot = next_slot(at.slot);
+      at.stage += 2;
+      at.x += 512;
+      at.low += 512;
+      at.table += 2 * kScales * VC * 8;
+      if (--turn == 0) {
+        turn = steps;
+        at.stage = 0;
+        if (!RUNS || ++in_run == runs) {
+          in_run = 0;
+          store_part(parts, at.tile, acc);
+          ++at.tile;
         }
+        enter(0);
       }
     }
-    // a warp without stages leaves zeros: its slot lies among its tile's parts
-    if (n == 0 || stage != 0) store_part(parts, tile, acc);
+    // a warp without steps leaves zeros: its slot lies among its tile's parts
+    if (n == 0 || turn != steps || in_run != 0) store_part(parts, at.tile, acc);
     cp_async_wait<0>();
   }
 };
 
 // Sum of a tile's parts at `at` (vector tile * 128 + row * 8 + vector), warp by
-// warp: warp_of(v) is the warp whose share has stage v of V.
+// warp: warp_of(v) is the warp whose share has step v of V.
 MOE_DEV int warp_of(int v, int V) { return (int)((uint32_t)(kW4Warps * (v + 1) - 1) / (uint32_t)V); }
 struct PartRange {
   int first, last;
-  MOE_DEV PartRange(int tile, int tiles, int stages)
-      : first(warp_of(tile * stages, tiles * stages)), last(warp_of(tile * stages + stages - 1, tiles * stages)) {}
+  // `per`: steps of a tile
+  MOE_DEV PartRange(int tile, int tiles, int per)
+      : first(warp_of(tile * per, tiles * per)), last(warp_of(tile * per + per - 1, tiles * per)) {}
 };
 MOE_DEV float sum_parts(const float* parts, int slot_floats, int tile, const PartRange& w, int at) {
   float s = 0.0f;
@@ -448,9 +507,9 @@ struct StagedAt {
   uint32_t table;         // entries [group][vectors of the table]
 };
 
-MOE_DEV void load_f8(const __nv_bfloat16* p, float* f) { widen8(load8<__nv_bfloat16, true>(p, 0, 8), f); }
-MOE_DEV void load_f8(const __half* p, float* f) { widen8(load8<__half, true>(p, 0, 8), f); }
-MOE_DEV void load_f8(const float* p, float* f) { widen8(load8<float, true>(p, 0, 8), f); }
+MOE_DEV void load_f8(const __nv_bfloat16* p, float* f) { widen8(load8<__nv_bfloat16, true>(p, 0, 1, 8), f); }
+MOE_DEV void load_f8(const __half* p, float* f) { widen8(load8<__half, true>(p, 0, 1, 8), f); }
+MOE_DEV void load_f8(const float* p, float* f) { widen8(load8<float, true>(p, 0, 1, 8), f); }
 
 // Stage `count` vectors of K values (K a multiple of 128); row(m) is vector m.
 // Every thread of the block calls; no barrier.
@@ -463,6 +522,7 @@ MOE_DEV void stage_vectors(const StagedAt& at, int count, int K, Row row) {
     int m[U], c[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (base + u * kW4Threads >= all) break;
       const int i = base + u * kW4Threads + threadIdx.x;
       m[u] = i / pieces;
       c[u] = i - m[u] * pieces;
@@ -476,6 +536,7 @@ MOE_DEV void stage_vectors(const StagedAt& at, int count, int K, Row row) {
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
+      if (base + u * kW4Threads >= all) break;
       float top = 0.0f, sum = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -512,6 +573,11 @@ MOE_DEV void stage_vectors(const StagedAt& at, int count, int K, Row row) {
       }
     }
   }
+}
+
+// Bring [at, at + bytes) (16-byte aligned, whole) into L2.
+MOE_DEV void prefetch_l2(const void* at, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
 }
 
 // Raise a kernel's dynamic shared memory limit (once, from moe_init).

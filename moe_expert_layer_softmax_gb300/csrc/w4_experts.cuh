@@ -10,6 +10,9 @@
 // (fp16, act in two parts); more: they read them from global memory, x as it is
 // and act as two bf16 parts in fragment order.  Either way act keeps 16 bits or
 // more, so that storing it costs no accuracy beside a bf16 or fp16 result.
+// (Included by one file per type, so that they compile side by side.)
+#pragma once
+
 #include "w4.cuh"
 
 namespace moe {
@@ -31,28 +34,31 @@ struct Lists {
   uint8_t* used;        // [256]
   int16_t* expert_of;   // [R], -1: none
   uint16_t* routes;     // [R]
+  float* gates;         // [R] gates of `routes` (first kernel)
 };
 constexpr int kListsFixed = (256 + 1 + kW4Warps + 257) * 4 + 256 + 8;
 static_assert(kListsFixed % 16 == 0, "the route lists follow");
-__host__ __device__ inline int lists_bytes(int R) { return kListsFixed + ((R * 4 + 15) & ~15); }
+__host__ __device__ inline int lists_bytes(int R) { return kListsFixed + ((R * 8 + 15) & ~15); }
 MOE_DEV Lists lists_at(uint8_t* p, int R) {
   Lists l;
   l.counts = reinterpret_cast<int32_t*>(p);
   l.before = l.counts + 257 + kW4Warps;
   l.used = reinterpret_cast<uint8_t*>(l.before + 257);
-  l.expert_of = reinterpret_cast<int16_t*>(p + kListsFixed);
+  l.gates = reinterpret_cast<float*>(p + kListsFixed);
+  l.expert_of = reinterpret_cast<int16_t*>(l.gates + R);
   l.routes = reinterpret_cast<uint16_t*>(l.expert_of + R);
   return l;
 }
 
-// Experts with routes, ascending; returns their number.  Every thread calls.
-MOE_DEV int find_used(const Lists& l, const int32_t* idx, int R, int E, int most) {
+// Experts with routes, ascending; returns their number.  Every thread calls;
+// mine0 is idx[threadIdx.x], loaded earlier (-1 past R).
+MOE_DEV int find_used(const Lists& l, const int32_t* idx, int mine0, int R, int E, int most) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* scratch = l.counts + 257;
   if (tid < 256) l.counts[tid] = 0;
   __syncthreads();
   for (int r = tid; r < R; r += kW4Threads) {
-    const int e = __ldcg(idx + r);
+    const int e = r == tid ? mine0 : __ldcg(idx + r);
     const bool ok = e >= 0 && e < E;
     l.expert_of[r] = (int16_t)(ok ? e : -1);
     if (ok) atomicAdd(l.counts + e, 1);
@@ -87,30 +93,39 @@ MOE_DEV int find_used(const Lists& l, const int32_t* idx, int R, int E, int most
   return n;
 }
 
-// The routes of expert e in l.routes; returns their number.  Every thread calls.
-MOE_DEV int find_routes(const Lists& l, int R, int e) {
+// The routes of expert e in l.routes (and their gates).  Every thread calls.
+MOE_DEV void find_routes(const Lists& l, int R, int e, const float* gates) {
   int32_t* count = l.counts + 256;
   if (threadIdx.x == 0) *count = 0;
   __syncthreads();
   for (int r = threadIdx.x; r < R; r += kW4Threads)
-    if (l.expert_of[r] == e) l.routes[atomicAdd(count, 1)] = (uint16_t)r;   // the order changes no result
+    if (l.expert_of[r] == e) {
+      const int at = atomicAdd(count, 1);   // the order changes no result
+      l.routes[at] = (uint16_t)r;
+      if (gates) l.gates[at] = gates[r];
+    }
   __syncthreads();
-  return *count;
 }
 
 // This block's share of all (used expert, tile) pairs: a range of work units, a
 // tile of an expert with w rounds being w of them.  Tiles belong to the block in
-// whose range their first unit lies.  Where every expert has one round and the
-// blocks divide among the experts with hardly a loss, they do not cross from
-// one expert to another, which would cost a drain of the pipeline.
+// whose range their first unit lies.  Going on to another expert costs a block
+// about as much as kTurnUnits tiles (the last warps, the sums, the next
+// vectors), so as many empty units lie between two experts.  Where every expert
+// has one round and the blocks divide among the experts with hardly a loss,
+// they do not cross from one to another.
+constexpr int kTurnUnits = 4;
 struct Share {
   int per;             // tiles of an expert
   int i;               // present expert (of the used ones)
+  int turn;            // empty units between experts
   int64_t first, last;
-  MOE_DEV Share(const Lists& l, int used, int per_) : per(per_), i(0) {
+  MOE_DEV int64_t start(const Lists& l, int e) const { return (int64_t)l.before[e] * per + (int64_t)e * turn; }
+  MOE_DEV Share(const Lists& l, int used, int per_) : per(per_), i(0), turn(kTurnUnits) {
     const int all = used > 0 ? l.before[used] : 0;
     const int c = used > 0 ? gridDim.x / used : 0;
     if (c > 0 && all == used && c * used * 20 >= (int)gridDim.x * 19) {
+      turn = 0;
       const int e = blockIdx.x / c, b = blockIdx.x - e * c;
       first = last = 0;
       if (e < used) {
@@ -119,20 +134,63 @@ struct Share {
         i = e;
       }
     } else {
-      first = (int64_t)blockIdx.x * all * per / gridDim.x;
-      last = (int64_t)(blockIdx.x + 1) * all * per / gridDim.x;
-      while (i < used && (int64_t)l.before[i + 1] * per <= first) ++i;
+      const int64_t units = start(l, used);
+      first = (int64_t)blockIdx.x * units / gridDim.x;
+      last = (int64_t)(blockIdx.x + 1) * units / gridDim.x;
+      while (i < used && start(l, i + 1) <= first) ++i;
     }
   }
   // The tiles [t0, t1) of expert i; false: past the share.
   MOE_DEV bool tiles(const Lists& l, int used, int* t0, int* t1) const {
     if (i >= used) return false;
-    const int64_t start = (int64_t)l.before[i] * per;
-    if (start >= last) return false;
+    const int64_t from = start(l, i);
+    if (from >= last) return false;
     const int w = l.before[i + 1] - l.before[i];
-    *t0 = first > start ? (int)((first - start + w - 1) / w) : 0;
-    *t1 = (int)min((int64_t)per, (last - start + w - 1) / w);
+    *t0 = first > from ? (int)min((int64_t)per, (first - from + w - 1) / w) : 0;
+    *t1 = (int)min((int64_t)per, (last - from + w - 1) / w);
     return true;
+  }
+};
+
+// The share as passes over weights: up to `seg` tiles of an expert for up to
+// `most` of its routes.
+struct Pass {
+  Share share;
+  int used, seg, most;
+  int expert, t0, tiles, m0, here;   // the present pass: its tiles, its routes
+  int end;                           // of the expert's tiles in the share
+  bool enter;                        // it is the first of its expert
+  bool valid;
+  MOE_DEV Pass(const Lists& l, int used_, int per, int seg_, int most_)
+      : share(l, used_, per), used(used_), seg(seg_), most(most_) {
+    open(l);
+  }
+  MOE_DEV void open(const Lists& l) {
+    int first;
+    while ((valid = share.tiles(l, used, &first, &end)) && first >= end) ++share.i;
+    if (!valid) return;
+    expert = l.used[share.i];
+    t0 = first;
+    tiles = min(end - first, seg);
+    m0 = 0;
+    here = min(l.counts[expert], most);
+    enter = true;
+  }
+  MOE_DEV void next(const Lists& l) {
+    const int n = l.counts[expert];
+    enter = false;
+    m0 += most;
+    if (m0 >= n) {
+      m0 = 0;
+      t0 += seg;
+      if (t0 >= end) {
+        ++share.i;
+        open(l);
+        return;
+      }
+      tiles = min(end - t0, seg);
+    }
+    here = min(n - m0, most);
   }
 };
 
@@ -140,37 +198,54 @@ struct Share {
 template <typename S, int W> struct UpRows {
   const ExpertsW4Params& p;
   int64_t row0;   // first row of tile 0, over all experts
-  MOE_DEV RowPtr operator()(int tile, int stage) const {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  MOE_DEV RowPtr operator()(int tile, int, int stage) const {
+    const int lane = threadIdx.x & 31;
     const int64_t base = row0 + tile * 8;
-    const int64_t at = (base + g) * (p.d / 2) + stage * 64 + t * 16;
+    const int64_t at = (base + (lane >> 3)) * (p.d / 2) + stage * 64 + (lane & 7) * 16, four = 4 * (int64_t)(p.d / 2);
     const S* sc = static_cast<const S*>(lane & 8 ? p.up_s : p.gate_s) + (base + (lane & 7)) * (p.d / (32 * W));
-    return {p.gate_q + at, p.up_q + at, reinterpret_cast<const uint8_t*>(sc + stage * (4 / W))};
+    return {{p.gate_q + at, p.gate_q + at + four, p.up_q + at, p.up_q + at + four},
+            reinterpret_cast<const uint8_t*>(sc + stage * (4 / W))};
   }
 };
 template <typename S, int W> struct DownRows {
   const ExpertsW4Params& p;
   int64_t row0;
-  MOE_DEV RowPtr operator()(int tile, int stage) const {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  MOE_DEV RowPtr operator()(int tile, int, int stage) const {
+    const int lane = threadIdx.x & 31;
     const int64_t base = row0 + tile * 16;
-    const int64_t at = (base + g) * (p.f / 2) + stage * 64 + t * 16;
+    const uint8_t* at = p.down_q + (base + (lane >> 3)) * (p.f / 2) + stage * 64 + (lane & 7) * 16;
+    const int64_t four = 4 * (int64_t)(p.f / 2);
     const S* sc = static_cast<const S*>(p.down_s) + (base + (lane & 15)) * (p.f / (32 * W));
-    return {p.down_q + at, p.down_q + at + 8 * (int64_t)(p.f / 2), reinterpret_cast<const uint8_t*>(sc + stage * (4 / W))};
+    return {{at, at + four, at + 2 * four, at + 3 * four}, reinterpret_cast<const uint8_t*>(sc + stage * (4 / W))};
   }
 };
-// W_down of all the experts of one token, side by side.
+// W_down of all the experts of one token, side by side: run j is expert j.
 template <typename S, int W> struct TokenRows {
   const ExpertsW4Params& p;
   const int16_t* expert_of;
   int64_t d0;
-  int run;   // stages of an expert
-  MOE_DEV RowPtr operator()(int tile, int stage) const {
-    const int j = stage / run;
+  MOE_DEV RowPtr operator()(int tile, int j, int stage) const {
     const DownRows<S, W> rows = {p, (int64_t)expert_of[j] * p.d + d0};
-    return rows(tile, stage - j * run);
+    return rows(tile, 0, stage);
   }
 };
+
+// Whoever is through with its own weights brings the second kernel's first ones
+// into L2 (up to kPrefetchMost of them): what its start, its staging and the end
+// of this kernel would leave idle of HBM.
+constexpr int64_t kPrefetchMost = 32 << 20;
+constexpr int kPrefetchPiece = 4096;
+MOE_DEV void prefetch_down(const ExpertsW4Params& p, const Lists& l, int used) {
+  const int64_t per = (int64_t)p.d * (p.f / 2);
+  const int64_t all = min(per * used, kPrefetchMost) / kPrefetchPiece;
+  const int warps = gridDim.x * kW4Warps, warp = blockIdx.x * kW4Warps + (threadIdx.x >> 5);
+  for (int64_t i = warp + (int64_t)(threadIdx.x & 31) * warps; i < all; i += (int64_t)32 * warps) {
+    const int64_t at = i * kPrefetchPiece;
+    const int e = (int)(at / per);
+    const int64_t in = at - e * per;
+    prefetch_l2(p.down_q + (int64_t)l.used[e] * per + in, (uint32_t)min(per - in, (int64_t)kPrefetchPiece));
+  }
+}
 
 template <typename T, int W, int NT, XSource XS>
 __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_up_kernel(ExpertsW4Params p, Plan plan) {
@@ -180,69 +255,73 @@ __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_up_kernel(ExpertsW4P
   pdl_wait();
   pdl_launch_dependents();
   const int R = p.T * p.k;
+  const int idx0 = threadIdx.x < R ? __ldcg(p.topk_idx + threadIdx.x) : -1;
   const uint32_t rings = smem_u32(smem);
   float* parts = reinterpret_cast<float*>(smem + kRingsBytes);
   const Lists l = lists_at(smem + plan.smem_lists, R);
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int stages = p.d / 128;
+  const int stages = p.d / 128, steps = (stages + 1) / 2;
   StagedAt at;
   at.x = rings + kRingsBytes + (plan.seg_tiles + kW4Warps) * NT * 512;
   at.low = 0;
   at.stride = staged_stride(p.d);
   at.table = at.x + plan.most * at.stride;
-  const int used = find_used(l, p.topk_idx, R, p.E, plan.most);
-  Share share(l, used, p.f / 8);
   const T* x = static_cast<const T*>(p.x);
   float* act = static_cast<float*>(p.act);
   __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(p.act);
   __nv_bfloat16* lo = hi + (int64_t)R * p.f;
-  int first, last;
-  for (; share.tiles(l, used, &first, &last); ++share.i) {
-    const int e = l.used[share.i];
-    const int n = first < last ? find_routes(l, R, e) : 0;
-    for (int t0 = first; t0 < last; t0 += plan.seg_tiles) {
-      const int tiles = min(last - t0, plan.seg_tiles);
-      const UpRows<T, W> rows = {p, (int64_t)e * p.f + t0 * 8};
-      for (int m0 = 0; m0 < n; m0 += plan.most) {
-        Segment<T, T, W, NT, false, XS, true, false, 8, UpRows<T, W>> seg(
-            rings, rows, tiles, stages, stages, p.d, reinterpret_cast<const void*>(~uintptr_t(0)));
-        seg.start();
-        const int here = min(n - m0, plan.most);   // vectors past it repeat the last one, unused
-        auto token = [&](int m) { return x + (int64_t)(l.routes[m0 + m] / p.k) * p.ld_x; };
-        if constexpr (XS == kStaged) {
-          stage_vectors<T, W, false, 8>(at, here, p.d, token);
-          __syncthreads();
-        }
-        Vectors<T, NT> v;
+  if (XS == kStaged && p.T == 1) stage_vectors<T, W, false, 8>(at, 1, p.d, [&](int) { return x; });
+  const int used = find_used(l, p.topk_idx, idx0, R, p.E, plan.most);
+  Pass ps(l, used, p.f / 8, plan.seg_tiles, plan.most);
+  using Seg = Segment<T, T, W, NT, false, XS, true, false, 8, UpRows<T, W>>;
+  const void* no_end = reinterpret_cast<const void*>(~uintptr_t(0));
+  UpRows<T, W> rows = {p, ps.valid ? (int64_t)ps.expert * p.f + ps.t0 * 8 : 0};
+  Seg seg(rings, rows, ps.valid ? ps.tiles : 0, 1, stages, p.d, no_end);
+  seg.start();
+  while (ps.valid) {
+    if (ps.enter) find_routes(l, R, ps.expert, p.gates);
+    auto token = [&](int m) { return x + (int64_t)(l.routes[ps.m0 + m] / p.k) * p.ld_x; };
+    if constexpr (XS == kStaged) {
+      if (p.T > 1) stage_vectors<T, W, false, 8>(at, ps.here, p.d, token);
+    }
+    __syncthreads();   // the vectors are staged, and the parts of the pass before are read
+    Vectors<T, NT> v;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) v.x[j] = token(min(j * 8 + g, here - 1));
-        v.low = 0;
-        v.s = at.x + min(g, here - 1) * at.stride;
-        v.s_low = 0;
+    for (int j = 0; j < NT; ++j) v.x[j] = token(min(j * 8 + g, ps.here - 1));   // vectors past the last repeat it, unused
+    v.low = 0;
+    v.s = at.x + min(g, ps.here - 1) * at.stride;
+    v.s_low = 0;
         v.table = at.table + t * 16;
-        seg.finish(v, (here + 7) / 8, parts);
-        __syncthreads();
-        for (int i = threadIdx.x; i < tiles * here * 8; i += kW4Threads) {
-          const int r8 = i & 7, tile = (i >> 3) / here, col = (i >> 3) - tile * here;
-          const PartRange w(tile, tiles, stages);
-          const int from = (col >> 3) * 128 + r8 * 8 + (col & 7);
-          const float h = sum_parts(parts, NT * 128, tile, w, from);
-          const float up = sum_parts(parts, NT * 128, tile, w, from + 64);
-          const int route = l.routes[m0 + col];
-          const float a = h / (1.0f + expf(-h)) * up * p.gates[route];
-          const int piece = t0 + tile;   // the tile's eight columns of d_ff
-          if constexpr (XS == kStaged) {
-            act[(int64_t)route * p.f + piece * 8 + r8] = a;
-          } else {
-            const __nv_bfloat16 ah = __float2bfloat16_rn(a);
-            const int64_t to = (int64_t)route * p.f + (piece >> 4) * 128 + piece_place<W>(piece & 15) * 8 + in_piece(r8);
-            hi[to] = ah;
-            lo[to] = __float2bfloat16_rn(a - __bfloat162float(ah));
-          }
-        }
-        __syncthreads();
+    seg.finish(v, (ps.here + 7) / 8, parts);
+    const Pass done = ps;
+    ps.next(l);
+    if (ps.valid) {   // the next pass's weights are on their way during what follows
+      seg.rows.row0 = (int64_t)ps.expert * p.f + ps.t0 * 8;
+      seg.reset(ps.tiles);
+      seg.start();
+    } else {
+      prefetch_down(p, l, used);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < done.tiles * done.here * 8; i += kW4Threads) {
+      const int r8 = i & 7, tile = (i >> 3) / done.here, col = (i >> 3) - tile * done.here;
+      const PartRange w(tile, done.tiles, steps);
+      const int from = (col >> 3) * 128 + r8 * 8 + (col & 7);
+      const float h = sum_parts(parts, NT * 128, tile, w, from);
+      const float up = sum_parts(parts, NT * 128, tile, w, from + 64);
+      const int route = l.routes[done.m0 + col];
+      const float a = h / (1.0f + expf(-h)) * up * l.gates[done.m0 + col];
+      const int piece = done.t0 + tile;   // the tile's eight columns of d_ff
+      if constexpr (XS == kStaged) {
+        act[(int64_t)route * p.f + piece * 8 + r8] = a;
+      } else {
+        const __nv_bfloat16 ah = __float2bfloat16_rn(a);
+        const int64_t to = (int64_t)route * p.f + (piece >> 4) * 128 + piece_place<W>(piece & 15) * 8 + in_piece(r8);
+        hi[to] = ah;
+        lo[to] = __float2bfloat16_rn(a - __bfloat162float(ah));
       }
     }
+    if (ps.valid && ps.enter) __syncthreads();   // the routes are read
   }
 }
 
@@ -251,63 +330,58 @@ template <typename T, int W, int NT, XSource XS>
 __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_down_kernel(ExpertsW4Params p, Plan plan) {
   extern __shared__ __align__(128) uint8_t smem[];
   const int R = p.T * p.k;
+  const int idx0 = threadIdx.x < R ? __ldcg(p.topk_idx + threadIdx.x) : -1;
   const uint32_t rings = smem_u32(smem);
   float* parts = reinterpret_cast<float*>(smem + kRingsBytes);
   const Lists l = lists_at(smem + plan.smem_lists, R);
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-  const int stages = p.f / 128;
+  const int stages = p.f / 128, steps = (stages + 1) / 2;
   StagedAt at;
   at.x = rings + kRingsBytes + (plan.seg_tiles + kW4Warps) * NT * 512;
   at.stride = staged_stride(p.f);
   at.low = at.x + plan.most * at.stride;
   at.table = at.low + plan.most * at.stride;
   // weights and routes were complete before the first kernel let this one start
-  const int used = find_used(l, p.topk_idx, R, p.E, plan.most);
-  Share share(l, used, p.d / 16);
+  const int used = find_used(l, p.topk_idx, idx0, R, p.E, plan.most);
   const float* act = static_cast<const float*>(p.act);
   const __nv_bfloat16* hi = static_cast<const __nv_bfloat16*>(p.act);
-  bool waited = false;
-  int first, last;
-  for (; share.tiles(l, used, &first, &last); ++share.i) {
-    const int e = l.used[share.i];
-    const int n = first < last ? find_routes(l, R, e) : 0;
-    for (int t0 = first; t0 < last; t0 += plan.seg_tiles) {
-      const int tiles = min(last - t0, plan.seg_tiles);
-      const DownRows<T, W> rows = {p, (int64_t)e * p.d + t0 * 16};
-      for (int m0 = 0; m0 < n; m0 += plan.most) {
-        Segment<__nv_bfloat16, T, W, NT, true, XS, true, false, 8, DownRows<T, W>> seg(
-            rings, rows, tiles, stages, stages, p.f, reinterpret_cast<const void*>(~uintptr_t(0)));
-        seg.start();
-        if (!waited) {
-          pdl_wait();   // act
-          pdl_launch_dependents();
-          waited = true;
-        }
-        const int here = min(n - m0, plan.most);
-        if constexpr (XS == kStaged) {
-          stage_vectors<float, W, true, 8>(at, here, p.f, [&](int m) { return act + (int64_t)l.routes[m0 + m] * p.f; });
-          __syncthreads();
-        }
-        Vectors<__nv_bfloat16, NT> v;
+  Pass ps(l, used, p.d / 16, plan.seg_tiles, plan.most);
+  using Seg = Segment<__nv_bfloat16, T, W, NT, true, XS, true, false, 8, DownRows<T, W>>;
+  const void* no_end = reinterpret_cast<const void*>(~uintptr_t(0));
+  DownRows<T, W> rows = {p, ps.valid ? (int64_t)ps.expert * p.d + ps.t0 * 16 : 0};
+  Seg seg(rings, rows, ps.valid ? ps.tiles : 0, 1, stages, p.f, no_end);
+  seg.start();
+  pdl_wait();   // act
+  pdl_launch_dependents();
+  while (ps.valid) {
+    if (ps.enter) find_routes(l, R, ps.expert, nullptr);
+    if constexpr (XS == kStaged)
+      stage_vectors<float, W, true, 8>(at, ps.here, p.f, [&](int m) { return act + (int64_t)l.routes[ps.m0 + m] * p.f; });
+    __syncthreads();   // the vectors are staged, and the parts of the pass before are read
+    Vectors<__nv_bfloat16, NT> v;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) v.x[j] = hi + (int64_t)l.routes[m0 + min(j * 8 + g, here - 1)] * p.f;
-        v.low = (int64_t)R * p.f;
-        v.s = at.x + min(g, here - 1) * at.stride;
-        v.s_low = v.s + plan.most * at.stride;
+    for (int j = 0; j < NT; ++j) v.x[j] = hi + (int64_t)l.routes[ps.m0 + min(j * 8 + g, ps.here - 1)] * p.f;
+    v.low = (int64_t)R * p.f;
+    v.s = at.x + min(g, ps.here - 1) * at.stride;
+    v.s_low = v.s + plan.most * at.stride;
         v.table = at.table + t * 16;
-        seg.finish(v, (here + 7) / 8, parts);
-        __syncthreads();
-        for (int i = threadIdx.x; i < tiles * here * 16; i += kW4Threads) {
-          const int r16 = i & 15, tile = (i >> 4) / here, col = (i >> 4) - tile * here;
-          const PartRange w(tile, tiles, stages);
-          p.y[(int64_t)l.routes[m0 + col] * p.d + (t0 + tile) * 16 + r16] =
-              sum_parts(parts, NT * 128, tile, w, (col >> 3) * 128 + r16 * 8 + (col & 7));
-        }
-        __syncthreads();
-      }
+    seg.finish(v, (ps.here + 7) / 8, parts);
+    const Pass done = ps;
+    ps.next(l);
+    if (ps.valid) {
+      seg.rows.row0 = (int64_t)ps.expert * p.d + ps.t0 * 16;
+      seg.reset(ps.tiles);
+      seg.start();
     }
+    __syncthreads();
+    for (int i = threadIdx.x; i < done.tiles * done.here * 16; i += kW4Threads) {
+      const int r16 = i & 15, tile = (i >> 4) / done.here, col = (i >> 4) - tile * done.here;
+      const PartRange w(tile, done.tiles, steps);
+      p.y[(int64_t)l.routes[done.m0 + col] * p.d + (done.t0 + tile) * 16 + r16] =
+          sum_parts(parts, NT * 128, tile, w, (col >> 3) * 128 + r16 * 8 + (col & 7));
+    }
+    if (ps.valid && ps.enter) __syncthreads();   // the routes are read
   }
-  if (!waited) pdl_wait();
 }
 
 // One token: out = sum over its routes of W_down act, as one product with k f
@@ -336,7 +410,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_token_kernel(Experts
   }
   __syncthreads();
   const int per = p.d / 16, run = p.f / 128;
-  const int n = n_routes, stages = n * run;
+  const int n = n_routes;
   StagedAt at;
   at.x = rings + kRingsBytes + (plan.seg_tiles + kW4Warps) * 512;
   at.stride = 2 * p.f;   // the routes one after the other
@@ -349,9 +423,9 @@ __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_token_kernel(Experts
   for (int t0 = first; t0 < last; t0 += plan.seg_tiles) {
     const int tiles = min(last - t0, plan.seg_tiles);
     if (n > 0) {
-      const TokenRows<T, W> rows = {p, expert_of, (int64_t)t0 * 16, run};
+      const TokenRows<T, W> rows = {p, expert_of, (int64_t)t0 * 16};
       Segment<__nv_bfloat16, T, W, 1, true, kStaged, true, true, 1, TokenRows<T, W>> seg(
-          rings, rows, tiles, stages, run, p.f, reinterpret_cast<const void*>(~uintptr_t(0)));
+          rings, rows, tiles, n, run, p.f, reinterpret_cast<const void*>(~uintptr_t(0)));
       seg.start();
       if (t0 == first) {
         pdl_wait();   // act
@@ -363,7 +437,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_token_kernel(Experts
       v.x[0] = nullptr;
       v.low = 0;
       v.s = at.x;   // every column of the fragment repeats the one vector
-      v.s_low = at.low;
+            v.s_low = at.low;
       v.table = at.table;
       seg.finish(v, 1, parts);
       __syncthreads();
@@ -373,7 +447,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_token_kernel(Experts
     for (int i = threadIdx.x; i < tiles * 16; i += kW4Threads) {
       const int r16 = i & 15, tile = i >> 4;
       float s = 0.0f;
-      if (n > 0) s = sum_parts(parts, 128, tile, PartRange(tile, tiles, stages), r16 * 8);
+      if (n > 0) s = sum_parts(parts, 128, tile, PartRange(tile, tiles, n * ((run + 1) / 2)), r16 * 8);
       out[(t0 + tile) * 16 + r16] = Elem<T>::from_f(s);
     }
     __syncthreads();
@@ -384,14 +458,17 @@ __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_token_kernel(Experts
 // (-1) adds nothing, an expert id out of range is reported and adds nothing.
 template <typename T>
 __global__ void __launch_bounds__(256) experts_w4_join_kernel(ExpertsW4Params p) {
-  pdl_begin();
+  pdl_launch_dependents();
   const int c = (blockIdx.x * 256 + threadIdx.x) * 4;
   const int t = blockIdx.y;
-  if (c >= p.d) return;
+  // the routes were complete before the first kernel let the others start
+  const int mine = (threadIdx.x & 31) < p.k ? __ldcg(p.topk_idx + t * p.k + (threadIdx.x & 31)) : -1;
+  pdl_wait();
   float a[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   for (int j = 0; j < p.k; ++j) {
     const int r = t * p.k + j;
-    const int e = p.topk_idx[r];
+    const int e = __shfl_sync(0xffffffffu, mine, j);
+    if (c >= p.d) continue;
     if (e >= 0 && e < p.E) {
       const float4 v = *reinterpret_cast<const float4*>(p.y + (int64_t)r * p.d + c);
       a[0] += v.x; a[1] += v.y; a[2] += v.z; a[3] += v.w;
@@ -399,6 +476,7 @@ __global__ void __launch_bounds__(256) experts_w4_join_kernel(ExpertsW4Params p)
       raise_error(p.err, MOE_DEVERR_BOUNDS);
     }
   }
+  if (c >= p.d) return;
   T* out = static_cast<T*>(p.out) + t * p.ld_out + c;
 #pragma unroll
   for (int i = 0; i < 4; ++i) out[i] = Elem<T>::from_f(a[i]);
@@ -506,18 +584,5 @@ template <typename T> cudaError_t experts_group(int group, const ExpertsW4Params
 }
 
 }  // namespace
-
-cudaError_t experts_w4_init() {
-  cudaError_t e = cudaSuccess;
-  for (int g = 32; g <= 128 && e == cudaSuccess; g *= 2) {
-    e = experts_group<__nv_bfloat16>(g, nullptr, nullptr);
-    if (e == cudaSuccess) e = experts_group<__half>(g, nullptr, nullptr);
-  }
-  return e;
-}
-
-cudaError_t launch_experts_w4(const ExpertsW4Params& p, int dtype, cudaStream_t s) {
-  return dtype == MOE_DT_BF16 ? experts_group<__nv_bfloat16>(p.group, &p, s) : experts_group<__half>(p.group, &p, s);
-}
 
 }  // namespace moe

@@ -23,12 +23,15 @@ template <typename S, int W> struct MatvecRows {
   const S* sc;
   int64_t n0;
   int N, K, groups;
-  MOE_DEV RowPtr operator()(int tile, int stage) const {
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  MOE_DEV RowPtr operator()(int tile, int, int stage) const {
+    const int lane = threadIdx.x & 31;
     const int64_t base = n0 + tile * 16, last = N - 1;
-    const int64_t at = (int64_t)stage * 64 + t * 16;
-    return {q + min(base + g, last) * (K / 2) + at, q + min(base + g + 8, last) * (K / 2) + at,
-            reinterpret_cast<const uint8_t*>(sc + min(base + (lane & 15), last) * groups + stage * (4 / W))};
+    RowPtr r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      r.row[i] = q + min(base + (lane >> 3) + 4 * i, last) * (K / 2) + (int64_t)stage * 64 + (lane & 7) * 16;
+    r.s = reinterpret_cast<const uint8_t*>(sc + min(base + (lane & 15), last) * groups + stage * (4 / W));
+    return r;
   }
   MOE_DEV void scales(int tile, const S** a, const S** b) const {
     const int g = (threadIdx.x & 31) >> 2;
@@ -61,7 +64,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) matvec_w4_kernel(MatvecArgs a) 
     const MatvecRows<T, W> rows = {a.q, sc, (int64_t)t0 * 16, a.N, a.K, a.K / (32 * W)};
     for (int m0 = 0; m0 < a.M; m0 += 8 * NT) {
       Segment<T, T, W, NT, false, XS, FULL, false, 8, MatvecRows<T, W>> seg(
-          rings, rows, tiles, stages, stages, a.K, sc + (int64_t)a.N * rows.groups);
+          rings, rows, tiles, 1, stages, a.K, sc + (int64_t)a.N * rows.groups);
       seg.start();
       const int here = min(a.M - m0, 8 * NT);   // vectors past it repeat the last one, unused
       if constexpr (XS == kStaged) {   // M <= 8: once
@@ -75,14 +78,14 @@ __global__ void __launch_bounds__(kW4Threads, 1) matvec_w4_kernel(MatvecArgs a) 
       v.low = 0;
       v.s = at.x + min(g, here - 1) * at.stride;
       v.s_low = 0;
-      v.table = at.table + t * 16;
+            v.table = at.table + t * 16;
       seg.finish(v, (here + 7) / 8, parts);
       __syncthreads();
       for (int i = threadIdx.x; i < tiles * here * 16; i += kW4Threads) {
         const int row = i & 15, tile = (i >> 4) / here, col = (i >> 4) - tile * here;
         const int64_t n = (int64_t)(t0 + tile) * 16 + row;
         if (n < a.N) {
-          const PartRange w(tile, tiles, stages);
+          const PartRange w(tile, tiles, (stages + 1) / 2);
           y[(m0 + col) * a.ld_y + n] = Elem<T>::from_f(
               sum_parts(parts, NT * 128, tile, w, (col >> 3) * 128 + row * 8 + (col & 7)));
         }
