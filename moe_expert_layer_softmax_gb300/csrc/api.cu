@@ -310,6 +310,7 @@ int moe_init(int device) {
   MOE_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device));
   MOE_CUDA(gemm_init_attributes());
   MOE_CUDA(norm_init());
+  MOE_CUDA(norm_bwd_init());
   MOE_CUDA(matvec_w4_init());
   MOE_CUDA(experts_w4_init_bf16());
   MOE_CUDA(experts_w4_init_f16());

@@ -130,7 +130,7 @@ int moe_add_norm(const moe_add_norm_args_t* a, void* stream) {
     vec = vec && vector_rows(a->y, a->ld_y, a->rows, a->dtype);
   }
   if (!ready()) return MOE_ERR_NOT_INIT;
-  p.rows = a->rows; p.d = a->d;
+  p.rows = a->rows; p.d = a->d; p.inv_d = 1.0f / (float)a->d;
   p.w_f32 = a->w_dtype == MOE_DT_F32; p.x_f16 = a->dtype == MOE_DT_F16;
   p.x = a->x; p.ld_x = a->ld_x;
   p.residual = a->residual; p.ld_residual = a->ld_residual;
@@ -179,7 +179,7 @@ int moe_add_norm_bwd(const moe_add_norm_bwd_args_t* a, void* ws, void* stream) {
                    vector_rows(a->dres, a->ld_dres, a->rows, a->res_dtype) &&
                    vector_rows(a->dh, a->ld_dh, a->rows, a->res_dtype) &&
                    vector_rows(a->dx, a->ld_dx, a->rows, a->dtype) && on_boundary(a->weight, 16);
-  p.rows = a->rows; p.d = a->d;
+  p.rows = a->rows; p.d = a->d; p.inv_d = 1.0f / (float)a->d;
   p.w_f32 = a->w_dtype == MOE_DT_F32; p.x_f16 = a->dtype == MOE_DT_F16;
   p.dy = a->dy; p.ld_dy = a->ld_dy;
   p.h = a->h; p.ld_h = a->ld_h;

@@ -72,9 +72,59 @@ template <typename T, bool VEC> MOE_DEV void store8(T* row, int c, int G, int d,
   }
 }
 
+// The same for a whole warp whose lanes hold neighbouring groups of eight columns
+// (VEC; each lane calls, `in`: its group is part of the row).  Eight fp32 values
+// are two 16-byte accesses; lanes go in pairs, so that each access of the pair
+// fills a 32-byte sector instead of two half sectors.
+template <typename T, bool VEC> MOE_DEV Raw8<T> load8_warp(const T* row, int c, int G, int d, bool in) {
+  Raw8<T> r = {};
+  if constexpr (VEC && sizeof(T) == 4) {
+    const bool odd = threadIdx.x & 1;
+    const bool other = __shfl_xor_sync(0xffffffffu, (int)in, 1);
+    const T* even = row + (odd ? c - 8 : c);   // the pair's sixteen columns
+    uint4 a = {}, b = {};
+    if (odd ? other : in) a = *(reinterpret_cast<const uint4*>(even) + odd);
+    if (odd ? in : other) b = *(reinterpret_cast<const uint4*>(even) + 2 + odd);
+    // even lanes keep a and take the odd lane's a; odd lanes keep b and take b
+    uint4 give = odd ? a : b, got;
+    got.x = __shfl_xor_sync(0xffffffffu, give.x, 1);
+    got.y = __shfl_xor_sync(0xffffffffu, give.y, 1);
+    got.z = __shfl_xor_sync(0xffffffffu, give.z, 1);
+    got.w = __shfl_xor_sync(0xffffffffu, give.w, 1);
+    uint4* q = reinterpret_cast<uint4*>(&r);
+    q[0] = odd ? got : a;
+    q[1] = odd ? b : got;
+  } else {
+    if (in) r = load8<T, VEC>(row, c, G, d);
+  }
+  return r;
+}
+template <typename T, bool VEC> MOE_DEV void store8_warp(T* row, int c, int G, int d, const Raw8<T>& r, bool in) {
+  if constexpr (VEC && sizeof(T) == 4) {
+    const bool odd = threadIdx.x & 1;
+    const bool other = __shfl_xor_sync(0xffffffffu, (int)in, 1);
+    T* even = row + (odd ? c - 8 : c);
+    const uint4* q = reinterpret_cast<const uint4*>(&r);
+    const uint4 give = odd ? q[0] : q[1];
+    uint4 got;
+    got.x = __shfl_xor_sync(0xffffffffu, give.x, 1);
+    got.y = __shfl_xor_sync(0xffffffffu, give.y, 1);
+    got.z = __shfl_xor_sync(0xffffffffu, give.z, 1);
+    got.w = __shfl_xor_sync(0xffffffffu, give.w, 1);
+    if (odd ? other : in) *(reinterpret_cast<uint4*>(even) + odd) = odd ? got : q[0];
+    if (odd ? in : other) *(reinterpret_cast<uint4*>(even) + 2 + odd) = odd ? q[1] : got;
+  } else {
+    if (in) store8<T, VEC>(row, c, G, d, r);
+  }
+}
+
 // ------------------------------------------------------------------ asynchronous copies
 MOE_DEV void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// bytes: 16, or 0 for zeros in place of the source
+MOE_DEV void cp_async16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 MOE_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> MOE_DEV void cp_async_wait() {
@@ -97,63 +147,62 @@ struct DropRng {
   float scale;
 };
 
-MOE_DEV uint4 philox4x32_10(uint4 c, uint32_t k0, uint32_t k1) {
+// Philox of N counters at once: the rounds' keys are made once.
+template <int N> MOE_DEV void philox4x32_10(uint4 (&c)[N], uint32_t k0, uint32_t k1) {
 #pragma unroll
   for (int i = 0; i < 10; ++i) {
-    const uint64_t a = (uint64_t)c.x * 0xD2511F53u;
-    const uint64_t b = (uint64_t)c.z * 0xCD9E8D57u;
-    c = make_uint4((uint32_t)(b >> 32) ^ c.y ^ k0, (uint32_t)b,
-                   (uint32_t)(a >> 32) ^ c.w ^ k1, (uint32_t)a);
+#pragma unroll
+    for (int n = 0; n < N; ++n) {
+      const uint64_t a = (uint64_t)c[n].x * 0xD2511F53u;
+      const uint64_t b = (uint64_t)c[n].z * 0xCD9E8D57u;
+      c[n] = make_uint4((uint32_t)(b >> 32) ^ c[n].y ^ k0, (uint32_t)b,
+                        (uint32_t)(a >> 32) ^ c[n].w ^ k1, (uint32_t)a);
+    }
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
-  return c;
 }
 
-// The eight numbers of columns [8 group, 8 group + 8) of a row.
-MOE_DEV uint4 drop_numbers(uint32_t group, uint32_t row, const DropRng& g) {
-  return philox4x32_10(make_uint4(group, row, g.o0, g.o1), g.k0, g.k1);
-}
-
-// Drop and scale eight values by those numbers.  Dropped places become zero
+// Drop and scale eight values by their numbers.  Dropped places become zero
 // whatever they held (a NaN there does not survive).
 MOE_DEV void drop8(float* f, const uint4& r, const DropRng& g) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-  // a half-word is compared in the upper half of a word: (w >> 16) >= t is w >=
-  // t << 16, and t = 65536 (drop everything) has scale 0 and is taken apart
-  const uint32_t t = g.threshold << 16;
-  if (g.threshold > 0xFFFFu) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = 0.0f;
-    return;
-  }
+  // A half-word is compared in the upper half of a word: (w >> 16) >= t is w > t
+  // 2^16 - 1.  `limit` is that, 0xFFFFFFFF (nothing is above) where t is 65536.
+  const uint32_t limit = (g.threshold << 16) - 1;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    f[2 * i] = (w[i] << 16) >= t ? f[2 * i] * g.scale : 0.0f;
-    f[2 * i + 1] = w[i] >= t ? f[2 * i + 1] * g.scale : 0.0f;
+    f[2 * i] = (w[i] << 16) > limit ? f[2 * i] * g.scale : 0.0f;
+    f[2 * i + 1] = w[i] > limit ? f[2 * i + 1] * g.scale : 0.0f;
   }
 }
 
-// The numbers of a thread's eight values: its own where they are neighbouring
-// columns; where they are G apart, each of the G threads makes those of eight
-// neighbouring columns and they change hands in shared memory (`xch`: G entries
-// of the group's own; `sync` is a barrier of the G threads at least, called
-// twice).
-template <bool VEC, typename Sync>
-MOE_DEV uint4 drop_numbers_of(int i, int lane, int G, uint32_t row, const DropRng& g, uint4* xch, Sync sync) {
-  const uint4 r = drop_numbers((uint32_t)(lane + i * G), row, g);
-  if constexpr (VEC) {
-    return r;
-  } else {
-    sync();   // the previous numbers have been read
-    xch[lane] = r;
-    sync();
-    const uint16_t* h = reinterpret_cast<const uint16_t*>(xch);
-    uint32_t w[4];
+// Numbers change hands: each of G threads has made those of eight neighbouring
+// columns, 8 G in a row, and gets those of the columns lane, lane + G, ...  `xch`:
+// G entries of the group's own; `sync`: a barrier of the G threads at least.
+template <typename Sync>
+MOE_DEV void exchange_numbers(uint4& r, int lane, int G, uint4* xch, Sync sync) {
+  sync();   // the previous numbers have been read
+  xch[lane] = r;
+  sync();
+  const uint16_t* h = reinterpret_cast<const uint16_t*>(xch);
+  uint32_t w[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      w[j] = (uint32_t)h[2 * j * G + lane] | (uint32_t)h[(2 * j + 1) * G + lane] << 16;
-    return make_uint4(w[0], w[1], w[2], w[3]);
+  for (int j = 0; j < 4; ++j)
+    w[j] = (uint32_t)h[2 * j * G + lane] | (uint32_t)h[(2 * j + 1) * G + lane] << 16;
+  r = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// The numbers of a thread's N times eight values of a row: groups lane, lane +
+// G, ... of neighbouring columns (VEC), or the columns first_column() says.
+template <bool VEC, int N, typename Sync>
+MOE_DEV void drop_numbers(uint4 (&r)[N], int lane, int G, uint32_t row, const DropRng& g, uint4* xch, Sync sync) {
+#pragma unroll
+  for (int n = 0; n < N; ++n) r[n] = make_uint4((uint32_t)(lane + n * G), row, g.o0, g.o1);
+  philox4x32_10(r, g.k0, g.k1);
+  if constexpr (!VEC) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) exchange_numbers(r[n], lane, G, xch, sync);
   }
 }
 

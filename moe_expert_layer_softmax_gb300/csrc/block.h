@@ -13,6 +13,7 @@ struct AddNormParams {
   int64_t rows, rows_pad;   // rows_pad: rows up to a whole 128-row tile (8-bit output)
   int32_t d;
   int32_t group;            // threads of a row group (set by the launcher)
+  float inv_d;
   bool w_f32, x_f16;
   const void* x;
   int64_t ld_x;
@@ -35,6 +36,7 @@ struct AddNormBwdParams {
   int64_t rows;
   int32_t d;
   int32_t group;
+  float inv_d;
   bool w_f32, x_f16;
   const void* dy;
   int64_t ld_dy;
@@ -66,8 +68,9 @@ constexpr int kNormMaxWidth = 32768;     // 1024 threads, four groups of eight c
 constexpr int kNormPartialRows = 1024;   // rows of partial weight gradients: blocks of the backward
 
 cudaError_t norm_init();   // dynamic shared memory limits (moe_init)
-cudaError_t launch_add_norm(AddNormParams p, int dtype, int res_dtype, bool vec, cudaStream_t s);
-cudaError_t launch_add_norm_bwd(AddNormBwdParams p, int dtype, int res_dtype, bool vec, float* dw,
+cudaError_t norm_bwd_init();
+cudaError_t launch_add_norm(const AddNormParams& p, int dtype, int res_dtype, bool vec, cudaStream_t s);
+cudaError_t launch_add_norm_bwd(const AddNormBwdParams& p, int dtype, int res_dtype, bool vec, float* dw,
                                 cudaStream_t s);
 cudaError_t launch_dropout(const DropoutParams& p, int dtype, bool vec, cudaStream_t s);
 

@@ -1,0 +1,172 @@
+// Residual addition with the root-mean-square norm, its backward, and dropout
+// (sm_103a).
+//
+//   u = dropout(x)                      (u = x without dropout)
+//   h = residual + u, rounded to the stream's type
+//   r = (mean(h^2) + eps)^(-1/2),  y = h r w
+// The norm is that of the rounded h: it is what the backward gets, so forward
+// and backward see the same values.  y leaves in the activations' type, or as
+// E4M3 codes with one E8M0 scale per 32 columns (rounded once, from the 32-bit
+// y), optionally with the values the codes stand for.  With g = w dy:
+//   dh = dres + r (g - h r^2 mean(g h)),  dx = dropout'(dh),  dw = sum dy h r.
+//
+// Every kernel here is bound by HBM: one read and one write of each matrix.  A
+// row stays in registers between the pass that sums it and the pass that writes
+// it.  A fixed grid takes the rows in turn while the rows to come (one to three)
+// are on their way into shared memory, each thread copying and reading its own
+// pieces, so that the pipeline needs no barrier and no registers: 512 threads a
+// multiprocessor keep 50 to 130 KB in flight.  A thread holds up to 32 columns
+// (backward: 16): what a row costs beside its elements (the sums over threads,
+// the square root, addresses) is then shared by that many.  With eight columns
+// a thread the 8192 x 2048 forward took 294 instructions per eight columns and
+// was bound by instruction issue.  Sums are taken in a fixed order (no atomics).
+#pragma once
+
+#include "block.cuh"
+#include "block.h"
+#include "kernels.h"
+
+namespace moe {
+
+constexpr int kNormThreads = 256;      // threads of a block whose row group is not larger
+constexpr int kNormMaxThreads = 1024;
+constexpr int kNormBlocks = 2;         // of kNormThreads on a multiprocessor (by registers and shared memory)
+constexpr int kNormRingBytes = 96 * 1024;   // of a block
+
+MOE_DEV float warp_sum(float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+// The threads of a block form groups of G (a power of two >= 32), one a row.
+struct RowGroup {
+  int G, lane, group, per;
+  MOE_DEV explicit RowGroup(int G_)
+      : G(G_), lane(threadIdx.x & (G_ - 1)), group(threadIdx.x / G_), per(blockDim.x / G_) {}
+  MOE_DEV void sync() const {
+    if (G == 32) __syncwarp(); else bar_sync(1 + group, G);
+  }
+  // Sum over the group, the same value in every thread.  `red`: a float for each
+  // warp of the block, another array in turn for the next call (so that one
+  // barrier is enough).
+  MOE_DEV float sum(float v, float* red) const {
+    v = warp_sum(v);
+    if (G == 32) return v;
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+    bar_sync(1 + group, G);
+    const int n = G >> 5;
+    const float* from = red + group * n;
+    if (n == 2) return from[0] + from[1];
+    float s = 0.0f;
+    for (int i = 0; i < n; i += 4) {
+      const float4 q = *reinterpret_cast<const float4*>(from + i);
+      s += (q.x + q.y) + (q.z + q.w);
+    }
+    return s;
+  }
+};
+
+// 1 / sqrt(v) to about an ulp: the approximation and one Newton step.
+MOE_DEV float inv_sqrt(float v) {
+  const float r = rsqrtf(v);
+  // zero, infinity and NaN: the approximation is the answer
+  if (!(v > 0.0f) || !(v < INFINITY)) return r;
+  return fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
+}
+
+template <bool VEC>
+MOE_DEV void load_weight8(const void* w, bool w_f32, bool w_f16, int c, int G, int d, float* f) {
+  if (c >= d) {   // columns past the row's end: zeros all through
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = 0.0f;
+  } else if (w_f32) {
+    widen8(load8<float, VEC>(static_cast<const float*>(w), c, G, d), f);
+  } else if (w_f16) {
+    widen8(load8<__half, VEC>(static_cast<const __half*>(w), c, G, d), f);
+  } else {
+    widen8(load8<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(w), c, G, d), f);
+  }
+}
+
+// The pieces (16 bytes) of the rows to come: cp.async into slots, BYTES for eight
+// columns of up to three matrices, NV times.  Slots are laid out piece by piece
+// (16 bytes a thread), so that neighbouring threads touch neighbouring banks.  A
+// thread copies and reads its own pieces; where eight columns are two pieces
+// (fp32) a warp copies its 64 pieces as they follow one another, which fills
+// whole sectors, and each lane reads its two: piece q lies at place q ^ (q >> 3 &
+// 1), so that eight lanes' reads miss each other's banks.
+template <int BYTES, int NV> struct RowRing {
+  static constexpr int kFit = kNormRingBytes / (kNormThreads * BYTES * NV);
+  static constexpr int kDepth = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
+  static constexpr int kBytes = BYTES * NV * kDepth;   // a thread
+  uint32_t mine, warp;   // slot 0, piece 0: this thread's, its warp's first
+  uint32_t piece;        // bytes between pieces
+  uint32_t slot;         // bytes: the next one to read
+  uint32_t ahead;        // bytes: the next one to fill
+  MOE_DEV explicit RowRing(void* smem)
+      : mine(smem_u32(smem) + threadIdx.x * 16), warp(smem_u32(smem) + (threadIdx.x & ~31u) * 16),
+        piece(blockDim.x * 16), slot(0), ahead(0) {}
+  MOE_DEV uint32_t next(uint32_t at) const {
+    at += piece * (BYTES / 16 * NV);
+    return at == piece * (BYTES / 16 * NV) * kDepth ? 0 : at;
+  }
+  // Copy columns c .. c + 7 of a row of d to piece `at` of the slot that is
+  // filled (c a multiple of 8; columns from d on become zeros).
+  template <typename T> MOE_DEV void put(int at, const T* row, int c, int d) const {
+    if constexpr (sizeof(T) == 2) {
+      const bool in = c < d;
+      cp_async16(mine + ahead + at * piece, row + (in ? c : 0), in ? 16 : 0);
+    } else {
+      const int lane = threadIdx.x & 31;
+      const int first = c - lane * 8;   // of the warp
+      const uint32_t to = warp + ahead + at * piece + (lane ^ (lane >> 3 & 1)) * 16;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int q = first + (lane + 32 * i) * 4;
+        const bool in = q < d;
+        cp_async16(to + i * piece, row + (in ? q : 0), in ? 16 : 0);
+      }
+    }
+  }
+  // This thread's eight columns at piece `at` of the slot that is read.
+  template <typename T> MOE_DEV Raw8<T> get(int at) const {
+    Raw8<T> r;
+    uint4* q = reinterpret_cast<uint4*>(&r);
+    if constexpr (sizeof(T) == 2) {
+      load(mine + slot + at * piece, q[0]);
+    } else {
+      const int lane = threadIdx.x & 31;
+      const uint32_t from = warp + slot + (at + (lane >> 4)) * piece;
+      const int first = (2 * lane & 31) ^ (lane >> 2 & 1);
+      load(from + first * 16, q[0]);
+      load(from + (first ^ 1) * 16, q[1]);
+    }
+    return r;
+  }
+  MOE_DEV static void load(uint32_t at, uint4& x) {
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
+  }
+};
+
+// Threads of a row group and how many times eight columns each holds: a power
+// of two of them, as many columns a thread as `most` allows down to a warp.
+struct RowSplit {
+  int group, nv;
+  RowSplit(int d, int most) {
+    const int g8 = (d + 7) / 8;
+    nv = 1;
+    while (nv < most && 32 * nv < g8) nv *= 2;
+    group = 32;
+    while (group * nv < g8) group *= 2;
+  }
+};
+
+// Blocks: enough row groups for every row, or as many as stay on the device.
+inline int row_blocks(int64_t rows, int group, int threads, int per_sm) {
+  const int per = threads / group;
+  const int64_t need = (rows + per - 1) / per, most = (int64_t)device_info()->sm_count * per_sm;
+  return (int)(need < most ? need : most);
+}
+
+}  // namespace moe

@@ -1,0 +1,247 @@
+// Backward of the residual addition with the root-mean-square norm: the formulas
+// and the pipeline are described in norm.cuh.
+#include "norm.cuh"
+
+namespace moe {
+
+namespace {
+
+// Backward: the weight gradient of a block's rows stays in registers; one row of
+// partial sums a block goes to `partial` [gridDim.x, d].
+template <typename TX, typename TR, bool VEC, bool RING, int NV, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlocks : 1) add_norm_bwd_kernel(AddNormBwdParams p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ __align__(16) float red[2][kNormMaxThreads / 32];
+  // drop numbers that change hands; at the end the sums of the row groups
+  // (eight floats a thread and NV, in the ring where there is one; only blocks of
+  // kNormThreads have groups)
+  __shared__ uint4 xch[RING ? 1 : MAXT <= kNormThreads ? MAXT * 2 * NV : VEC ? 1 : MAXT];
+  using Ring = RowRing<8 * (sizeof(TX) + 2 * sizeof(TR)), NV>;
+  constexpr int XP = sizeof(TX) / 2, RP = sizeof(TR) / 2;   // 16-byte pieces of eight columns
+  pdl_begin();
+  const RowGroup rg(p.group);
+  const int G = rg.G, lane = rg.lane, d = p.d;
+  auto sync = [&]() { rg.sync(); };
+  float w[NV][8], dw[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = first_column<VEC>(i, lane, G);
+    load_weight8<VEC>(p.weight, p.w_f32, sizeof(TX) == 2 && p.x_f16, c, G, d, w[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  }
+  const int64_t step = (int64_t)gridDim.x * rg.per;
+  int64_t row = (int64_t)blockIdx.x * rg.per + rg.group;
+  Ring ring(smem);
+  // RING: where the next row to copy starts
+  const TX* cy = static_cast<const TX*>(p.dy) + row * p.ld_dy;
+  const TR* ch = static_cast<const TR*>(p.h) + row * p.ld_h;
+  const TR* cd = p.dres ? static_cast<const TR*>(p.dres) + row * p.ld_dres : nullptr;
+  int64_t copy_row = row;
+  auto copy = [&]() {
+    if (copy_row < p.rows) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (lane + i * G) * 8;
+        ring.put(i * XP, cy, c, d);
+        ring.put(NV * XP + i * RP, ch, c, d);
+        if (cd) ring.put(NV * (XP + RP) + i * RP, cd, c, d);
+      }
+      cy += step * p.ld_dy;
+      ch += step * p.ld_h;
+      if (cd) cd += step * p.ld_dres;
+      copy_row += step;
+    }
+    ring.ahead = ring.next(ring.ahead);
+    cp_async_commit();
+  };
+  if constexpr (RING) {
+#pragma unroll 1
+    for (int i = 0; i < Ring::kDepth - 1; ++i) copy();
+  }
+  float rn = row < p.rows ? p.rstd[row] : 0.0f;
+  for (int turn = 0; row < p.rows; row += step, turn ^= 1) {
+    Raw8<TX> yr[NV] = {};
+    Raw8<TR> hr[NV] = {};
+    const float r = rn;
+    if (row + step < p.rows) rn = p.rstd[row + step];
+    if constexpr (RING) {
+      __syncwarp();   // every lane has read the slot that is filled now
+      copy();
+      cp_async_wait<Ring::kDepth - 1>();
+      __syncwarp();
+    }
+    float dot = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = first_column<VEC>(i, lane, G);
+      if constexpr (RING) {
+        yr[i] = ring.template get<TX>(i * XP);
+        hr[i] = ring.template get<TR>(NV * XP + i * RP);
+      } else {
+        yr[i] = load8_warp<TX, VEC>(static_cast<const TX*>(p.dy) + row * p.ld_dy, c, G, d, c < d);
+        hr[i] = load8_warp<TR, VEC>(static_cast<const TR*>(p.h) + row * p.ld_h, c, G, d, c < d);
+      }
+      float a[8], b[8];
+      widen8(yr[i], a);
+      widen8(hr[i], b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float ah = a[j] * b[j];
+        dw[i][j] = fmaf(ah, r, dw[i][j]);
+        dot = fmaf(ah, w[i][j], dot);
+      }
+    }
+    dot = rg.sum(dot, red[turn]);
+    const float k = r * r * (dot * p.inv_d);
+    uint4 numbers[NV];
+    if (p.dx && p.rng.threshold)
+      drop_numbers<VEC>(numbers, lane, G, (uint32_t)row, p.rng, xch + rg.group * G, sync);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = first_column<VEC>(i, lane, G);
+      const bool in = c < d;
+      float a[8], b[8];
+      widen8(yr[i], a);
+      widen8(hr[i], b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[j] = r * (a[j] * w[i][j] - b[j] * k);
+      if (cd) {
+        Raw8<TR> dr = {};
+        if constexpr (RING)
+          dr = ring.template get<TR>(NV * (XP + RP) + i * RP);
+        else
+          dr = load8_warp<TR, VEC>(static_cast<const TR*>(p.dres) + row * p.ld_dres, c, G, d, in);
+        widen8(dr, b);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] += b[j];
+      }
+      if (p.dh) store8_warp<TR, VEC>(static_cast<TR*>(p.dh) + row * p.ld_dh, c, G, d, narrow8<TR>(a), in);
+      if (p.dx) {
+        if (p.rng.threshold) drop8(a, numbers[i], p.rng);
+        store8_warp<TX, VEC>(static_cast<TX*>(p.dx) + row * p.ld_dx, c, G, d, narrow8<TX>(a), in);
+      }
+    }
+    if constexpr (RING) ring.slot = ring.next(ring.slot);
+  }
+  if (!p.partial) return;
+  float* out = p.partial + (int64_t)blockIdx.x * d;
+  const int cs = column_step<VEC>(G);
+  if (rg.per > 1) {   // the row groups' sums, added in their order
+    float* all = RING ? reinterpret_cast<float*>(smem) : reinterpret_cast<float*>(xch);
+    const int width = G * NV * 8;
+    cp_async_wait<0>();
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) all[rg.group * width + first_column<VEC>(i, lane, G) + j * cs] = dw[i][j];
+    __syncthreads();
+    for (int c = threadIdx.x; c < d; c += blockDim.x) {
+      float s = 0.0f;
+      for (int g = 0; g < rg.per; ++g) s += all[g * width + c];
+      out[c] = s;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = first_column<VEC>(i, lane, G);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c + j * cs < d) out[c + j * cs] = dw[i][j];
+    }
+  }
+}
+
+// dw[c] = sum of the partial rows, 32 columns a block: 32 warps take every
+// 32nd row, their sums are added in warp order.
+__global__ void __launch_bounds__(1024) add_norm_dw_kernel(const float* __restrict__ partial,
+                                                           int n_partial, int d,
+                                                           float* __restrict__ dw) {
+  __shared__ float s[32][33];
+  pdl_begin();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  float acc = 0.0f;
+  if (c < d) {
+#pragma unroll 8
+    for (int i = warp; i < n_partial; i += 32) acc += partial[(int64_t)i * d + c];
+  }
+  s[warp][lane] = acc;
+  __syncthreads();
+  const float sum = warp_sum(s[lane][warp]);   // column `warp` of the 32
+  if (lane == 0 && blockIdx.x * 32 + warp < d) dw[blockIdx.x * 32 + warp] = sum;
+}
+
+// p = NULL: raise the kernel's shared memory limit.
+template <typename TX, typename TR, bool VEC, bool RING, int NV, int MAXT>
+cudaError_t bwd_run(const AddNormBwdParams* p, int* blocks, cudaStream_t s) {
+  auto* kernel = &add_norm_bwd_kernel<TX, TR, VEC, RING, NV, MAXT>;
+  constexpr int ring = RING ? RowRing<8 * (sizeof(TX) + 2 * sizeof(TR)), NV>::kBytes : 0;
+  if (p == nullptr)
+    return ring ? cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, MAXT * ring)
+                : cudaSuccess;
+  const int threads = p->group > kNormThreads ? p->group : kNormThreads;
+  *blocks = row_blocks(p->rows, p->group, threads, threads <= kNormThreads ? (RING ? kNormBlocks : 2) : 1);
+  return launch_pdl(kernel, dim3(*blocks), dim3(threads), (size_t)threads * ring, s, *p);
+}
+
+// Rows up to 8192 columns (512 threads) come through the ring; wider ones are
+// read as they are needed.
+template <typename TX, typename TR, bool VEC>
+cudaError_t bwd_types(const AddNormBwdParams* p, int* blocks, cudaStream_t s) {
+  cudaError_t e = cudaSuccess;
+  if (p == nullptr) {
+    if constexpr (VEC) {
+      e = bwd_run<TX, TR, true, true, 1, kNormThreads>(p, blocks, s);
+      if (e == cudaSuccess) e = bwd_run<TX, TR, true, true, 2, kNormThreads>(p, blocks, s);
+      if (e == cudaSuccess) e = bwd_run<TX, TR, true, true, 2, 512>(p, blocks, s);
+    }
+    return e;
+  }
+  AddNormBwdParams q = *p;
+  RowSplit split(p->d, 2);
+  if (split.group > kNormMaxThreads) split = RowSplit(p->d, 4);
+  q.group = split.group;
+  if (split.nv == 4) return bwd_run<TX, TR, VEC, false, 4, kNormMaxThreads>(&q, blocks, s);
+  if (split.group > 512) return bwd_run<TX, TR, VEC, false, 2, kNormMaxThreads>(&q, blocks, s);
+  if (split.nv == 1) return bwd_run<TX, TR, VEC, VEC, 1, kNormThreads>(&q, blocks, s);
+  return split.group <= kNormThreads ? bwd_run<TX, TR, VEC, VEC, 2, kNormThreads>(&q, blocks, s)
+                                     : bwd_run<TX, TR, VEC, VEC, 2, 512>(&q, blocks, s);
+}
+
+template <typename TX, typename TR>
+cudaError_t bwd_vec(const AddNormBwdParams* p, bool vec, int* blocks, cudaStream_t s) {
+  return vec ? bwd_types<TX, TR, true>(p, blocks, s) : bwd_types<TX, TR, false>(p, blocks, s);
+}
+
+}  // namespace
+
+cudaError_t norm_bwd_init() {
+  cudaError_t e = bwd_vec<__nv_bfloat16, __nv_bfloat16>(nullptr, true, nullptr, nullptr);
+  if (e == cudaSuccess) e = bwd_vec<__nv_bfloat16, float>(nullptr, true, nullptr, nullptr);
+  if (e == cudaSuccess) e = bwd_vec<__half, __half>(nullptr, true, nullptr, nullptr);
+  if (e == cudaSuccess) e = bwd_vec<__half, float>(nullptr, true, nullptr, nullptr);
+  if (e == cudaSuccess) e = bwd_vec<float, float>(nullptr, true, nullptr, nullptr);
+  return e;
+}
+
+cudaError_t launch_add_norm_bwd(const AddNormBwdParams& p, int dtype, int res_dtype, bool vec, float* dw,
+                                cudaStream_t s) {
+  const bool same = dtype == res_dtype;
+  int blocks = 0;
+  cudaError_t e;
+  if (dtype == MOE_DT_BF16)
+    e = same ? bwd_vec<__nv_bfloat16, __nv_bfloat16>(&p, vec, &blocks, s)
+             : bwd_vec<__nv_bfloat16, float>(&p, vec, &blocks, s);
+  else if (dtype == MOE_DT_F16)
+    e = same ? bwd_vec<__half, __half>(&p, vec, &blocks, s) : bwd_vec<__half, float>(&p, vec, &blocks, s);
+  else
+    e = bwd_vec<float, float>(&p, vec, &blocks, s);
+  if (e != cudaSuccess || dw == nullptr) return e;
+  return launch_pdl(add_norm_dw_kernel, dim3((unsigned)((p.d + 31) / 32)), dim3(1024), 0, s,
+                    static_cast<const float*>(p.partial), blocks, p.d, dw);
+}
+
+}  // namespace moe
