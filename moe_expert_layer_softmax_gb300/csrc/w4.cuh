@@ -5,20 +5,28 @@
 // Two codes a byte, the even column in the low nibble; row-major, so one row of
 // K columns is K/2 contiguous bytes.
 //
-// Bound by the weights' bytes: every weight is read once and used for a handful
-// of vectors.  The products run on mma.sync m16n8k16 with 16 weight rows as A
-// and eight vectors as B: the tensor core only has to keep up with HBM here, and
-// the fragment form lets each lane turn its 4-bit words into operands itself.
-// What comes next to bounding it is that conversion (two logic operations and
-// one subtraction for two weights, a third of the issue slots at full HBM rate).
+// The least a call costs is the weights' bytes: every weight is read once and
+// used for a handful of vectors.  The products run on mma.sync m16n8k16 with 16
+// weight rows as A and eight vectors as B: each lane turns its own 4-bit words
+// into operands, and eight vectors do not fill a larger matrix instruction.
+// What bounds it in fact is issue: about 150 instructions for each 128 columns
+// of 16 rows, 40 of them the conversion of the codes, at 45-50% of the issue
+// slots, half of the rest waits between dependent ones.  Weights that already
+// lie in L2 take the same time.  64 experts (2048 x 1408, 64 tokens) stream 3.5
+// TB/s, eight tokens on experts of 4096 x 2048 4.6 TB/s.  Weights fetched by TMA
+// tiles (one lane, 128-byte boxes) came out the same, 88.8 against 87.8 us, and
+// by one bulk copy a row slower (104 us), so the copies stay with the lanes.
 // The sum over k may visit columns in any order as long as A and B agree, so a
 // lane's fragment columns are simply those of the words it holds.  Products of
 // a group are exact integers times activations, summed in fp32; the group's
 // scale multiplies the fp32 sum.
 //
 // One block of 16 warps runs on each SM and takes an equal share of the tiles;
-// its warps split the share's (tile, stage) pairs evenly, whatever the number
-// of tiles, and add up a tile's parts in shared memory in a fixed order.
+// its warps split the share's (tile, step) pairs evenly, whatever the number
+// of tiles, and add up a tile's parts in shared memory in a fixed order.  (64
+// experts as above, 64 tokens, and one token on eight of 4096 x 2048: 16 warps
+// with three steps in flight 87.8 and 32.9 us, 12 with three 90.6 and 32.4, 12
+// with four 88.0 and 31.9, 24 and more spill.)
 #pragma once
 
 #include "block.cuh"
@@ -148,7 +156,8 @@ MOE_DEV uint4 order_piece(const uint4& x) {
 template <typename T, int NT> struct Vectors {
   const T* x[NT];        // kOrdered, kNatural
   int64_t low;           // kOrdered: distance of the low parts
-  uint32_t s, s_low;     // kStaged: the vector and its low parts
+  uint32_t s, s_low;     // kStaged: the first tile's vector and its low parts
+  uint32_t to[NT];       // kStaged: bytes from it to each tile's
   uint32_t table;        // kStaged: (factor, 8 sum) of this lane's two columns
 };
 
@@ -182,7 +191,7 @@ struct RowPtr {
 //          32 or 64 more than that) the last stage is cut and the scales are
 //          read directly
 //   T      type of the vectors, S of the scales;  LOW: a vector has two parts
-//   VC     vectors that the table of kStaged is for: 8 or 1
+//   VC     vectors that the table of kStaged is for: 8 NT, or 1 (the same in all columns)
 template <typename T, typename S, int W, int NT, bool LOW, XSource XS, bool FULL, bool RUNS, int VC, typename Rows>
 struct Segment {
   static constexpr int kScales = 4 / W;   // of a row in a stage
@@ -323,8 +332,8 @@ struct Segment {
     }
   }
 
-  // Stage h of the present step.
-  MOE_DEV void product(int h, const At& at, const Vectors<T, NT>& v, int nt, float (*acc)[4]) const {
+  // Stage h of the present step, for M tiles of vectors.
+  template <int M> MOE_DEV void product(int h, const At& at, const Vectors<T, NT>& v, float (*acc)[4]) const {
     const int t = threadIdx.x & 3;
     float fa[kScales], fb[kScales];
     load_scales(h, at, fa, fb);
@@ -336,70 +345,75 @@ struct Segment {
       const uint32_t p = get + ((byte & 112) ^ swz) + (byte & 15) + at.slot;
       const Words<W> wa = load_words<W>(p), wb = load_words<W>(p + 1024);
       if constexpr (XS == kStaged) {
-        float c[4], cl[4];
+        // low parts of a single tile sum on their own: two chains of products
+        constexpr bool own = LOW && M == 1;
+        float c[M][4], cl[4];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
           uint32_t a[4], b[4];
           codes_fp16(wa.w[i], a);
           codes_fp16(wb.w[i], b);
           const int to = h * 256 + (j * W + i) * 64;
-          const Words<4> x = load_words<4>(at.x + to);
-          MmaT<__half>::mma(c, i == 0 ? zero : c, a[0], b[0], a[1], b[1], x.w[0], x.w[1]);
-          MmaT<__half>::mma(c, c, a[2], b[2], a[3], b[3], x.w[2], x.w[3]);
-          if constexpr (LOW) {
-            const Words<4> y = load_words<4>(at.low + to);
-            MmaT<__half>::mma(cl, i == 0 ? zero : cl, a[0], b[0], a[1], b[1], y.w[0], y.w[1]);
-            MmaT<__half>::mma(cl, cl, a[2], b[2], a[3], b[3], y.w[2], y.w[3]);
+#pragma unroll
+          for (int m = 0; m < M; ++m) {
+            const Words<4> x = load_words<4>(at.x + (m ? v.to[m] : 0) + to);
+            MmaT<__half>::mma(c[m], i == 0 ? zero : c[m], a[0], b[0], a[1], b[1], x.w[0], x.w[1]);
+            MmaT<__half>::mma(c[m], c[m], a[2], b[2], a[3], b[3], x.w[2], x.w[3]);
+            if constexpr (LOW) {
+              const Words<4> y = load_words<4>(at.low + (m ? v.to[m] : 0) + to);
+              float* l = own ? cl : c[m];
+              MmaT<__half>::mma(l, own && i == 0 ? zero : l, a[0], b[0], a[1], b[1], y.w[0], y.w[1]);
+              MmaT<__half>::mma(l, l, a[2], b[2], a[3], b[3], y.w[2], y.w[3]);
+            }
           }
         }
-        float f0, s0, f1, s1;   // factor and 8 times the group's sum, of two columns
-        const uint32_t entry = at.table + (h * kScales + j) * (VC * 8);
-        if constexpr (VC == 8) {
-          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f0), "=f"(s0), "=f"(f1), "=f"(s1) : "r"(entry));
-        } else {
-          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f0), "=f"(s0) : "r"(entry));
-          f1 = f0;
-          s1 = s0;
-        }
-        if constexpr (LOW) {
+        if constexpr (own) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) c[i] += cl[i];
+          for (int i = 0; i < 4; ++i) c[0][i] += cl[i];
         }
-        acc[0][0] = fmaf(fa[j], fmaf(c[0], f0, -s0), acc[0][0]);
-        acc[0][1] = fmaf(fa[j], fmaf(c[1], f1, -s1), acc[0][1]);
-        acc[0][2] = fmaf(fb[j], fmaf(c[2], f0, -s0), acc[0][2]);
-        acc[0][3] = fmaf(fb[j], fmaf(c[3], f1, -s1), acc[0][3]);
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          float f0, s0, f1, s1;   // factor and 8 times the group's sum, of two columns
+          const uint32_t entry = at.table + (h * kScales + j) * (VC * 8) + m * 64;
+          if constexpr (VC > 1) {
+            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f0), "=f"(s0), "=f"(f1), "=f"(s1) : "r"(entry));
+          } else {
+            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f0), "=f"(s0) : "r"(entry));
+            f1 = f0;
+            s1 = s0;
+          }
+          acc[m][0] = fmaf(fa[j], fmaf(c[m][0], f0, -s0), acc[m][0]);
+          acc[m][1] = fmaf(fa[j], fmaf(c[m][1], f1, -s1), acc[m][1]);
+          acc[m][2] = fmaf(fb[j], fmaf(c[m][2], f0, -s0), acc[m][2]);
+          acc[m][3] = fmaf(fb[j], fmaf(c[m][3], f1, -s1), acc[m][3]);
+        }
       } else {
-        float c[NT][4];
+        float c[M][4];
 #pragma unroll
         for (int i = 0; i < W; ++i) {
           uint32_t a[4], b[4];
           Mma::widen(wa.w[i], a);
           Mma::widen(wb.w[i], b);
 #pragma unroll
-          for (int m = 0; m < NT; ++m) {
-            if (m < nt) {
+          for (int m = 0; m < M; ++m) {
 #pragma unroll
-              for (int part = 0; part < (LOW ? 2 : 1); ++part) {
-                uint4 x;
-                if constexpr (XS == kOrdered)
-                  x = *reinterpret_cast<const uint4*>(v.x[m] + part * v.low + (at.stage + h) * 128 + ((j * W + i) * 4 + t) * 8);
-                else
-                  x = order_piece(*reinterpret_cast<const uint4*>(v.x[m] + (at.stage + h) * 128 + j * 32 * W + t * 8 * W + i * 8));
-                Mma::mma(c[m], i == 0 && part == 0 ? zero : c[m], a[0], b[0], a[1], b[1], x.x, x.y);
-                Mma::mma(c[m], c[m], a[2], b[2], a[3], b[3], x.z, x.w);
-              }
+            for (int part = 0; part < (LOW ? 2 : 1); ++part) {
+              uint4 x;
+              if constexpr (XS == kOrdered)
+                x = *reinterpret_cast<const uint4*>(v.x[m] + part * v.low + (at.stage + h) * 128 + ((j * W + i) * 4 + t) * 8);
+              else
+                x = order_piece(*reinterpret_cast<const uint4*>(v.x[m] + (at.stage + h) * 128 + j * 32 * W + t * 8 * W + i * 8));
+              Mma::mma(c[m], i == 0 && part == 0 ? zero : c[m], a[0], b[0], a[1], b[1], x.x, x.y);
+              Mma::mma(c[m], c[m], a[2], b[2], a[3], b[3], x.z, x.w);
             }
           }
         }
 #pragma unroll
-        for (int m = 0; m < NT; ++m) {
-          if (m < nt) {
-            acc[m][0] = fmaf(fa[j], c[m][0], acc[m][0]);
-            acc[m][1] = fmaf(fa[j], c[m][1], acc[m][1]);
-            acc[m][2] = fmaf(fb[j], c[m][2], acc[m][2]);
-            acc[m][3] = fmaf(fb[j], c[m][3], acc[m][3]);
-          }
+        for (int m = 0; m < M; ++m) {
+          acc[m][0] = fmaf(fa[j], c[m][0], acc[m][0]);
+          acc[m][1] = fmaf(fa[j], c[m][1], acc[m][1]);
+          acc[m][2] = fmaf(fb[j], c[m][2], acc[m][2]);
+          acc[m][3] = fmaf(fb[j], c[m][3], acc[m][3]);
         }
       }
     }
@@ -417,7 +431,11 @@ struct Segment {
     }
   }
 
+  // The share's products with `nt` tiles of vectors.
   MOE_DEV void finish(const Vectors<T, NT>& v, int nt, float* parts) {
+    if (NT == 1 || nt == 1) run_share<1>(v, parts); else run_share<NT>(v, parts);
+  }
+  template <int M> MOE_DEV void run_share(const Vectors<T, NT>& v, float* parts) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     float acc[NT][4];
 #pragma unroll
@@ -445,10 +463,10 @@ struct Segment {
       cp_async_wait<kRing - 1>();
       __syncwarp();
       if (at.stage + 1 < run) {
-        product(0, at, v, nt, acc);
-        product(1, at, v, nt, acc);
+        product<M>(0, at, v, acc);
+        product<M>(1, at, v, acc);
       } else {
-        product(0, at, v, nt, acc);
+        product<M>(0, at, v, acc);
       }
       __syncwarp();   // the slot is free for every lane's next copy
       at.slot = next_slot(at.slot);
@@ -568,16 +586,22 @@ MOE_DEV void stage_vectors(const StagedAt& at, int count, int K, Row row) {
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at.low + to), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
       if (c[u] % (4 * W) == 0) {
         const int group = c[u] / (4 * W);
-        const uint32_t entry = at.table + (VC == 8 ? (group * 8 + m[u]) * 8 : (m[u] * (K / (32 * W)) + group) * 8);
+        const uint32_t entry = at.table + (VC > 1 ? (group * VC + m[u]) * 8 : (m[u] * (K / (32 * W)) + group) * 8);
         asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(entry), "f"(exp2i(24 - k)), "f"(8.0f * sum) : "memory");
       }
     }
   }
 }
 
-// Bring [at, at + bytes) (16-byte aligned, whole) into L2.
-MOE_DEV void prefetch_l2(const void* at, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
+// Where this lane finds its staged vectors, `here` of them (places past the last
+// repeat it, unused).
+template <typename T, int NT> MOE_DEV void staged_at(Vectors<T, NT>& v, const StagedAt& at, int here) {
+  const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+  v.s = at.x + min(g, here - 1) * at.stride;
+  v.s_low = v.s + (at.low - at.x);
+#pragma unroll
+  for (int m = 0; m < NT; ++m) v.to[m] = (min(m * 8 + g, here - 1) - min(g, here - 1)) * at.stride;
+  v.table = at.table + t * 16;
 }
 
 // Raise a kernel's dynamic shared memory limit (once, from moe_init).

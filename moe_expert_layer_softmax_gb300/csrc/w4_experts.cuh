@@ -6,10 +6,19 @@
 // experts that have routes and writes act.  For one token the second kernel
 // takes W_down of all its experts as one matrix of k f columns and writes out;
 // for more it writes each route's product, and a third kernel adds them up.
-// Few routes an expert (up to six on average): both kernels stage their vectors
-// (fp16, act in two parts); more: they read them from global memory, x as it is
-// and act as two bf16 parts in fragment order.  Either way act keeps 16 bits or
-// more, so that storing it costs no accuracy beside a bf16 or fp16 result.
+// Both kernels stage their vectors (fp16, act in two parts) while shared memory
+// has room for four at a time (or half the tokens, if those are fewer);
+// otherwise (d above 12 K, f above 6 K, or many routes) they read them from
+// global memory, x as it is and act as two bf16 parts in fragment order.  Either way act keeps 16 bits or more, so that storing it costs no
+// accuracy beside a bf16 or fp16 result.
+//
+// Measured (us, bf16, weights from HBM): 64 experts of 2048 x 1408, four a token,
+// groups of 64: 13.0 for one token, 38.7 for eight, 68.6 for 32, 85.0 for 64 (294
+// MB, 3.5 TB/s), 123 for 128, 375 for 512.  64 experts of 4096 x 2048, eight a
+// token, groups of 128: 30.9 for one token (104 MB, 3.4 TB/s), 115 for eight (4.6
+// TB/s).  Read from global memory instead, the first took 155 us with 64 tokens
+// and the second 46 us with one; 32 experts of 4096 x 4096, where seven vectors
+// are staged at a time, 64 tokens, 504 us rather than 305.
 // (Included by one file per type, so that they compile side by side.)
 #pragma once
 
@@ -111,7 +120,9 @@ MOE_DEV void find_routes(const Lists& l, int R, int e, const float* gates) {
 // tile of an expert with w rounds being w of them.  Tiles belong to the block in
 // whose range their first unit lies.  Going on to another expert costs a block
 // about as much as kTurnUnits tiles (the last warps, the sums, the next
-// vectors), so as many empty units lie between two experts.  Where every expert
+// vectors), so as many empty units lie between two experts (64 experts of 2048 x
+// 1408: 40.9 us with them, 44.1 without for eight tokens, 87.8 and 88.7 for 64).
+// Where every expert
 // has one round and the blocks divide among the experts with hardly a loss,
 // they do not cross from one to another.
 constexpr int kTurnUnits = 4;
@@ -160,6 +171,7 @@ struct Pass {
   int expert, t0, tiles, m0, here;   // the present pass: its tiles, its routes
   int end;                           // of the expert's tiles in the share
   bool enter;                        // it is the first of its expert
+  bool other;                        // its routes are not those of the pass before
   bool valid;
   MOE_DEV Pass(const Lists& l, int used_, int per, int seg_, int most_)
       : share(l, used_, per), used(used_), seg(seg_), most(most_) {
@@ -174,11 +186,12 @@ struct Pass {
     tiles = min(end - first, seg);
     m0 = 0;
     here = min(l.counts[expert], most);
-    enter = true;
+    enter = other = true;
   }
   MOE_DEV void next(const Lists& l) {
     const int n = l.counts[expert];
     enter = false;
+    other = n > most;
     m0 += most;
     if (m0 >= n) {
       m0 = 0;
@@ -230,23 +243,6 @@ template <typename S, int W> struct TokenRows {
   }
 };
 
-// Whoever is through with its own weights brings the second kernel's first ones
-// into L2 (up to kPrefetchMost of them): what its start, its staging and the end
-// of this kernel would leave idle of HBM.
-constexpr int64_t kPrefetchMost = 32 << 20;
-constexpr int kPrefetchPiece = 4096;
-MOE_DEV void prefetch_down(const ExpertsW4Params& p, const Lists& l, int used) {
-  const int64_t per = (int64_t)p.d * (p.f / 2);
-  const int64_t all = min(per * used, kPrefetchMost) / kPrefetchPiece;
-  const int warps = gridDim.x * kW4Warps, warp = blockIdx.x * kW4Warps + (threadIdx.x >> 5);
-  for (int64_t i = warp + (int64_t)(threadIdx.x & 31) * warps; i < all; i += (int64_t)32 * warps) {
-    const int64_t at = i * kPrefetchPiece;
-    const int e = (int)(at / per);
-    const int64_t in = at - e * per;
-    prefetch_l2(p.down_q + (int64_t)l.used[e] * per + in, (uint32_t)min(per - in, (int64_t)kPrefetchPiece));
-  }
-}
-
 template <typename T, int W, int NT, XSource XS>
 __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_up_kernel(ExpertsW4Params p, Plan plan) {
   extern __shared__ __align__(128) uint8_t smem[];
@@ -259,7 +255,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_up_kernel(ExpertsW4P
   const uint32_t rings = smem_u32(smem);
   float* parts = reinterpret_cast<float*>(smem + kRingsBytes);
   const Lists l = lists_at(smem + plan.smem_lists, R);
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int g = (threadIdx.x & 31) >> 2;
   const int stages = p.d / 128, steps = (stages + 1) / 2;
   StagedAt at;
   at.x = rings + kRingsBytes + (plan.seg_tiles + kW4Warps) * NT * 512;
@@ -270,10 +266,10 @@ __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_up_kernel(ExpertsW4P
   float* act = static_cast<float*>(p.act);
   __nv_bfloat16* hi = static_cast<__nv_bfloat16*>(p.act);
   __nv_bfloat16* lo = hi + (int64_t)R * p.f;
-  if (XS == kStaged && p.T == 1) stage_vectors<T, W, false, 8>(at, 1, p.d, [&](int) { return x; });
+  if (XS == kStaged && p.T == 1) stage_vectors<T, W, false, 8 * NT>(at, 1, p.d, [&](int) { return x; });
   const int used = find_used(l, p.topk_idx, idx0, R, p.E, plan.most);
   Pass ps(l, used, p.f / 8, plan.seg_tiles, plan.most);
-  using Seg = Segment<T, T, W, NT, false, XS, true, false, 8, UpRows<T, W>>;
+  using Seg = Segment<T, T, W, NT, false, XS, true, false, 8 * NT, UpRows<T, W>>;
   const void* no_end = reinterpret_cast<const void*>(~uintptr_t(0));
   UpRows<T, W> rows = {p, ps.valid ? (int64_t)ps.expert * p.f + ps.t0 * 8 : 0};
   Seg seg(rings, rows, ps.valid ? ps.tiles : 0, 1, stages, p.d, no_end);
@@ -282,16 +278,16 @@ __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_up_kernel(ExpertsW4P
     if (ps.enter) find_routes(l, R, ps.expert, p.gates);
     auto token = [&](int m) { return x + (int64_t)(l.routes[ps.m0 + m] / p.k) * p.ld_x; };
     if constexpr (XS == kStaged) {
-      if (p.T > 1) stage_vectors<T, W, false, 8>(at, ps.here, p.d, token);
+      if (p.T > 1 && ps.other) stage_vectors<T, W, false, 8 * NT>(at, ps.here, p.d, token);
     }
     __syncthreads();   // the vectors are staged, and the parts of the pass before are read
     Vectors<T, NT> v;
+    if constexpr (XS == kStaged) {
+      staged_at(v, at, ps.here);
+    } else {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) v.x[j] = token(min(j * 8 + g, ps.here - 1));   // vectors past the last repeat it, unused
-    v.low = 0;
-    v.s = at.x + min(g, ps.here - 1) * at.stride;
-    v.s_low = 0;
-        v.table = at.table + t * 16;
+      for (int j = 0; j < NT; ++j) v.x[j] = token(min(j * 8 + g, ps.here - 1));   // past the last: unused
+    }
     seg.finish(v, (ps.here + 7) / 8, parts);
     const Pass done = ps;
     ps.next(l);
@@ -299,8 +295,6 @@ __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_up_kernel(ExpertsW4P
       seg.rows.row0 = (int64_t)ps.expert * p.f + ps.t0 * 8;
       seg.reset(ps.tiles);
       seg.start();
-    } else {
-      prefetch_down(p, l, used);
     }
     __syncthreads();
     for (int i = threadIdx.x; i < done.tiles * done.here * 8; i += kW4Threads) {
@@ -334,7 +328,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_down_kernel(ExpertsW
   const uint32_t rings = smem_u32(smem);
   float* parts = reinterpret_cast<float*>(smem + kRingsBytes);
   const Lists l = lists_at(smem + plan.smem_lists, R);
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int g = (threadIdx.x & 31) >> 2;
   const int stages = p.f / 128, steps = (stages + 1) / 2;
   StagedAt at;
   at.x = rings + kRingsBytes + (plan.seg_tiles + kW4Warps) * NT * 512;
@@ -346,7 +340,7 @@ __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_down_kernel(ExpertsW
   const float* act = static_cast<const float*>(p.act);
   const __nv_bfloat16* hi = static_cast<const __nv_bfloat16*>(p.act);
   Pass ps(l, used, p.d / 16, plan.seg_tiles, plan.most);
-  using Seg = Segment<__nv_bfloat16, T, W, NT, true, XS, true, false, 8, DownRows<T, W>>;
+  using Seg = Segment<__nv_bfloat16, T, W, NT, true, XS, true, false, 8 * NT, DownRows<T, W>>;
   const void* no_end = reinterpret_cast<const void*>(~uintptr_t(0));
   DownRows<T, W> rows = {p, ps.valid ? (int64_t)ps.expert * p.d + ps.t0 * 16 : 0};
   Seg seg(rings, rows, ps.valid ? ps.tiles : 0, 1, stages, p.f, no_end);
@@ -355,16 +349,17 @@ __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_down_kernel(ExpertsW
   pdl_launch_dependents();
   while (ps.valid) {
     if (ps.enter) find_routes(l, R, ps.expert, nullptr);
-    if constexpr (XS == kStaged)
-      stage_vectors<float, W, true, 8>(at, ps.here, p.f, [&](int m) { return act + (int64_t)l.routes[ps.m0 + m] * p.f; });
+    if (XS == kStaged && ps.other)
+      stage_vectors<float, W, true, 8 * NT>(at, ps.here, p.f, [&](int m) { return act + (int64_t)l.routes[ps.m0 + m] * p.f; });
     __syncthreads();   // the vectors are staged, and the parts of the pass before are read
     Vectors<__nv_bfloat16, NT> v;
+    if constexpr (XS == kStaged) {
+      staged_at(v, at, ps.here);
+    } else {
 #pragma unroll
-    for (int j = 0; j < NT; ++j) v.x[j] = hi + (int64_t)l.routes[ps.m0 + min(j * 8 + g, ps.here - 1)] * p.f;
-    v.low = (int64_t)R * p.f;
-    v.s = at.x + min(g, ps.here - 1) * at.stride;
-    v.s_low = v.s + plan.most * at.stride;
-        v.table = at.table + t * 16;
+      for (int j = 0; j < NT; ++j) v.x[j] = hi + (int64_t)l.routes[ps.m0 + min(j * 8 + g, ps.here - 1)] * p.f;
+      v.low = (int64_t)R * p.f;
+    }
     seg.finish(v, (ps.here + 7) / 8, parts);
     const Pass done = ps;
     ps.next(l);
@@ -434,10 +429,9 @@ __global__ void __launch_bounds__(kW4Threads, 1) experts_w4_token_kernel(Experts
         __syncthreads();
       }
       Vectors<__nv_bfloat16, 1> v;
-      v.x[0] = nullptr;
-      v.low = 0;
       v.s = at.x;   // every column of the fragment repeats the one vector
-            v.s_low = at.low;
+      v.s_low = at.low;
+      v.to[0] = 0;
       v.table = at.table;
       seg.finish(v, 1, parts);
       __syncthreads();
@@ -482,7 +476,6 @@ __global__ void __launch_bounds__(256) experts_w4_join_kernel(ExpertsW4Params p)
   for (int i = 0; i < 4; ++i) out[i] = Elem<T>::from_f(a[i]);
 }
 
-
 // Shared memory of a kernel with `lists` bytes of lists and `x` of vectors, and
 // the most tiles that the parts of a segment have room for.
 size_t plan_smem(int share, int NT, int x, int lists, Plan* plan) {
@@ -497,8 +490,14 @@ size_t plan_smem(int share, int NT, int x, int lists, Plan* plan) {
 int64_t staged_bytes(int count, int K, int parts, int cols, int W) {
   return (int64_t)count * parts * staged_stride(K) + (int64_t)K / (32 * W) * cols * 8;
 }
-bool staged_fits(int64_t bytes, int lists) {
-  return bytes <= kSmemMost - kRingsBytes - lists - 16 - (8 + kW4Warps) * 512;
+bool staged_fits(int64_t bytes, int lists, int NT) {
+  return bytes <= kSmemMost - kRingsBytes - lists - 16 - (8 + kW4Warps) * NT * 512;
+}
+// The most vectors a round can stage, up to 8 NT and the tokens there are.
+int most_staged(const ExpertsW4Params& p, int K, int parts, int NT, int W) {
+  int n = p.T < 8 * NT ? p.T : 8 * NT;
+  while (n > 0 && !staged_fits(staged_bytes(n, K, parts, 8 * NT, W), lists_bytes(p.T * p.k), NT)) --n;
+  return n;
 }
 
 int share_of(const ExpertsW4Params& p, int per) {
@@ -506,26 +505,34 @@ int share_of(const ExpertsW4Params& p, int per) {
   return (int)(((int64_t)used * per + sms - 1) / sms) + 1;
 }
 
+// The plan of a kernel with `per` tiles of an expert and vectors of K values in
+// `parts` parts.
+struct Launch {
+  Plan plan;
+  size_t smem;
+  Launch(const ExpertsW4Params& p, int per, int K, int parts, int NT, int W, bool staged) {
+    plan.most = staged ? most_staged(p, K, parts, NT, W) : 8 * NT;
+    smem = plan_smem(share_of(p, per), NT, staged ? (int)staged_bytes(plan.most, K, parts, 8 * NT, W) : 0,
+                     lists_bytes(p.T * p.k), &plan);
+  }
+  // Sixteen vectors a round: they are staged, and a block's tiles are one segment.
+  bool serves(const ExpertsW4Params& p, int per) const { return plan.most > 8 && plan.seg_tiles >= share_of(p, per); }
+};
+
 template <typename T, int W, int NT, XSource XS>
 cudaError_t up_launch(const ExpertsW4Params* p, cudaStream_t s) {
   auto* kernel = &experts_w4_up_kernel<T, W, NT, XS>;
   if (p == nullptr) return allow_smem(kernel);
-  Plan plan;
-  plan.most = XS == kStaged && p->T < 8 ? p->T : 8 * NT;
-  const int x = XS == kStaged ? (int)staged_bytes(plan.most, p->d, 1, 8, W) : 0;
-  const size_t smem = plan_smem(share_of(*p, p->f / 8), NT, x, lists_bytes(p->T * p->k), &plan);
-  return launch_pdl(kernel, dim3(device_info()->sm_count), dim3(kW4Threads), smem, s, *p, plan);
+  const Launch l(*p, p->f / 8, p->d, 1, NT, W, XS == kStaged);
+  return launch_pdl(kernel, dim3(device_info()->sm_count), dim3(kW4Threads), l.smem, s, *p, l.plan);
 }
 
 template <typename T, int W, int NT, XSource XS>
 cudaError_t down_launch(const ExpertsW4Params* p, cudaStream_t s) {
   auto* kernel = &experts_w4_down_kernel<T, W, NT, XS>;
   if (p == nullptr) return allow_smem(kernel);
-  Plan plan;
-  plan.most = XS == kStaged && p->T < 8 ? p->T : 8 * NT;
-  const int x = XS == kStaged ? (int)staged_bytes(plan.most, p->f, 2, 8, W) : 0;
-  const size_t smem = plan_smem(share_of(*p, p->d / 16), NT, x, lists_bytes(p->T * p->k), &plan);
-  cudaError_t e = launch_pdl(kernel, dim3(device_info()->sm_count), dim3(kW4Threads), smem, s, *p, plan);
+  const Launch l(*p, p->d / 16, p->f, 2, NT, W, XS == kStaged);
+  cudaError_t e = launch_pdl(kernel, dim3(device_info()->sm_count), dim3(kW4Threads), l.smem, s, *p, l.plan);
   if (e != cudaSuccess) return e;
   return launch_pdl(experts_w4_join_kernel<T>, dim3((p->d + 1023) / 1024, p->T), dim3(256), 0, s, *p);
 }
@@ -546,35 +553,40 @@ template <typename T, int W> cudaError_t token_launch(const ExpertsW4Params* p, 
   return launch_pdl(kernel, dim3(blocks), dim3(kW4Threads), smem, s, *p, plan);
 }
 
-// p = NULL: raise every variant's shared memory limit.  Staged vectors serve up
-// to eight routes a round; where experts have more than six on average a second
-// round would read most weights again, and 16 or 32 vectors a pass are read from
-// global memory instead.
+// p = NULL: raise every variant's shared memory limit.
+// Staged rounds serve eight routes of an expert, or sixteen where the experts
+// have more than six on average and a block still takes its tiles of an expert
+// in one segment.  Measured, eight and sixteen (us): 8 experts of 1536 x 1024, 12
+// tokens on all of them 29.4 and 25.3, 64 tokens 92 and 77; 64 experts of 2048 x
+// 1408, whose tiles would become two and more segments, 128 tokens 123 and 166.
+// One token: W_down of all its experts as one product, 13.0 us, or a product for
+// each and their sum, 16.4 (2048 x 1408, four experts).
 template <typename T, int W> cudaError_t experts_nt(const ExpertsW4Params* p, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (p == nullptr) {
     e = up_launch<T, W, 1, kStaged>(p, s);
+    if (e == cudaSuccess) e = up_launch<T, W, 2, kStaged>(p, s);
     if (e == cudaSuccess) e = up_launch<T, W, 2, kNatural>(p, s);
-    if (e == cudaSuccess) e = up_launch<T, W, 4, kNatural>(p, s);
     if (e == cudaSuccess) e = down_launch<T, W, 1, kStaged>(p, s);
+    if (e == cudaSuccess) e = down_launch<T, W, 2, kStaged>(p, s);
     if (e == cudaSuccess) e = down_launch<T, W, 2, kOrdered>(p, s);
-    if (e == cudaSuccess) e = down_launch<T, W, 4, kOrdered>(p, s);
     return e == cudaSuccess ? token_launch<T, W>(p, s) : e;
   }
-  const int R = p->T * p->k, lists = lists_bytes(R);
-  const int few = p->T < 8 ? p->T : 8;
-  const bool token = p->T == 1 && staged_fits(token_bytes(*p, W), kTokenStatic);
-  const bool staged = (p->T <= 8 || R <= 6 * p->E) && staged_fits(staged_bytes(few, p->d, 1, 8, W), lists) &&
-                      (token || staged_fits(staged_bytes(few, p->f, 2, 8, W), lists));
-  if (staged) {
-    e = up_launch<T, W, 1, kStaged>(p, s);
-    if (e != cudaSuccess) return e;
-    return token ? token_launch<T, W>(p, s) : down_launch<T, W, 1, kStaged>(p, s);
+  const int R = p->T * p->k, few = p->T < 8 ? p->T : 8;
+  const bool token = p->T == 1 && staged_fits(token_bytes(*p, W), kTokenStatic, 1);
+  // both kernels or none: they agree on the form of act
+  const bool staged = most_staged(*p, p->d, 1, 1, W) * 2 >= few && (token || most_staged(*p, p->f, 2, 1, W) * 2 >= few);
+  if (!staged) {
+    e = up_launch<T, W, 2, kNatural>(p, s);
+    return e == cudaSuccess ? down_launch<T, W, 2, kOrdered>(p, s) : e;
   }
-  const bool two = R <= 16 * p->E;
-  e = two ? up_launch<T, W, 2, kNatural>(p, s) : up_launch<T, W, 4, kNatural>(p, s);
+  const bool many = R > 6 * p->E;
+  const bool up2 = many && Launch(*p, p->f / 8, p->d, 1, 2, W, true).serves(*p, p->f / 8);
+  e = up2 ? up_launch<T, W, 2, kStaged>(p, s) : up_launch<T, W, 1, kStaged>(p, s);
   if (e != cudaSuccess) return e;
-  return two ? down_launch<T, W, 2, kOrdered>(p, s) : down_launch<T, W, 4, kOrdered>(p, s);
+  if (token) return token_launch<T, W>(p, s);
+  const bool down2 = many && Launch(*p, p->d / 16, p->f, 2, 2, W, true).serves(*p, p->d / 16);
+  return down2 ? down_launch<T, W, 2, kStaged>(p, s) : down_launch<T, W, 1, kStaged>(p, s);
 }
 
 template <typename T> cudaError_t experts_group(int group, const ExpertsW4Params* p, cudaStream_t s) {

@@ -1,5 +1,9 @@
 // Products of a few vectors with 4-bit weights (sm_103a): y[m, n] = sum_k x[m, k]
-// W[n, k].  How the weights are streamed: w4.cuh.
+// W[n, k].  How the weights are streamed, and what bounds it: w4.cuh.  Measured
+// back to back from HBM: one vector and 4096 x 4096 6.0 us (8.9 MB, 1.5 TB/s;
+// about 4 us of it start and end of the kernel), 20011 x 2048 8.7, 4096 x 14336
+// 11.1 us (2.7 TB/s); eight vectors 6.7, 11.0 and 15.2 us; 64 vectors 24, 48 and
+// 80 us.
 #include "w4.cuh"
 
 namespace moe {
@@ -47,13 +51,13 @@ __global__ void __launch_bounds__(kW4Threads, 1) matvec_w4_kernel(MatvecArgs a) 
   pdl_begin();
   const uint32_t rings = smem_u32(smem);
   float* parts = reinterpret_cast<float*>(smem + kRingsBytes);
-  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int g = (threadIdx.x & 31) >> 2;
   const int all = (a.N + 15) / 16, stages = (a.K + 127) / 128;
   StagedAt at;
   at.x = rings + kRingsBytes + (a.seg_tiles + kW4Warps) * NT * 512;
   at.low = 0;
   at.stride = staged_stride(a.K);
-  at.table = at.x + min(a.M, 8) * at.stride;
+  at.table = at.x + a.M * at.stride;
   const int first = (int)((int64_t)blockIdx.x * all / gridDim.x);
   const int last = (int)((int64_t)(blockIdx.x + 1) * all / gridDim.x);
   const T* x = static_cast<const T*>(a.x);
@@ -63,22 +67,19 @@ __global__ void __launch_bounds__(kW4Threads, 1) matvec_w4_kernel(MatvecArgs a) 
     const int tiles = min(last - t0, a.seg_tiles);
     const MatvecRows<T, W> rows = {a.q, sc, (int64_t)t0 * 16, a.N, a.K, a.K / (32 * W)};
     for (int m0 = 0; m0 < a.M; m0 += 8 * NT) {
-      Segment<T, T, W, NT, false, XS, FULL, false, 8, MatvecRows<T, W>> seg(
+      Segment<T, T, W, NT, false, XS, FULL, false, 8 * NT, MatvecRows<T, W>> seg(
           rings, rows, tiles, 1, stages, a.K, sc + (int64_t)a.N * rows.groups);
       seg.start();
-      const int here = min(a.M - m0, 8 * NT);   // vectors past it repeat the last one, unused
-      if constexpr (XS == kStaged) {   // M <= 8: once
-        if (t0 == first)
-          stage_vectors<T, W, false, 8>(at, here, a.K, [&](int m) { return x + m * a.ld_x; });
-        __syncthreads();
-      }
+      const int here = min(a.M - m0, 8 * NT);   // kStaged: all of them
       Vectors<T, NT> v;
+      if constexpr (XS == kStaged) {
+        if (t0 == first) stage_vectors<T, W, false, 8>(at, here, a.K, [&](int m) { return x + m * a.ld_x; });
+        __syncthreads();
+        staged_at(v, at, here);
+      } else {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) v.x[j] = x + (m0 + min(j * 8 + g, here - 1)) * a.ld_x;
-      v.low = 0;
-      v.s = at.x + min(g, here - 1) * at.stride;
-      v.s_low = 0;
-            v.table = at.table + t * 16;
+        for (int j = 0; j < NT; ++j) v.x[j] = x + (m0 + min(j * 8 + g, here - 1)) * a.ld_x;
+      }
       seg.finish(v, (here + 7) / 8, parts);
       __syncthreads();
       for (int i = threadIdx.x; i < tiles * here * 16; i += kW4Threads) {
@@ -95,39 +96,44 @@ __global__ void __launch_bounds__(kW4Threads, 1) matvec_w4_kernel(MatvecArgs a) 
   }
 }
 
-int staged_bytes(int M, int K, int W) { return M * staged_stride(K) + K / (32 * W) * 64; }
+int64_t staged_bytes(int M, int K, int W) { return (int64_t)M * staged_stride(K) + (int64_t)K / (32 * W) * 64; }
+
+// Most tiles of a block.
+int share_of(int N) {
+  const int all = (N + 15) / 16, sms = device_info()->sm_count;
+  return (all + sms - 1) / sms;
+}
 
 // a = NULL: raise the kernel's shared memory limit.
 template <typename T, int W, int NT, XSource XS, bool FULL>
 cudaError_t matvec_launch(const MatvecArgs* a, cudaStream_t s) {
   auto* kernel = &matvec_w4_kernel<T, W, NT, XS, FULL>;
   if (a == nullptr) return allow_smem(kernel);
-  const int all = (a->N + 15) / 16;
-  const int sms = device_info()->sm_count;
-  const int blocks = all < sms ? all : sms;
-  const int x_bytes = XS == kStaged ? staged_bytes(a->M, a->K, W) : 0;
+  const int all = (a->N + 15) / 16, sms = device_info()->sm_count;
+  const int x_bytes = XS == kStaged ? (int)staged_bytes(a->M, a->K, W) : 0;
   const int room = (kSmemMost - kRingsBytes - x_bytes) / (NT * 512) - kW4Warps;
-  const int share = (all + blocks - 1) / blocks;
+  const int share = share_of(a->N);
   MatvecArgs args = *a;
   args.seg_tiles = share < room ? share : room;
   const size_t smem = kRingsBytes + (size_t)(args.seg_tiles + kW4Warps) * NT * 512 + x_bytes;
-  return launch_pdl(kernel, dim3(blocks), dim3(kW4Threads), smem, s, args);
+  return launch_pdl(kernel, dim3(all < sms ? all : sms), dim3(kW4Threads), smem, s, args);
 }
 
-// Up to eight vectors are staged while they leave room for the parts of eight
-// tiles; more of them are read where they are.
+// Vectors are staged (whole stages only) where each block has a tile for every
+// vector that it stages, and they leave room for the parts of eight tiles;
+// otherwise they are read where they are, sixteen a pass over the weights.
+// Measured, staged and read (us): 4096 x 4096, two tiles a block: 6.1 and 6.4
+// with one vector, 9.5 and 6.7 with eight; 20011 x 2048, nine tiles: 8.7 and 10.0
+// with one, 11.0 and 11.2 with eight; staged rounds of sixteen 15.9 and 14.1.
 template <typename T, int W, bool FULL>
 cudaError_t matvec_nt(const MatvecArgs* a, cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
   if constexpr (FULL) {
-    const bool fits = a != nullptr && a->M <= 8 && a->K <= 65536 &&
-                      staged_bytes(a->M, a->K, W) <= kSmemMost - kRingsBytes - (8 + kW4Warps) * 512;
-    if (a == nullptr || fits) e = matvec_launch<T, W, 1, kStaged, FULL>(a, s);
-    if (fits || e != cudaSuccess) return e;
+    const bool staged = a == nullptr || (a->M <= 8 && a->M <= share_of(a->N) &&
+                                         staged_bytes(a->M, a->K, W) <= kSmemMost - kRingsBytes - (8 + kW4Warps) * 512);
+    const cudaError_t e = staged ? matvec_launch<T, W, 1, kStaged, FULL>(a, s) : cudaSuccess;
+    if ((a != nullptr && staged) || e != cudaSuccess) return e;
   }
-  if (a == nullptr || a->M <= 16) e = matvec_launch<T, W, 2, kNatural, FULL>(a, s);
-  if (e == cudaSuccess && (a == nullptr || a->M > 16)) e = matvec_launch<T, W, 4, kNatural, FULL>(a, s);
-  return e;
+  return matvec_launch<T, W, 2, kNatural, FULL>(a, s);
 }
 
 template <typename T> cudaError_t matvec_group(int group, const MatvecArgs* a, cudaStream_t s) {
