@@ -525,7 +525,8 @@ MOE_API int moe_layer_bwd(const moe_shape_t* shape, const moe_bwd_args_t* args, 
  * The operators that stand next to the layer in a transformer block: the
  * residual addition with the norm before it (and the dropout of its output),
  * and the experts on 4-bit weights for serving.  The pages have no counterpart
- * to these calls; their arithmetic is written out with each.
+ * to these calls; their arithmetic is written out with each.  examples/block.py
+ * runs them together with the layer.
  *
  * Matrices here have a row stride `ld` (elements, >= the row's length); their
  * pointers need only the alignment of their element type.  Rows whose groups
@@ -544,7 +545,8 @@ typedef enum { MOE_DT_BF16 = 0, MOE_DT_F16 = 1, MOE_DT_F32 = 2 } moe_dtype_t;
  * and MOE_SF layout as moe_quantize_mxfp8 (block_axis 1).  These buffers hold
  * roundup(rows, 128) rows, the ones past `rows` are written as zero codes with
  * scale 2^0: they can be given to moe_grouped_gemm and moe_dequantize_mxfp8.
- * y_dq (nullable): also the values that the codes stand for, bf16.
+ * y_dq (nullable): also the values that the codes stand for, bf16.  The 8-bit
+ * output needs rows that take vector loads (MOE_ERR_ALIGN otherwise).
  *   x, y       dtype [rows, d]            residual, h  res_dtype [rows, d]
  *   weight     w_dtype [d]                rstd         fp32 [rows] or NULL
  *   res_dtype and w_dtype: dtype, or fp32.
@@ -643,7 +645,16 @@ MOE_API int moe_dequantize_w4(int64_t rows, int32_t K, int32_t group, int32_t dt
 
 /* y[m, n] = sum_k x[m, k] W[n, k], fp32 sums, for a few vectors: x dtype
  * [M, K] (16-byte aligned rows), W as above with N rows, y dtype [M, N].
- * N <= 1048560, K <= 2^18. */
+ * N <= 1048560, K <= 2^18.  The fastest with up to eight vectors; each sixteen
+ * more are one more pass over the weights.
+ * Here and in moe_experts_w4 a few vectors are held as fp16 times a power of two
+ * for each 128 columns (a bf16 or fp16 value is exact down to 2^-24 of the
+ * largest of them, off by less than 2^-34 of it below), and 8 times a group's sum
+ * comes off the products with its codes: errors of about 2^-20 of the group's
+ * largest |x| times its scale, far below a rounding of y, but not zero where the
+ * weights are.  A vector with a value of 2^118 or more, an infinity or a NaN gives
+ * results that are not finite (in its own rows alone).  The same call gives the
+ * same bits; another M may round differently. */
 MOE_API int moe_matvec_w4(int32_t M, int32_t N, int32_t K, int32_t group, int32_t dtype,
                           const void* x, int64_t ld_x, const uint8_t* q, const void* scales,
                           void* y, int64_t ld_y, void* stream);
@@ -651,8 +662,8 @@ MOE_API int moe_matvec_w4(int32_t M, int32_t N, int32_t K, int32_t group, int32_
 /* The layer's SwiGLU experts on 4-bit weights for a few tokens (decoding):
  *   out[t] = sum_j gates[t, j] * W_down[e] (silu(W_gate[e] x[t]) * (W_up[e] x[t])),
  *   e = topk_idx[t, j]
- * fp32 sums; the activations between the products keep 16 bits (two bf16
- * parts), out is rounded once.  An index of -1 stands for no expert and adds
+ * fp32 sums; the activations between the products keep 16 bits or more (two
+ * fp16 or two bf16 parts), out is rounded once.  An index of -1 stands for no expert and adds
  * nothing (a token without any gets zeros: unused places of a batch); any
  * other index outside [0, E) adds nothing and sets MOE_DEVERR_BOUNDS in the
  * workspace's error word.  Only the weights of experts with routes are read.

@@ -57,6 +57,7 @@ struct AddNormBwdParams {
 struct DropoutParams {
   int64_t rows;
   int32_t cols;
+  int32_t group;   // lanes of a row (set by the launcher)
   const void* x;
   int64_t ld_x;
   void* y;
@@ -65,7 +66,7 @@ struct DropoutParams {
 };
 
 constexpr int kNormMaxWidth = 32768;     // 1024 threads, four groups of eight columns each
-constexpr int kNormPartialRows = 1024;   // rows of partial weight gradients: blocks of the backward
+constexpr int kNormPartialRows = 1024;   // most blocks of the backward: rows of partial weight gradients
 
 cudaError_t norm_init();   // dynamic shared memory limits (moe_init)
 cudaError_t norm_bwd_init();

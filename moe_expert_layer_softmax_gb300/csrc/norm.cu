@@ -10,14 +10,14 @@ namespace {
 // scales and (dq) their values instead of y; the rows from `rows` on are the
 // padding of the last 128-row tile.
 template <typename TX, typename TR, bool MX, bool VEC, bool RING, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlocks : 1) add_norm_kernel(AddNormParams p) {
+__global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_kernel(AddNormParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float red[2][kNormMaxThreads / 32];
   __shared__ uint4 xch[VEC ? 1 : MAXT];
   using Ring = RowRing<8 * (sizeof(TX) + sizeof(TR)), NV>;
   constexpr int XP = sizeof(TX) / 2, RP = sizeof(TR) / 2;   // 16-byte pieces of eight columns
   pdl_begin();
-  const RowGroup rg(p.group);
+  const RowGroup<NV == 1> rg(p.group);
   const int G = rg.G, lane = rg.lane, d = p.d;
   auto sync = [&]() { rg.sync(); };
   float w[NV][8];
@@ -28,7 +28,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlock
   }
   const int64_t step = (int64_t)gridDim.x * rg.per;
   int64_t row = (int64_t)blockIdx.x * rg.per + rg.group;
-  Ring ring(smem);
+  Ring ring(smem, G);
   // RING: where the next row to copy starts
   const TX* cx = static_cast<const TX*>(p.x) + row * p.ld_x;
   const TR* cr = p.residual ? static_cast<const TR*>(p.residual) + row * p.ld_residual : nullptr;
@@ -51,7 +51,9 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlock
 #pragma unroll 1
     for (int i = 0; i < Ring::kDepth - 1; ++i) copy();
   }
-  for (int turn = 0; row < p.rows; row += step, turn ^= 1) {
+  // a warp goes on while its first group has a row
+  for (int turn = 0; row - rg.before() < p.rows; row += step, turn ^= 1) {
+    const bool live = NV > 1 || row < p.rows;
     float h[NV][8];
     if constexpr (RING) {
       __syncwarp();   // every lane has read the slot that is filled now
@@ -65,7 +67,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlock
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = first_column<VEC>(i, lane, G);
-      const bool in = c < d;
+      const bool in = c < d && live;
       Raw8<TX> xr = {};
       Raw8<TR> rr = {};
       if constexpr (RING) {
@@ -94,7 +96,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlock
     if constexpr (RING) ring.slot = ring.next(ring.slot);
     ss = rg.sum(ss, red[turn]);
     const float rstd = inv_sqrt(fmaf(ss, p.inv_d, p.eps));
-    if (lane == 0 && p.rstd) p.rstd[row] = rstd;
+    if (lane == 0 && p.rstd && live) p.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = first_column<VEC>(i, lane, G);
@@ -105,7 +107,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlock
         if (MX) amax = fmaxf(amax, fabsf(h[i][j]));
       }
       if constexpr (!MX) {
-        store8_warp<TX, VEC>(static_cast<TX*>(p.y) + row * p.ld_y, c, G, d, narrow8<TX>(h[i]), c < d);
+        store8_warp<TX, VEC>(static_cast<TX*>(p.y) + row * p.ld_y, c, G, d, narrow8<TX>(h[i]), c < d && live);
       } else {
         // d is a multiple of 128: the 16 lanes of four 32-column blocks are all
         // within the row or all past its end
@@ -116,7 +118,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlock
         uint32_t four = (uint32_t)(s + 127) << (8 * ((lane >> 2) & 3));
         four |= __shfl_xor_sync(0xffffffffu, four, 4);
         four |= __shfl_xor_sync(0xffffffffu, four, 8);
-        if (c < d) {
+        if (c < d && live) {
           const float inv = exp2i(-s);
           float v[8];
 #pragma unroll
@@ -140,6 +142,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlock
     }
   }
   if constexpr (MX) {   // the padding: zero codes, scale 2^0
+    if (row - step >= p.rows) row -= step;   // it went on with its warp
     for (; row < p.rows_pad; row += step) {
       for (int c = lane * 8; c < d; c += G * 8) {
         *reinterpret_cast<uint2*>(p.y_q + row * d + c) = make_uint2(0, 0);
@@ -150,33 +153,37 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlock
   }
 }
 
-// y = dropout(x): a warp takes 256 columns of two rows at a time.
-template <typename T, bool VEC>
+// y = dropout(x): a warp, or (SMALL, rows up to 64 and 128 columns) 8 or 16 lanes,
+// takes eight columns a lane of two rows at a time.  Bound by the generator (bf16)
+// and HBM (fp32): 16384 x 2048 bf16 27.6 us, 4.9 TB/s; fp32 5.7 TB/s.
+template <typename T, bool VEC, bool SMALL>
 __global__ void __launch_bounds__(256, 4) dropout_kernel(DropoutParams p) {
   __shared__ uint4 xch[VEC ? 1 : 256];
   pdl_begin();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int L = SMALL ? p.group : 32, lane = threadIdx.x & (L - 1), group = threadIdx.x / L, per = 256 / L * 2;
+  const int before = (threadIdx.x & 31) / L * 2;   // rows of the warp's lanes before this one
   auto sync = []() { __syncwarp(); };
-  const int64_t step = (int64_t)gridDim.y * 16;
-  for (int i = blockIdx.x; i * (int64_t)256 < p.cols; i += gridDim.x) {
-    const int c = first_column<VEC>(i, lane, 32);
+  const int64_t step = (int64_t)gridDim.y * per;
+  for (int i = blockIdx.x; i * (int64_t)(8 * L) < p.cols; i += gridDim.x) {
+    const int c = first_column<VEC>(i, lane, L);
     const bool in = c < p.cols;
-    int64_t row = (int64_t)blockIdx.y * 16 + warp * 2;
+    int64_t row = (int64_t)blockIdx.y * per + group * 2;
     const T* x = static_cast<const T*>(p.x) + row * p.ld_x;
     T* y = static_cast<T*>(p.y) + row * p.ld_y;
-    for (; row < p.rows; row += step, x += step * p.ld_x, y += step * p.ld_y) {
-      const bool two = row + 1 < p.rows;
-      const Raw8<T> raw[2] = {load8_warp<T, VEC>(x, c, 32, p.cols, in),
-                              load8_warp<T, VEC>(x + p.ld_x, c, 32, p.cols, in && two)};
+    // a warp goes on while its first lanes have a row
+    for (; row - before < p.rows; row += step, x += step * p.ld_x, y += step * p.ld_y) {
+      const bool one = in && row < p.rows, two = in && row + 1 < p.rows;
+      const Raw8<T> raw[2] = {load8_warp<T, VEC>(x, c, L, p.cols, one),
+                              load8_warp<T, VEC>(x + p.ld_x, c, L, p.cols, two)};
       uint4 numbers[2];
       if (p.rng.threshold) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          numbers[u] = make_uint4((uint32_t)(lane + 32 * i), (uint32_t)(row + u), p.rng.o0, p.rng.o1);
+          numbers[u] = make_uint4((uint32_t)(lane + L * i), (uint32_t)(row + u), p.rng.o0, p.rng.o1);
         philox4x32_10(numbers, p.rng.k0, p.rng.k1);
         if constexpr (!VEC) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) exchange_numbers(numbers[u], lane, 32, xch + warp * 32, sync);
+          for (int u = 0; u < 2; ++u) exchange_numbers(numbers[u], lane, L, xch + group * L, sync);
         }
       }
 #pragma unroll
@@ -184,7 +191,7 @@ __global__ void __launch_bounds__(256, 4) dropout_kernel(DropoutParams p) {
         float f[8];
         widen8(raw[u], f);
         if (p.rng.threshold) drop8(f, numbers[u], p.rng);
-        store8_warp<T, VEC>(y + u * p.ld_y, c, 32, p.cols, narrow8<T>(f), in && (u == 0 || two));
+        store8_warp<T, VEC>(y + u * p.ld_y, c, L, p.cols, narrow8<T>(f), u == 0 ? one : two);
       }
     }
   }
@@ -192,48 +199,73 @@ __global__ void __launch_bounds__(256, 4) dropout_kernel(DropoutParams p) {
 
 // p = NULL: raise the kernel's shared memory limit.
 template <typename TX, typename TR, bool MX, bool VEC, bool RING, int NV, int MAXT>
-cudaError_t fwd_run(const AddNormParams* p, cudaStream_t s) {
+cudaError_t fwd_run(const AddNormParams* p, int threads, cudaStream_t s) {
   auto* kernel = &add_norm_kernel<TX, TR, MX, VEC, RING, NV, MAXT>;
   constexpr int ring = RING ? RowRing<8 * (sizeof(TX) + sizeof(TR)), NV>::kBytes : 0;
   if (p == nullptr)
     return ring ? cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, MAXT * ring)
                 : cudaSuccess;
-  const int threads = p->group > kNormThreads ? p->group : kNormThreads;
-  const int blocks = row_blocks(MX ? p->rows_pad : p->rows, p->group, threads, RING ? kNormBlocks : threads <= kNormThreads ? (RING ? kNormBlocks : 2) : 1);
+  const int blocks = row_blocks(MX ? p->rows_pad : p->rows, p->group, threads, norm_blocks(RING, NV, MAXT) * MAXT);
   return launch_pdl(kernel, dim3(blocks), dim3(threads), (size_t)threads * ring, s, *p);
 }
 
-// Rows up to 8192 columns (256 threads; 4096 where both matrices are fp32) come
-// through the ring; wider ones are read as they are needed.
+// Rows up to 8192 columns come through the ring of 256 threads, up to 16384 (but
+// where both matrices are fp32) of 512; wider ones are read as they are needed.
+// A thread holds two groups of eight columns, more where the threads need it (rows
+// without vector loads: one), for the 8-bit output three or four.  Measured at 32768 x 4096 (8-bit, dropout) 243
+// us with four, 266 with two; at 8192 x 2048 (bf16) 26 and 24.
 template <typename TX, typename TR, bool MX, bool VEC>
 cudaError_t fwd_types(const AddNormParams* p, cudaStream_t s) {
-  // measured at 32768 x 4096 (8-bit, dropout) 243 us with four, 266 with two; at
-  // 8192 x 2048 (bf16) 26 and 24
-  constexpr int most = MX ? 4 : 2;
-  cudaError_t e = cudaSuccess;
+  constexpr bool wide = VEC && RowRing<8 * (sizeof(TX) + sizeof(TR)), 4>::kFits512;
   if (p == nullptr) {
+    cudaError_t e = cudaSuccess;
     if constexpr (VEC) {
-      e = fwd_run<TX, TR, MX, true, true, 1, kNormThreads>(p, s);
-      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, true, true, 2, kNormThreads>(p, s);
-      if constexpr (most == 4)
-        if (e == cudaSuccess) e = fwd_run<TX, TR, MX, true, true, 4, kNormThreads>(p, s);
+      e = fwd_run<TX, TR, MX, true, true, 1, kNormThreads>(p, 0, s);
+      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, true, true, 2, kNormThreads>(p, 0, s);
+      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, true, true, 3, kNormThreads>(p, 0, s);
+      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, true, true, 4, kNormThreads>(p, 0, s);
+    }
+    if constexpr (wide) {
+      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, true, true, 3, 512>(p, 0, s);
+      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, true, true, 4, 512>(p, 0, s);
     }
     return e;
   }
   AddNormParams q = *p;
-  RowSplit split(p->d, most);
-  if (split.group <= kNormThreads) {
+  if constexpr (VEC) {
+    RowSplit split(p->d, !MX || p->d <= 512 ? 2 : 3, 4, kNormThreads);
     q.group = split.group;
-    if (split.nv == 1) return fwd_run<TX, TR, MX, VEC, VEC, 1, kNormThreads>(&q, s);
-    if (split.nv == 2) return fwd_run<TX, TR, MX, VEC, VEC, 2, kNormThreads>(&q, s);
-    if constexpr (most == 4) return fwd_run<TX, TR, MX, VEC, VEC, 4, kNormThreads>(&q, s);
+    if (split.group) {
+      const int threads = split.threads();
+      if (split.nv == 1) return fwd_run<TX, TR, MX, true, true, 1, kNormThreads>(&q, threads, s);
+      if (split.nv == 2) return fwd_run<TX, TR, MX, true, true, 2, kNormThreads>(&q, threads, s);
+      if (split.nv == 3) return fwd_run<TX, TR, MX, true, true, 3, kNormThreads>(&q, threads, s);
+      return fwd_run<TX, TR, MX, true, true, 4, kNormThreads>(&q, threads, s);
+    }
+    if constexpr (wide) {
+      split = RowSplit(p->d, 3, 4, 512);
+      q.group = split.group;
+      if (split.group)
+        return split.nv == 3 ? fwd_run<TX, TR, MX, true, true, 3, 512>(&q, q.group, s)
+                             : fwd_run<TX, TR, MX, true, true, 4, 512>(&q, q.group, s);
+    }
+  } else {
+    const RowSplit split(p->d, 1, 2, 512);
+    q.group = split.group;
+    if (split.group) {
+      const int threads = split.threads();
+      if (split.nv == 2) return fwd_run<TX, TR, MX, false, false, 2, 512>(&q, threads, s);
+      return split.group <= kNormThreads ? fwd_run<TX, TR, MX, false, false, 1, kNormThreads>(&q, threads, s)
+                                         : fwd_run<TX, TR, MX, false, false, 1, 512>(&q, threads, s);
+    }
   }
-  split = RowSplit(p->d, 2);
-  if (split.group > kNormMaxThreads) split = RowSplit(p->d, 4);
+  const RowSplit split(p->d, wide ? 3 : 2, 4, kNormMaxThreads);
   q.group = split.group;
-  return split.nv == 4 ? fwd_run<TX, TR, MX, VEC, false, 4, kNormMaxThreads>(&q, s)
-                       : fwd_run<TX, TR, MX, VEC, false, 2, kNormMaxThreads>(&q, s);
+  if constexpr (!wide)
+    if (split.nv == 2) return fwd_run<TX, TR, MX, VEC, false, 2, kNormMaxThreads>(&q, q.group, s);
+  return split.nv == 3 ? fwd_run<TX, TR, MX, VEC, false, 3, kNormMaxThreads>(&q, q.group, s)
+                       : fwd_run<TX, TR, MX, VEC, false, 4, kNormMaxThreads>(&q, q.group, s);
 }
 
 template <typename TX, typename TR>
@@ -266,21 +298,29 @@ cudaError_t launch_add_norm(const AddNormParams& p, int dtype, int res_dtype, bo
   return fwd_vec<float, float>(&p, vec, s);
 }
 
-cudaError_t launch_dropout(const DropoutParams& p, int dtype, bool vec, cudaStream_t s) {
-  // four blocks a multiprocessor stay; as many rows a block as that leaves
+template <typename T> static cudaError_t dropout_types(const DropoutParams& p, bool vec, dim3 grid, cudaStream_t s) {
+  if (p.group < 32)
+    return vec ? launch_pdl(dropout_kernel<T, true, true>, grid, dim3(256), 0, s, p)
+               : launch_pdl(dropout_kernel<T, false, true>, grid, dim3(256), 0, s, p);
+  return vec ? launch_pdl(dropout_kernel<T, true, false>, grid, dim3(256), 0, s, p)
+             : launch_pdl(dropout_kernel<T, false, false>, grid, dim3(256), 0, s, p);
+}
+
+cudaError_t launch_dropout(const DropoutParams& args, int dtype, bool vec, cudaStream_t s) {
+  DropoutParams p = args;
+  p.group = p.cols <= 64 ? 8 : p.cols <= 128 ? 16 : 32;
+  // four blocks a multiprocessor, all of them there at once (one block more than
+  // that costs a second round: 3.4 and 5.0 TB/s at 768 columns); as many rows a
+  // block as that leaves
+  const int per = 256 / p.group * 2;
   const int64_t chunks = ((int64_t)p.cols + 255) / 256, most = (int64_t)device_info()->sm_count * 4;
-  const int64_t gx = chunks < 65535 ? chunks : 65535, need = (p.rows + 15) / 16;
-  int64_t gy = (most + gx - 1) / gx;
+  const int64_t gx = chunks < 65535 ? chunks : 65535, need = (p.rows + per - 1) / per;
+  int64_t gy = gx < most ? most / gx : 1;
   gy = gy < need ? gy : need;
-  const dim3 grid((unsigned)gx, (unsigned)(gy < 65535 ? gy : 65535)), block(256);
-  if (dtype == MOE_DT_BF16)
-    return vec ? launch_pdl(dropout_kernel<__nv_bfloat16, true>, grid, block, 0, s, p)
-               : launch_pdl(dropout_kernel<__nv_bfloat16, false>, grid, block, 0, s, p);
-  if (dtype == MOE_DT_F16)
-    return vec ? launch_pdl(dropout_kernel<__half, true>, grid, block, 0, s, p)
-               : launch_pdl(dropout_kernel<__half, false>, grid, block, 0, s, p);
-  return vec ? launch_pdl(dropout_kernel<float, true>, grid, block, 0, s, p)
-             : launch_pdl(dropout_kernel<float, false>, grid, block, 0, s, p);
+  const dim3 grid((unsigned)gx, (unsigned)(gy < 65535 ? gy : 65535));
+  if (dtype == MOE_DT_BF16) return dropout_types<__nv_bfloat16>(p, vec, grid, s);
+  if (dtype == MOE_DT_F16) return dropout_types<__half>(p, vec, grid, s);
+  return dropout_types<float>(p, vec, grid, s);
 }
 
 }  // namespace moe

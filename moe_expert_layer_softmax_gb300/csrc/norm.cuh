@@ -30,7 +30,11 @@ namespace moe {
 
 constexpr int kNormThreads = 256;      // threads of a block whose row group is not larger
 constexpr int kNormMaxThreads = 1024;
-constexpr int kNormBlocks = 2;         // of kNormThreads on a multiprocessor (by registers and shared memory)
+// Blocks of kNormThreads on a multiprocessor: with a ring by registers and shared
+// memory, without one as many as hide the loads.
+constexpr int norm_blocks(bool ring, int nv, int most) {
+  return most > kNormThreads ? 1 : ring || nv > 1 ? 2 : 3;
+}
 constexpr int kNormRingBytes = 96 * 1024;   // of a block
 
 MOE_DEV float warp_sum(float v) {
@@ -39,29 +43,39 @@ MOE_DEV float warp_sum(float v) {
   return v;
 }
 
-// The threads of a block form groups of G (a power of two >= 32), one a row.
-struct RowGroup {
+// The threads of a block form groups of G, one a row: a multiple of 32, or (SMALL)
+// 8 or 16.
+template <bool SMALL> struct RowGroup {
   int G, lane, group, per;
   MOE_DEV explicit RowGroup(int G_)
-      : G(G_), lane(threadIdx.x & (G_ - 1)), group(threadIdx.x / G_), per(blockDim.x / G_) {}
+      : G(G_), lane(threadIdx.x % G_), group(threadIdx.x / G_), per(blockDim.x / G_) {}
+  // Groups that start earlier in the same warp.
+  MOE_DEV int before() const { return SMALL ? (threadIdx.x & 31) / min(G, 32) : 0; }
   MOE_DEV void sync() const {
-    if (G == 32) __syncwarp(); else bar_sync(1 + group, G);
+    if (G <= 32) __syncwarp(); else bar_sync(1 + group, G);
   }
   // Sum over the group, the same value in every thread.  `red`: a float for each
   // warp of the block, another array in turn for the next call (so that one
   // barrier is enough).
   MOE_DEV float sum(float v, float* red) const {
-    v = warp_sum(v);
-    if (G == 32) return v;
+    if (!SMALL || G >= 32) {
+      v = warp_sum(v);
+    } else {
+      for (int off = G >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    }
+    if (G <= 32) return v;
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     bar_sync(1 + group, G);
     const int n = G >> 5;
     const float* from = red + group * n;
-    if (n == 2) return from[0] + from[1];
     float s = 0.0f;
-    for (int i = 0; i < n; i += 4) {
-      const float4 q = *reinterpret_cast<const float4*>(from + i);
-      s += (q.x + q.y) + (q.z + q.w);
+    if (n & 3) {
+      for (int i = 0; i < n; ++i) s += from[i];
+    } else {
+      for (int i = 0; i < n; i += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(from + i);
+        s += (q.x + q.y) + (q.z + q.w);
+      }
     }
     return s;
   }
@@ -93,20 +107,26 @@ MOE_DEV void load_weight8(const void* w, bool w_f32, bool w_f16, int c, int G, i
 // columns of up to three matrices, NV times.  Slots are laid out piece by piece
 // (16 bytes a thread), so that neighbouring threads touch neighbouring banks.  A
 // thread copies and reads its own pieces; where eight columns are two pieces
-// (fp32) a warp copies its 64 pieces as they follow one another, which fills
-// whole sectors, and each lane reads its two: piece q lies at place q ^ (q >> 3 &
-// 1), so that eight lanes' reads miss each other's banks.
+// (fp32) a warp (or a smaller group) copies its pieces as they follow one another,
+// which fills whole sectors, and each lane reads its two: piece q lies at place q
+// ^ (q >> 3 & 1), so that eight lanes' reads miss each other's banks.
 template <int BYTES, int NV> struct RowRing {
   static constexpr int kFit = kNormRingBytes / (kNormThreads * BYTES * NV);
   static constexpr int kDepth = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
   static constexpr int kBytes = BYTES * NV * kDepth;   // a thread
-  uint32_t mine, warp;   // slot 0, piece 0: this thread's, its warp's first
+  static constexpr bool kFits512 = kFit >= 2;          // 512 threads' rings, in twice kNormRingBytes
+  uint32_t mine, warp;   // slot 0, piece 0: this thread's, that of lane 0
   uint32_t piece;        // bytes between pieces
   uint32_t slot;         // bytes: the next one to read
   uint32_t ahead;        // bytes: the next one to fill
-  MOE_DEV explicit RowRing(void* smem)
-      : mine(smem_u32(smem) + threadIdx.x * 16), warp(smem_u32(smem) + (threadIdx.x & ~31u) * 16),
-        piece(blockDim.x * 16), slot(0), ahead(0) {}
+  int width_;            // NV = 1: groups may be smaller than a warp
+  MOE_DEV RowRing(void* smem, int G)
+      : mine(smem_u32(smem) + threadIdx.x * 16), piece(blockDim.x * 16), slot(0), ahead(0), width_(G < 32 ? G : 32) {
+    warp = mine - lane() * 16;
+  }
+  // Threads of a warp, or of a smaller group, and this one among them.
+  MOE_DEV int width() const { return NV == 1 ? width_ : 32; }
+  MOE_DEV int lane() const { return threadIdx.x & (width() - 1); }
   MOE_DEV uint32_t next(uint32_t at) const {
     at += piece * (BYTES / 16 * NV);
     return at == piece * (BYTES / 16 * NV) * kDepth ? 0 : at;
@@ -118,14 +138,12 @@ template <int BYTES, int NV> struct RowRing {
       const bool in = c < d;
       cp_async16(mine + ahead + at * piece, row + (in ? c : 0), in ? 16 : 0);
     } else {
-      const int lane = threadIdx.x & 31;
-      const int first = c - lane * 8;   // of the warp
-      const uint32_t to = warp + ahead + at * piece + (lane ^ (lane >> 3 & 1)) * 16;
+      const int lane = this->lane(), first = c - lane * 8;   // of lane 0
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int q = first + (lane + 32 * i) * 4;
-        const bool in = q < d;
-        cp_async16(to + i * piece, row + (in ? q : 0), in ? 16 : 0);
+        const int q = lane + width() * i;
+        const bool in = first + q * 4 < d;
+        cp_async16(warp + ahead + (at + i) * piece + (lane ^ (q >> 3 & 1)) * 16, row + (in ? first + q * 4 : 0), in ? 16 : 0);
       }
     }
   }
@@ -136,9 +154,9 @@ template <int BYTES, int NV> struct RowRing {
     if constexpr (sizeof(T) == 2) {
       load(mine + slot + at * piece, q[0]);
     } else {
-      const int lane = threadIdx.x & 31;
-      const uint32_t from = warp + slot + (at + (lane >> 4)) * piece;
-      const int first = (2 * lane & 31) ^ (lane >> 2 & 1);
+      const int lane = this->lane();
+      const uint32_t from = warp + slot + (at + (2 * lane >= width())) * piece;
+      const int first = (2 * lane & (width() - 1)) ^ (lane >> 2 & 1);
       load(from + first * 16, q[0]);
       load(from + (first ^ 1) * 16, q[1]);
     }
@@ -149,23 +167,34 @@ template <int BYTES, int NV> struct RowRing {
   }
 };
 
-// Threads of a row group and how many times eight columns each holds: a power
-// of two of them, as many columns a thread as `most` allows down to a warp.
+// Threads of a row group (8, 16 or a multiple of 32) and how many times eight
+// columns each holds: as few as `least` and up to `most`, so that the group is no
+// larger than `limit` and the fewest places stay empty; group 0: it does not fit.
 struct RowSplit {
   int group, nv;
-  RowSplit(int d, int most) {
+  RowSplit(int d, int least, int most, int limit) : group(0), nv(1) {
     const int g8 = (d + 7) / 8;
-    nv = 1;
-    while (nv < most && 32 * nv < g8) nv *= 2;
-    group = 32;
-    while (group * nv < g8) group *= 2;
+    if (g8 <= 32) {
+      group = g8 <= 8 ? 8 : g8 <= 16 ? 16 : 32;
+      return;
+    }
+    for (int n = least; n <= most; ++n) {
+      const int g = ((g8 + n - 1) / n + 31) / 32 * 32;
+      if (g > limit || (group && g * n > group * nv)) continue;
+      if (group && least < 3) break;   // the fewest columns a thread that fit
+      group = g;
+      nv = n;
+    }
   }
+  // Threads of a block: whole groups in kNormThreads, or a larger one.
+  int threads() const { return group > kNormThreads ? group : kNormThreads / group * group; }
 };
 
-// Blocks: enough row groups for every row, or as many as stay on the device.
-inline int row_blocks(int64_t rows, int group, int threads, int per_sm) {
+// Blocks: enough row groups for every row, or as many as stay on the device,
+// `resident` threads on a multiprocessor.
+inline int row_blocks(int64_t rows, int group, int threads, int resident) {
   const int per = threads / group;
-  const int64_t need = (rows + per - 1) / per, most = (int64_t)device_info()->sm_count * per_sm;
+  const int64_t need = (rows + per - 1) / per, most = (int64_t)device_info()->sm_count * (resident / threads);
   return (int)(need < most ? need : most);
 }
 

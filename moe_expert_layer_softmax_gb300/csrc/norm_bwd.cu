@@ -9,7 +9,7 @@ namespace {
 // Backward: the weight gradient of a block's rows stays in registers; one row of
 // partial sums a block goes to `partial` [gridDim.x, d].
 template <typename TX, typename TR, bool VEC, bool RING, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlocks : 1) add_norm_bwd_kernel(AddNormBwdParams p) {
+__global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_bwd_kernel(AddNormBwdParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float red[2][kNormMaxThreads / 32];
   // drop numbers that change hands; at the end the sums of the row groups
@@ -19,7 +19,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlock
   using Ring = RowRing<8 * (sizeof(TX) + 2 * sizeof(TR)), NV>;
   constexpr int XP = sizeof(TX) / 2, RP = sizeof(TR) / 2;   // 16-byte pieces of eight columns
   pdl_begin();
-  const RowGroup rg(p.group);
+  const RowGroup<NV == 1> rg(p.group);
   const int G = rg.G, lane = rg.lane, d = p.d;
   auto sync = [&]() { rg.sync(); };
   float w[NV][8], dw[NV][8];
@@ -32,7 +32,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlock
   }
   const int64_t step = (int64_t)gridDim.x * rg.per;
   int64_t row = (int64_t)blockIdx.x * rg.per + rg.group;
-  Ring ring(smem);
+  Ring ring(smem, G);
   // RING: where the next row to copy starts
   const TX* cy = static_cast<const TX*>(p.dy) + row * p.ld_dy;
   const TR* ch = static_cast<const TR*>(p.h) + row * p.ld_h;
@@ -60,7 +60,9 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlock
     for (int i = 0; i < Ring::kDepth - 1; ++i) copy();
   }
   float rn = row < p.rows ? p.rstd[row] : 0.0f;
-  for (int turn = 0; row < p.rows; row += step, turn ^= 1) {
+  // a warp goes on while its first group has a row; one without adds zeros
+  for (int turn = 0; row - rg.before() < p.rows; row += step, turn ^= 1) {
+    const bool live = NV > 1 || row < p.rows;
     Raw8<TX> yr[NV] = {};
     Raw8<TR> hr[NV] = {};
     const float r = rn;
@@ -76,11 +78,13 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlock
     for (int i = 0; i < NV; ++i) {
       const int c = first_column<VEC>(i, lane, G);
       if constexpr (RING) {
-        yr[i] = ring.template get<TX>(i * XP);
-        hr[i] = ring.template get<TR>(NV * XP + i * RP);
+        if (live) {
+          yr[i] = ring.template get<TX>(i * XP);
+          hr[i] = ring.template get<TR>(NV * XP + i * RP);
+        }
       } else {
-        yr[i] = load8_warp<TX, VEC>(static_cast<const TX*>(p.dy) + row * p.ld_dy, c, G, d, c < d);
-        hr[i] = load8_warp<TR, VEC>(static_cast<const TR*>(p.h) + row * p.ld_h, c, G, d, c < d);
+        yr[i] = load8_warp<TX, VEC>(static_cast<const TX*>(p.dy) + row * p.ld_dy, c, G, d, c < d && live);
+        hr[i] = load8_warp<TR, VEC>(static_cast<const TR*>(p.h) + row * p.ld_h, c, G, d, c < d && live);
       }
       float a[8], b[8];
       widen8(yr[i], a);
@@ -100,7 +104,7 @@ __global__ void __launch_bounds__(MAXT, MAXT <= kNormThreads && VEC ? kNormBlock
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = first_column<VEC>(i, lane, G);
-      const bool in = c < d;
+      const bool in = c < d && live;
       float a[8], b[8];
       widen8(yr[i], a);
       widen8(hr[i], b);
@@ -175,40 +179,61 @@ __global__ void __launch_bounds__(1024) add_norm_dw_kernel(const float* __restri
 
 // p = NULL: raise the kernel's shared memory limit.
 template <typename TX, typename TR, bool VEC, bool RING, int NV, int MAXT>
-cudaError_t bwd_run(const AddNormBwdParams* p, int* blocks, cudaStream_t s) {
+cudaError_t bwd_run(const AddNormBwdParams* p, int threads, int* blocks, cudaStream_t s) {
   auto* kernel = &add_norm_bwd_kernel<TX, TR, VEC, RING, NV, MAXT>;
   constexpr int ring = RING ? RowRing<8 * (sizeof(TX) + 2 * sizeof(TR)), NV>::kBytes : 0;
   if (p == nullptr)
     return ring ? cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, MAXT * ring)
                 : cudaSuccess;
-  const int threads = p->group > kNormThreads ? p->group : kNormThreads;
-  *blocks = row_blocks(p->rows, p->group, threads, threads <= kNormThreads ? (RING ? kNormBlocks : 2) : 1);
+  *blocks = row_blocks(p->rows, p->group, threads, norm_blocks(RING, NV, MAXT) * MAXT);
+  if (*blocks > kNormPartialRows) *blocks = kNormPartialRows;   // rows of the workspace
   return launch_pdl(kernel, dim3(*blocks), dim3(threads), (size_t)threads * ring, s, *p);
 }
 
-// Rows up to 8192 columns (512 threads) come through the ring; wider ones are
-// read as they are needed.
+// Rows up to 8192 columns (512 threads; 16384 where both matrices are 16 bits)
+// come through the ring; wider ones are read as they are needed.
 template <typename TX, typename TR, bool VEC>
 cudaError_t bwd_types(const AddNormBwdParams* p, int* blocks, cudaStream_t s) {
+  constexpr bool wide = VEC && RowRing<8 * (sizeof(TX) + 2 * sizeof(TR)), 4>::kFits512;
   cudaError_t e = cudaSuccess;
   if (p == nullptr) {
     if constexpr (VEC) {
-      e = bwd_run<TX, TR, true, true, 1, kNormThreads>(p, blocks, s);
-      if (e == cudaSuccess) e = bwd_run<TX, TR, true, true, 2, kNormThreads>(p, blocks, s);
-      if (e == cudaSuccess) e = bwd_run<TX, TR, true, true, 2, 512>(p, blocks, s);
+      e = bwd_run<TX, TR, true, true, 1, kNormThreads>(p, 0, blocks, s);
+      if (e == cudaSuccess) e = bwd_run<TX, TR, true, true, 2, kNormThreads>(p, 0, blocks, s);
+      if (e == cudaSuccess) e = bwd_run<TX, TR, true, true, 2, 512>(p, 0, blocks, s);
+    }
+    if constexpr (wide) {
+      if (e == cudaSuccess) e = bwd_run<TX, TR, true, true, 3, 512>(p, 0, blocks, s);
+      if (e == cudaSuccess) e = bwd_run<TX, TR, true, true, 4, 512>(p, 0, blocks, s);
     }
     return e;
   }
   AddNormBwdParams q = *p;
-  RowSplit split(p->d, 2);
-  if (split.group > kNormMaxThreads) split = RowSplit(p->d, 4);
+  RowSplit split(p->d, VEC ? 2 : 1, wide ? 4 : 2, 512);
   q.group = split.group;
-  if (split.nv == 4) return bwd_run<TX, TR, VEC, false, 4, kNormMaxThreads>(&q, blocks, s);
-  if (split.group > 512) return bwd_run<TX, TR, VEC, false, 2, kNormMaxThreads>(&q, blocks, s);
-  if (split.nv == 1) return bwd_run<TX, TR, VEC, VEC, 1, kNormThreads>(&q, blocks, s);
-  return split.group <= kNormThreads ? bwd_run<TX, TR, VEC, VEC, 2, kNormThreads>(&q, blocks, s)
-                                     : bwd_run<TX, TR, VEC, VEC, 2, 512>(&q, blocks, s);
+  if (split.group) {
+    const int threads = split.threads();
+    if constexpr (wide) {
+      if (split.nv == 3) return bwd_run<TX, TR, VEC, true, 3, 512>(&q, threads, blocks, s);
+      if (split.nv == 4) return bwd_run<TX, TR, VEC, true, 4, 512>(&q, threads, blocks, s);
+    }
+    if constexpr (VEC) {
+      if (split.nv == 2 && split.group <= kNormThreads)
+        return bwd_run<TX, TR, VEC, true, 2, kNormThreads>(&q, threads, blocks, s);
+    } else {
+      if (split.nv == 1 && split.group > kNormThreads)
+        return bwd_run<TX, TR, VEC, false, 1, 512>(&q, threads, blocks, s);
+    }
+    return split.nv == 1 ? bwd_run<TX, TR, VEC, VEC, 1, kNormThreads>(&q, threads, blocks, s)
+                         : bwd_run<TX, TR, VEC, VEC, 2, 512>(&q, threads, blocks, s);
+  }
+  split = RowSplit(p->d, wide ? 3 : 2, 4, kNormMaxThreads);
+  q.group = split.group;
+  if constexpr (!wide)
+    if (split.nv == 2) return bwd_run<TX, TR, VEC, false, 2, kNormMaxThreads>(&q, q.group, blocks, s);
+  return split.nv == 3 ? bwd_run<TX, TR, VEC, false, 3, kNormMaxThreads>(&q, q.group, blocks, s)
+                       : bwd_run<TX, TR, VEC, false, 4, kNormMaxThreads>(&q, q.group, blocks, s);
 }
 
 template <typename TX, typename TR>

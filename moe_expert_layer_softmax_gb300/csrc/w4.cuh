@@ -508,11 +508,14 @@ MOE_DEV float sum_parts(const float* parts, int slot_floats, int tile, const Par
 
 // ------------------------------------------------------------------ staged vectors
 // Each 128 columns (a stage) of a vector become fp16 after a power of two that
-// puts their largest value into [2^13, 2^14): 8 or 11 significant bits stay 31
-// binary orders below the largest value, and what is lost further down (2^-35 of
-// it) is below the rounding of the fp32 sums.  LOW keeps a second fp16 part, 22
-// bits together.  A vector with an infinity or NaN gives results that are not
-// finite.  The table has, for each group, the factor back to the vector's units
+// puts their largest value into [2^13, 2^14): the 8 or 11 significant bits are
+// all there down to 2^-24 of the largest value, and what is lost further down
+// (2^-35 of it) is below the rounding of the fp32 sums.  LOW keeps a second fp16
+// part, 22 bits together.  A vector with an infinity or NaN, or with 2^118 or more
+// (the factor back would pass fp32), gives results that are not finite.  Taking 8
+// times the sum off the products costs roundings of 2^-24 of both: next to a bf16
+// or fp16 result nothing, unless the group's weights are all but zero where its
+// values are large.  The table has, for each group, the factor back to the vector's units
 // (2^24 of the codes included) and 8 times the sum of its values.
 
 // Bytes between staged vectors: 64 more than a multiple of 128, so that two
