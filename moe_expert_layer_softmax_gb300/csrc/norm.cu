@@ -8,7 +8,9 @@ namespace {
 
 // One row group per row; each thread holds NV times eight columns.  MX: codes,
 // scales and (dq) their values instead of y; the rows from `rows` on are the
-// padding of the last 128-row tile.
+// padding of the last 128-row tile.  Measured: 8192 x 2048 bf16 23.7 us (5.7 TB/s),
+// bound by HBM and, at 60% of the issue slots, by waits between instructions; 8
+// bits, dropout, 32768 x 4096 238 us (5.1 TB/s), 65% of the issue slots.
 template <typename TX, typename TR, bool MX, bool VEC, bool RING, int NV, int MAXT>
 __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_kernel(AddNormParams p) {
   extern __shared__ __align__(16) uint8_t smem[];

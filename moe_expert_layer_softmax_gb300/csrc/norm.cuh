@@ -10,16 +10,28 @@
 // y), optionally with the values the codes stand for.  With g = w dy:
 //   dh = dres + r (g - h r^2 mean(g h)),  dx = dropout'(dh),  dw = sum dy h r.
 //
-// Every kernel here is bound by HBM: one read and one write of each matrix.  A
-// row stays in registers between the pass that sums it and the pass that writes
-// it.  A fixed grid takes the rows in turn while the rows to come (one to three)
-// are on their way into shared memory, each thread copying and reading its own
-// pieces, so that the pipeline needs no barrier and no registers: 512 threads a
-// multiprocessor keep 50 to 130 KB in flight.  A thread holds up to 32 columns
-// (backward: 16): what a row costs beside its elements (the sums over threads,
-// the square root, addresses) is then shared by that many.  With eight columns
-// a thread the 8192 x 2048 forward took 294 instructions per eight columns and
-// was bound by instruction issue.  Sums are taken in a fixed order (no atomics).
+// The least a call costs is one read and one write of each matrix.  A row stays in
+// registers between the pass that sums it and the pass that writes it.  A fixed
+// grid takes the rows in turn while the rows to come (one to three) are on their
+// way into shared memory, each thread copying and reading its own pieces, so that
+// the pipeline needs no barrier and no registers: 512 threads a multiprocessor
+// keep 50 to 130 KB in flight.  A thread holds 16 columns (rows up to 256: 8; the
+// 8-bit output and wide rows: up to 32), so that what a row costs beside its
+// elements (the sums over threads, the square root, addresses) is shared: with
+// eight columns a thread the 8192 x 2048 forward took 294 instructions per eight
+// columns and 28.5 us, bound by issue.  A row has a group of 8, 16 or any multiple
+// of 32 threads: with whole warps alone rows of 64 columns ran at 1.8 TB/s, with
+// powers of two alone 768 columns left a quarter of the lanes idle.  Rows that
+// take no vector loads are read element by element, neighbours by neighbours, one
+// group of columns a thread (two spilled: 1001 columns in fp32 4.3 and 5.6 TB/s).
+// Sums are taken in a fixed order (no atomics).
+//
+// Measured (TB/s of HBM against a copy's 6.7; bf16 matrices, bf16 stream / fp32
+// stream, without dropout): forward 64 to 8192 columns 5.4-6.5 / 5.5-6.4, 12288
+// and 16384 5.6-5.9 / 5.7; backward 5.4-6.2 / 5.7-6.4, 12288 4.2 / 3.0.  With
+// dropout the generator adds its instructions: bf16 stream 4.3-6.0, fp32 stream
+// 5.3-6.5.  8-bit output, 4096 columns: 4.95 / 6.0, with dropout 4.05 / 5.5.  Wider
+// rows than a ring holds 3.3-4.5 forward, 1.4-3.4 backward; odd widths 1.7-5.6.
 #pragma once
 
 #include "block.cuh"

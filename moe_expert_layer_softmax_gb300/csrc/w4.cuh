@@ -9,13 +9,15 @@
 // used for a handful of vectors.  The products run on mma.sync m16n8k16 with 16
 // weight rows as A and eight vectors as B: each lane turns its own 4-bit words
 // into operands, and eight vectors do not fill a larger matrix instruction.
-// What bounds it in fact is issue: about 150 instructions for each 128 columns
-// of 16 rows, 40 of them the conversion of the codes, at 45-50% of the issue
-// slots, half of the rest waits between dependent ones.  Weights that already
-// lie in L2 take the same time.  64 experts (2048 x 1408, 64 tokens) stream 3.5
-// TB/s, eight tokens on experts of 4096 x 2048 4.6 TB/s.  Weights fetched by TMA
-// tiles (one lane, 128-byte boxes) came out the same, 88.8 against 87.8 us, and
-// by one bulk copy a row slower (104 us), so the copies stay with the lanes.
+// What bounds it in fact is issue: about 145 instructions for each 128 columns of
+// 16 rows (200 with two-part vectors), 40 of them the conversion of the codes, at
+// 49-57% of the issue slots; the rest waits on instructions before it (fixed
+// latencies first, then shared memory, whose path is at 45-57%).  Weights that
+// already lie in L2 take the same time.  64 experts (2048 x 1408, 64 tokens) stream
+// 3.5 TB/s, eight tokens on experts of 4096 x 2048 4.6 TB/s.  Tried without gain:
+// weights fetched by TMA tiles (one lane, 128-byte boxes: 88.8 against 87.8 us) or
+// by one bulk copy a row (104 us), and two chains of matrix instructions for one
+// (87.2 against 85.2 us).
 // The sum over k may visit columns in any order as long as A and B agree, so a
 // lane's fragment columns are simply those of the words it holds.  Products of
 // a group are exact integers times activations, summed in fp32; the group's

@@ -13,9 +13,9 @@
 // accuracy beside a bf16 or fp16 result.
 //
 // Measured (us, bf16, weights from HBM): 64 experts of 2048 x 1408, four a token,
-// groups of 64: 13.0 for one token, 38.7 for eight, 68.6 for 32, 85.0 for 64 (294
-// MB, 3.5 TB/s), 123 for 128, 375 for 512.  64 experts of 4096 x 2048, eight a
-// token, groups of 128: 30.9 for one token (104 MB, 3.4 TB/s), 115 for eight (4.6
+// groups of 64: 13.0 for one token, 38.2 for eight, 67.8 for 32, 84.7 for 64 (294
+// MB, 3.5 TB/s), 119 for 128, 373 for 512.  64 experts of 4096 x 2048, eight a
+// token, groups of 128: 31.2 for one token (104 MB, 3.3 TB/s), 114 for eight (4.6
 // TB/s).  Read from global memory instead, the first took 155 us with 64 tokens
 // and the second 46 us with one; 32 experts of 4096 x 4096, where seven vectors
 // are staged at a time, 64 tokens, 504 us rather than 305.
@@ -120,12 +120,13 @@ MOE_DEV void find_routes(const Lists& l, int R, int e, const float* gates) {
 // tile of an expert with w rounds being w of them.  Tiles belong to the block in
 // whose range their first unit lies.  Going on to another expert costs a block
 // about as much as kTurnUnits tiles (the last warps, the sums, the next
-// vectors), so as many empty units lie between two experts (64 experts of 2048 x
-// 1408: 40.9 us with them, 44.1 without for eight tokens, 87.8 and 88.7 for 64).
-// Where every expert
-// has one round and the blocks divide among the experts with hardly a loss,
-// they do not cross from one to another.
-constexpr int kTurnUnits = 4;
+// vectors), so as many empty units lie between two experts.  Measured with 2, 4, 8
+// and 12 (us): 64 experts of 2048 x 1408, eight tokens 40.3, 38.7, 38.2, 39.1; 64
+// tokens 85.8, 85.1, 84.7, 85.6; 128 tokens 123.2, 122.6, 119.4, 118.0; 8 experts of
+// 1536 x 1024, two a token, 64 tokens 38.3, 36.9, 31.7, 31.9.  Where every expert
+// has one round and the blocks divide among the experts with hardly a loss, they
+// do not cross from one to another.
+constexpr int kTurnUnits = 8;
 struct Share {
   int per;             // tiles of an expert
   int i;               // present expert (of the used ones)
@@ -558,7 +559,8 @@ template <typename T, int W> cudaError_t token_launch(const ExpertsW4Params* p, 
 // have more than six on average and a block still takes its tiles of an expert
 // in one segment.  Measured, eight and sixteen (us): 8 experts of 1536 x 1024, 12
 // tokens on all of them 29.4 and 25.3, 64 tokens 92 and 77; 64 experts of 2048 x
-// 1408, whose tiles would become two and more segments, 128 tokens 123 and 166.
+// 1408, whose tiles would become two and more segments, 128 tokens 123 and 166
+// (with four empty units between experts).
 // One token: W_down of all its experts as one product, 13.0 us, or a product for
 // each and their sum, 16.4 (2048 x 1408, four experts).
 template <typename T, int W> cudaError_t experts_nt(const ExpertsW4Params* p, cudaStream_t s) {
