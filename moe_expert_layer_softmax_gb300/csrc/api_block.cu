@@ -29,10 +29,16 @@ int check_matrix(const void* p, int64_t ld, int64_t cols, int dtype) {
   return on_boundary(p, size_of(dtype)) ? MOE_OK : MOE_ERR_ALIGN;
 }
 
-// Whether groups of eight columns of every row lie on 16-byte boundaries.
-bool vector_rows(const void* p, int64_t ld, int64_t rows, int dtype) {
-  return p == nullptr || (on_boundary(p, 16) && (rows == 1 || ld * size_of(dtype) % 16 == 0));
+// The largest access (columns: 8, 2 or 1, at most `most`) that every row of a
+// matrix takes: eight columns from a 16-byte boundary, or a pair from its own.
+int row_access(const void* p, int64_t ld, int64_t rows, int dtype, int most = 8) {
+  if (p == nullptr) return most;
+  const int64_t size = size_of(dtype), stride = rows == 1 ? 0 : ld * size;
+  if (most == 8 && (!on_boundary(p, 16) || stride % 16 != 0)) most = 2;
+  if (most == 2 && (!on_boundary(p, 2 * size) || stride % (2 * size) != 0)) most = 1;
+  return most;
 }
+int width_access(int32_t d) { return d % 8 == 0 ? 8 : d % 2 == 0 ? 2 : 1; }
 
 // p in [0, 1]; the keep probability is a multiple of 2^-16.
 int make_rng(float p, uint64_t seed, uint64_t offset, DropRng* g) {
@@ -111,9 +117,10 @@ int moe_add_norm(const moe_add_norm_args_t* a, void* stream) {
     return MOE_ERR_INVALID;   // the stream that the norm and the backward read
   }
   if (a->rstd && !on_boundary(a->rstd, 4)) return MOE_ERR_ALIGN;
-  bool vec = a->d % 8 == 0 && vector_rows(a->x, a->ld_x, a->rows, a->dtype) &&
-             vector_rows(a->residual, a->ld_residual, a->rows, a->res_dtype) &&
-             vector_rows(a->h, a->ld_h, a->rows, a->res_dtype) && on_boundary(a->weight, 16);
+  int vec = row_access(a->x, a->ld_x, a->rows, a->dtype, width_access(a->d));
+  vec = row_access(a->residual, a->ld_residual, a->rows, a->res_dtype, vec);
+  vec = row_access(a->h, a->ld_h, a->rows, a->res_dtype, vec);
+  vec = row_access(a->weight, 0, 1, a->w_dtype, vec);
   p.rows_pad = a->rows;
   if (a->y_q) {
     // codes and scales for whole 128-row tiles, 128-column scale atoms
@@ -122,12 +129,12 @@ int moe_add_norm(const moe_add_norm_args_t* a, void* stream) {
     MOE_BUFFER(a->y_q);
     MOE_BUFFER(a->y_scales);
     if (a->y_dq) MOE_BUFFER(a->y_dq);
-    if (!vec) return MOE_ERR_ALIGN;
+    if (vec != 8) return MOE_ERR_ALIGN;
     p.rows_pad = (a->rows + kTileM - 1) / kTileM * kTileM;
   } else {
     if (a->y_scales || a->y_dq) return MOE_ERR_INVALID;
     MOE_TRY(check_matrix(a->y, a->ld_y, a->d, a->dtype));
-    vec = vec && vector_rows(a->y, a->ld_y, a->rows, a->dtype);
+    vec = row_access(a->y, a->ld_y, a->rows, a->dtype, vec);
   }
   if (!ready()) return MOE_ERR_NOT_INIT;
   p.rows = a->rows; p.d = a->d; p.inv_d = 1.0f / (float)a->d;
@@ -174,11 +181,12 @@ int moe_add_norm_bwd(const moe_add_norm_bwd_args_t* a, void* ws, void* stream) {
   if (!on_boundary(a->rstd, 4) || !on_boundary(a->weight, size_of(a->w_dtype))) return MOE_ERR_ALIGN;
   if (a->dw) MOE_BUFFER(ws);
   if (!ready()) return MOE_ERR_NOT_INIT;
-  const bool vec = a->d % 8 == 0 && vector_rows(a->dy, a->ld_dy, a->rows, a->dtype) &&
-                   vector_rows(a->h, a->ld_h, a->rows, a->res_dtype) &&
-                   vector_rows(a->dres, a->ld_dres, a->rows, a->res_dtype) &&
-                   vector_rows(a->dh, a->ld_dh, a->rows, a->res_dtype) &&
-                   vector_rows(a->dx, a->ld_dx, a->rows, a->dtype) && on_boundary(a->weight, 16);
+  int vec = row_access(a->dy, a->ld_dy, a->rows, a->dtype, width_access(a->d));
+  vec = row_access(a->h, a->ld_h, a->rows, a->res_dtype, vec);
+  vec = row_access(a->dres, a->ld_dres, a->rows, a->res_dtype, vec);
+  vec = row_access(a->dh, a->ld_dh, a->rows, a->res_dtype, vec);
+  vec = row_access(a->dx, a->ld_dx, a->rows, a->dtype, vec);
+  vec = row_access(a->weight, 0, 1, a->w_dtype, vec);
   p.rows = a->rows; p.d = a->d; p.inv_d = 1.0f / (float)a->d;
   p.w_f32 = a->w_dtype == MOE_DT_F32; p.x_f16 = a->dtype == MOE_DT_F16;
   p.dy = a->dy; p.ld_dy = a->ld_dy;
@@ -206,8 +214,7 @@ int moe_dropout(int64_t rows, int32_t cols, int32_t dtype, const void* x, int64_
   p.rows = rows; p.cols = cols;
   p.x = x; p.ld_x = ld_x;
   p.y = y; p.ld_y = ld_y;
-  const bool vec = cols % 8 == 0 && vector_rows(x, ld_x, rows, dtype) &&
-                   vector_rows(y, ld_y, rows, dtype);
+  const int vec = row_access(y, ld_y, rows, dtype, row_access(x, ld_x, rows, dtype, width_access(cols)));
   return launch_dropout(p, dtype, vec, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;

@@ -36,35 +36,55 @@ template <typename T> MOE_DEV Raw8<T> narrow8(const float* f) {
   return r;
 }
 
-// Eight values of a row that one of `G` neighbouring threads holds.  VEC: the
+// Eight values of a row that one of `G` neighbouring threads holds.  V = 8: the
 // columns [8 l, 8 l + 8), one or two 16-byte accesses (rows on 16-byte boundaries,
-// whole groups).  Otherwise the columns l, l + G, ... l + 7 G: single elements,
-// but neighbouring threads touch neighbouring ones; columns at or past d read as
-// zero and are not written.  `l` counts from a multiple of G (VEC) or of 8 G.
-template <bool VEC> MOE_DEV int first_column(int i, int lane, int G) {
-  return VEC ? (lane + i * G) * 8 : i * 8 * G + lane;
+// whole groups).  V = 2: the pairs of columns 2 l, 2 (l + G), 2 (l + 2 G) and 2 (l +
+// 3 G) (an even width, rows on a pair's boundary); V = 1: the columns l, l + G, ... l
+// + 7 G.  Narrow accesses, but neighbouring threads touch neighbouring ones; columns
+// at or past d read as zero and are not written.  `l` counts from a multiple of G (V
+// = 8) or of 8 G columns.
+template <int V> MOE_DEV int first_column(int i, int lane, int G) {
+  return V == 8 ? (lane + i * G) * 8 : i * 8 * G + lane * V;
 }
-template <bool VEC> MOE_DEV int column_step(int G) { return VEC ? 1 : G; }
+// Column of value j of those that start at c.
+template <int V> MOE_DEV int column_of(int c, int j, int G) { return c + j / V * (V * G) + j % V; }
 
-template <typename T, bool VEC> MOE_DEV Raw8<T> load8(const T* row, int c, int G, int d) {
+template <typename T> struct alignas(2 * sizeof(T)) Pair { T v[2]; };
+
+template <typename T, int V> MOE_DEV Raw8<T> load8(const T* row, int c, int G, int d) {
   Raw8<T> r;
-  if constexpr (VEC) {
+  if constexpr (V == 8) {
     constexpr int n = sizeof(Raw8<T>) / 16;
     uint4* q = reinterpret_cast<uint4*>(&r);
 #pragma unroll
     for (int i = 0; i < n; ++i) q[i] = *(reinterpret_cast<const uint4*>(row + c) + i);
+  } else if constexpr (V == 2) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const int at = column_of<V>(c, j, G);
+      Pair<T> q = {Elem<T>::from_f(0.0f), Elem<T>::from_f(0.0f)};
+      if (at < d) q = *reinterpret_cast<const Pair<T>*>(row + at);
+      r.v[j] = q.v[0];
+      r.v[j + 1] = q.v[1];
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) r.v[j] = c + j * G < d ? row[c + j * G] : Elem<T>::from_f(0.0f);
   }
   return r;
 }
-template <typename T, bool VEC> MOE_DEV void store8(T* row, int c, int G, int d, const Raw8<T>& r) {
-  if constexpr (VEC) {
+template <typename T, int V> MOE_DEV void store8(T* row, int c, int G, int d, const Raw8<T>& r) {
+  if constexpr (V == 8) {
     constexpr int n = sizeof(Raw8<T>) / 16;
     const uint4* q = reinterpret_cast<const uint4*>(&r);
 #pragma unroll
     for (int i = 0; i < n; ++i) *(reinterpret_cast<uint4*>(row + c) + i) = q[i];
+  } else if constexpr (V == 2) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const int at = column_of<V>(c, j, G);
+      if (at < d) *reinterpret_cast<Pair<T>*>(row + at) = {r.v[j], r.v[j + 1]};
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
@@ -73,12 +93,12 @@ template <typename T, bool VEC> MOE_DEV void store8(T* row, int c, int G, int d,
 }
 
 // The same for a whole warp whose lanes hold neighbouring groups of eight columns
-// (VEC; each lane calls, `in`: its group is part of the row).  Eight fp32 values
+// (V = 8; each lane calls, `in`: its group is part of the row).  Eight fp32 values
 // are two 16-byte accesses; lanes go in pairs, so that each access of the pair
 // fills a 32-byte sector instead of two half sectors.
-template <typename T, bool VEC> MOE_DEV Raw8<T> load8_warp(const T* row, int c, int G, int d, bool in) {
+template <typename T, int V> MOE_DEV Raw8<T> load8_warp(const T* row, int c, int G, int d, bool in) {
   Raw8<T> r = {};
-  if constexpr (VEC && sizeof(T) == 4) {
+  if constexpr (V == 8 && sizeof(T) == 4) {
     const bool odd = threadIdx.x & 1;
     const bool other = __shfl_xor_sync(0xffffffffu, (int)in, 1);
     const T* even = row + (odd ? c - 8 : c);   // the pair's sixteen columns
@@ -95,12 +115,12 @@ template <typename T, bool VEC> MOE_DEV Raw8<T> load8_warp(const T* row, int c, 
     q[0] = odd ? got : a;
     q[1] = odd ? b : got;
   } else {
-    if (in) r = load8<T, VEC>(row, c, G, d);
+    if (in) r = load8<T, V>(row, c, G, d);
   }
   return r;
 }
-template <typename T, bool VEC> MOE_DEV void store8_warp(T* row, int c, int G, int d, const Raw8<T>& r, bool in) {
-  if constexpr (VEC && sizeof(T) == 4) {
+template <typename T, int V> MOE_DEV void store8_warp(T* row, int c, int G, int d, const Raw8<T>& r, bool in) {
+  if constexpr (V == 8 && sizeof(T) == 4) {
     const bool odd = threadIdx.x & 1;
     const bool other = __shfl_xor_sync(0xffffffffu, (int)in, 1);
     T* even = row + (odd ? c - 8 : c);
@@ -114,7 +134,7 @@ template <typename T, bool VEC> MOE_DEV void store8_warp(T* row, int c, int G, i
     if (odd ? other : in) *(reinterpret_cast<uint4*>(even) + odd) = odd ? got : q[0];
     if (odd ? in : other) *(reinterpret_cast<uint4*>(even) + 2 + odd) = odd ? q[1] : got;
   } else {
-    if (in) store8<T, VEC>(row, c, G, d, r);
+    if (in) store8<T, V>(row, c, G, d, r);
   }
 }
 
@@ -178,31 +198,36 @@ MOE_DEV void drop8(float* f, const uint4& r, const DropRng& g) {
 }
 
 // Numbers change hands: each of G threads has made those of eight neighbouring
-// columns, 8 G in a row, and gets those of the columns lane, lane + G, ...  `xch`:
-// G entries of the group's own; `sync`: a barrier of the G threads at least.
-template <typename Sync>
+// columns, 8 G in a row, and gets those of the columns that it holds (V = 2, 1).
+// `xch`: G entries of the group's own; `sync`: a barrier of the G threads at least.
+template <int V, typename Sync>
 MOE_DEV void exchange_numbers(uint4& r, int lane, int G, uint4* xch, Sync sync) {
   sync();   // the previous numbers have been read
   xch[lane] = r;
   sync();
-  const uint16_t* h = reinterpret_cast<const uint16_t*>(xch);
-  uint32_t w[4];
+  if constexpr (V == 2) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(xch);
+    r = make_uint4(w[lane], w[lane + G], w[lane + 2 * G], w[lane + 3 * G]);
+  } else {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(xch);
+    uint32_t w[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    w[j] = (uint32_t)h[2 * j * G + lane] | (uint32_t)h[(2 * j + 1) * G + lane] << 16;
-  r = make_uint4(w[0], w[1], w[2], w[3]);
+    for (int j = 0; j < 4; ++j)
+      w[j] = (uint32_t)h[2 * j * G + lane] | (uint32_t)h[(2 * j + 1) * G + lane] << 16;
+    r = make_uint4(w[0], w[1], w[2], w[3]);
+  }
 }
 
 // The numbers of a thread's N times eight values of a row: groups lane, lane +
-// G, ... of neighbouring columns (VEC), or the columns first_column() says.
-template <bool VEC, int N, typename Sync>
+// G, ... of neighbouring columns (V = 8), or the columns first_column() says.
+template <int V, int N, typename Sync>
 MOE_DEV void drop_numbers(uint4 (&r)[N], int lane, int G, uint32_t row, const DropRng& g, uint4* xch, Sync sync) {
 #pragma unroll
   for (int n = 0; n < N; ++n) r[n] = make_uint4((uint32_t)(lane + n * G), row, g.o0, g.o1);
   philox4x32_10(r, g.k0, g.k1);
-  if constexpr (!VEC) {
+  if constexpr (V != 8) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) exchange_numbers(r[n], lane, G, xch, sync);
+    for (int n = 0; n < N; ++n) exchange_numbers<V>(r[n], lane, G, xch, sync);
   }
 }
 

@@ -70,10 +70,11 @@ constexpr int kNormPartialRows = 1024;   // most blocks of the backward: rows of
 
 cudaError_t norm_init();   // dynamic shared memory limits (moe_init)
 cudaError_t norm_bwd_init();
-cudaError_t launch_add_norm(const AddNormParams& p, int dtype, int res_dtype, bool vec, cudaStream_t s);
-cudaError_t launch_add_norm_bwd(const AddNormBwdParams& p, int dtype, int res_dtype, bool vec, float* dw,
+// vec: neighbouring columns that an access takes, 8, 2 or 1 (block.cuh, V)
+cudaError_t launch_add_norm(const AddNormParams& p, int dtype, int res_dtype, int vec, cudaStream_t s);
+cudaError_t launch_add_norm_bwd(const AddNormBwdParams& p, int dtype, int res_dtype, int vec, float* dw,
                                 cudaStream_t s);
-cudaError_t launch_dropout(const DropoutParams& p, int dtype, bool vec, cudaStream_t s);
+cudaError_t launch_dropout(const DropoutParams& p, int dtype, int vec, cudaStream_t s);
 
 // ---------------------------------------------------------------- 4-bit weights
 constexpr int kW4MaxColumns = 1 << 18;   // K, d and f: stages of a block's share count in 32 bits

@@ -11,11 +11,11 @@ namespace {
 // padding of the last 128-row tile.  Measured: 8192 x 2048 bf16 23.7 us (5.7 TB/s),
 // bound by HBM and, at 60% of the issue slots, by waits between instructions; 8
 // bits, dropout, 32768 x 4096 238 us (5.1 TB/s), 65% of the issue slots.
-template <typename TX, typename TR, bool MX, bool VEC, bool RING, int NV, int MAXT>
+template <typename TX, typename TR, bool MX, int V, bool RING, int NV, int MAXT>
 __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_kernel(AddNormParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float red[2][kNormMaxThreads / 32];
-  __shared__ uint4 xch[VEC ? 1 : MAXT];
+  __shared__ uint4 xch[V == 8 ? 1 : MAXT];
   using Ring = RowRing<8 * (sizeof(TX) + sizeof(TR)), NV>;
   constexpr int XP = sizeof(TX) / 2, RP = sizeof(TR) / 2;   // 16-byte pieces of eight columns
   pdl_begin();
@@ -25,8 +25,8 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
   float w[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = first_column<VEC>(i, lane, G);
-    load_weight8<VEC>(p.weight, p.w_f32, sizeof(TX) == 2 && p.x_f16, c, G, d, w[i]);
+    const int c = first_column<V>(i, lane, G);
+    load_weight8<V>(p.weight, p.w_f32, sizeof(TX) == 2 && p.x_f16, c, G, d, w[i]);
   }
   const int64_t step = (int64_t)gridDim.x * rg.per;
   int64_t row = (int64_t)blockIdx.x * rg.per + rg.group;
@@ -64,11 +64,11 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
       __syncwarp();
     }
     uint4 numbers[NV];
-    if (p.rng.threshold) drop_numbers<VEC>(numbers, lane, G, (uint32_t)row, p.rng, xch + rg.group * G, sync);
+    if (p.rng.threshold) drop_numbers<V>(numbers, lane, G, (uint32_t)row, p.rng, xch + rg.group * G, sync);
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = first_column<VEC>(i, lane, G);
+      const int c = first_column<V>(i, lane, G);
       const bool in = c < d && live;
       Raw8<TX> xr = {};
       Raw8<TR> rr = {};
@@ -76,8 +76,8 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
         xr = ring.template get<TX>(i * XP);
         if (cr) rr = ring.template get<TR>(NV * XP + i * RP);
       } else {
-        xr = load8_warp<TX, VEC>(static_cast<const TX*>(p.x) + row * p.ld_x, c, G, d, in);
-        if (cr) rr = load8_warp<TR, VEC>(static_cast<const TR*>(p.residual) + row * p.ld_residual, c, G, d, in);
+        xr = load8_warp<TX, V>(static_cast<const TX*>(p.x) + row * p.ld_x, c, G, d, in);
+        if (cr) rr = load8_warp<TR, V>(static_cast<const TR*>(p.residual) + row * p.ld_residual, c, G, d, in);
       }
       widen8(xr, h[i]);
       if (p.rng.threshold) drop8(h[i], numbers[i], p.rng);
@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
       }
       if (p.h) {
         const Raw8<TR> hr = narrow8<TR>(h[i]);
-        store8_warp<TR, VEC>(static_cast<TR*>(p.h) + row * p.ld_h, c, G, d, hr, in);
+        store8_warp<TR, V>(static_cast<TR*>(p.h) + row * p.ld_h, c, G, d, hr, in);
         widen8(hr, h[i]);
       }
 #pragma unroll
@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
     if (lane == 0 && p.rstd && live) p.rstd[row] = rstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = first_column<VEC>(i, lane, G);
+      const int c = first_column<V>(i, lane, G);
       float amax = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
         if (MX) amax = fmaxf(amax, fabsf(h[i][j]));
       }
       if constexpr (!MX) {
-        store8_warp<TX, VEC>(static_cast<TX*>(p.y) + row * p.ld_y, c, G, d, narrow8<TX>(h[i]), c < d && live);
+        store8_warp<TX, V>(static_cast<TX*>(p.y) + row * p.ld_y, c, G, d, narrow8<TX>(h[i]), c < d && live);
       } else {
         // d is a multiple of 128: the 16 lanes of four 32-column blocks are all
         // within the row or all past its end
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
             e4m3x2_to_f32(q.y >> 16, v[6], v[7]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) v[j] *= up;
-            store8<__nv_bfloat16, true>(static_cast<__nv_bfloat16*>(p.y_dq) + row * d, c, 1, d,
+            store8<__nv_bfloat16, 8>(static_cast<__nv_bfloat16*>(p.y_dq) + row * d, c, 1, d,
                                         narrow8<__nv_bfloat16>(v));
           }
         }
@@ -158,16 +158,16 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
 // y = dropout(x): a warp, or (SMALL, rows up to 64 and 128 columns) 8 or 16 lanes,
 // takes eight columns a lane of two rows at a time.  Bound by the generator (bf16)
 // and HBM (fp32): 16384 x 2048 bf16 27.6 us, 4.9 TB/s; fp32 5.7 TB/s.
-template <typename T, bool VEC, bool SMALL>
+template <typename T, int V, bool SMALL>
 __global__ void __launch_bounds__(256, 4) dropout_kernel(DropoutParams p) {
-  __shared__ uint4 xch[VEC ? 1 : 256];
+  __shared__ uint4 xch[V == 8 ? 1 : 256];
   pdl_begin();
   const int L = SMALL ? p.group : 32, lane = threadIdx.x & (L - 1), group = threadIdx.x / L, per = 256 / L * 2;
   const int before = (threadIdx.x & 31) / L * 2;   // rows of the warp's lanes before this one
   auto sync = []() { __syncwarp(); };
   const int64_t step = (int64_t)gridDim.y * per;
   for (int i = blockIdx.x; i * (int64_t)(8 * L) < p.cols; i += gridDim.x) {
-    const int c = first_column<VEC>(i, lane, L);
+    const int c = first_column<V>(i, lane, L);
     const bool in = c < p.cols;
     int64_t row = (int64_t)blockIdx.y * per + group * 2;
     const T* x = static_cast<const T*>(p.x) + row * p.ld_x;
@@ -175,17 +175,17 @@ __global__ void __launch_bounds__(256, 4) dropout_kernel(DropoutParams p) {
     // a warp goes on while its first lanes have a row
     for (; row - before < p.rows; row += step, x += step * p.ld_x, y += step * p.ld_y) {
       const bool one = in && row < p.rows, two = in && row + 1 < p.rows;
-      const Raw8<T> raw[2] = {load8_warp<T, VEC>(x, c, L, p.cols, one),
-                              load8_warp<T, VEC>(x + p.ld_x, c, L, p.cols, two)};
+      const Raw8<T> raw[2] = {load8_warp<T, V>(x, c, L, p.cols, one),
+                              load8_warp<T, V>(x + p.ld_x, c, L, p.cols, two)};
       uint4 numbers[2];
       if (p.rng.threshold) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
           numbers[u] = make_uint4((uint32_t)(lane + L * i), (uint32_t)(row + u), p.rng.o0, p.rng.o1);
         philox4x32_10(numbers, p.rng.k0, p.rng.k1);
-        if constexpr (!VEC) {
+        if constexpr (V != 8) {
 #pragma unroll
-          for (int u = 0; u < 2; ++u) exchange_numbers(numbers[u], lane, L, xch + group * L, sync);
+          for (int u = 0; u < 2; ++u) exchange_numbers<V>(numbers[u], lane, L, xch + group * L, sync);
         }
       }
 #pragma unroll
@@ -193,16 +193,16 @@ __global__ void __launch_bounds__(256, 4) dropout_kernel(DropoutParams p) {
         float f[8];
         widen8(raw[u], f);
         if (p.rng.threshold) drop8(f, numbers[u], p.rng);
-        store8_warp<T, VEC>(y + u * p.ld_y, c, L, p.cols, narrow8<T>(f), u == 0 ? one : two);
+        store8_warp<T, V>(y + u * p.ld_y, c, L, p.cols, narrow8<T>(f), u == 0 ? one : two);
       }
     }
   }
 }
 
 // p = NULL: raise the kernel's shared memory limit.
-template <typename TX, typename TR, bool MX, bool VEC, bool RING, int NV, int MAXT>
+template <typename TX, typename TR, bool MX, int V, bool RING, int NV, int MAXT>
 cudaError_t fwd_run(const AddNormParams* p, int threads, cudaStream_t s) {
-  auto* kernel = &add_norm_kernel<TX, TR, MX, VEC, RING, NV, MAXT>;
+  auto* kernel = &add_norm_kernel<TX, TR, MX, V, RING, NV, MAXT>;
   constexpr int ring = RING ? RowRing<8 * (sizeof(TX) + sizeof(TR)), NV>::kBytes : 0;
   if (p == nullptr)
     return ring ? cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -217,82 +217,84 @@ cudaError_t fwd_run(const AddNormParams* p, int threads, cudaStream_t s) {
 // A thread holds two groups of eight columns, more where the threads need it (rows
 // without vector loads: one), for the 8-bit output three or four.  Measured at 32768 x 4096 (8-bit, dropout) 243
 // us with four, 266 with two; at 8192 x 2048 (bf16) 26 and 24.
-template <typename TX, typename TR, bool MX, bool VEC>
+template <typename TX, typename TR, bool MX, int V>
 cudaError_t fwd_types(const AddNormParams* p, cudaStream_t s) {
-  constexpr bool wide = VEC && RowRing<8 * (sizeof(TX) + sizeof(TR)), 4>::kFits512;
+  constexpr bool wide = V == 8 && RowRing<8 * (sizeof(TX) + sizeof(TR)), 4>::kFits512;
   if (p == nullptr) {
     cudaError_t e = cudaSuccess;
-    if constexpr (VEC) {
-      e = fwd_run<TX, TR, MX, true, true, 1, kNormThreads>(p, 0, s);
-      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, true, true, 2, kNormThreads>(p, 0, s);
-      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, true, true, 3, kNormThreads>(p, 0, s);
-      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, true, true, 4, kNormThreads>(p, 0, s);
+    if constexpr (V == 8) {
+      e = fwd_run<TX, TR, MX, 8, true, 1, kNormThreads>(p, 0, s);
+      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, 8, true, 2, kNormThreads>(p, 0, s);
+      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, 8, true, 3, kNormThreads>(p, 0, s);
+      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, 8, true, 4, kNormThreads>(p, 0, s);
     }
     if constexpr (wide) {
-      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, true, true, 3, 512>(p, 0, s);
-      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, true, true, 4, 512>(p, 0, s);
+      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, 8, true, 3, 512>(p, 0, s);
+      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, 8, true, 4, 512>(p, 0, s);
     }
     return e;
   }
   AddNormParams q = *p;
-  if constexpr (VEC) {
+  if constexpr (V == 8) {
     RowSplit split(p->d, !MX || p->d <= 512 ? 2 : 3, 4, kNormThreads);
     q.group = split.group;
     if (split.group) {
       const int threads = split.threads();
-      if (split.nv == 1) return fwd_run<TX, TR, MX, true, true, 1, kNormThreads>(&q, threads, s);
-      if (split.nv == 2) return fwd_run<TX, TR, MX, true, true, 2, kNormThreads>(&q, threads, s);
-      if (split.nv == 3) return fwd_run<TX, TR, MX, true, true, 3, kNormThreads>(&q, threads, s);
-      return fwd_run<TX, TR, MX, true, true, 4, kNormThreads>(&q, threads, s);
+      if (split.nv == 1) return fwd_run<TX, TR, MX, 8, true, 1, kNormThreads>(&q, threads, s);
+      if (split.nv == 2) return fwd_run<TX, TR, MX, 8, true, 2, kNormThreads>(&q, threads, s);
+      if (split.nv == 3) return fwd_run<TX, TR, MX, 8, true, 3, kNormThreads>(&q, threads, s);
+      return fwd_run<TX, TR, MX, 8, true, 4, kNormThreads>(&q, threads, s);
     }
     if constexpr (wide) {
       split = RowSplit(p->d, 3, 4, 512);
       q.group = split.group;
       if (split.group)
-        return split.nv == 3 ? fwd_run<TX, TR, MX, true, true, 3, 512>(&q, q.group, s)
-                             : fwd_run<TX, TR, MX, true, true, 4, 512>(&q, q.group, s);
+        return split.nv == 3 ? fwd_run<TX, TR, MX, 8, true, 3, 512>(&q, q.group, s)
+                             : fwd_run<TX, TR, MX, 8, true, 4, 512>(&q, q.group, s);
     }
   } else {
     const RowSplit split(p->d, 1, 2, 512);
     q.group = split.group;
     if (split.group) {
       const int threads = split.threads();
-      if (split.nv == 2) return fwd_run<TX, TR, MX, false, false, 2, 512>(&q, threads, s);
-      return split.group <= kNormThreads ? fwd_run<TX, TR, MX, false, false, 1, kNormThreads>(&q, threads, s)
-                                         : fwd_run<TX, TR, MX, false, false, 1, 512>(&q, threads, s);
+      if (split.nv == 2) return fwd_run<TX, TR, MX, V, false, 2, 512>(&q, threads, s);
+      return split.group <= kNormThreads ? fwd_run<TX, TR, MX, V, false, 1, kNormThreads>(&q, threads, s)
+                                         : fwd_run<TX, TR, MX, V, false, 1, 512>(&q, threads, s);
     }
   }
   const RowSplit split(p->d, wide ? 3 : 2, 4, kNormMaxThreads);
   q.group = split.group;
   if constexpr (!wide)
-    if (split.nv == 2) return fwd_run<TX, TR, MX, VEC, false, 2, kNormMaxThreads>(&q, q.group, s);
-  return split.nv == 3 ? fwd_run<TX, TR, MX, VEC, false, 3, kNormMaxThreads>(&q, q.group, s)
-                       : fwd_run<TX, TR, MX, VEC, false, 4, kNormMaxThreads>(&q, q.group, s);
+    if (split.nv == 2) return fwd_run<TX, TR, MX, V, false, 2, kNormMaxThreads>(&q, q.group, s);
+  return split.nv == 3 ? fwd_run<TX, TR, MX, V, false, 3, kNormMaxThreads>(&q, q.group, s)
+                       : fwd_run<TX, TR, MX, V, false, 4, kNormMaxThreads>(&q, q.group, s);
 }
 
 template <typename TX, typename TR>
-cudaError_t fwd_vec(const AddNormParams* p, bool vec, cudaStream_t s) {
-  return vec ? fwd_types<TX, TR, false, true>(p, s) : fwd_types<TX, TR, false, false>(p, s);
+cudaError_t fwd_vec(const AddNormParams* p, int vec, cudaStream_t s) {
+  return vec == 8   ? fwd_types<TX, TR, false, 8>(p, s)
+         : vec == 2 ? fwd_types<TX, TR, false, 2>(p, s)
+                    : fwd_types<TX, TR, false, 1>(p, s);
 }
 
 }  // namespace
 
 cudaError_t norm_init() {
-  cudaError_t e = fwd_vec<__nv_bfloat16, __nv_bfloat16>(nullptr, true, nullptr);
-  if (e == cudaSuccess) e = fwd_vec<__nv_bfloat16, float>(nullptr, true, nullptr);
-  if (e == cudaSuccess) e = fwd_vec<__half, __half>(nullptr, true, nullptr);
-  if (e == cudaSuccess) e = fwd_vec<__half, float>(nullptr, true, nullptr);
-  if (e == cudaSuccess) e = fwd_vec<float, float>(nullptr, true, nullptr);
-  if (e == cudaSuccess) e = fwd_types<__nv_bfloat16, __nv_bfloat16, true, true>(nullptr, nullptr);
-  if (e == cudaSuccess) e = fwd_types<__nv_bfloat16, float, true, true>(nullptr, nullptr);
+  cudaError_t e = fwd_vec<__nv_bfloat16, __nv_bfloat16>(nullptr, 8, nullptr);
+  if (e == cudaSuccess) e = fwd_vec<__nv_bfloat16, float>(nullptr, 8, nullptr);
+  if (e == cudaSuccess) e = fwd_vec<__half, __half>(nullptr, 8, nullptr);
+  if (e == cudaSuccess) e = fwd_vec<__half, float>(nullptr, 8, nullptr);
+  if (e == cudaSuccess) e = fwd_vec<float, float>(nullptr, 8, nullptr);
+  if (e == cudaSuccess) e = fwd_types<__nv_bfloat16, __nv_bfloat16, true, 8>(nullptr, nullptr);
+  if (e == cudaSuccess) e = fwd_types<__nv_bfloat16, float, true, 8>(nullptr, nullptr);
   return e;
 }
 
-cudaError_t launch_add_norm(const AddNormParams& p, int dtype, int res_dtype, bool vec, cudaStream_t s) {
+cudaError_t launch_add_norm(const AddNormParams& p, int dtype, int res_dtype, int vec, cudaStream_t s) {
   const bool same = dtype == res_dtype;
   if (p.y_q)
-    return same ? fwd_types<__nv_bfloat16, __nv_bfloat16, true, true>(&p, s)
-                : fwd_types<__nv_bfloat16, float, true, true>(&p, s);
+    return same ? fwd_types<__nv_bfloat16, __nv_bfloat16, true, 8>(&p, s)
+                : fwd_types<__nv_bfloat16, float, true, 8>(&p, s);
   if (dtype == MOE_DT_BF16)
     return same ? fwd_vec<__nv_bfloat16, __nv_bfloat16>(&p, vec, s) : fwd_vec<__nv_bfloat16, float>(&p, vec, s);
   if (dtype == MOE_DT_F16)
@@ -300,15 +302,19 @@ cudaError_t launch_add_norm(const AddNormParams& p, int dtype, int res_dtype, bo
   return fwd_vec<float, float>(&p, vec, s);
 }
 
-template <typename T> static cudaError_t dropout_types(const DropoutParams& p, bool vec, dim3 grid, cudaStream_t s) {
-  if (p.group < 32)
-    return vec ? launch_pdl(dropout_kernel<T, true, true>, grid, dim3(256), 0, s, p)
-               : launch_pdl(dropout_kernel<T, false, true>, grid, dim3(256), 0, s, p);
-  return vec ? launch_pdl(dropout_kernel<T, true, false>, grid, dim3(256), 0, s, p)
-             : launch_pdl(dropout_kernel<T, false, false>, grid, dim3(256), 0, s, p);
+template <typename T> static cudaError_t dropout_types(const DropoutParams& p, int vec, dim3 grid, cudaStream_t s) {
+  const bool small = p.group < 32;
+  if (vec == 8)
+    return small ? launch_pdl(dropout_kernel<T, 8, true>, grid, dim3(256), 0, s, p)
+                 : launch_pdl(dropout_kernel<T, 8, false>, grid, dim3(256), 0, s, p);
+  if (vec == 2)
+    return small ? launch_pdl(dropout_kernel<T, 2, true>, grid, dim3(256), 0, s, p)
+                 : launch_pdl(dropout_kernel<T, 2, false>, grid, dim3(256), 0, s, p);
+  return small ? launch_pdl(dropout_kernel<T, 1, true>, grid, dim3(256), 0, s, p)
+               : launch_pdl(dropout_kernel<T, 1, false>, grid, dim3(256), 0, s, p);
 }
 
-cudaError_t launch_dropout(const DropoutParams& args, int dtype, bool vec, cudaStream_t s) {
+cudaError_t launch_dropout(const DropoutParams& args, int dtype, int vec, cudaStream_t s) {
   DropoutParams p = args;
   p.group = p.cols <= 64 ? 8 : p.cols <= 128 ? 16 : 32;
   // four blocks a multiprocessor, all of them there at once (one block more than

@@ -101,17 +101,17 @@ MOE_DEV float inv_sqrt(float v) {
   return fmaf(0.5f * r, fmaf(-v * r, r, 1.0f), r);
 }
 
-template <bool VEC>
+template <int V>
 MOE_DEV void load_weight8(const void* w, bool w_f32, bool w_f16, int c, int G, int d, float* f) {
   if (c >= d) {   // columns past the row's end: zeros all through
 #pragma unroll
     for (int j = 0; j < 8; ++j) f[j] = 0.0f;
   } else if (w_f32) {
-    widen8(load8<float, VEC>(static_cast<const float*>(w), c, G, d), f);
+    widen8(load8<float, V>(static_cast<const float*>(w), c, G, d), f);
   } else if (w_f16) {
-    widen8(load8<__half, VEC>(static_cast<const __half*>(w), c, G, d), f);
+    widen8(load8<__half, V>(static_cast<const __half*>(w), c, G, d), f);
   } else {
-    widen8(load8<__nv_bfloat16, VEC>(static_cast<const __nv_bfloat16*>(w), c, G, d), f);
+    widen8(load8<__nv_bfloat16, V>(static_cast<const __nv_bfloat16*>(w), c, G, d), f);
   }
 }
 

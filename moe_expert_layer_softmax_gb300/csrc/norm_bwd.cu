@@ -10,14 +10,14 @@ namespace {
 // partial sums a block goes to `partial` [gridDim.x, d].  Measured: 8192 x 2048
 // bf16 33.2 us (5.05 TB/s; 4 us of it the sum of the partial rows), 32768 x 4096 on
 // an fp32 stream with dropout 317 us (6.8 TB/s, a plain copy's rate).
-template <typename TX, typename TR, bool VEC, bool RING, int NV, int MAXT>
+template <typename TX, typename TR, int V, bool RING, int NV, int MAXT>
 __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_bwd_kernel(AddNormBwdParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float red[2][kNormMaxThreads / 32];
   // drop numbers that change hands; at the end the sums of the row groups
   // (eight floats a thread and NV, in the ring where there is one; only blocks of
   // kNormThreads have groups)
-  __shared__ uint4 xch[RING ? 1 : MAXT <= kNormThreads ? MAXT * 2 * NV : VEC ? 1 : MAXT];
+  __shared__ uint4 xch[RING ? 1 : MAXT <= kNormThreads ? MAXT * 2 * NV : V == 8 ? 1 : MAXT];
   using Ring = RowRing<8 * (sizeof(TX) + 2 * sizeof(TR)), NV>;
   constexpr int XP = sizeof(TX) / 2, RP = sizeof(TR) / 2;   // 16-byte pieces of eight columns
   pdl_begin();
@@ -27,8 +27,8 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_bw
   float w[NV][8], dw[NV][8];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int c = first_column<VEC>(i, lane, G);
-    load_weight8<VEC>(p.weight, p.w_f32, sizeof(TX) == 2 && p.x_f16, c, G, d, w[i]);
+    const int c = first_column<V>(i, lane, G);
+    load_weight8<V>(p.weight, p.w_f32, sizeof(TX) == 2 && p.x_f16, c, G, d, w[i]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   }
@@ -78,15 +78,15 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_bw
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = first_column<VEC>(i, lane, G);
+      const int c = first_column<V>(i, lane, G);
       if constexpr (RING) {
         if (live) {
           yr[i] = ring.template get<TX>(i * XP);
           hr[i] = ring.template get<TR>(NV * XP + i * RP);
         }
       } else {
-        yr[i] = load8_warp<TX, VEC>(static_cast<const TX*>(p.dy) + row * p.ld_dy, c, G, d, c < d && live);
-        hr[i] = load8_warp<TR, VEC>(static_cast<const TR*>(p.h) + row * p.ld_h, c, G, d, c < d && live);
+        yr[i] = load8_warp<TX, V>(static_cast<const TX*>(p.dy) + row * p.ld_dy, c, G, d, c < d && live);
+        hr[i] = load8_warp<TR, V>(static_cast<const TR*>(p.h) + row * p.ld_h, c, G, d, c < d && live);
       }
       float a[8], b[8];
       widen8(yr[i], a);
@@ -102,10 +102,10 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_bw
     const float k = r * r * (dot * p.inv_d);
     uint4 numbers[NV];
     if (p.dx && p.rng.threshold)
-      drop_numbers<VEC>(numbers, lane, G, (uint32_t)row, p.rng, xch + rg.group * G, sync);
+      drop_numbers<V>(numbers, lane, G, (uint32_t)row, p.rng, xch + rg.group * G, sync);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = first_column<VEC>(i, lane, G);
+      const int c = first_column<V>(i, lane, G);
       const bool in = c < d && live;
       float a[8], b[8];
       widen8(yr[i], a);
@@ -117,22 +117,21 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_bw
         if constexpr (RING)
           dr = ring.template get<TR>(NV * (XP + RP) + i * RP);
         else
-          dr = load8_warp<TR, VEC>(static_cast<const TR*>(p.dres) + row * p.ld_dres, c, G, d, in);
+          dr = load8_warp<TR, V>(static_cast<const TR*>(p.dres) + row * p.ld_dres, c, G, d, in);
         widen8(dr, b);
 #pragma unroll
         for (int j = 0; j < 8; ++j) a[j] += b[j];
       }
-      if (p.dh) store8_warp<TR, VEC>(static_cast<TR*>(p.dh) + row * p.ld_dh, c, G, d, narrow8<TR>(a), in);
+      if (p.dh) store8_warp<TR, V>(static_cast<TR*>(p.dh) + row * p.ld_dh, c, G, d, narrow8<TR>(a), in);
       if (p.dx) {
         if (p.rng.threshold) drop8(a, numbers[i], p.rng);
-        store8_warp<TX, VEC>(static_cast<TX*>(p.dx) + row * p.ld_dx, c, G, d, narrow8<TX>(a), in);
+        store8_warp<TX, V>(static_cast<TX*>(p.dx) + row * p.ld_dx, c, G, d, narrow8<TX>(a), in);
       }
     }
     if constexpr (RING) ring.slot = ring.next(ring.slot);
   }
   if (!p.partial) return;
   float* out = p.partial + (int64_t)blockIdx.x * d;
-  const int cs = column_step<VEC>(G);
   if (rg.per > 1) {   // the row groups' sums, added in their order
     float* all = RING ? reinterpret_cast<float*>(smem) : reinterpret_cast<float*>(xch);
     const int width = G * NV * 8;
@@ -141,7 +140,7 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_bw
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) all[rg.group * width + first_column<VEC>(i, lane, G) + j * cs] = dw[i][j];
+      for (int j = 0; j < 8; ++j) all[rg.group * width + column_of<V>(first_column<V>(i, lane, G), j, G)] = dw[i][j];
     __syncthreads();
     for (int c = threadIdx.x; c < d; c += blockDim.x) {
       float s = 0.0f;
@@ -151,10 +150,10 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_bw
   } else {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int c = first_column<VEC>(i, lane, G);
+      const int c = first_column<V>(i, lane, G);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (c + j * cs < d) out[c + j * cs] = dw[i][j];
+        if (column_of<V>(c, j, G) < d) out[column_of<V>(c, j, G)] = dw[i][j];
     }
   }
 }
@@ -180,9 +179,9 @@ __global__ void __launch_bounds__(1024) add_norm_dw_kernel(const float* __restri
 }
 
 // p = NULL: raise the kernel's shared memory limit.
-template <typename TX, typename TR, bool VEC, bool RING, int NV, int MAXT>
+template <typename TX, typename TR, int V, bool RING, int NV, int MAXT>
 cudaError_t bwd_run(const AddNormBwdParams* p, int threads, int* blocks, cudaStream_t s) {
-  auto* kernel = &add_norm_bwd_kernel<TX, TR, VEC, RING, NV, MAXT>;
+  auto* kernel = &add_norm_bwd_kernel<TX, TR, V, RING, NV, MAXT>;
   constexpr int ring = RING ? RowRing<8 * (sizeof(TX) + 2 * sizeof(TR)), NV>::kBytes : 0;
   if (p == nullptr)
     return ring ? cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
@@ -195,66 +194,68 @@ cudaError_t bwd_run(const AddNormBwdParams* p, int threads, int* blocks, cudaStr
 
 // Rows up to 8192 columns (512 threads; 16384 where both matrices are 16 bits)
 // come through the ring; wider ones are read as they are needed.
-template <typename TX, typename TR, bool VEC>
+template <typename TX, typename TR, int V>
 cudaError_t bwd_types(const AddNormBwdParams* p, int* blocks, cudaStream_t s) {
-  constexpr bool wide = VEC && RowRing<8 * (sizeof(TX) + 2 * sizeof(TR)), 4>::kFits512;
+  constexpr bool wide = V == 8 && RowRing<8 * (sizeof(TX) + 2 * sizeof(TR)), 4>::kFits512;
   cudaError_t e = cudaSuccess;
   if (p == nullptr) {
-    if constexpr (VEC) {
-      e = bwd_run<TX, TR, true, true, 1, kNormThreads>(p, 0, blocks, s);
-      if (e == cudaSuccess) e = bwd_run<TX, TR, true, true, 2, kNormThreads>(p, 0, blocks, s);
-      if (e == cudaSuccess) e = bwd_run<TX, TR, true, true, 2, 512>(p, 0, blocks, s);
+    if constexpr (V == 8) {
+      e = bwd_run<TX, TR, 8, true, 1, kNormThreads>(p, 0, blocks, s);
+      if (e == cudaSuccess) e = bwd_run<TX, TR, 8, true, 2, kNormThreads>(p, 0, blocks, s);
+      if (e == cudaSuccess) e = bwd_run<TX, TR, 8, true, 2, 512>(p, 0, blocks, s);
     }
     if constexpr (wide) {
-      if (e == cudaSuccess) e = bwd_run<TX, TR, true, true, 3, 512>(p, 0, blocks, s);
-      if (e == cudaSuccess) e = bwd_run<TX, TR, true, true, 4, 512>(p, 0, blocks, s);
+      if (e == cudaSuccess) e = bwd_run<TX, TR, 8, true, 3, 512>(p, 0, blocks, s);
+      if (e == cudaSuccess) e = bwd_run<TX, TR, 8, true, 4, 512>(p, 0, blocks, s);
     }
     return e;
   }
   AddNormBwdParams q = *p;
-  RowSplit split(p->d, VEC ? 2 : 1, wide ? 4 : 2, 512);
+  RowSplit split(p->d, V == 8 ? 2 : 1, wide ? 4 : 2, 512);
   q.group = split.group;
   if (split.group) {
     const int threads = split.threads();
     if constexpr (wide) {
-      if (split.nv == 3) return bwd_run<TX, TR, VEC, true, 3, 512>(&q, threads, blocks, s);
-      if (split.nv == 4) return bwd_run<TX, TR, VEC, true, 4, 512>(&q, threads, blocks, s);
+      if (split.nv == 3) return bwd_run<TX, TR, V, true, 3, 512>(&q, threads, blocks, s);
+      if (split.nv == 4) return bwd_run<TX, TR, V, true, 4, 512>(&q, threads, blocks, s);
     }
-    if constexpr (VEC) {
+    if constexpr (V == 8) {
       if (split.nv == 2 && split.group <= kNormThreads)
-        return bwd_run<TX, TR, VEC, true, 2, kNormThreads>(&q, threads, blocks, s);
+        return bwd_run<TX, TR, V, true, 2, kNormThreads>(&q, threads, blocks, s);
     } else {
       if (split.nv == 1 && split.group > kNormThreads)
-        return bwd_run<TX, TR, VEC, false, 1, 512>(&q, threads, blocks, s);
+        return bwd_run<TX, TR, V, false, 1, 512>(&q, threads, blocks, s);
     }
-    return split.nv == 1 ? bwd_run<TX, TR, VEC, VEC, 1, kNormThreads>(&q, threads, blocks, s)
-                         : bwd_run<TX, TR, VEC, VEC, 2, 512>(&q, threads, blocks, s);
+    return split.nv == 1 ? bwd_run<TX, TR, V, V == 8, 1, kNormThreads>(&q, threads, blocks, s)
+                         : bwd_run<TX, TR, V, V == 8, 2, 512>(&q, threads, blocks, s);
   }
   split = RowSplit(p->d, wide ? 3 : 2, 4, kNormMaxThreads);
   q.group = split.group;
   if constexpr (!wide)
-    if (split.nv == 2) return bwd_run<TX, TR, VEC, false, 2, kNormMaxThreads>(&q, q.group, blocks, s);
-  return split.nv == 3 ? bwd_run<TX, TR, VEC, false, 3, kNormMaxThreads>(&q, q.group, blocks, s)
-                       : bwd_run<TX, TR, VEC, false, 4, kNormMaxThreads>(&q, q.group, blocks, s);
+    if (split.nv == 2) return bwd_run<TX, TR, V, false, 2, kNormMaxThreads>(&q, q.group, blocks, s);
+  return split.nv == 3 ? bwd_run<TX, TR, V, false, 3, kNormMaxThreads>(&q, q.group, blocks, s)
+                       : bwd_run<TX, TR, V, false, 4, kNormMaxThreads>(&q, q.group, blocks, s);
 }
 
 template <typename TX, typename TR>
-cudaError_t bwd_vec(const AddNormBwdParams* p, bool vec, int* blocks, cudaStream_t s) {
-  return vec ? bwd_types<TX, TR, true>(p, blocks, s) : bwd_types<TX, TR, false>(p, blocks, s);
+cudaError_t bwd_vec(const AddNormBwdParams* p, int vec, int* blocks, cudaStream_t s) {
+  return vec == 8   ? bwd_types<TX, TR, 8>(p, blocks, s)
+         : vec == 2 ? bwd_types<TX, TR, 2>(p, blocks, s)
+                    : bwd_types<TX, TR, 1>(p, blocks, s);
 }
 
 }  // namespace
 
 cudaError_t norm_bwd_init() {
-  cudaError_t e = bwd_vec<__nv_bfloat16, __nv_bfloat16>(nullptr, true, nullptr, nullptr);
-  if (e == cudaSuccess) e = bwd_vec<__nv_bfloat16, float>(nullptr, true, nullptr, nullptr);
-  if (e == cudaSuccess) e = bwd_vec<__half, __half>(nullptr, true, nullptr, nullptr);
-  if (e == cudaSuccess) e = bwd_vec<__half, float>(nullptr, true, nullptr, nullptr);
-  if (e == cudaSuccess) e = bwd_vec<float, float>(nullptr, true, nullptr, nullptr);
+  cudaError_t e = bwd_vec<__nv_bfloat16, __nv_bfloat16>(nullptr, 8, nullptr, nullptr);
+  if (e == cudaSuccess) e = bwd_vec<__nv_bfloat16, float>(nullptr, 8, nullptr, nullptr);
+  if (e == cudaSuccess) e = bwd_vec<__half, __half>(nullptr, 8, nullptr, nullptr);
+  if (e == cudaSuccess) e = bwd_vec<__half, float>(nullptr, 8, nullptr, nullptr);
+  if (e == cudaSuccess) e = bwd_vec<float, float>(nullptr, 8, nullptr, nullptr);
   return e;
 }
 
-cudaError_t launch_add_norm_bwd(const AddNormBwdParams& p, int dtype, int res_dtype, bool vec, float* dw,
+cudaError_t launch_add_norm_bwd(const AddNormBwdParams& p, int dtype, int res_dtype, int vec, float* dw,
                                 cudaStream_t s) {
   const bool same = dtype == res_dtype;
   int blocks = 0;

@@ -22,7 +22,7 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(int64_t n8, int group,
   float v[8];
   float amax = 0.0f;
   if (i < n8) {
-    widen8(load8<T, true>(src + i * 8, 0, 1, 8), v);
+    widen8(load8<T, 8>(src + i * 8, 0, 1, 8), v);
 #pragma unroll
     for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
   }

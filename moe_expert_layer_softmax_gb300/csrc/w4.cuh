@@ -530,9 +530,9 @@ struct StagedAt {
   uint32_t table;         // entries [group][vectors of the table]
 };
 
-MOE_DEV void load_f8(const __nv_bfloat16* p, float* f) { widen8(load8<__nv_bfloat16, true>(p, 0, 1, 8), f); }
-MOE_DEV void load_f8(const __half* p, float* f) { widen8(load8<__half, true>(p, 0, 1, 8), f); }
-MOE_DEV void load_f8(const float* p, float* f) { widen8(load8<float, true>(p, 0, 1, 8), f); }
+MOE_DEV void load_f8(const __nv_bfloat16* p, float* f) { widen8(load8<__nv_bfloat16, 8>(p, 0, 1, 8), f); }
+MOE_DEV void load_f8(const __half* p, float* f) { widen8(load8<__half, 8>(p, 0, 1, 8), f); }
+MOE_DEV void load_f8(const float* p, float* f) { widen8(load8<float, 8>(p, 0, 1, 8), f); }
 
 // Stage `count` vectors of K values (K a multiple of 128); row(m) is vector m.
 // Every thread of the block calls; no barrier.
