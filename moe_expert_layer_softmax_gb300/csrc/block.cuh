@@ -49,7 +49,9 @@ template <int V> MOE_DEV int first_column(int i, int lane, int G) {
 // Column of value j of those that start at c.
 template <int V> MOE_DEV int column_of(int c, int j, int G) { return c + j / V * (V * G) + j % V; }
 
-template <typename T> struct alignas(2 * sizeof(T)) Pair { T v[2]; };
+// A pair of columns as one word (16-bit types) or two.
+template <typename T> struct PairOf { using type = uint32_t; };
+template <> struct PairOf<float> { using type = uint2; };
 
 template <typename T, int V> MOE_DEV Raw8<T> load8(const T* row, int c, int G, int d) {
   Raw8<T> r;
@@ -59,13 +61,12 @@ template <typename T, int V> MOE_DEV Raw8<T> load8(const T* row, int c, int G, i
 #pragma unroll
     for (int i = 0; i < n; ++i) q[i] = *(reinterpret_cast<const uint4*>(row + c) + i);
   } else if constexpr (V == 2) {
+    using P = typename PairOf<T>::type;
+    P* q = reinterpret_cast<P*>(&r);
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const int at = column_of<V>(c, j, G);
-      Pair<T> q = {Elem<T>::from_f(0.0f), Elem<T>::from_f(0.0f)};
-      if (at < d) q = *reinterpret_cast<const Pair<T>*>(row + at);
-      r.v[j] = q.v[0];
-      r.v[j + 1] = q.v[1];
+    for (int i = 0; i < 4; ++i) {
+      const int at = column_of<V>(c, 2 * i, G);
+      q[i] = at < d ? *reinterpret_cast<const P*>(row + at) : P{};
     }
   } else {
 #pragma unroll
@@ -80,10 +81,12 @@ template <typename T, int V> MOE_DEV void store8(T* row, int c, int G, int d, co
 #pragma unroll
     for (int i = 0; i < n; ++i) *(reinterpret_cast<uint4*>(row + c) + i) = q[i];
   } else if constexpr (V == 2) {
+    using P = typename PairOf<T>::type;
+    const P* q = reinterpret_cast<const P*>(&r);
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      const int at = column_of<V>(c, j, G);
-      if (at < d) *reinterpret_cast<Pair<T>*>(row + at) = {r.v[j], r.v[j + 1]};
+    for (int i = 0; i < 4; ++i) {
+      const int at = column_of<V>(c, 2 * i, G);
+      if (at < d) *reinterpret_cast<P*>(row + at) = q[i];
     }
   } else {
 #pragma unroll

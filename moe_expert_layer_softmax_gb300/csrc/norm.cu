@@ -53,6 +53,17 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
 #pragma unroll 1
     for (int i = 0; i < Ring::kDepth - 1; ++i) copy();
   }
+  // without a ring: the next row, on its way in registers
+  constexpr bool AHEAD = !RING && NV == 1;
+  Raw8<TX> ax = {};
+  Raw8<TR> ar = {};
+  auto fetch = [&](int64_t at) {
+    const int c = first_column<V>(0, lane, G);
+    const bool in = c < d && at < p.rows;
+    ax = load8_warp<TX, V>(static_cast<const TX*>(p.x) + at * p.ld_x, c, G, d, in);
+    if (cr) ar = load8_warp<TR, V>(static_cast<const TR*>(p.residual) + at * p.ld_residual, c, G, d, in);
+  };
+  if constexpr (AHEAD) fetch(row);
   // a warp goes on while its first group has a row
   for (int turn = 0; row - rg.before() < p.rows; row += step, turn ^= 1) {
     const bool live = NV > 1 || row < p.rows;
@@ -75,6 +86,10 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
       if constexpr (RING) {
         xr = ring.template get<TX>(i * XP);
         if (cr) rr = ring.template get<TR>(NV * XP + i * RP);
+      } else if constexpr (AHEAD) {
+        xr = ax;
+        rr = ar;
+        fetch(row + step);
       } else {
         xr = load8_warp<TX, V>(static_cast<const TX*>(p.x) + row * p.ld_x, c, G, d, in);
         if (cr) rr = load8_warp<TR, V>(static_cast<const TR*>(p.residual) + row * p.ld_residual, c, G, d, in);

@@ -22,8 +22,9 @@
 // columns and 28.5 us, bound by issue.  A row has a group of 8, 16 or any multiple
 // of 32 threads: with whole warps alone rows of 64 columns ran at 1.8 TB/s, with
 // powers of two alone 768 columns left a quarter of the lanes idle.  Rows that
-// take no vector loads are read element by element, neighbours by neighbours, one
-// group of columns a thread (two spilled: 1001 columns in fp32 4.3 and 5.6 TB/s).
+// take no vector loads are read by elements or pairs, neighbours by neighbours, one
+// group of columns a thread (two spilled: 1001 columns in fp32 4.3 and 5.6 TB/s),
+// the next row on its way in registers (6.1).
 // Sums are taken in a fixed order (no atomics).
 //
 // Measured (TB/s of HBM against a copy's 6.7; bf16 matrices, bf16 stream / fp32
@@ -31,7 +32,8 @@
 // and 16384 5.6-5.9 / 5.7; backward 5.4-6.2 / 5.7-6.4, 12288 4.2 / 3.0.  With
 // dropout the generator adds its instructions: bf16 stream 4.3-6.0, fp32 stream
 // 5.3-6.5.  8-bit output, 4096 columns: 4.95 / 6.0, with dropout 4.05 / 5.5.  Wider
-// rows than a ring holds 3.3-4.5 forward, 1.4-3.4 backward; odd widths 1.7-5.6.
+// rows than a ring holds 3.3-4.5 forward, 1.4-3.4 backward; other widths up to 4096
+// in bf16 2.1-3.0, on an fp32 stream 3.3-5.2, in fp32 4.7-6.8.
 #pragma once
 
 #include "block.cuh"

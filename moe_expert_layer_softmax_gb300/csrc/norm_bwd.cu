@@ -6,12 +6,19 @@ namespace moe {
 
 namespace {
 
+// Rows that take no vector loads: whether the next one is fetched into registers
+// (two blocks a multiprocessor then, three otherwise).  Measured with and without,
+// TB/s: 1001 columns bf16 3.0 and 2.6, on an fp32 stream 5.0 and 4.1; 1002 columns
+// on an fp32 stream 4.8 and 4.2, but bf16 throughout 2.2 and 2.95.
+template <typename TR, int V, bool RING, int NV>
+constexpr bool kNextInRegisters = !RING && NV == 1 && !(V == 2 && sizeof(TR) == 2);
+
 // Backward: the weight gradient of a block's rows stays in registers; one row of
 // partial sums a block goes to `partial` [gridDim.x, d].  Measured: 8192 x 2048
 // bf16 33.2 us (5.05 TB/s; 4 us of it the sum of the partial rows), 32768 x 4096 on
 // an fp32 stream with dropout 317 us (6.8 TB/s, a plain copy's rate).
 template <typename TX, typename TR, int V, bool RING, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_bwd_kernel(AddNormBwdParams p) {
+__global__ void __launch_bounds__(MAXT, norm_blocks(RING || kNextInRegisters<TR, V, RING, NV>, NV, MAXT)) add_norm_bwd_kernel(AddNormBwdParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float red[2][kNormMaxThreads / 32];
   // drop numbers that change hands; at the end the sums of the row groups
@@ -62,6 +69,18 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_bw
     for (int i = 0; i < Ring::kDepth - 1; ++i) copy();
   }
   float rn = row < p.rows ? p.rstd[row] : 0.0f;
+  // without a ring: the next row, on its way in registers
+  constexpr bool AHEAD = kNextInRegisters<TR, V, RING, NV>;
+  Raw8<TX> ay = {};
+  Raw8<TR> ah = {}, ad = {}, dr0 = {};
+  auto fetch = [&](int64_t at) {
+    const int c = first_column<V>(0, lane, G);
+    const bool in = c < d && at < p.rows;
+    ay = load8_warp<TX, V>(static_cast<const TX*>(p.dy) + at * p.ld_dy, c, G, d, in);
+    ah = load8_warp<TR, V>(static_cast<const TR*>(p.h) + at * p.ld_h, c, G, d, in);
+    if (cd) ad = load8_warp<TR, V>(static_cast<const TR*>(p.dres) + at * p.ld_dres, c, G, d, in);
+  };
+  if constexpr (AHEAD) fetch(row);
   // a warp goes on while its first group has a row; one without adds zeros
   for (int turn = 0; row - rg.before() < p.rows; row += step, turn ^= 1) {
     const bool live = NV > 1 || row < p.rows;
@@ -84,6 +103,11 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_bw
           yr[i] = ring.template get<TX>(i * XP);
           hr[i] = ring.template get<TR>(NV * XP + i * RP);
         }
+      } else if constexpr (AHEAD) {
+        yr[i] = ay;
+        hr[i] = ah;
+        dr0 = ad;
+        fetch(row + step);
       } else {
         yr[i] = load8_warp<TX, V>(static_cast<const TX*>(p.dy) + row * p.ld_dy, c, G, d, c < d && live);
         hr[i] = load8_warp<TR, V>(static_cast<const TR*>(p.h) + row * p.ld_h, c, G, d, c < d && live);
@@ -116,6 +140,8 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_bw
         Raw8<TR> dr = {};
         if constexpr (RING)
           dr = ring.template get<TR>(NV * (XP + RP) + i * RP);
+        else if constexpr (AHEAD)
+          dr = dr0;
         else
           dr = load8_warp<TR, V>(static_cast<const TR*>(p.dres) + row * p.ld_dres, c, G, d, in);
         widen8(dr, b);
@@ -187,7 +213,7 @@ cudaError_t bwd_run(const AddNormBwdParams* p, int threads, int* blocks, cudaStr
     return ring ? cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, MAXT * ring)
                 : cudaSuccess;
-  *blocks = row_blocks(p->rows, p->group, threads, norm_blocks(RING, NV, MAXT) * MAXT);
+  *blocks = row_blocks(p->rows, p->group, threads, norm_blocks(RING || kNextInRegisters<TR, V, RING, NV>, NV, MAXT) * MAXT);
   if (*blocks > kNormPartialRows) *blocks = kNormPartialRows;   // rows of the workspace
   return launch_pdl(kernel, dim3(*blocks), dim3(threads), (size_t)threads * ring, s, *p);
 }
