@@ -645,8 +645,8 @@ MOE_API int moe_dequantize_w4(int64_t rows, int32_t K, int32_t group, int32_t dt
 
 /* y[m, n] = sum_k x[m, k] W[n, k], fp32 sums, for a few vectors: x dtype
  * [M, K] (16-byte aligned rows), W as above with N rows, y dtype [M, N].
- * N <= 1048560, K <= 2^18.  The fastest with up to eight vectors; each sixteen
- * more are one more pass over the weights.
+ * N <= 1048560, K <= 2^18.  The fastest with up to eight vectors; more than
+ * 32 are one pass over the weights for each 32.
  * Here and in moe_experts_w4 a few vectors are held as fp16 times a power of two
  * for each 128 columns (a bf16 or fp16 value is exact down to 2^-24 of the
  * largest of them, off by less than 2^-34 of it below), and 8 times a group's sum

@@ -435,7 +435,12 @@ struct Segment {
 
   // The share's products with `nt` tiles of vectors.
   MOE_DEV void finish(const Vectors<T, NT>& v, int nt, float* parts) {
-    if (NT == 1 || nt == 1) run_share<1>(v, parts); else run_share<NT>(v, parts);
+    if (NT == 1 || nt == 1)
+      run_share<1>(v, parts);
+    else if (NT == 2 || nt == 2)
+      run_share<NT == 1 ? 1 : 2>(v, parts);
+    else
+      run_share<NT>(v, parts);
   }
   template <int M> MOE_DEV void run_share(const Vectors<T, NT>& v, float* parts) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;

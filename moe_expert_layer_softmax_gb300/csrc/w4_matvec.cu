@@ -2,8 +2,8 @@
 // W[n, k].  How the weights are streamed, and what bounds it: w4.cuh.  Measured
 // back to back from HBM: one vector and 4096 x 4096 6.0 us (8.9 MB, 1.5 TB/s;
 // about 4 us of it start and end of the kernel), 20011 x 2048 8.7, 4096 x 14336
-// 11.1 us (2.7 TB/s); eight vectors 6.7, 11.0 and 15.2 us; 64 vectors 24, 48 and
-// 80 us.
+// 11.1 us (2.7 TB/s); eight vectors 6.7, 11.0 and 15.2 us; 64 vectors 19, 41 and
+// 74 us.
 #include "w4.cuh"
 
 namespace moe {
@@ -121,7 +121,10 @@ cudaError_t matvec_launch(const MatvecArgs* a, cudaStream_t s) {
 
 // Vectors are staged (whole stages only) where each block has a tile for every
 // vector that it stages, and they leave room for the parts of eight tiles;
-// otherwise they are read where they are, sixteen a pass over the weights.
+// otherwise they are read where they are, sixteen a pass over the weights or, of
+// more than that, 32 (64 vectors, sixteen and 32 a pass: 4096 x 4096 24.3 and 19.1,
+// 20011 x 2048 48.5 and 40.8, 4096 x 14336 79.6 and 74.3 us; 17 vectors 12.0 and
+// 10.0, 21.5 and 17.9, 31.6 and 31.1).
 // Measured, staged and read (us): 4096 x 4096, two tiles a block: 6.1 and 6.4
 // with one vector, 9.5 and 6.7 with eight; 20011 x 2048, nine tiles: 8.7 and 10.0
 // with one, 11.0 and 11.2 with eight; staged rounds of sixteen 15.9 and 14.1.
@@ -133,6 +136,8 @@ cudaError_t matvec_nt(const MatvecArgs* a, cudaStream_t s) {
     const cudaError_t e = staged ? matvec_launch<T, W, 1, kStaged, FULL>(a, s) : cudaSuccess;
     if ((a != nullptr && staged) || e != cudaSuccess) return e;
   }
+  const cudaError_t e = a == nullptr || a->M > 16 ? matvec_launch<T, W, 4, kNatural, FULL>(a, s) : cudaSuccess;
+  if ((a != nullptr && a->M > 16) || e != cudaSuccess) return e;
   return matvec_launch<T, W, 2, kNatural, FULL>(a, s);
 }
 
