@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
     for (int i = 0; i < Ring::kDepth - 1; ++i) copy();
   }
   // without a ring: the next row, on its way in registers
-  constexpr bool AHEAD = !RING && NV == 1;
+  constexpr bool AHEAD = !RING && NV == 1 && MAXT < kNormMaxThreads;
   Raw8<TX> ax = {};
   Raw8<TR> ar = {};
   auto fetch = [&](int64_t at) {
@@ -268,11 +268,11 @@ cudaError_t fwd_types(const AddNormParams* p, cudaStream_t s) {
                              : fwd_run<TX, TR, MX, 8, true, 4, 512>(&q, q.group, s);
     }
   } else {
-    const RowSplit split(p->d, 1, 2, 512);
+    const RowSplit split(p->d, 1, 1, kNormMaxThreads);
     q.group = split.group;
     if (split.group) {
       const int threads = split.threads();
-      if (split.nv == 2) return fwd_run<TX, TR, MX, V, false, 2, 512>(&q, threads, s);
+      if (split.group > 512) return fwd_run<TX, TR, MX, V, false, 1, kNormMaxThreads>(&q, threads, s);
       return split.group <= kNormThreads ? fwd_run<TX, TR, MX, V, false, 1, kNormThreads>(&q, threads, s)
                                          : fwd_run<TX, TR, MX, V, false, 1, 512>(&q, threads, s);
     }

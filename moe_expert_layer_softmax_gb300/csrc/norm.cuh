@@ -33,7 +33,9 @@
 // dropout the generator adds its instructions: bf16 stream 4.3-6.0, fp32 stream
 // 5.3-6.5.  8-bit output, 4096 columns: 4.95 / 6.0, with dropout 4.05 / 5.5.  Wider
 // rows than a ring holds 3.3-4.5 forward, 1.4-3.4 backward; other widths up to 4096
-// in bf16 2.1-3.0, on an fp32 stream 3.3-5.2, in fp32 4.7-6.8.
+// in bf16 2.1-3.2, on an fp32 stream 3.3-5.2, in fp32 4.7-6.8, up to 8192 1.7-3.0,
+// 2.6-4.3 and 3.2-5.8 (with 1024 threads; 512 with twice the columns spilled: 4999
+// columns in fp32 3.2 and 4.1 forward, 2.3 and 3.2 backward).
 #pragma once
 
 #include "block.cuh"

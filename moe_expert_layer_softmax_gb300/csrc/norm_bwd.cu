@@ -10,15 +10,15 @@ namespace {
 // (two blocks a multiprocessor then, three otherwise).  Measured with and without,
 // TB/s: 1001 columns bf16 3.0 and 2.6, on an fp32 stream 5.0 and 4.1; 1002 columns
 // on an fp32 stream 4.8 and 4.2, but bf16 throughout 2.2 and 2.95.
-template <typename TR, int V, bool RING, int NV>
-constexpr bool kNextInRegisters = !RING && NV == 1 && !(V == 2 && sizeof(TR) == 2);
+template <typename TR, int V, bool RING, int NV, int MAXT>
+constexpr bool kNextInRegisters = !RING && NV == 1 && MAXT < kNormMaxThreads && !(V == 2 && sizeof(TR) == 2);
 
 // Backward: the weight gradient of a block's rows stays in registers; one row of
 // partial sums a block goes to `partial` [gridDim.x, d].  Measured: 8192 x 2048
 // bf16 33.2 us (5.05 TB/s; 4 us of it the sum of the partial rows), 32768 x 4096 on
 // an fp32 stream with dropout 317 us (6.8 TB/s, a plain copy's rate).
 template <typename TX, typename TR, int V, bool RING, int NV, int MAXT>
-__global__ void __launch_bounds__(MAXT, norm_blocks(RING || kNextInRegisters<TR, V, RING, NV>, NV, MAXT)) add_norm_bwd_kernel(AddNormBwdParams p) {
+__global__ void __launch_bounds__(MAXT, norm_blocks(RING || kNextInRegisters<TR, V, RING, NV, MAXT>, NV, MAXT)) add_norm_bwd_kernel(AddNormBwdParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float red[2][kNormMaxThreads / 32];
   // drop numbers that change hands; at the end the sums of the row groups
@@ -70,7 +70,7 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING || kNextInRegisters<TR,
   }
   float rn = row < p.rows ? p.rstd[row] : 0.0f;
   // without a ring: the next row, on its way in registers
-  constexpr bool AHEAD = kNextInRegisters<TR, V, RING, NV>;
+  constexpr bool AHEAD = kNextInRegisters<TR, V, RING, NV, MAXT>;
   Raw8<TX> ay = {};
   Raw8<TR> ah = {}, ad = {}, dr0 = {};
   auto fetch = [&](int64_t at) {
@@ -213,7 +213,7 @@ cudaError_t bwd_run(const AddNormBwdParams* p, int threads, int* blocks, cudaStr
     return ring ? cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, MAXT * ring)
                 : cudaSuccess;
-  *blocks = row_blocks(p->rows, p->group, threads, norm_blocks(RING || kNextInRegisters<TR, V, RING, NV>, NV, MAXT) * MAXT);
+  *blocks = row_blocks(p->rows, p->group, threads, norm_blocks(RING || kNextInRegisters<TR, V, RING, NV, MAXT>, NV, MAXT) * MAXT);
   if (*blocks > kNormPartialRows) *blocks = kNormPartialRows;   // rows of the workspace
   return launch_pdl(kernel, dim3(*blocks), dim3(threads), (size_t)threads * ring, s, *p);
 }
@@ -237,7 +237,7 @@ cudaError_t bwd_types(const AddNormBwdParams* p, int* blocks, cudaStream_t s) {
     return e;
   }
   AddNormBwdParams q = *p;
-  RowSplit split(p->d, V == 8 ? 2 : 1, wide ? 4 : 2, 512);
+  RowSplit split = V == 8 ? RowSplit(p->d, 2, wide ? 4 : 2, 512) : RowSplit(p->d, 1, 1, kNormMaxThreads);
   q.group = split.group;
   if (split.group) {
     const int threads = split.threads();
@@ -248,12 +248,13 @@ cudaError_t bwd_types(const AddNormBwdParams* p, int* blocks, cudaStream_t s) {
     if constexpr (V == 8) {
       if (split.nv == 2 && split.group <= kNormThreads)
         return bwd_run<TX, TR, V, true, 2, kNormThreads>(&q, threads, blocks, s);
+      return split.nv == 1 ? bwd_run<TX, TR, V, true, 1, kNormThreads>(&q, threads, blocks, s)
+                           : bwd_run<TX, TR, V, true, 2, 512>(&q, threads, blocks, s);
     } else {
-      if (split.nv == 1 && split.group > kNormThreads)
-        return bwd_run<TX, TR, V, false, 1, 512>(&q, threads, blocks, s);
+      if (split.group > 512) return bwd_run<TX, TR, V, false, 1, kNormMaxThreads>(&q, threads, blocks, s);
+      return split.group <= kNormThreads ? bwd_run<TX, TR, V, false, 1, kNormThreads>(&q, threads, blocks, s)
+                                         : bwd_run<TX, TR, V, false, 1, 512>(&q, threads, blocks, s);
     }
-    return split.nv == 1 ? bwd_run<TX, TR, V, V == 8, 1, kNormThreads>(&q, threads, blocks, s)
-                         : bwd_run<TX, TR, V, V == 8, 2, 512>(&q, threads, blocks, s);
   }
   split = RowSplit(p->d, wide ? 3 : 2, 4, kNormMaxThreads);
   q.group = split.group;
