@@ -230,8 +230,9 @@ cudaError_t fwd_run(const AddNormParams* p, int threads, cudaStream_t s) {
 // Rows up to 8192 columns come through the ring of 256 threads, up to 16384 (but
 // where both matrices are fp32) of 512; wider ones are read as they are needed.
 // A thread holds two groups of eight columns, more where the threads need it (rows
-// without vector loads: one), for the 8-bit output three or four.  Measured at 32768 x 4096 (8-bit, dropout) 243
-// us with four, 266 with two; at 8192 x 2048 (bf16) 26 and 24.
+// without vector loads: one), for the 8-bit output three or four.  Measured at 32768
+// x 4096 (8-bit, dropout) 243 us with four, 266 with two; at 8192 x 2048 (bf16) 26
+// with four, 24 with two.
 template <typename TX, typename TR, bool MX, int V>
 cudaError_t fwd_types(const AddNormParams* p, cudaStream_t s) {
   constexpr bool wide = V == 8 && RowRing<8 * (sizeof(TX) + sizeof(TR)), 4>::kFits512;
