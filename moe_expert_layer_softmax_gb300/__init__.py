@@ -40,7 +40,7 @@ DEVERR_BOUNDS = 0x4
 
 _ERRORS = {-1: "MOE_ERR_INVALID", -2: "MOE_ERR_UNSUPPORTED", -3: "MOE_ERR_ALIGN",
            -4: "MOE_ERR_CUDA", -5: "MOE_ERR_NOT_INIT", -6: "MOE_ERR_SCRATCH_LIMIT"}
-ERR_SCRATCH_LIMIT = -6
+ERR_NOT_INIT, ERR_SCRATCH_LIMIT = -5, -6
 
 # every symbol the C header declares
 EXPORTS = (
@@ -404,7 +404,8 @@ def layer_bwd(s, bwd: BwdArgs, saved: Saved, ws, stream=None):
 # ------------------------------------------------------------------ around the layer
 # The operators before and after the layer in a block (include/moe.h, "around the
 # layer").  These wrappers check what the C entry points cannot see: types, shapes,
-# devices and strides of the tensors.
+# devices and strides of the tensors.  The first call on a device sets it up
+# (init()), unless its stream is being captured: then it raises MOE_ERR_NOT_INIT.
 DT_BF16, DT_F16, DT_F32 = 0, 1, 2
 W4_MAX_ROUTES = 4096
 _ADD_NORM = struct.Struct("@qiiii" + "Pq" * 2 + "P" + "Pq" * 2 + "PPPP" + "QQff")
@@ -425,6 +426,26 @@ def _dtype(t, what):
         _dtypes.update({torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32})
         return _dtype(t, what)
     raise TypeError(f"{what}: {t.dtype} is not bf16, fp16 or fp32")
+
+
+def _capturing(handle):
+    """Whether the current stream or the one of this handle is being captured."""
+    import torch
+    if torch.cuda.is_current_stream_capturing():
+        return True
+    if not handle:   # the legacy default stream takes no part in a capture
+        return False
+    with torch.cuda.stream(torch.cuda.ExternalStream(handle)):
+        return torch.cuda.is_current_stream_capturing()
+
+
+def _failed(fn, rc, *args):
+    """What follows a call that returned `rc`, not MOE_OK, for `args` (the stream
+    last): on a device that has not been set up, set it up and call again."""
+    if rc == ERR_NOT_INIT and not _capturing(args[-1]):
+        init()
+        rc = getattr(load(), fn)(*args)
+    _check(fn, rc)
 
 
 def _shape(x):
@@ -487,9 +508,10 @@ def add_norm(x, weight, y, residual=None, h=None, rstd=None, eps=1e-5, p=0.0, se
         rows, d, dt, dt if like is None else _dtype(like, "residual"), _dtype(weight, "weight"),
         px, ld_x, pr, ld_r, _flat(weight, "weight", d, weight.dtype), ph, ld_h, py, ld_y,
         _flat(rstd, "rstd", rows, _torch.float32), pq, ps, pd, seed, offset, eps, p)
-    rc = load().moe_add_norm(args, _stream(stream))
+    st = _stream(stream)
+    rc = load().moe_add_norm(args, st)
     if rc:
-        raise MoEError("moe_add_norm", rc)
+        _failed("moe_add_norm", rc, args, st)
 
 
 def add_norm_bwd_workspace(rows, d) -> int:
@@ -518,9 +540,10 @@ def add_norm_bwd(dy, h, rstd, weight, dres=None, dh=None, dx=None, dw=None, ws=N
         rows, d, dt, _dtype(h, "h"), _dtype(weight, "weight"), pdy, ld_dy, ph, ld_h, pdr, ld_dr,
         _flat(rstd, "rstd", rows, _torch.float32), _flat(weight, "weight", d, weight.dtype),
         pdh, ld_dh, pdx, ld_dx, _flat(dw, "dw", d, _torch.float32), seed, offset, p)
-    rc = load().moe_add_norm_bwd(args, pws, _stream(stream))
+    st = _stream(stream)
+    rc = load().moe_add_norm_bwd(args, pws, st)
     if rc:
-        raise MoEError("moe_add_norm_bwd", rc)
+        _failed("moe_add_norm_bwd", rc, args, pws, st)
 
 
 def dropout(x, y, p, seed, offset=0, stream=None):
@@ -530,9 +553,10 @@ def dropout(x, y, p, seed, offset=0, stream=None):
     rows, d = _shape(x)
     px, ld_x = _matrix(x, "x", rows, d, x.dtype)
     py, ld_y = _matrix(y, "y", rows, d, x.dtype)
-    rc = load().moe_dropout(rows, d, dt, px, ld_x, py, ld_y, p, seed, offset, _stream(stream))
+    args = (rows, d, dt, px, ld_x, py, ld_y, p, seed, offset, _stream(stream))
+    rc = load().moe_dropout(*args)
     if rc:
-        raise MoEError("moe_dropout", rc)
+        _failed("moe_dropout", rc, *args)
 
 
 def _w4(q, scales, what):
@@ -554,16 +578,20 @@ def quantize_w4(src, q, scales, stream=None):
     [..., K/G] of the same type."""
     rows, K, g = _w4(q, scales, "quantize_w4")
     ps = _flat(src, "src", rows * K, scales.dtype)
-    _check("moe_quantize_w4", load().moe_quantize_w4(rows, K, g, _dtype(src, "src"), ps, q.data_ptr(),
-                                                     scales.data_ptr(), _stream(stream)))
+    args = (rows, K, g, _dtype(src, "src"), ps, q.data_ptr(), scales.data_ptr(), _stream(stream))
+    rc = load().moe_quantize_w4(*args)
+    if rc:
+        _failed("moe_quantize_w4", rc, *args)
 
 
 def dequantize_w4(q, scales, out, stream=None):
     """moe_dequantize_w4: the weights that codes and scales stand for, fp32."""
     rows, K, g = _w4(q, scales, "dequantize_w4")
     po = _flat(out, "out", rows * K, _torch.float32)
-    _check("moe_dequantize_w4", load().moe_dequantize_w4(
-        rows, K, g, _dtype(scales, "scales"), q.data_ptr(), scales.data_ptr(), po, _stream(stream)))
+    args = (rows, K, g, _dtype(scales, "scales"), q.data_ptr(), scales.data_ptr(), po, _stream(stream))
+    rc = load().moe_dequantize_w4(*args)
+    if rc:
+        _failed("moe_dequantize_w4", rc, *args)
 
 
 def matvec_w4(x, q, scales, y, stream=None):
@@ -573,10 +601,10 @@ def matvec_w4(x, q, scales, y, stream=None):
     M = x.numel() // K if K else 0
     px, ld_x = _matrix(x, "x", M, K, dt)
     py, ld_y = _matrix(y, "y", M, N, dt)
-    rc = load().moe_matvec_w4(M, N, K, g, _dtypes[dt], px, ld_x, q.data_ptr(), scales.data_ptr(),
-                              py, ld_y, _stream(stream))
+    args = (M, N, K, g, _dtypes[dt], px, ld_x, q.data_ptr(), scales.data_ptr(), py, ld_y, _stream(stream))
+    rc = load().moe_matvec_w4(*args)
     if rc:
-        raise MoEError("moe_matvec_w4", rc)
+        _failed("moe_matvec_w4", rc, *args)
 
 
 def experts_w4_workspace(T, d, E, k, f) -> int:
@@ -609,9 +637,10 @@ def experts_w4(x, topk_idx, gates, w: dict, out, ws, stream=None):
         gq.data_ptr(), gs.data_ptr(), uq.data_ptr(), us.data_ptr(), dq.data_ptr(), ds.data_ptr(),
         _flat(out, "out", T * d, dt))
     pws = _flat(ws, "ws", experts_w4_workspace(T, d, E, k, f), _torch.uint8, True)
-    rc = load().moe_experts_w4(args, pws, _stream(stream))
+    st = _stream(stream)
+    rc = load().moe_experts_w4(args, pws, st)
     if rc:
-        raise MoEError("moe_experts_w4", rc)
+        _failed("moe_experts_w4", rc, args, pws, st)
 
 
 # ------------------------------------------------------------------ buffers
