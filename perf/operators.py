@@ -230,22 +230,10 @@ def plain(st):
     return {"out": (a @ w4_values(n["down_q"], n["down_s"]).transpose(1, 2)).sum(0).to(st["x"].dtype)}
 
 
-moe = None
-
-
-def library():
-    """The library, initialised on this device once, as a program does at its start."""
-    global moe
-    import moe_expert_layer_softmax_gb300
-    moe = moe_expert_layer_softmax_gb300
-    moe.init()
-
-
 def run(st):
     if not own:
         return plain(st)
-    if moe is None:
-        library()
+    import moe_expert_layer_softmax_gb300 as moe
     op = st["op"]
     if op == "dropout":
         moe.dropout(st["x"], st["y"], st["p"], st["seed"], st["offset"])
