@@ -347,8 +347,10 @@ struct Segment {
       const uint32_t p = get + ((byte & 112) ^ swz) + (byte & 15) + at.slot;
       const Words<W> wa = load_words<W>(p), wb = load_words<W>(p + 1024);
       if constexpr (XS == kStaged) {
-        // low parts of a single tile sum on their own: two chains of products
-        constexpr bool own = LOW && M == 1;
+        // low parts of a single tile sum on their own: two chains of products.
+        // Not where a round may serve more than one tile: a vector's sum must not
+        // depend on the round that it falls into (M is the round's).
+        constexpr bool own = LOW && NT == 1;
         float c[M][4], cl[4];
 #pragma unroll
         for (int i = 0; i < W; ++i) {

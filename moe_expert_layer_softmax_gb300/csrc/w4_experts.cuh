@@ -109,7 +109,9 @@ MOE_DEV void find_routes(const Lists& l, int R, int e, const float* gates) {
   __syncthreads();
   for (int r = threadIdx.x; r < R; r += kW4Threads)
     if (l.expert_of[r] == e) {
-      const int at = atomicAdd(count, 1);   // the order changes no result
+      // the order, and so the round and the column of a route, changes no result:
+      // a column's products are the same instructions whatever lies beside it
+      const int at = atomicAdd(count, 1);
       l.routes[at] = (uint16_t)r;
       if (gates) l.gates[at] = gates[r];
     }
