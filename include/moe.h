@@ -636,7 +636,9 @@ MOE_API int moe_dropout(int64_t rows, int32_t cols, int32_t dtype, const void* x
  *   scales  dtype [rows, K/G] (bf16 or fp16, the activations' type)
  * moe_quantize_w4: scale = max |w| / 7 of the group, rounded to dtype; code =
  * w / scale rounded to nearest even, clamped to [-8, 7], plus 8 (an all-zero
- * group: scale 0, codes 8).  Batches of matrices are more rows.
+ * group: scale 0, codes 8).  A NaN or an infinity among a group's weights makes
+ * its scale a NaN (codes 8): the group and what is multiplied with it are NaN.
+ * Batches of matrices are more rows.
  * moe_dequantize_w4 writes fp32 [rows, K] (exact). */
 MOE_API int moe_quantize_w4(int64_t rows, int32_t K, int32_t group, int32_t dtype, const void* src,
                             uint8_t* q, void* scales, void* stream);

@@ -10,7 +10,10 @@ namespace {
 
 // ------------------------------------------------------------------ quantiser
 // A thread takes eight columns, G / 8 lanes a group: scale = max|w| / 7 rounded
-// to the weights' type, code = w / scale rounded to nearest even, plus 8.
+// to the weights' type, code = w / scale rounded to nearest even, plus 8.  The
+// maximum is that of the bits of |w|, which order as the values do, infinity above
+// all numbers and NaN above infinity: a group with either gets a NaN for its scale
+// (no scale stands for it, and a number would hide it).
 template <typename T>
 __global__ void __launch_bounds__(256) quantize_w4_kernel(int64_t n8, int group,
                                                           const T* __restrict__ src,
@@ -20,22 +23,25 @@ __global__ void __launch_bounds__(256) quantize_w4_kernel(int64_t n8, int group,
   const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int lanes = group / 8;
   float v[8];
-  float amax = 0.0f;
+  uint32_t two = 0;   // the maxima of even and odd columns
   if (i < n8) {
-    widen8(load8<T, 8>(src + i * 8, 0, 1, 8), v);
+    const Raw8<T> r = load8<T, 8>(src + i * 8, 0, 1, 8);
+    const uint32_t* pair = reinterpret_cast<const uint32_t*>(&r);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(v[j]));
+    for (int j = 0; j < 4; ++j) two = __vmaxu2(two, pair[j] & 0x7FFF7FFFu);
+    widen8(r, v);
   }
-  for (int off = 1; off < lanes; off <<= 1)
-    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+  for (int off = 1; off < lanes; off <<= 1) two = __vmaxu2(two, __shfl_xor_sync(0xffffffffu, two, off));
   if (i >= n8) return;
-  const T st = Elem<T>::from_f(amax / 7.0f);
+  const uint16_t top = (uint16_t)max(two & 0xFFFFu, two >> 16);
+  const float amax = Elem<T>::to_f(*reinterpret_cast<const T*>(&top));
+  const T st = Elem<T>::from_f((amax < INFINITY ? amax : NAN) / 7.0f);
   const float s = Elem<T>::to_f(st);
   uint32_t w = 0;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
-    const float z = s > 0.0f ? rintf(v[j] / s) : 0.0f;
-    w |= (uint32_t)((int)fminf(fmaxf(z, -8.0f), 7.0f) + 8) << (4 * j);
+    const int z = s > 0.0f ? __float2int_rn(v[j] / s) : 0;   // scale zero or NaN: code 8
+    w |= (uint32_t)(min(max(z, -8), 7) + 8) << (4 * j);
   }
   q[i] = w;
   if (i % lanes == 0) scales[i / lanes] = st;
