@@ -206,11 +206,22 @@ struct RowSplit {
   int threads() const { return group > kNormThreads ? group : kNormThreads / group * group; }
 };
 
+// Blocks of `threads` that stay on a multiprocessor: what the registers are for
+// (`blocks` of `maxt` threads) and, with a ring of `ring` bytes a thread, what the
+// shared memory has room for (four groups of columns of two fp32 matrices: a ring of
+// up to 128 KB, one block and not two).
+constexpr int kSmShared = 228 * 1024;
+constexpr int kBlockShared = 1024 + 512;   // beside the ring: what the system keeps, and the static arrays
+constexpr int norm_resident(int blocks, int maxt, int threads, int ring) {
+  const int by_threads = blocks * maxt / threads, by_shared = kSmShared / (threads * ring + kBlockShared);
+  return ring && by_shared < by_threads ? by_shared : by_threads;
+}
+
 // Blocks: enough row groups for every row, or as many as stay on the device,
-// `resident` threads on a multiprocessor.
+// `resident` on a multiprocessor.
 inline int row_blocks(int64_t rows, int group, int threads, int resident) {
   const int per = threads / group;
-  const int64_t need = (rows + per - 1) / per, most = (int64_t)device_info()->sm_count * (resident / threads);
+  const int64_t need = (rows + per - 1) / per, most = (int64_t)device_info()->sm_count * resident;
   return (int)(need < most ? need : most);
 }
 

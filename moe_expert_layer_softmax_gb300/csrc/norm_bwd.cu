@@ -213,7 +213,8 @@ cudaError_t bwd_run(const AddNormBwdParams* p, int threads, int* blocks, cudaStr
     return ring ? cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
                                        cudaFuncAttributeMaxDynamicSharedMemorySize, MAXT * ring)
                 : cudaSuccess;
-  *blocks = row_blocks(p->rows, p->group, threads, norm_blocks(RING || kNextInRegisters<TR, V, RING, NV, MAXT>, NV, MAXT) * MAXT);
+  constexpr int most = norm_blocks(RING || kNextInRegisters<TR, V, RING, NV, MAXT>, NV, MAXT);
+  *blocks = row_blocks(p->rows, p->group, threads, norm_resident(most, MAXT, threads, ring));
   if (*blocks > kNormPartialRows) *blocks = kNormPartialRows;   // rows of the workspace
   return launch_pdl(kernel, dim3(*blocks), dim3(threads), (size_t)threads * ring, s, *p);
 }
