@@ -413,16 +413,17 @@ _ADD_NORM_BWD = struct.Struct("@qiiii" + "Pq" * 3 + "PP" + "Pq" * 2 + "P" + "QQf
 _EXPERTS_W4 = struct.Struct("@7i" + "P" * 10)
 _torch = None
 _dtypes = {}
+_several = False   # more than one device: tensors may lie on another than the current one
 
 
 def _dtype(t, what):
     dt = _dtypes.get(t.dtype)
     if dt is not None:
         return dt
-    global _torch
+    global _torch, _several
     if _torch is None:
         import torch
-        _torch = torch
+        _torch, _several = torch, torch.cuda.device_count() > 1
         _dtypes.update({torch.bfloat16: DT_BF16, torch.float16: DT_F16, torch.float32: DT_F32})
         return _dtype(t, what)
     raise TypeError(f"{what}: {t.dtype} is not bf16, fp16 or fp32")
@@ -454,6 +455,12 @@ def _shape(x):
     return (x.numel() // d if d else 0), d
 
 
+def _elsewhere(t):
+    """Whether a CUDA tensor lies on another device than the current one, whose stream
+    and kernels a call takes."""
+    return t.get_device() != _torch.cuda.current_device()
+
+
 def _matrix(t, what, rows, cols, dtype):
     """(address, row stride) of a matrix on the device, its last axis contiguous;
     axes before the last one are rows (more than one of them: contiguous)."""
@@ -461,6 +468,8 @@ def _matrix(t, what, rows, cols, dtype):
         return 0, 0
     if not t.is_cuda:
         raise ValueError(f"{what}: not a CUDA tensor")
+    if _several and _elsewhere(t):
+        raise ValueError(f"{what}: on {t.device}, not on the current device")
     if t.dtype is not dtype:
         raise TypeError(f"{what}: {t.dtype}, expected {dtype}")
     if t.numel() != rows * cols or t.size(-1) != cols:
@@ -478,6 +487,8 @@ def _flat(t, what, numel, dtype, at_least=False):
         return 0
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{what}: not a contiguous CUDA tensor")
+    if _several and _elsewhere(t):
+        raise ValueError(f"{what}: on {t.device}, not on the current device")
     if t.dtype is not dtype:
         raise TypeError(f"{what}: {t.dtype}, expected {dtype}")
     if t.numel() != numel and not (at_least and t.numel() > numel):
@@ -570,6 +581,8 @@ def _w4(q, scales, what):
         raise ValueError(f"{what}: codes {tuple(q.shape)} and scales {tuple(scales.shape)} do not belong together")
     if not (q.is_cuda and scales.is_cuda and q.is_contiguous() and scales.is_contiguous()):
         raise ValueError(f"{what}: not contiguous CUDA tensors")
+    if _several and (_elsewhere(q) or _elsewhere(scales)):
+        raise ValueError(f"{what}: codes on {q.device}, scales on {scales.device}, not on the current device")
     return rows, K, K // ng
 
 
