@@ -650,13 +650,12 @@ MOE_API int moe_dequantize_w4(int64_t rows, int32_t K, int32_t group, int32_t dt
  * N <= 1048560, K <= 2^18.  The fastest with up to eight vectors; more than
  * 32 are one pass over the weights for each 32.
  * Here and in moe_experts_w4 a few vectors are held as fp16 times a power of two
- * for each 128 columns (a bf16 or fp16 value is exact down to 2^-24 of the
- * largest of them, off by less than 2^-34 of it below), and 8 times a group's sum
- * comes off the products with its codes: errors of about 2^-20 of the group's
- * largest |x| times its scale, far below a rounding of y, but not zero where the
- * weights are.  A vector with a value of 2^118 or more, an infinity or a NaN gives
- * results that are not finite (in its own rows alone).  The same call gives the
- * same bits; another M may round differently. */
+ * for each 128 columns: a bf16 or fp16 value is exact down to 2^-27 of the
+ * largest of them, off by at most 2^-38 of it below.  Products with code - 8 are
+ * exact, and a group's are summed before its scale is applied: where 8 times the
+ * group's |x| add up to more than fp32 holds, or x has an infinity or a NaN,
+ * results may not be finite (in that vector's own row alone).  The same call gives
+ * the same bits; another M may round differently. */
 MOE_API int moe_matvec_w4(int32_t M, int32_t N, int32_t K, int32_t group, int32_t dtype,
                           const void* x, int64_t ld_x, const uint8_t* q, const void* scales,
                           void* y, int64_t ld_y, void* stream);

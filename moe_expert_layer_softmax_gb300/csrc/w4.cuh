@@ -9,12 +9,13 @@
 // used for a handful of vectors.  The products run on mma.sync m16n8k16 with 16
 // weight rows as A and eight vectors as B: each lane turns its own 4-bit words
 // into operands, and eight vectors do not fill a larger matrix instruction.
-// What bounds it in fact is issue: about 145 instructions for each 128 columns of
-// 16 rows (200 with two-part vectors), 40 of them the conversion of the codes, at
-// 49-57% of the issue slots; the rest waits on instructions before it (fixed
-// latencies first, then shared memory, whose path is at 45-57%).  Weights that
-// already lie in L2 take the same time.  64 experts (2048 x 1408, 64 tokens) stream
-// 3.5 TB/s, eight tokens on experts of 4096 x 2048 4.6 TB/s.  Tried without gain:
+// What bounds it in fact is issue: about 185 instructions for each 128 columns of
+// 16 rows (220 with two-part vectors), 72 of them the conversion of the codes, at
+// 47-65% of the issue slots; the rest waits on instructions before it (fixed
+// latencies first, then the 16-bit arithmetic of the conversion, then shared memory,
+// whose path is at 38-48%).  Weights that already lie in L2 take the same time.  64
+// experts (2048 x 1408, 64 tokens) stream 3.3 TB/s, eight tokens on experts of 4096 x
+// 2048 4.4 TB/s.  Tried without gain, with a shorter conversion (stage_vectors):
 // weights fetched by TMA tiles (one lane, 128-byte boxes: 88.8 against 87.8 us) or
 // by one bulk copy a row (104 us), and two chains of matrix instructions for one
 // (87.2 against 85.2 us).
@@ -26,9 +27,9 @@
 // One block of 16 warps runs on each SM and takes an equal share of the tiles;
 // its warps split the share's (tile, step) pairs evenly, whatever the number
 // of tiles, and add up a tile's parts in shared memory in a fixed order.  (64
-// experts as above, 64 tokens, and one token on eight of 4096 x 2048: 16 warps
-// with three steps in flight 87.8 and 32.9 us, 12 with three 90.6 and 32.4, 12
-// with four 88.0 and 31.9, 24 and more spill.)
+// experts as above, 64 tokens, and one token on eight of 4096 x 2048, with the
+// shorter conversion: 16 warps with rings of three steps 87.8 and 32.9 us, 12 with
+// three 90.6 and 32.4, 12 with four 88.0 and 31.9, 24 and more spill.)
 #pragma once
 
 #include "block.cuh"
@@ -70,6 +71,8 @@ template <> struct MmaT<__nv_bfloat16> {
   }
 };
 template <> struct MmaT<__half> {
+  // (Y. J. Kim, R. Henry, R. Fahim, H. H. Awadalla, "Who Says Elephants Can't Run:
+  // Bringing Large Scale MoE Models into Cloud Scale Production", SustaiNLP 2022.)
   // 1024 (0x6400) holds a nibble in bits 0-3 as 1024 + code, in bits 4-7 as
   // 1024 + 16 code: one shift serves four pairs
   static MOE_DEV void widen(uint32_t w, uint32_t* a) {
@@ -95,20 +98,6 @@ template <> struct MmaT<__half> {
   }
 };
 
-// Staged vectors take the codes themselves as fp16 subnormals: a nibble in bits
-// 0-3 is code 2^-24, in bits 4-7 code 2^-20 (the vector's columns 1 3 5 7 are
-// divided by 16 for that).  No subtraction: the group's sum of the vector, times
-// 8, comes off the fp32 result.  One shift and four ands for eight weights,
-// against three, four and four for the exact bf16 operands: with one token the
-// products of the first expert matrices took 197 instructions a stage that way.
-MOE_DEV void codes_fp16(uint32_t w, uint32_t* a) {
-  const uint32_t u = w >> 8;
-  a[0] = w & 0x000F000Fu;
-  a[1] = w & 0x00F000F0u;
-  a[2] = u & 0x000F000Fu;
-  a[3] = u & 0x00F000F0u;
-}
-
 // The warp's number, known to be the same in all its lanes: what follows from it
 // (shares, counters, slots) then stays in uniform registers.
 MOE_DEV int warp_id() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
@@ -118,7 +107,7 @@ MOE_DEV int warp_id() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5),
 // KB of codes and the scales), a step two stages; the lanes copy a step in
 // 16-byte pieces with cp.async into the warp's own ring, kRing - 1 steps ahead,
 // past L1.  Only the warp itself waits for its ring, so no barrier of the block
-// lies in the loop, and six stages a warp stay in flight without registers.  The
+// lies in the loop, and four stages a warp stay in flight without registers.  The
 // two stages of a step are independent chains of matrix instructions.
 constexpr int kRing = 3;
 constexpr int kStepBytes = 2048 + 256;   // 16 rows of 128 bytes of codes, 16 of 16 bytes for scales
@@ -136,7 +125,7 @@ MOE_DEV int piece_swizzle(int g) { return (g & 1) << 2 | ((g >> 1) & 1) << 1 | (
 
 // Where a lane finds its vectors.
 //   kStaged   in shared memory, as fp16 with a power of two per 128 columns
-//             (below); the products run in fp16 whatever the vectors' type
+//             (below); the products take fp16 whatever the vectors' type
 //   kOrdered  in global memory, in fragment order (bf16, a high and a low part)
 //   kNatural  in global memory, column by column
 // Fragment order of a stage's 128 values: sixteen pieces of eight; the piece of
@@ -160,7 +149,7 @@ template <typename T, int NT> struct Vectors {
   int64_t low;           // kOrdered: distance of the low parts
   uint32_t s, s_low;     // kStaged: the first tile's vector and its low parts
   uint32_t to[NT];       // kStaged: bytes from it to each tile's
-  uint32_t table;        // kStaged: (factor, 8 sum) of this lane's two columns
+  uint32_t table;        // kStaged: the factors of this lane's two columns
 };
 
 template <int W> struct Words { uint32_t w[W]; };
@@ -340,6 +329,7 @@ struct Segment {
     float fa[kScales], fb[kScales];
     load_scales(h, at, fa, fb);
     const float zero[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float sum[M][4];   // kStaged: of the stage, in the units of its vectors
 #pragma unroll
     for (int j = 0; j < kScales; ++j) {
       if (!FULL && (at.stage + h) * kScales + j >= groups) break;
@@ -355,8 +345,8 @@ struct Segment {
 #pragma unroll
         for (int i = 0; i < W; ++i) {
           uint32_t a[4], b[4];
-          codes_fp16(wa.w[i], a);
-          codes_fp16(wb.w[i], b);
+          MmaT<__half>::widen(wa.w[i], a);
+          MmaT<__half>::widen(wb.w[i], b);
           const int to = h * 256 + (j * W + i) * 64;
 #pragma unroll
           for (int m = 0; m < M; ++m) {
@@ -377,19 +367,10 @@ struct Segment {
         }
 #pragma unroll
         for (int m = 0; m < M; ++m) {
-          float f0, s0, f1, s1;   // factor and 8 times the group's sum, of two columns
-          const uint32_t entry = at.table + (h * kScales + j) * (VC * 8) + m * 64;
-          if constexpr (VC > 1) {
-            asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(f0), "=f"(s0), "=f"(f1), "=f"(s1) : "r"(entry));
-          } else {
-            asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f0), "=f"(s0) : "r"(entry));
-            f1 = f0;
-            s1 = s0;
-          }
-          acc[m][0] = fmaf(fa[j], fmaf(c[m][0], f0, -s0), acc[m][0]);
-          acc[m][1] = fmaf(fa[j], fmaf(c[m][1], f1, -s1), acc[m][1]);
-          acc[m][2] = fmaf(fb[j], fmaf(c[m][2], f0, -s0), acc[m][2]);
-          acc[m][3] = fmaf(fb[j], fmaf(c[m][3], f1, -s1), acc[m][3]);
+          sum[m][0] = j ? fmaf(fa[j], c[m][0], sum[m][0]) : fa[j] * c[m][0];
+          sum[m][1] = j ? fmaf(fa[j], c[m][1], sum[m][1]) : fa[j] * c[m][1];
+          sum[m][2] = j ? fmaf(fb[j], c[m][2], sum[m][2]) : fb[j] * c[m][2];
+          sum[m][3] = j ? fmaf(fb[j], c[m][3], sum[m][3]) : fb[j] * c[m][3];
         }
       } else {
         float c[M][4];
@@ -419,6 +400,23 @@ struct Segment {
           acc[m][2] = fmaf(fb[j], c[m][2], acc[m][2]);
           acc[m][3] = fmaf(fb[j], c[m][3], acc[m][3]);
         }
+      }
+    }
+    if constexpr (XS == kStaged) {
+#pragma unroll
+      for (int m = 0; m < M; ++m) {
+        float f0, f1;   // factors of two columns
+        const uint32_t entry = at.table + h * (VC * 4) + m * 32;
+        if constexpr (VC > 1) {
+          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(f0), "=f"(f1) : "r"(entry));
+        } else {
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f0) : "r"(entry));
+          f1 = f0;
+        }
+        acc[m][0] = fmaf(sum[m][0], f0, acc[m][0]);
+        acc[m][1] = fmaf(sum[m][1], f1, acc[m][1]);
+        acc[m][2] = fmaf(sum[m][2], f0, acc[m][2]);
+        acc[m][3] = fmaf(sum[m][3], f1, acc[m][3]);
       }
     }
   }
@@ -463,7 +461,7 @@ struct Segment {
       const int stage = (RUNS ? in_run * run : 0) + step * 2;
       at.x = v.s + t * 16 + stage * 256;
       at.low = v.s_low + t * 16 + stage * 256;
-      at.table = v.table + stage * kScales * VC * 8;
+      at.table = v.table + stage * VC * 4;
     };
     enter(step0);
 #pragma unroll 1
@@ -482,7 +480,7 @@ struct Segment {
       at.stage += 2;
       at.x += 512;
       at.low += 512;
-      at.table += 2 * kScales * VC * 8;
+      at.table += 2 * VC * 4;
       if (--turn == 0) {
         turn = steps;
         at.stage = 0;
@@ -518,14 +516,14 @@ MOE_DEV float sum_parts(const float* parts, int slot_floats, int tile, const Par
 // ------------------------------------------------------------------ staged vectors
 // Each 128 columns (a stage) of a vector become fp16 after a power of two that
 // puts their largest value into [2^13, 2^14): the 8 or 11 significant bits are
-// all there down to 2^-24 of the largest value, and what is lost further down
-// (2^-35 of it) is below the rounding of the fp32 sums.  LOW keeps a second fp16
-// part, 22 bits together.  A vector with an infinity or NaN, or with 2^118 or more
-// (the factor back would pass fp32), gives results that are not finite.  Taking 8
-// times the sum off the products costs roundings of 2^-24 of both: next to a bf16
-// or fp16 result nothing, unless the group's weights are all but zero where its
-// values are large.  The table has, for each group, the factor back to the vector's units
-// (2^24 of the codes included) and 8 times the sum of its values.
+// all there down to 2^-27 of the largest value, and what is lost further down
+// (2^-38 of it) is below the rounding of the fp32 sums.  LOW keeps a second fp16
+// part, 22 bits together.  The table has, for each stage, the factor back to the
+// vector's units.
+// (The codes themselves as fp16 subnormals, with 8 times a group's sum taken off
+// its products, take four instructions fewer for eight weights, but the matrix
+// instruction then keeps about 17 bits below the largest value times 8: beside
+// a value 1000 times the others whose weight is zero, results were off by 7%.)
 
 // Bytes between staged vectors: 64 more than a multiple of 128, so that two
 // rows do not share banks.
@@ -534,7 +532,7 @@ __host__ __device__ inline int staged_stride(int K) { return K * 2 + 64; }
 struct StagedAt {
   uint32_t x, low;        // vector 0 and its low parts
   int stride;             // bytes between vectors
-  uint32_t table;         // entries [group][vectors of the table]
+  uint32_t table;         // entries [stage][vectors of the table]
 };
 
 MOE_DEV void load_f8(const __nv_bfloat16* p, float* f) { widen8(load8<__nv_bfloat16, 8>(p, 0, 1, 8), f); }
@@ -567,23 +565,17 @@ MOE_DEV void stage_vectors(const StagedAt& at, int count, int K, Row row) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (base + u * kW4Threads >= all) break;
-      float top = 0.0f, sum = 0.0f;
+      float top = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        top = fmaxf(top, fabsf(f[u][j]));
-        sum += f[u][j];
-      }
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(f[u][j]));
 #pragma unroll
       for (int off = 1; off < 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-#pragma unroll
-      for (int off = 1; off < 4 * W; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      const int k = top > 0.0f ? max(min(140 - (int)(__float_as_uint(top) >> 23), 126), -103) : 0;
+      const int k = top > 0.0f ? max(min(140 - (int)(__float_as_uint(top) >> 23), 126), -114) : 0;
       const float scale = exp2i(k);
       uint32_t hi[4], lo[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {   // columns q and q + 4
-        const float sc = q & 1 ? scale * 0.0625f : scale;
-        const float a = f[u][q] * sc, b = f[u][q + 4] * sc;
+        const float a = f[u][q] * scale, b = f[u][q + 4] * scale;
         const __half2 h = __floats2half2_rn(a, b);
         hi[q] = *reinterpret_cast<const uint32_t*>(&h);
         if (LOW) {
@@ -596,10 +588,10 @@ MOE_DEV void stage_vectors(const StagedAt& at, int count, int K, Row row) {
       asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at.x + to), "r"(hi[0]), "r"(hi[1]), "r"(hi[2]), "r"(hi[3]) : "memory");
       if (LOW)
         asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at.low + to), "r"(lo[0]), "r"(lo[1]), "r"(lo[2]), "r"(lo[3]) : "memory");
-      if (c[u] % (4 * W) == 0) {
-        const int group = c[u] / (4 * W);
-        const uint32_t entry = at.table + (VC > 1 ? (group * VC + m[u]) * 8 : (m[u] * (K / (32 * W)) + group) * 8);
-        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(entry), "f"(exp2i(24 - k)), "f"(8.0f * sum) : "memory");
+      if ((c[u] & 15) == 0) {
+        const int stage = c[u] >> 4;
+        const uint32_t entry = at.table + (VC > 1 ? stage * VC + m[u] : m[u] * (K / 128) + stage) * 4;
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(entry), "f"(exp2i(-k)) : "memory");
       }
     }
   }
@@ -613,7 +605,7 @@ template <typename T, int NT> MOE_DEV void staged_at(Vectors<T, NT>& v, const St
   v.s_low = v.s + (at.low - at.x);
 #pragma unroll
   for (int m = 0; m < NT; ++m) v.to[m] = (min(m * 8 + g, here - 1) - min(g, here - 1)) * at.stride;
-  v.table = at.table + t * 16;
+  v.table = at.table + t * 8;
 }
 
 // Raise a kernel's dynamic shared memory limit (once, from moe_init).

@@ -12,13 +12,13 @@
 // global memory, x as it is and act as two bf16 parts in fragment order.  Either way act keeps 16 bits or more, so that storing it costs no
 // accuracy beside a bf16 or fp16 result.
 //
-// Measured (us, bf16, weights from HBM): 64 experts of 2048 x 1408, four a token,
-// groups of 64: 13.0 for one token, 38.2 for eight, 67.8 for 32, 84.7 for 64 (294
-// MB, 3.5 TB/s), 119 for 128, 373 for 512.  64 experts of 4096 x 2048, eight a
-// token, groups of 128: 31.2 for one token (104 MB, 3.3 TB/s), 114 for eight (4.6
+// Measured (us, bf16, weights from HBM, random routes): 64 experts of 2048 x 1408,
+// four a token, groups of 64: 14.4 for one token, 41.9 for eight, 78.0 for 32, 88.3 for
+// 64 (285 MB, 3.2 TB/s), 123 for 128, 381 for 512.  64 experts of 4096 x 2048, eight a
+// token, groups of 128: 32.0 for one token (104 MB, 3.2 TB/s), 131 for eight (4.4
 // TB/s).  Read from global memory instead, the first took 155 us with 64 tokens
 // and the second 46 us with one; 32 experts of 4096 x 4096, where seven vectors
-// are staged at a time, 64 tokens, 504 us rather than 305.
+// are staged at a time, 64 tokens, 504 us rather than 304.
 // (Included by one file per type, so that they compile side by side.)
 #pragma once
 
@@ -123,7 +123,7 @@ MOE_DEV void find_routes(const Lists& l, int R, int e, const float* gates) {
 // whose range their first unit lies.  Going on to another expert costs a block
 // about as much as kTurnUnits tiles (the last warps, the sums, the next
 // vectors), so as many empty units lie between two experts.  Measured with 2, 4, 8
-// and 12 (us): 64 experts of 2048 x 1408, eight tokens 40.3, 38.7, 38.2, 39.1; 64
+// and 12 (us; with the shorter conversion of stage_vectors' comment): 64 experts of 2048 x 1408, eight tokens 40.3, 38.7, 38.2, 39.1; 64
 // tokens 85.8, 85.1, 84.7, 85.6; 128 tokens 123.2, 122.6, 119.4, 118.0; 8 experts of
 // 1536 x 1024, two a token, 64 tokens 38.3, 36.9, 31.7, 31.9.  Where every expert
 // has one round and the blocks divide among the experts with hardly a loss, they
@@ -490,16 +490,16 @@ size_t plan_smem(int share, int NT, int x, int lists, Plan* plan) {
 
 // Staged vectors of K values in `parts` parts with a table for `cols` columns,
 // and whether they leave room for the parts of eight tiles.
-int64_t staged_bytes(int count, int K, int parts, int cols, int W) {
-  return (int64_t)count * parts * staged_stride(K) + (int64_t)K / (32 * W) * cols * 8;
+int64_t staged_bytes(int count, int K, int parts, int cols) {
+  return (int64_t)count * parts * staged_stride(K) + (int64_t)K / 128 * cols * 4;
 }
 bool staged_fits(int64_t bytes, int lists, int NT) {
   return bytes <= kSmemMost - kRingsBytes - lists - 16 - (8 + kW4Warps) * NT * 512;
 }
 // The most vectors a round can stage, up to 8 NT and the tokens there are.
-int most_staged(const ExpertsW4Params& p, int K, int parts, int NT, int W) {
+int most_staged(const ExpertsW4Params& p, int K, int parts, int NT) {
   int n = p.T < 8 * NT ? p.T : 8 * NT;
-  while (n > 0 && !staged_fits(staged_bytes(n, K, parts, 8 * NT, W), lists_bytes(p.T * p.k), NT)) --n;
+  while (n > 0 && !staged_fits(staged_bytes(n, K, parts, 8 * NT), lists_bytes(p.T * p.k), NT)) --n;
   return n;
 }
 
@@ -513,9 +513,9 @@ int share_of(const ExpertsW4Params& p, int per) {
 struct Launch {
   Plan plan;
   size_t smem;
-  Launch(const ExpertsW4Params& p, int per, int K, int parts, int NT, int W, bool staged) {
-    plan.most = staged ? most_staged(p, K, parts, NT, W) : 8 * NT;
-    smem = plan_smem(share_of(p, per), NT, staged ? (int)staged_bytes(plan.most, K, parts, 8 * NT, W) : 0,
+  Launch(const ExpertsW4Params& p, int per, int K, int parts, int NT, bool staged) {
+    plan.most = staged ? most_staged(p, K, parts, NT) : 8 * NT;
+    smem = plan_smem(share_of(p, per), NT, staged ? (int)staged_bytes(plan.most, K, parts, 8 * NT) : 0,
                      lists_bytes(p.T * p.k), &plan);
   }
   // Sixteen vectors a round: they are staged, and a block's tiles are one segment.
@@ -526,7 +526,7 @@ template <typename T, int W, int NT, XSource XS>
 cudaError_t up_launch(const ExpertsW4Params* p, cudaStream_t s) {
   auto* kernel = &experts_w4_up_kernel<T, W, NT, XS>;
   if (p == nullptr) return allow_smem(kernel);
-  const Launch l(*p, p->f / 8, p->d, 1, NT, W, XS == kStaged);
+  const Launch l(*p, p->f / 8, p->d, 1, NT, XS == kStaged);
   return launch_pdl(kernel, dim3(device_info()->sm_count), dim3(kW4Threads), l.smem, s, *p, l.plan);
 }
 
@@ -534,15 +534,13 @@ template <typename T, int W, int NT, XSource XS>
 cudaError_t down_launch(const ExpertsW4Params* p, cudaStream_t s) {
   auto* kernel = &experts_w4_down_kernel<T, W, NT, XS>;
   if (p == nullptr) return allow_smem(kernel);
-  const Launch l(*p, p->d / 16, p->f, 2, NT, W, XS == kStaged);
+  const Launch l(*p, p->d / 16, p->f, 2, NT, XS == kStaged);
   cudaError_t e = launch_pdl(kernel, dim3(device_info()->sm_count), dim3(kW4Threads), l.smem, s, *p, l.plan);
   if (e != cudaSuccess) return e;
   return launch_pdl(experts_w4_join_kernel<T>, dim3((p->d + 1023) / 1024, p->T), dim3(256), 0, s, *p);
 }
 
-int64_t token_bytes(const ExpertsW4Params& p, int W) {
-  return (int64_t)p.k * p.f * 4 + (int64_t)p.k * p.f / (32 * W) * 8;
-}
+int64_t token_bytes(const ExpertsW4Params& p) { return (int64_t)p.k * p.f * 4 + (int64_t)p.k * p.f / 128 * 4; }
 constexpr int kTokenStatic = 256;   // its static shared memory, rounded up
 
 template <typename T, int W> cudaError_t token_launch(const ExpertsW4Params* p, cudaStream_t s) {
@@ -552,7 +550,7 @@ template <typename T, int W> cudaError_t token_launch(const ExpertsW4Params* p, 
   const int blocks = per < sms ? per : sms;
   Plan plan;
   plan.most = 1;
-  const size_t smem = plan_smem((per + blocks - 1) / blocks, 1, (int)token_bytes(*p, W), kTokenStatic, &plan) - kTokenStatic;
+  const size_t smem = plan_smem((per + blocks - 1) / blocks, 1, (int)token_bytes(*p), kTokenStatic, &plan) - kTokenStatic;
   return launch_pdl(kernel, dim3(blocks), dim3(kW4Threads), smem, s, *p, plan);
 }
 
@@ -560,9 +558,8 @@ template <typename T, int W> cudaError_t token_launch(const ExpertsW4Params* p, 
 // Staged rounds serve eight routes of an expert, or sixteen where the experts
 // have more than six on average and a block still takes its tiles of an expert
 // in one segment.  Measured, eight and sixteen (us): 8 experts of 1536 x 1024, 12
-// tokens on all of them 29.4 and 25.3, 64 tokens 92 and 77; 64 experts of 2048 x
-// 1408, whose tiles would become two and more segments, 128 tokens 123 and 166
-// (with four empty units between experts).
+// tokens on all of them 30.9 and 26.7, 64 tokens 96 and 80; 64 experts of 2048 x
+// 1408, whose tiles would become two and more segments, 128 tokens 123 and 139.
 // One token: W_down of all its experts as one product, 13.0 us, or a product for
 // each and their sum, 16.4 (2048 x 1408, four experts).
 template <typename T, int W> cudaError_t experts_nt(const ExpertsW4Params* p, cudaStream_t s) {
@@ -577,19 +574,19 @@ template <typename T, int W> cudaError_t experts_nt(const ExpertsW4Params* p, cu
     return e == cudaSuccess ? token_launch<T, W>(p, s) : e;
   }
   const int R = p->T * p->k, few = p->T < 8 ? p->T : 8;
-  const bool token = p->T == 1 && staged_fits(token_bytes(*p, W), kTokenStatic, 1);
+  const bool token = p->T == 1 && staged_fits(token_bytes(*p), kTokenStatic, 1);
   // both kernels or none: they agree on the form of act
-  const bool staged = most_staged(*p, p->d, 1, 1, W) * 2 >= few && (token || most_staged(*p, p->f, 2, 1, W) * 2 >= few);
+  const bool staged = most_staged(*p, p->d, 1, 1) * 2 >= few && (token || most_staged(*p, p->f, 2, 1) * 2 >= few);
   if (!staged) {
     e = up_launch<T, W, 2, kNatural>(p, s);
     return e == cudaSuccess ? down_launch<T, W, 2, kOrdered>(p, s) : e;
   }
   const bool many = R > 6 * p->E;
-  const bool up2 = many && Launch(*p, p->f / 8, p->d, 1, 2, W, true).serves(*p, p->f / 8);
+  const bool up2 = many && Launch(*p, p->f / 8, p->d, 1, 2, true).serves(*p, p->f / 8);
   e = up2 ? up_launch<T, W, 2, kStaged>(p, s) : up_launch<T, W, 1, kStaged>(p, s);
   if (e != cudaSuccess) return e;
   if (token) return token_launch<T, W>(p, s);
-  const bool down2 = many && Launch(*p, p->d / 16, p->f, 2, 2, W, true).serves(*p, p->d / 16);
+  const bool down2 = many && Launch(*p, p->d / 16, p->f, 2, 2, true).serves(*p, p->d / 16);
   return down2 ? down_launch<T, W, 2, kStaged>(p, s) : down_launch<T, W, 1, kStaged>(p, s);
 }
 

@@ -1,8 +1,8 @@
 // Products of a few vectors with 4-bit weights (sm_103a): y[m, n] = sum_k x[m, k]
 // W[n, k].  How the weights are streamed, and what bounds it: w4.cuh.  Measured
-// back to back from HBM: one vector and 4096 x 4096 6.0 us (8.9 MB, 1.5 TB/s;
-// about 4 us of it start and end of the kernel), 20011 x 2048 8.7, 4096 x 14336
-// 11.1 us (2.7 TB/s); eight vectors 6.7, 11.0 and 15.2 us; 64 vectors 19, 41 and
+// back to back from HBM: one vector and 4096 x 4096 5.8 us (8.9 MB, 1.5 TB/s;
+// about 4 us of it start and end of the kernel), 20011 x 2048 8.5, 4096 x 14336
+// 11.8 us (2.6 TB/s); eight vectors 6.8, 10.7 and 15.1 us; 64 vectors 19, 41 and
 // 74 us.
 #include "w4.cuh"
 
@@ -96,7 +96,8 @@ __global__ void __launch_bounds__(kW4Threads, 1) matvec_w4_kernel(MatvecArgs a) 
   }
 }
 
-int64_t staged_bytes(int M, int K, int W) { return (int64_t)M * staged_stride(K) + (int64_t)K / (32 * W) * 64; }
+// Staged vectors and the factors of eight for each stage.
+int64_t staged_bytes(int M, int K) { return (int64_t)M * staged_stride(K) + (int64_t)K / 128 * 32; }
 
 // Most tiles of a block.
 int share_of(int N) {
@@ -110,7 +111,7 @@ cudaError_t matvec_launch(const MatvecArgs* a, cudaStream_t s) {
   auto* kernel = &matvec_w4_kernel<T, W, NT, XS, FULL>;
   if (a == nullptr) return allow_smem(kernel);
   const int all = (a->N + 15) / 16, sms = device_info()->sm_count;
-  const int x_bytes = XS == kStaged ? (int)staged_bytes(a->M, a->K, W) : 0;
+  const int x_bytes = XS == kStaged ? (int)staged_bytes(a->M, a->K) : 0;
   const int room = (kSmemMost - kRingsBytes - x_bytes) / (NT * 512) - kW4Warps;
   const int share = share_of(a->N);
   MatvecArgs args = *a;
@@ -125,14 +126,15 @@ cudaError_t matvec_launch(const MatvecArgs* a, cudaStream_t s) {
 // more than that, 32 (64 vectors, sixteen and 32 a pass: 4096 x 4096 24.3 and 19.1,
 // 20011 x 2048 48.5 and 40.8, 4096 x 14336 79.6 and 74.3 us; 17 vectors 12.0 and
 // 10.0, 21.5 and 17.9, 31.6 and 31.1).
-// Measured, staged and read (us): 4096 x 4096, two tiles a block: 6.1 and 6.4
-// with one vector, 9.5 and 6.7 with eight; 20011 x 2048, nine tiles: 8.7 and 10.0
-// with one, 11.0 and 11.2 with eight; staged rounds of sixteen 15.9 and 14.1.
+// Measured, staged and read (us): 4096 x 4096, two tiles a block: 5.8 and 6.0
+// with one vector, 7.2 and 6.4 with four, 9.1 and 6.8 with eight; 20011 x 2048, nine
+// tiles: 8.5 and 9.7 with one, 10.7 and 12.1 with eight (in groups of 32 9.7 and 10.2,
+// 11.9 and 11.6); staged rounds of sixteen, when last tried, 15.9 and 14.1.
 template <typename T, int W, bool FULL>
 cudaError_t matvec_nt(const MatvecArgs* a, cudaStream_t s) {
   if constexpr (FULL) {
     const bool staged = a == nullptr || (a->M <= 8 && a->M <= share_of(a->N) &&
-                                         staged_bytes(a->M, a->K, W) <= kSmemMost - kRingsBytes - (8 + kW4Warps) * 512);
+                                         staged_bytes(a->M, a->K) <= kSmemMost - kRingsBytes - (8 + kW4Warps) * 512);
     const cudaError_t e = staged ? matvec_launch<T, W, 1, kStaged, FULL>(a, s) : cudaSuccess;
     if ((a != nullptr && staged) || e != cudaSuccess) return e;
   }
