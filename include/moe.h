@@ -102,7 +102,7 @@ typedef struct {
 
 /* Cache device properties and raise the kernels' shared-memory limits on
  * `device`.  Call once per device (not on the hot path) before the other
- * calls, with that device current. */
+ * calls, with that device current.  (About 35 ms: the limits load the kernels.) */
 MOE_API int moe_init(int device);
 
 /* Upper bound on the rows of the dispatched (expert-contiguous, tile-padded)
@@ -528,10 +528,14 @@ MOE_API int moe_layer_bwd(const moe_shape_t* shape, const moe_bwd_args_t* args, 
  * to these calls; their arithmetic is written out with each.  examples/block.py
  * runs them together with the layer.
  *
- * Matrices here have a row stride `ld` (elements, >= the row's length); their
- * pointers need only the alignment of their element type.  Rows whose groups
- * of eight columns lie on 16-byte boundaries (base 16-byte aligned, row stride
- * a multiple of 16 bytes, the width a multiple of 8) take vector loads.
+ * Matrices with a row stride `ld` (elements, >= the row's length), the norm's
+ * weight and rstd and dw need only the alignment of their element type; every
+ * other pointer (codes, scales, 8-bit outputs, workspaces, and all of
+ * moe_experts_w4, topk_idx and gates among them) a 16-byte boundary, as does the x
+ * of moe_matvec_w4 (its rows too).  Rows whose groups of eight columns lie on
+ * 16-byte boundaries (base 16-byte aligned, row stride a multiple of 16 bytes, the
+ * width a multiple of 8) take vector loads, other even widths on a pair's boundary
+ * loads of pairs.
  * A call with no rows (rows, T or M = 0) is valid and writes nothing. */
 typedef enum { MOE_DT_BF16 = 0, MOE_DT_F16 = 1, MOE_DT_F32 = 2 } moe_dtype_t;
 

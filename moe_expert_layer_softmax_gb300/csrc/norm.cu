@@ -171,8 +171,10 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
 }
 
 // y = dropout(x): a warp, or (SMALL, rows up to 64 and 128 columns) 8 or 16 lanes,
-// takes eight columns a lane of two rows at a time.  Bound by the generator (bf16)
-// and HBM (fp32): 16384 x 2048 bf16 27.6 us, 4.9 TB/s; fp32 5.7 TB/s.
+// takes eight columns a lane of two rows at a time.  Bound by the generator (16-bit
+// types) and HBM (fp32): 16384 x 2048 bf16 26.6 us, 5.0 TB/s; fp32 5.7 TB/s.  Four
+// blocks a multiprocessor leave 64 registers: with vector loads 12 to 40 bytes a thread
+// spill (fp32 12, fp16 20, bf16 40; without them at most 12).
 template <typename T, int V, bool SMALL>
 __global__ void __launch_bounds__(256, 4) dropout_kernel(DropoutParams p) {
   __shared__ uint4 xch[V == 8 ? 1 : 256];

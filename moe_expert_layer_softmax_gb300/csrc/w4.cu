@@ -1,5 +1,9 @@
 // Quantiser and its inverse of 4-bit weights with group scales (sm_103a); the
-// format is described in w4.cuh.  Bound by HBM: one read and one write.
+// format is described in w4.cuh.  One read and one write.  The quantiser is bound by
+// issue (85% of the slots): 297 instructions for eight columns, most of them the
+// divisions, 2.1-2.4 TB/s (4096 x 4096 20.0 us, 131072 x 4096 573 us, bf16,
+// groups of 128); the inverse by the fp32 values that it writes, 4.3-5.2 TB/s (17.4
+// and 466 us).
 #include "block.cuh"
 #include "block.h"
 #include "kernels.h"

@@ -560,8 +560,9 @@ template <typename T, int W> cudaError_t token_launch(const ExpertsW4Params* p, 
 // in one segment.  Measured, eight and sixteen (us): 8 experts of 1536 x 1024, 12
 // tokens on all of them 30.9 and 26.7, 64 tokens 96 and 80; 64 experts of 2048 x
 // 1408, whose tiles would become two and more segments, 128 tokens 123 and 139.
-// One token: W_down of all its experts as one product, 13.0 us, or a product for
-// each and their sum, 16.4 (2048 x 1408, four experts).
+// One token: W_down of all its experts as one product, 14.4 us, or a product for
+// each and their sum, 17.2 (2048 x 1408, four experts); 32.2 and 35.0 (4096 x 2048,
+// eight).
 template <typename T, int W> cudaError_t experts_nt(const ExpertsW4Params* p, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   if (p == nullptr) {
