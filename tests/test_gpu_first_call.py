@@ -45,7 +45,8 @@ def matvec_w4():
 def experts_w4():
     e = {}
     for n in ("gate", "up", "down"):
-        e[n + "_q"], e[n + "_s"] = torch.full((1, 256, 128), 0x5B, **U), torch.full((1, 256, 4), 0.01, **B)
+        # columns of 4 and -3 in turn (of 3 and -3, the sum over equal activations is zero)
+        e[n + "_q"], e[n + "_s"] = torch.full((1, 256, 128), 0x5C, **U), torch.full((1, 256, 4), 0.01, **B)
     m.experts_w4(x, idx, g, e, y, torch.zeros(m.experts_w4_workspace(4, 256, 1, 1, 256), **U))
     return y
 '''
