@@ -100,9 +100,10 @@ typedef struct {
 
 /* ---------------------------------------------------------------- set-up */
 
-/* Cache device properties and raise the kernels' shared-memory limits on
- * `device`.  Call once per device (not on the hot path) before the other
- * calls, with that device current.  (About 35 ms: the limits load the kernels.) */
+/* Cache device properties and raise the grouped GEMMs' shared-memory limits on
+ * `device` (the kernels around the layer raise theirs at their first launch).
+ * Call once per device (not on the hot path) before the other calls, with that
+ * device current. */
 MOE_API int moe_init(int device);
 
 /* Upper bound on the rows of the dispatched (expert-contiguous, tile-padded)

@@ -7,7 +7,6 @@
 #include <mutex>
 
 #include "moe.h"
-#include "block.h"
 #include "common.cuh"
 #include "kernels.h"
 
@@ -15,7 +14,6 @@ namespace moe {
 
 namespace {
 
-constexpr int kMaxDevices = 64;
 DeviceInfo g_dev[kMaxDevices];
 
 int current_device() {
@@ -309,13 +307,10 @@ int moe_init(int device) {
   int sms = 0;
   MOE_CUDA(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device));
   MOE_CUDA(gemm_init_attributes());
-  MOE_CUDA(norm_init());
-  MOE_CUDA(norm_bwd_init());
-  MOE_CUDA(matvec_w4_init());
-  MOE_CUDA(experts_w4_init_bf16());
-  MOE_CUDA(experts_w4_init_f16());
   noalloc_forget_device(device);
   g_dev[device].sm_count = sms;
+  g_dev[device].index = device;
+  g_dev[device].inits.fetch_add(1);
   g_dev[device].ready = true;
   return MOE_OK;
 }

@@ -68,8 +68,6 @@ struct DropoutParams {
 constexpr int kNormMaxWidth = 32768;     // 1024 threads, four groups of eight columns each
 constexpr int kNormPartialRows = 1024;   // most blocks of the backward: rows of partial weight gradients
 
-cudaError_t norm_init();   // dynamic shared memory limits (moe_init)
-cudaError_t norm_bwd_init();
 // vec: neighbouring columns that an access takes, 8, 2 or 1 (block.cuh, V)
 cudaError_t launch_add_norm(const AddNormParams& p, int dtype, int res_dtype, int vec, cudaStream_t s);
 cudaError_t launch_add_norm_bwd(const AddNormBwdParams& p, int dtype, int res_dtype, int vec, float* dw,
@@ -94,9 +92,6 @@ struct ExpertsW4Params {
   int32_t* err;
 };
 
-cudaError_t matvec_w4_init();    // dynamic shared memory limits (moe_init)
-cudaError_t experts_w4_init_bf16();
-cudaError_t experts_w4_init_f16();
 cudaError_t launch_quantize_w4(int64_t rows, int K, int group, int dtype, const void* src,
                                uint8_t* q, void* scales, cudaStream_t s);
 cudaError_t launch_dequantize_w4(int64_t rows, int K, int group, int dtype, const uint8_t* q,

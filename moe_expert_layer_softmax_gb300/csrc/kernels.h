@@ -6,6 +6,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <utility>
 
 namespace moe {
@@ -32,11 +33,31 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 // block and each route's rank within its expert among the block's routes.
 constexpr int kRouteTokensPerBlock = 128;
 
+constexpr int kMaxDevices = 64;
 struct DeviceInfo {
   int sm_count = 0;
   bool ready = false;
+  int index = 0;                       // the device's number
+  std::atomic<uint32_t> inits{0};      // moe_init calls so far
 };
 const DeviceInfo* device_info();
+
+// Raises a kernel's dynamic shared memory limit at its first launch on a device
+// (again after another moe_init of it: a reset takes the limit away).  For kernels
+// of many variants: raising a limit loads the kernel, 0.2 ms each.
+class SmemLimit {
+  std::atomic<uint32_t> raised_[kMaxDevices] = {};   // at which number of moe_init calls
+
+ public:
+  cudaError_t raise(const void* kernel, int bytes) {
+    const DeviceInfo* d = device_info();
+    const uint32_t now = d->inits.load(std::memory_order_acquire);
+    if (raised_[d->index].load(std::memory_order_acquire) == now) return cudaSuccess;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) raised_[d->index].store(now, std::memory_order_release);
+    return e;
+  }
+};
 
 // ---------------------------------------------------------------- routing
 cudaError_t launch_route_topk(const float* logits, int T, int E, int k, int32_t* topk_idx,

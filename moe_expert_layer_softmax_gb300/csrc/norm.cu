@@ -216,25 +216,25 @@ __global__ void __launch_bounds__(256, 4) dropout_kernel(DropoutParams p) {
   }
 }
 
-// p = NULL: raise the kernel's shared memory limit.
 template <typename TX, typename TR, bool MX, int V, bool RING, int NV, int MAXT>
-cudaError_t fwd_run(const AddNormParams* p, int threads, cudaStream_t s) {
+cudaError_t fwd_run(const AddNormParams& p, int threads, cudaStream_t s) {
   auto* kernel = &add_norm_kernel<TX, TR, MX, V, RING, NV, MAXT>;
   constexpr int ring = RING ? RowRing<8 * (sizeof(TX) + sizeof(TR)), NV>::kBytes : 0;
-  if (p == nullptr)
-    return ring ? cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, MAXT * ring)
-                : cudaSuccess;
+  if constexpr (RING) {
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kernel), MAXT * ring);
+    if (e != cudaSuccess) return e;
+  }
   constexpr int planned = norm_blocks(RING, NV, MAXT);
   int resident = norm_resident(planned, MAXT, threads, ring);
   // Where the ring leaves room for one block and not two, two rounds of blocks all
   // the same when each has many rows and no numbers to draw.  Measured in one and in
   // two rounds (us): fp32, 8192 columns, 600 rows 14.9 and 17.8, 2000 rows 42.7 and
   // 42.7, 8192 rows 176 and 166; with dropout 16.2 and 19.0, 44.9 and 45.8, 162 and 164.
-  if (resident < planned * MAXT / threads && p->rng.threshold == 0 && p->rows > (int64_t)device_info()->sm_count * 13)
+  if (resident < planned * MAXT / threads && p.rng.threshold == 0 && p.rows > (int64_t)device_info()->sm_count * 13)
     resident = planned * MAXT / threads;
-  const int blocks = row_blocks(MX ? p->rows_pad : p->rows, p->group, threads, resident);
-  return launch_pdl(kernel, dim3(blocks), dim3(threads), (size_t)threads * ring, s, *p);
+  const int blocks = row_blocks(MX ? p.rows_pad : p.rows, p.group, threads, resident);
+  return launch_pdl(kernel, dim3(blocks), dim3(threads), (size_t)threads * ring, s, p);
 }
 
 // Rows up to 8192 columns come through the ring of 256 threads, up to 16384 (but
@@ -244,60 +244,46 @@ cudaError_t fwd_run(const AddNormParams* p, int threads, cudaStream_t s) {
 // x 4096 (8-bit, dropout) 243 us with four, 266 with two; at 8192 x 2048 (bf16) 26
 // with four, 24 with two.
 template <typename TX, typename TR, bool MX, int V>
-cudaError_t fwd_types(const AddNormParams* p, cudaStream_t s) {
+cudaError_t fwd_types(const AddNormParams& p, cudaStream_t s) {
   constexpr bool wide = V == 8 && RowRing<8 * (sizeof(TX) + sizeof(TR)), 4>::kFits512;
-  if (p == nullptr) {
-    cudaError_t e = cudaSuccess;
-    if constexpr (V == 8) {
-      e = fwd_run<TX, TR, MX, 8, true, 1, kNormThreads>(p, 0, s);
-      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, 8, true, 2, kNormThreads>(p, 0, s);
-      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, 8, true, 3, kNormThreads>(p, 0, s);
-      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, 8, true, 4, kNormThreads>(p, 0, s);
-    }
-    if constexpr (wide) {
-      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, 8, true, 3, 512>(p, 0, s);
-      if (e == cudaSuccess) e = fwd_run<TX, TR, MX, 8, true, 4, 512>(p, 0, s);
-    }
-    return e;
-  }
-  AddNormParams q = *p;
+  AddNormParams q = p;
   if constexpr (V == 8) {
-    RowSplit split(p->d, !MX || p->d <= 512 ? 2 : 3, 4, kNormThreads);
+    RowSplit split(p.d, !MX || p.d <= 512 ? 2 : 3, 4, kNormThreads);
     q.group = split.group;
     if (split.group) {
       const int threads = split.threads();
-      if (split.nv == 1) return fwd_run<TX, TR, MX, 8, true, 1, kNormThreads>(&q, threads, s);
-      if (split.nv == 2) return fwd_run<TX, TR, MX, 8, true, 2, kNormThreads>(&q, threads, s);
-      if (split.nv == 3) return fwd_run<TX, TR, MX, 8, true, 3, kNormThreads>(&q, threads, s);
-      return fwd_run<TX, TR, MX, 8, true, 4, kNormThreads>(&q, threads, s);
+      if (split.nv == 1) return fwd_run<TX, TR, MX, 8, true, 1, kNormThreads>(q, threads, s);
+      if (split.nv == 2) return fwd_run<TX, TR, MX, 8, true, 2, kNormThreads>(q, threads, s);
+      if (split.nv == 3) return fwd_run<TX, TR, MX, 8, true, 3, kNormThreads>(q, threads, s);
+      return fwd_run<TX, TR, MX, 8, true, 4, kNormThreads>(q, threads, s);
     }
     if constexpr (wide) {
-      split = RowSplit(p->d, 3, 4, 512);
+      split = RowSplit(p.d, 3, 4, 512);
       q.group = split.group;
       if (split.group)
-        return split.nv == 3 ? fwd_run<TX, TR, MX, 8, true, 3, 512>(&q, q.group, s)
-                             : fwd_run<TX, TR, MX, 8, true, 4, 512>(&q, q.group, s);
+        return split.nv == 3 ? fwd_run<TX, TR, MX, 8, true, 3, 512>(q, q.group, s)
+                             : fwd_run<TX, TR, MX, 8, true, 4, 512>(q, q.group, s);
     }
   } else {
-    const RowSplit split(p->d, 1, 1, kNormMaxThreads);
+    const RowSplit split(p.d, 1, 1, kNormMaxThreads);
     q.group = split.group;
     if (split.group) {
       const int threads = split.threads();
-      if (split.group > 512) return fwd_run<TX, TR, MX, V, false, 1, kNormMaxThreads>(&q, threads, s);
-      return split.group <= kNormThreads ? fwd_run<TX, TR, MX, V, false, 1, kNormThreads>(&q, threads, s)
-                                         : fwd_run<TX, TR, MX, V, false, 1, 512>(&q, threads, s);
+      if (split.group > 512) return fwd_run<TX, TR, MX, V, false, 1, kNormMaxThreads>(q, threads, s);
+      return split.group <= kNormThreads ? fwd_run<TX, TR, MX, V, false, 1, kNormThreads>(q, threads, s)
+                                         : fwd_run<TX, TR, MX, V, false, 1, 512>(q, threads, s);
     }
   }
-  const RowSplit split(p->d, wide ? 3 : 2, 4, kNormMaxThreads);
+  const RowSplit split(p.d, wide ? 3 : 2, 4, kNormMaxThreads);
   q.group = split.group;
   if constexpr (!wide)
-    if (split.nv == 2) return fwd_run<TX, TR, MX, V, false, 2, kNormMaxThreads>(&q, q.group, s);
-  return split.nv == 3 ? fwd_run<TX, TR, MX, V, false, 3, kNormMaxThreads>(&q, q.group, s)
-                       : fwd_run<TX, TR, MX, V, false, 4, kNormMaxThreads>(&q, q.group, s);
+    if (split.nv == 2) return fwd_run<TX, TR, MX, V, false, 2, kNormMaxThreads>(q, q.group, s);
+  return split.nv == 3 ? fwd_run<TX, TR, MX, V, false, 3, kNormMaxThreads>(q, q.group, s)
+                       : fwd_run<TX, TR, MX, V, false, 4, kNormMaxThreads>(q, q.group, s);
 }
 
 template <typename TX, typename TR>
-cudaError_t fwd_vec(const AddNormParams* p, int vec, cudaStream_t s) {
+cudaError_t fwd_vec(const AddNormParams& p, int vec, cudaStream_t s) {
   return vec == 8   ? fwd_types<TX, TR, false, 8>(p, s)
          : vec == 2 ? fwd_types<TX, TR, false, 2>(p, s)
                     : fwd_types<TX, TR, false, 1>(p, s);
@@ -305,27 +291,16 @@ cudaError_t fwd_vec(const AddNormParams* p, int vec, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t norm_init() {
-  cudaError_t e = fwd_vec<__nv_bfloat16, __nv_bfloat16>(nullptr, 8, nullptr);
-  if (e == cudaSuccess) e = fwd_vec<__nv_bfloat16, float>(nullptr, 8, nullptr);
-  if (e == cudaSuccess) e = fwd_vec<__half, __half>(nullptr, 8, nullptr);
-  if (e == cudaSuccess) e = fwd_vec<__half, float>(nullptr, 8, nullptr);
-  if (e == cudaSuccess) e = fwd_vec<float, float>(nullptr, 8, nullptr);
-  if (e == cudaSuccess) e = fwd_types<__nv_bfloat16, __nv_bfloat16, true, 8>(nullptr, nullptr);
-  if (e == cudaSuccess) e = fwd_types<__nv_bfloat16, float, true, 8>(nullptr, nullptr);
-  return e;
-}
-
 cudaError_t launch_add_norm(const AddNormParams& p, int dtype, int res_dtype, int vec, cudaStream_t s) {
   const bool same = dtype == res_dtype;
   if (p.y_q)
-    return same ? fwd_types<__nv_bfloat16, __nv_bfloat16, true, 8>(&p, s)
-                : fwd_types<__nv_bfloat16, float, true, 8>(&p, s);
+    return same ? fwd_types<__nv_bfloat16, __nv_bfloat16, true, 8>(p, s)
+                : fwd_types<__nv_bfloat16, float, true, 8>(p, s);
   if (dtype == MOE_DT_BF16)
-    return same ? fwd_vec<__nv_bfloat16, __nv_bfloat16>(&p, vec, s) : fwd_vec<__nv_bfloat16, float>(&p, vec, s);
+    return same ? fwd_vec<__nv_bfloat16, __nv_bfloat16>(p, vec, s) : fwd_vec<__nv_bfloat16, float>(p, vec, s);
   if (dtype == MOE_DT_F16)
-    return same ? fwd_vec<__half, __half>(&p, vec, s) : fwd_vec<__half, float>(&p, vec, s);
-  return fwd_vec<float, float>(&p, vec, s);
+    return same ? fwd_vec<__half, __half>(p, vec, s) : fwd_vec<__half, float>(p, vec, s);
+  return fwd_vec<float, float>(p, vec, s);
 }
 
 template <typename T> static cudaError_t dropout_types(const DropoutParams& p, int vec, dim3 grid, cudaStream_t s) {

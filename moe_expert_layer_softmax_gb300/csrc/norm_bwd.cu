@@ -204,69 +204,56 @@ __global__ void __launch_bounds__(1024) add_norm_dw_kernel(const float* __restri
   if (lane == 0 && blockIdx.x * 32 + warp < d) dw[blockIdx.x * 32 + warp] = sum;
 }
 
-// p = NULL: raise the kernel's shared memory limit.
 template <typename TX, typename TR, int V, bool RING, int NV, int MAXT>
-cudaError_t bwd_run(const AddNormBwdParams* p, int threads, int* blocks, cudaStream_t s) {
+cudaError_t bwd_run(const AddNormBwdParams& p, int threads, int* blocks, cudaStream_t s) {
   auto* kernel = &add_norm_bwd_kernel<TX, TR, V, RING, NV, MAXT>;
   constexpr int ring = RING ? RowRing<8 * (sizeof(TX) + 2 * sizeof(TR)), NV>::kBytes : 0;
-  if (p == nullptr)
-    return ring ? cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, MAXT * ring)
-                : cudaSuccess;
+  if constexpr (RING) {
+    static SmemLimit limit;
+    const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kernel), MAXT * ring);
+    if (e != cudaSuccess) return e;
+  }
   constexpr int most = norm_blocks(RING || kNextInRegisters<TR, V, RING, NV, MAXT>, NV, MAXT);
-  *blocks = row_blocks(p->rows, p->group, threads, norm_resident(most, MAXT, threads, ring));
+  *blocks = row_blocks(p.rows, p.group, threads, norm_resident(most, MAXT, threads, ring));
   if (*blocks > kNormPartialRows) *blocks = kNormPartialRows;   // rows of the workspace
-  return launch_pdl(kernel, dim3(*blocks), dim3(threads), (size_t)threads * ring, s, *p);
+  return launch_pdl(kernel, dim3(*blocks), dim3(threads), (size_t)threads * ring, s, p);
 }
 
 // Rows up to 8192 columns (512 threads; 16384 where both matrices are 16 bits)
 // come through the ring; wider ones are read as they are needed.
 template <typename TX, typename TR, int V>
-cudaError_t bwd_types(const AddNormBwdParams* p, int* blocks, cudaStream_t s) {
+cudaError_t bwd_types(const AddNormBwdParams& p, int* blocks, cudaStream_t s) {
   constexpr bool wide = V == 8 && RowRing<8 * (sizeof(TX) + 2 * sizeof(TR)), 4>::kFits512;
-  cudaError_t e = cudaSuccess;
-  if (p == nullptr) {
-    if constexpr (V == 8) {
-      e = bwd_run<TX, TR, 8, true, 1, kNormThreads>(p, 0, blocks, s);
-      if (e == cudaSuccess) e = bwd_run<TX, TR, 8, true, 2, kNormThreads>(p, 0, blocks, s);
-      if (e == cudaSuccess) e = bwd_run<TX, TR, 8, true, 2, 512>(p, 0, blocks, s);
-    }
-    if constexpr (wide) {
-      if (e == cudaSuccess) e = bwd_run<TX, TR, 8, true, 3, 512>(p, 0, blocks, s);
-      if (e == cudaSuccess) e = bwd_run<TX, TR, 8, true, 4, 512>(p, 0, blocks, s);
-    }
-    return e;
-  }
-  AddNormBwdParams q = *p;
-  RowSplit split = V == 8 ? RowSplit(p->d, 2, wide ? 4 : 2, 512) : RowSplit(p->d, 1, 1, kNormMaxThreads);
+  AddNormBwdParams q = p;
+  RowSplit split = V == 8 ? RowSplit(p.d, 2, wide ? 4 : 2, 512) : RowSplit(p.d, 1, 1, kNormMaxThreads);
   q.group = split.group;
   if (split.group) {
     const int threads = split.threads();
     if constexpr (wide) {
-      if (split.nv == 3) return bwd_run<TX, TR, V, true, 3, 512>(&q, threads, blocks, s);
-      if (split.nv == 4) return bwd_run<TX, TR, V, true, 4, 512>(&q, threads, blocks, s);
+      if (split.nv == 3) return bwd_run<TX, TR, V, true, 3, 512>(q, threads, blocks, s);
+      if (split.nv == 4) return bwd_run<TX, TR, V, true, 4, 512>(q, threads, blocks, s);
     }
     if constexpr (V == 8) {
       if (split.nv == 2 && split.group <= kNormThreads)
-        return bwd_run<TX, TR, V, true, 2, kNormThreads>(&q, threads, blocks, s);
-      return split.nv == 1 ? bwd_run<TX, TR, V, true, 1, kNormThreads>(&q, threads, blocks, s)
-                           : bwd_run<TX, TR, V, true, 2, 512>(&q, threads, blocks, s);
+        return bwd_run<TX, TR, V, true, 2, kNormThreads>(q, threads, blocks, s);
+      return split.nv == 1 ? bwd_run<TX, TR, V, true, 1, kNormThreads>(q, threads, blocks, s)
+                           : bwd_run<TX, TR, V, true, 2, 512>(q, threads, blocks, s);
     } else {
-      if (split.group > 512) return bwd_run<TX, TR, V, false, 1, kNormMaxThreads>(&q, threads, blocks, s);
-      return split.group <= kNormThreads ? bwd_run<TX, TR, V, false, 1, kNormThreads>(&q, threads, blocks, s)
-                                         : bwd_run<TX, TR, V, false, 1, 512>(&q, threads, blocks, s);
+      if (split.group > 512) return bwd_run<TX, TR, V, false, 1, kNormMaxThreads>(q, threads, blocks, s);
+      return split.group <= kNormThreads ? bwd_run<TX, TR, V, false, 1, kNormThreads>(q, threads, blocks, s)
+                                         : bwd_run<TX, TR, V, false, 1, 512>(q, threads, blocks, s);
     }
   }
-  split = RowSplit(p->d, wide ? 3 : 2, 4, kNormMaxThreads);
+  split = RowSplit(p.d, wide ? 3 : 2, 4, kNormMaxThreads);
   q.group = split.group;
   if constexpr (!wide)
-    if (split.nv == 2) return bwd_run<TX, TR, V, false, 2, kNormMaxThreads>(&q, q.group, blocks, s);
-  return split.nv == 3 ? bwd_run<TX, TR, V, false, 3, kNormMaxThreads>(&q, q.group, blocks, s)
-                       : bwd_run<TX, TR, V, false, 4, kNormMaxThreads>(&q, q.group, blocks, s);
+    if (split.nv == 2) return bwd_run<TX, TR, V, false, 2, kNormMaxThreads>(q, q.group, blocks, s);
+  return split.nv == 3 ? bwd_run<TX, TR, V, false, 3, kNormMaxThreads>(q, q.group, blocks, s)
+                       : bwd_run<TX, TR, V, false, 4, kNormMaxThreads>(q, q.group, blocks, s);
 }
 
 template <typename TX, typename TR>
-cudaError_t bwd_vec(const AddNormBwdParams* p, int vec, int* blocks, cudaStream_t s) {
+cudaError_t bwd_vec(const AddNormBwdParams& p, int vec, int* blocks, cudaStream_t s) {
   return vec == 8   ? bwd_types<TX, TR, 8>(p, blocks, s)
          : vec == 2 ? bwd_types<TX, TR, 2>(p, blocks, s)
                     : bwd_types<TX, TR, 1>(p, blocks, s);
@@ -274,27 +261,18 @@ cudaError_t bwd_vec(const AddNormBwdParams* p, int vec, int* blocks, cudaStream_
 
 }  // namespace
 
-cudaError_t norm_bwd_init() {
-  cudaError_t e = bwd_vec<__nv_bfloat16, __nv_bfloat16>(nullptr, 8, nullptr, nullptr);
-  if (e == cudaSuccess) e = bwd_vec<__nv_bfloat16, float>(nullptr, 8, nullptr, nullptr);
-  if (e == cudaSuccess) e = bwd_vec<__half, __half>(nullptr, 8, nullptr, nullptr);
-  if (e == cudaSuccess) e = bwd_vec<__half, float>(nullptr, 8, nullptr, nullptr);
-  if (e == cudaSuccess) e = bwd_vec<float, float>(nullptr, 8, nullptr, nullptr);
-  return e;
-}
-
 cudaError_t launch_add_norm_bwd(const AddNormBwdParams& p, int dtype, int res_dtype, int vec, float* dw,
                                 cudaStream_t s) {
   const bool same = dtype == res_dtype;
   int blocks = 0;
   cudaError_t e;
   if (dtype == MOE_DT_BF16)
-    e = same ? bwd_vec<__nv_bfloat16, __nv_bfloat16>(&p, vec, &blocks, s)
-             : bwd_vec<__nv_bfloat16, float>(&p, vec, &blocks, s);
+    e = same ? bwd_vec<__nv_bfloat16, __nv_bfloat16>(p, vec, &blocks, s)
+             : bwd_vec<__nv_bfloat16, float>(p, vec, &blocks, s);
   else if (dtype == MOE_DT_F16)
-    e = same ? bwd_vec<__half, __half>(&p, vec, &blocks, s) : bwd_vec<__half, float>(&p, vec, &blocks, s);
+    e = same ? bwd_vec<__half, __half>(p, vec, &blocks, s) : bwd_vec<__half, float>(p, vec, &blocks, s);
   else
-    e = bwd_vec<float, float>(&p, vec, &blocks, s);
+    e = bwd_vec<float, float>(p, vec, &blocks, s);
   if (e != cudaSuccess || dw == nullptr) return e;
   return launch_pdl(add_norm_dw_kernel, dim3((unsigned)((p.d + 31) / 32)), dim3(1024), 0, s,
                     static_cast<const float*>(p.partial), blocks, p.d, dw);

@@ -608,10 +608,14 @@ template <typename T, int NT> MOE_DEV void staged_at(Vectors<T, NT>& v, const St
   v.table = at.table + t * 8;
 }
 
-// Raise a kernel's dynamic shared memory limit (once, from moe_init).
-template <typename F> cudaError_t allow_smem(F* kernel, int static_bytes = 0) {
-  return cudaFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                              cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost - static_bytes);
+// Launch a kernel that may have as much dynamic shared memory as there is beside its
+// `static_bytes`.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_w4(SmemLimit& limit, void (*kernel)(KArgs...), dim3 grid, size_t smem, int static_bytes,
+                      cudaStream_t s, Args&&... args) {
+  const cudaError_t e = limit.raise(reinterpret_cast<const void*>(kernel), kSmemMost - static_bytes);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kernel, grid, dim3(kW4Threads), smem, s, std::forward<Args>(args)...);
 }
 
 }  // namespace moe

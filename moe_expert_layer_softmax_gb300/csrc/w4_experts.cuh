@@ -523,38 +523,35 @@ struct Launch {
 };
 
 template <typename T, int W, int NT, XSource XS>
-cudaError_t up_launch(const ExpertsW4Params* p, cudaStream_t s) {
-  auto* kernel = &experts_w4_up_kernel<T, W, NT, XS>;
-  if (p == nullptr) return allow_smem(kernel);
-  const Launch l(*p, p->f / 8, p->d, 1, NT, XS == kStaged);
-  return launch_pdl(kernel, dim3(device_info()->sm_count), dim3(kW4Threads), l.smem, s, *p, l.plan);
+cudaError_t up_launch(const ExpertsW4Params& p, cudaStream_t s) {
+  static SmemLimit limit;
+  const Launch l(p, p.f / 8, p.d, 1, NT, XS == kStaged);
+  return launch_w4(limit, &experts_w4_up_kernel<T, W, NT, XS>, dim3(device_info()->sm_count), l.smem, 0, s, p, l.plan);
 }
 
 template <typename T, int W, int NT, XSource XS>
-cudaError_t down_launch(const ExpertsW4Params* p, cudaStream_t s) {
-  auto* kernel = &experts_w4_down_kernel<T, W, NT, XS>;
-  if (p == nullptr) return allow_smem(kernel);
-  const Launch l(*p, p->d / 16, p->f, 2, NT, XS == kStaged);
-  cudaError_t e = launch_pdl(kernel, dim3(device_info()->sm_count), dim3(kW4Threads), l.smem, s, *p, l.plan);
+cudaError_t down_launch(const ExpertsW4Params& p, cudaStream_t s) {
+  static SmemLimit limit;
+  const Launch l(p, p.d / 16, p.f, 2, NT, XS == kStaged);
+  const cudaError_t e = launch_w4(limit, &experts_w4_down_kernel<T, W, NT, XS>, dim3(device_info()->sm_count), l.smem,
+                                  0, s, p, l.plan);
   if (e != cudaSuccess) return e;
-  return launch_pdl(experts_w4_join_kernel<T>, dim3((p->d + 1023) / 1024, p->T), dim3(256), 0, s, *p);
+  return launch_pdl(experts_w4_join_kernel<T>, dim3((p.d + 1023) / 1024, p.T), dim3(256), 0, s, p);
 }
 
 int64_t token_bytes(const ExpertsW4Params& p) { return (int64_t)p.k * p.f * 4 + (int64_t)p.k * p.f / 128 * 4; }
 constexpr int kTokenStatic = 256;   // its static shared memory, rounded up
 
-template <typename T, int W> cudaError_t token_launch(const ExpertsW4Params* p, cudaStream_t s) {
-  auto* kernel = &experts_w4_token_kernel<T, W>;
-  if (p == nullptr) return allow_smem(kernel, kTokenStatic);
-  const int sms = device_info()->sm_count, per = p->d / 16;
+template <typename T, int W> cudaError_t token_launch(const ExpertsW4Params& p, cudaStream_t s) {
+  static SmemLimit limit;
+  const int sms = device_info()->sm_count, per = p.d / 16;
   const int blocks = per < sms ? per : sms;
   Plan plan;
   plan.most = 1;
-  const size_t smem = plan_smem((per + blocks - 1) / blocks, 1, (int)token_bytes(*p), kTokenStatic, &plan) - kTokenStatic;
-  return launch_pdl(kernel, dim3(blocks), dim3(kW4Threads), smem, s, *p, plan);
+  const size_t smem = plan_smem((per + blocks - 1) / blocks, 1, (int)token_bytes(p), kTokenStatic, &plan) - kTokenStatic;
+  return launch_w4(limit, &experts_w4_token_kernel<T, W>, dim3(blocks), smem, kTokenStatic, s, p, plan);
 }
 
-// p = NULL: raise every variant's shared memory limit.
 // Staged rounds serve eight routes of an expert, or sixteen where the experts
 // have more than six on average and a block still takes its tiles of an expert
 // in one segment.  Measured, eight and sixteen (us): 8 experts of 1536 x 1024, 12
@@ -563,35 +560,25 @@ template <typename T, int W> cudaError_t token_launch(const ExpertsW4Params* p, 
 // One token: W_down of all its experts as one product, 14.4 us, or a product for
 // each and their sum, 17.2 (2048 x 1408, four experts); 32.2 and 35.0 (4096 x 2048,
 // eight).
-template <typename T, int W> cudaError_t experts_nt(const ExpertsW4Params* p, cudaStream_t s) {
-  cudaError_t e = cudaSuccess;
-  if (p == nullptr) {
-    e = up_launch<T, W, 1, kStaged>(p, s);
-    if (e == cudaSuccess) e = up_launch<T, W, 2, kStaged>(p, s);
-    if (e == cudaSuccess) e = up_launch<T, W, 2, kNatural>(p, s);
-    if (e == cudaSuccess) e = down_launch<T, W, 1, kStaged>(p, s);
-    if (e == cudaSuccess) e = down_launch<T, W, 2, kStaged>(p, s);
-    if (e == cudaSuccess) e = down_launch<T, W, 2, kOrdered>(p, s);
-    return e == cudaSuccess ? token_launch<T, W>(p, s) : e;
-  }
-  const int R = p->T * p->k, few = p->T < 8 ? p->T : 8;
-  const bool token = p->T == 1 && staged_fits(token_bytes(*p), kTokenStatic, 1);
+template <typename T, int W> cudaError_t experts_nt(const ExpertsW4Params& p, cudaStream_t s) {
+  const int R = p.T * p.k, few = p.T < 8 ? p.T : 8;
+  const bool token = p.T == 1 && staged_fits(token_bytes(p), kTokenStatic, 1);
   // both kernels or none: they agree on the form of act
-  const bool staged = most_staged(*p, p->d, 1, 1) * 2 >= few && (token || most_staged(*p, p->f, 2, 1) * 2 >= few);
+  const bool staged = most_staged(p, p.d, 1, 1) * 2 >= few && (token || most_staged(p, p.f, 2, 1) * 2 >= few);
   if (!staged) {
-    e = up_launch<T, W, 2, kNatural>(p, s);
+    const cudaError_t e = up_launch<T, W, 2, kNatural>(p, s);
     return e == cudaSuccess ? down_launch<T, W, 2, kOrdered>(p, s) : e;
   }
-  const bool many = R > 6 * p->E;
-  const bool up2 = many && Launch(*p, p->f / 8, p->d, 1, 2, true).serves(*p, p->f / 8);
-  e = up2 ? up_launch<T, W, 2, kStaged>(p, s) : up_launch<T, W, 1, kStaged>(p, s);
+  const bool many = R > 6 * p.E;
+  const bool up2 = many && Launch(p, p.f / 8, p.d, 1, 2, true).serves(p, p.f / 8);
+  const cudaError_t e = up2 ? up_launch<T, W, 2, kStaged>(p, s) : up_launch<T, W, 1, kStaged>(p, s);
   if (e != cudaSuccess) return e;
   if (token) return token_launch<T, W>(p, s);
-  const bool down2 = many && Launch(*p, p->d / 16, p->f, 2, 2, true).serves(*p, p->d / 16);
+  const bool down2 = many && Launch(p, p.d / 16, p.f, 2, 2, true).serves(p, p.d / 16);
   return down2 ? down_launch<T, W, 2, kStaged>(p, s) : down_launch<T, W, 1, kStaged>(p, s);
 }
 
-template <typename T> cudaError_t experts_group(int group, const ExpertsW4Params* p, cudaStream_t s) {
+template <typename T> cudaError_t experts_group(int group, const ExpertsW4Params& p, cudaStream_t s) {
   if (group == 32) return experts_nt<T, 1>(p, s);
   if (group == 64) return experts_nt<T, 2>(p, s);
   return experts_nt<T, 4>(p, s);

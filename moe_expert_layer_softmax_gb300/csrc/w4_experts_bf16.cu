@@ -3,14 +3,8 @@
 
 namespace moe {
 
-cudaError_t experts_w4_init_bf16() {
-  cudaError_t e = cudaSuccess;
-  for (int g = 32; g <= 128 && e == cudaSuccess; g *= 2) e = experts_group<__nv_bfloat16>(g, nullptr, nullptr);
-  return e;
-}
-
 cudaError_t launch_experts_w4_bf16(const ExpertsW4Params& p, cudaStream_t s) {
-  return experts_group<__nv_bfloat16>(p.group, &p, s);
+  return experts_group<__nv_bfloat16>(p.group, p, s);
 }
 
 }  // namespace moe

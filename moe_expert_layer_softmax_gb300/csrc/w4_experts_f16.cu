@@ -3,14 +3,8 @@
 
 namespace moe {
 
-cudaError_t experts_w4_init_f16() {
-  cudaError_t e = cudaSuccess;
-  for (int g = 32; g <= 128 && e == cudaSuccess; g *= 2) e = experts_group<__half>(g, nullptr, nullptr);
-  return e;
-}
-
 cudaError_t launch_experts_w4_f16(const ExpertsW4Params& p, cudaStream_t s) {
-  return experts_group<__half>(p.group, &p, s);
+  return experts_group<__half>(p.group, p, s);
 }
 
 }  // namespace moe

@@ -105,19 +105,17 @@ int share_of(int N) {
   return (all + sms - 1) / sms;
 }
 
-// a = NULL: raise the kernel's shared memory limit.
 template <typename T, int W, int NT, XSource XS, bool FULL>
-cudaError_t matvec_launch(const MatvecArgs* a, cudaStream_t s) {
-  auto* kernel = &matvec_w4_kernel<T, W, NT, XS, FULL>;
-  if (a == nullptr) return allow_smem(kernel);
-  const int all = (a->N + 15) / 16, sms = device_info()->sm_count;
-  const int x_bytes = XS == kStaged ? (int)staged_bytes(a->M, a->K) : 0;
+cudaError_t matvec_launch(const MatvecArgs& a, cudaStream_t s) {
+  const int all = (a.N + 15) / 16, sms = device_info()->sm_count;
+  const int x_bytes = XS == kStaged ? (int)staged_bytes(a.M, a.K) : 0;
   const int room = (kSmemMost - kRingsBytes - x_bytes) / (NT * 512) - kW4Warps;
-  const int share = share_of(a->N);
-  MatvecArgs args = *a;
+  const int share = share_of(a.N);
+  MatvecArgs args = a;
   args.seg_tiles = share < room ? share : room;
   const size_t smem = kRingsBytes + (size_t)(args.seg_tiles + kW4Warps) * NT * 512 + x_bytes;
-  return launch_pdl(kernel, dim3(all < sms ? all : sms), dim3(kW4Threads), smem, s, args);
+  static SmemLimit limit;
+  return launch_w4(limit, &matvec_w4_kernel<T, W, NT, XS, FULL>, dim3(all < sms ? all : sms), smem, 0, s, args);
 }
 
 // Vectors are staged (whole stages only) where each block has a tile for every
@@ -131,45 +129,28 @@ cudaError_t matvec_launch(const MatvecArgs* a, cudaStream_t s) {
 // tiles: 8.5 and 9.7 with one, 10.7 and 12.1 with eight (in groups of 32 9.7 and 10.2,
 // 11.9 and 11.6); staged rounds of sixteen, when last tried, 15.9 and 14.1.
 template <typename T, int W, bool FULL>
-cudaError_t matvec_nt(const MatvecArgs* a, cudaStream_t s) {
+cudaError_t matvec_nt(const MatvecArgs& a, cudaStream_t s) {
   if constexpr (FULL) {
-    const bool staged = a == nullptr || (a->M <= 8 && a->M <= share_of(a->N) &&
-                                         staged_bytes(a->M, a->K) <= kSmemMost - kRingsBytes - (8 + kW4Warps) * 512);
-    const cudaError_t e = staged ? matvec_launch<T, W, 1, kStaged, FULL>(a, s) : cudaSuccess;
-    if ((a != nullptr && staged) || e != cudaSuccess) return e;
+    if (a.M <= 8 && a.M <= share_of(a.N) && staged_bytes(a.M, a.K) <= kSmemMost - kRingsBytes - (8 + kW4Warps) * 512)
+      return matvec_launch<T, W, 1, kStaged, FULL>(a, s);
   }
-  const cudaError_t e = a == nullptr || a->M > 16 ? matvec_launch<T, W, 4, kNatural, FULL>(a, s) : cudaSuccess;
-  if ((a != nullptr && a->M > 16) || e != cudaSuccess) return e;
-  return matvec_launch<T, W, 2, kNatural, FULL>(a, s);
+  return a.M > 16 ? matvec_launch<T, W, 4, kNatural, FULL>(a, s) : matvec_launch<T, W, 2, kNatural, FULL>(a, s);
 }
 
-template <typename T> cudaError_t matvec_group(int group, const MatvecArgs* a, cudaStream_t s) {
-  const bool full = a == nullptr || a->K % 128 == 0, cut = a == nullptr || !full;
-  cudaError_t e = cudaSuccess;
-  if (group == 32 && full) e = matvec_nt<T, 1, true>(a, s);
-  if (e == cudaSuccess && group == 32 && cut) e = matvec_nt<T, 1, false>(a, s);
-  if (e == cudaSuccess && group == 64 && full) e = matvec_nt<T, 2, true>(a, s);
-  if (e == cudaSuccess && group == 64 && cut) e = matvec_nt<T, 2, false>(a, s);
-  if (e == cudaSuccess && group == 128) e = matvec_nt<T, 4, true>(a, s);
-  return e;
+template <typename T> cudaError_t matvec_group(int group, const MatvecArgs& a, cudaStream_t s) {
+  const bool full = a.K % 128 == 0;
+  if (group == 32) return full ? matvec_nt<T, 1, true>(a, s) : matvec_nt<T, 1, false>(a, s);
+  if (group == 64) return full ? matvec_nt<T, 2, true>(a, s) : matvec_nt<T, 2, false>(a, s);
+  return matvec_nt<T, 4, true>(a, s);
 }
 
 }  // namespace
-
-cudaError_t matvec_w4_init() {
-  cudaError_t e = cudaSuccess;
-  for (int g = 32; g <= 128 && e == cudaSuccess; g *= 2) {
-    e = matvec_group<__nv_bfloat16>(g, nullptr, nullptr);
-    if (e == cudaSuccess) e = matvec_group<__half>(g, nullptr, nullptr);
-  }
-  return e;
-}
 
 cudaError_t launch_matvec_w4(int M, int N, int K, int group, int dtype, const void* x, int64_t ld_x,
                              const uint8_t* q, const void* scales, void* y, int64_t ld_y,
                              cudaStream_t s) {
   const MatvecArgs a = {M, N, K, x, ld_x, q, scales, y, ld_y, 0};
-  return dtype == MOE_DT_BF16 ? matvec_group<__nv_bfloat16>(group, &a, s) : matvec_group<__half>(group, &a, s);
+  return dtype == MOE_DT_BF16 ? matvec_group<__nv_bfloat16>(group, a, s) : matvec_group<__half>(group, a, s);
 }
 
 }  // namespace moe
