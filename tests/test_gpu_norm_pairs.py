@@ -1,6 +1,7 @@
 """Norm, backward and dropout where rows are read by pairs of columns (an even width
 that is no multiple of eight, or rows on a pair's boundary alone), from one warp a
-row to the widest rows, and the 8-bit output's inverse root mean square.  GPU only."""
+row to the widest rows, fp32 rows with the largest ring, and the 8-bit output's inverse
+root mean square.  GPU only."""
 import numpy as np
 import pytest
 import torch
@@ -49,6 +50,13 @@ def test_many_rows(moe_gpu):
     check_forward(m, dev, 2003, 1002, "f32", "f32", "f32", p=0.2)
     check_backward(m, dev, 5003, 126, "bf16", "f32", "bf16", p=0.2)
     check_backward(m, dev, 2003, 1002, "f16", "f16", "f16")
+
+
+@pytest.mark.parametrize("rows,p", [(310, 0.0), (2003, 0.0), (701, 0.2)], ids=str)
+def test_rows_with_the_largest_ring(moe_gpu, rows, p):
+    """fp32 rows whose ring leaves room for one block: one round of blocks, or two."""
+    m, dev = moe_gpu
+    check_forward(m, dev, rows, 7176, "f32", "f32", "f32", p=p)
 
 
 @pytest.mark.parametrize("cols", [2, 10, 62, 66, 126, 130, 254, 258, 1002, 2050])
