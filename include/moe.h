@@ -622,6 +622,76 @@ typedef struct {
 MOE_API int moe_add_norm_bwd_workspace_size(int64_t rows, int32_t d, size_t* ws_bytes);
 MOE_API int moe_add_norm_bwd(const moe_add_norm_bwd_args_t* args, void* ws, void* stream);
 
+/* The same with layer norm in place of the root-mean-square norm:
+ *   u = dropout(x), h = residual + u as above
+ *   mean = mean over d of h, rstd = (mean over d of (h - mean)^2 + eps)^(-1/2)
+ *   y = (h - mean) * rstd * weight + bias
+ * all of the rounded h, the deviations taken from the mean before they are squared.
+ * Types, layouts, strides, the 8-bit output and the envelope are those of
+ * moe_add_norm; bias is w_dtype [d] or NULL (none), mean like rstd fp32 [rows] or
+ * NULL (not wanted). */
+typedef struct {
+  int64_t rows;
+  int32_t d;
+  int32_t dtype;
+  int32_t res_dtype;
+  int32_t w_dtype;
+  const void* x;
+  int64_t ld_x;
+  const void* residual;
+  int64_t ld_residual;
+  const void* weight;
+  const void* bias;
+  void* h;
+  int64_t ld_h;
+  void* y;
+  int64_t ld_y;
+  float* mean;
+  float* rstd;
+  uint8_t* y_q;
+  uint8_t* y_scales;
+  void* y_dq;
+  uint64_t seed;
+  uint64_t offset;
+  float eps;
+  float p;
+} moe_add_layer_norm_args_t;
+MOE_API int moe_add_layer_norm(const moe_add_layer_norm_args_t* args, void* stream);
+
+/* Backward of moe_add_layer_norm from the h, mean and rstd that it wrote.  With
+ * g = weight * dy and n = (h - mean) * rstd:
+ *   dh = dres + rstd * (g - mean(g) - n * mean(g * n))
+ *   dx = dropout of dh;  dw = sum over rows of dy * n;  db = sum over rows of dy
+ * dh, dx, dw and db may each be NULL (not all); dw and db need `ws`, of
+ * moe_add_layer_norm_bwd_workspace_size bytes.  All else as moe_add_norm_bwd. */
+typedef struct {
+  int64_t rows;
+  int32_t d;
+  int32_t dtype;
+  int32_t res_dtype;
+  int32_t w_dtype;
+  const void* dy;
+  int64_t ld_dy;
+  const void* h;
+  int64_t ld_h;
+  const void* dres;
+  int64_t ld_dres;
+  const float* mean;
+  const float* rstd;
+  const void* weight;
+  void* dh;
+  int64_t ld_dh;
+  void* dx;
+  int64_t ld_dx;
+  float* dw;
+  float* db;
+  uint64_t seed;
+  uint64_t offset;
+  float p;
+} moe_add_layer_norm_bwd_args_t;
+MOE_API int moe_add_layer_norm_bwd_workspace_size(int64_t rows, int32_t d, size_t* ws_bytes);
+MOE_API int moe_add_layer_norm_bwd(const moe_add_layer_norm_bwd_args_t* args, void* ws, void* stream);
+
 /* Dropout of a [rows, cols] matrix with a mask that is computed, not stored:
  *   thr = round(p * 2^16);  y = x * 2^16 / (2^16 - thr) where the element's
  *   16-bit number is at least thr, else 0 (whatever x holds there).

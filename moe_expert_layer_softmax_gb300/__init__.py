@@ -50,7 +50,8 @@ EXPORTS = (
     "moe_route_noalloc", "moe_dequantize_mxfp8", "moe_build_mx_weights",
     "moe_debug_inject_stall", "moe_profile_start", "moe_profile_stop", "moe_load_balance",
     "moe_checks_read",
-    "moe_add_norm", "moe_add_norm_bwd_workspace_size", "moe_add_norm_bwd", "moe_dropout",
+    "moe_add_norm", "moe_add_norm_bwd_workspace_size", "moe_add_norm_bwd", "moe_add_layer_norm",
+    "moe_add_layer_norm_bwd_workspace_size", "moe_add_layer_norm_bwd", "moe_dropout",
     "moe_quantize_w4", "moe_dequantize_w4", "moe_matvec_w4", "moe_experts_w4_workspace_size",
     "moe_experts_w4",
 )
@@ -152,6 +153,9 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_add_norm": [_vp, _vp],
         "moe_add_norm_bwd_workspace_size": [i64, i32, P(ctypes.c_size_t)],
         "moe_add_norm_bwd": [_vp, _vp, _vp],
+        "moe_add_layer_norm": [_vp, _vp],
+        "moe_add_layer_norm_bwd_workspace_size": [i64, i32, P(ctypes.c_size_t)],
+        "moe_add_layer_norm_bwd": [_vp, _vp, _vp],
         "moe_dropout": [i64, i32, i32, _vp, i64, _vp, i64, ctypes.c_float, ctypes.c_uint64,
                         ctypes.c_uint64, _vp],
         "moe_quantize_w4": [i64, i32, i32, i32, _vp, _vp, _vp, _vp],
@@ -410,6 +414,8 @@ DT_BF16, DT_F16, DT_F32 = 0, 1, 2
 W4_MAX_ROUTES = 4096
 _ADD_NORM = struct.Struct("@qiiii" + "Pq" * 2 + "P" + "Pq" * 2 + "PPPP" + "QQff")
 _ADD_NORM_BWD = struct.Struct("@qiiii" + "Pq" * 3 + "PP" + "Pq" * 2 + "P" + "QQf0q")
+_ADD_LAYER_NORM = struct.Struct("@qiiii" + "Pq" * 2 + "PP" + "Pq" * 2 + "PPPPP" + "QQff")
+_ADD_LAYER_NORM_BWD = struct.Struct("@qiiii" + "Pq" * 3 + "PPP" + "Pq" * 2 + "PP" + "QQf0q")
 _EXPERTS_W4 = struct.Struct("@7i" + "P" * 10)
 _torch = None
 _dtypes = {}
@@ -555,6 +561,71 @@ def add_norm_bwd(dy, h, rstd, weight, dres=None, dh=None, dx=None, dw=None, ws=N
     rc = load().moe_add_norm_bwd(args, pws, st)
     if rc:
         _failed("moe_add_norm_bwd", rc, args, pws, st)
+
+
+def add_layer_norm(x, weight, bias, y, residual=None, h=None, mean=None, rstd=None, eps=1e-5, p=0.0, seed=0, offset=0,
+                   y_q=None, y_scales=None, y_dq=None, stream=None):
+    """moe_add_layer_norm: h = residual + dropout(x), y = (h - mean) * rstd * weight + bias
+    (bias=None: none).  y=None with y_q, y_scales (and y_dq): the MXFP8 output, buffers
+    of roundup(rows, 128) rows."""
+    xt = x.dtype
+    dt = _dtype(x, "x")
+    rows, d = _shape(x)
+    px, ld_x = _matrix(x, "x", rows, d, xt)
+    like = residual if residual is not None else h   # the stream's type
+    st = xt if like is None else like.dtype
+    pr, ld_r = _matrix(residual, "residual", rows, d, st)
+    ph, ld_h = _matrix(h, "h", rows, d, st)
+    py, ld_y = _matrix(y, "y", rows, d, xt)
+    pq = ps = pd = 0
+    if y_q is not None or y_scales is not None or y_dq is not None:
+        pad = (rows + 127) // 128 * 128
+        pq = _flat(y_q, "y_q", pad * d, _torch.uint8, True)
+        ps = _flat(y_scales, "y_scales", pad * d // 32, _torch.uint8, True)
+        pd = _flat(y_dq, "y_dq", pad * d, _torch.bfloat16, True)
+    f32 = _torch.float32
+    args = _ADD_LAYER_NORM.pack(
+        rows, d, dt, dt if like is None else _dtype(like, "residual"), _dtype(weight, "weight"),
+        px, ld_x, pr, ld_r, _flat(weight, "weight", d, weight.dtype), _flat(bias, "bias", d, weight.dtype), ph, ld_h,
+        py, ld_y, _flat(mean, "mean", rows, f32), _flat(rstd, "rstd", rows, f32), pq, ps, pd, seed, offset, eps, p)
+    st = _stream(stream)
+    rc = load().moe_add_layer_norm(args, st)
+    if rc:
+        _failed("moe_add_layer_norm", rc, args, st)
+
+
+def add_layer_norm_bwd_workspace(rows, d) -> int:
+    """Bytes of workspace that add_layer_norm_bwd needs for dw and db."""
+    v = ctypes.c_size_t()
+    _check("moe_add_layer_norm_bwd_workspace_size",
+           load().moe_add_layer_norm_bwd_workspace_size(int(rows), int(d), ctypes.byref(v)))
+    return v.value
+
+
+def add_layer_norm_bwd(dy, h, mean, rstd, weight, dres=None, dh=None, dx=None, dw=None, db=None, ws=None, p=0.0, seed=0,
+                       offset=0, stream=None):
+    """moe_add_layer_norm_bwd: dh (gradient of the stream), dx (of the dropped input),
+    dw and db."""
+    xt, ht = dy.dtype, h.dtype
+    dt = _dtype(dy, "dy")
+    rows, d = _shape(dy)
+    pdy, ld_dy = _matrix(dy, "dy", rows, d, xt)
+    ph, ld_h = _matrix(h, "h", rows, d, ht)
+    pdr, ld_dr = _matrix(dres, "dres", rows, d, ht)
+    pdh, ld_dh = _matrix(dh, "dh", rows, d, ht)
+    pdx, ld_dx = _matrix(dx, "dx", rows, d, xt)
+    pws = None
+    if dw is not None or db is not None:
+        pws = _flat(ws, "ws", add_layer_norm_bwd_workspace(rows, d), _torch.uint8, True) or None
+    f32 = _torch.float32
+    args = _ADD_LAYER_NORM_BWD.pack(
+        rows, d, dt, _dtype(h, "h"), _dtype(weight, "weight"), pdy, ld_dy, ph, ld_h, pdr, ld_dr,
+        _flat(mean, "mean", rows, f32), _flat(rstd, "rstd", rows, f32), _flat(weight, "weight", d, weight.dtype),
+        pdh, ld_dh, pdx, ld_dx, _flat(dw, "dw", d, f32), _flat(db, "db", d, f32), seed, offset, p)
+    st = _stream(stream)
+    rc = load().moe_add_layer_norm_bwd(args, pws, st)
+    if rc:
+        _failed("moe_add_layer_norm_bwd", rc, args, pws, st)
 
 
 def dropout(x, y, p, seed, offset=0, stream=None):

@@ -92,18 +92,11 @@ int check_experts(int32_t T, int32_t d, int32_t E, int32_t k, int32_t f, int32_t
   return MOE_OK;
 }
 
-}  // namespace
-
-}  // namespace moe
-
-using namespace moe;
-
-extern "C" {
-
-int moe_add_norm(const moe_add_norm_args_t* a, void* stream) {
-  if (a == nullptr) return MOE_ERR_INVALID;
+// Checks and parameters of either norm's forward; without rows p.rows
+// stays zero and nothing is launched.  The layer norm's bias and mean may be NULL.
+template <typename Args>
+int add_norm_params(const Args* a, const void* bias, float* mean, AddNormParams& p, int& vec) {
   MOE_TRY(check_norm_types(a->rows, a->d, a->dtype, a->res_dtype, a->w_dtype));
-  AddNormParams p = {};
   MOE_TRY(make_rng(a->p, a->seed, a->offset, &p.rng));
   if (!(a->eps >= 0.0f) || std::isinf(a->eps)) return MOE_ERR_INVALID;
   if (a->rows == 0) return MOE_OK;
@@ -117,10 +110,13 @@ int moe_add_norm(const moe_add_norm_args_t* a, void* stream) {
     return MOE_ERR_INVALID;   // the stream that the norm and the backward read
   }
   if (a->rstd && !on_boundary(a->rstd, 4)) return MOE_ERR_ALIGN;
-  int vec = row_access(a->x, a->ld_x, a->rows, a->dtype, width_access(a->d));
+  if (mean && !on_boundary(mean, 4)) return MOE_ERR_ALIGN;
+  if (bias && !on_boundary(bias, size_of(a->w_dtype))) return MOE_ERR_ALIGN;
+  vec = row_access(a->x, a->ld_x, a->rows, a->dtype, width_access(a->d));
   vec = row_access(a->residual, a->ld_residual, a->rows, a->res_dtype, vec);
   vec = row_access(a->h, a->ld_h, a->rows, a->res_dtype, vec);
   vec = row_access(a->weight, 0, 1, a->w_dtype, vec);
+  vec = row_access(bias, 0, 1, a->w_dtype, vec);
   p.rows_pad = a->rows;
   if (a->y_q) {
     // codes and scales for whole 128-row tiles, 128-column scale atoms
@@ -142,13 +138,72 @@ int moe_add_norm(const moe_add_norm_args_t* a, void* stream) {
   p.x = a->x; p.ld_x = a->ld_x;
   p.residual = a->residual; p.ld_residual = a->ld_residual;
   p.weight = a->weight;
+  p.bias = bias;
+  p.mean = mean;
   p.h = a->h; p.ld_h = a->ld_h;
   p.y = a->y; p.ld_y = a->ld_y;
   p.rstd = a->rstd;
   p.y_q = a->y_q; p.y_scales = a->y_scales; p.y_dq = a->y_dq;
   p.eps = a->eps;
-  return launch_add_norm(p, a->dtype, a->res_dtype, vec, static_cast<cudaStream_t>(stream)) ==
-                 cudaSuccess
+  return MOE_OK;
+}
+
+// The same for the backward.
+template <typename Args>
+int add_norm_bwd_params(const Args* a, const float* mean, bool sums, void* ws, AddNormBwdParams& p, int& vec) {
+  MOE_TRY(check_matrix(a->dy, a->ld_dy, a->d, a->dtype));
+  MOE_TRY(check_matrix(a->h, a->ld_h, a->d, a->res_dtype));
+  if (a->dres) MOE_TRY(check_matrix(a->dres, a->ld_dres, a->d, a->res_dtype));
+  if (a->dh) MOE_TRY(check_matrix(a->dh, a->ld_dh, a->d, a->res_dtype));
+  if (a->dx) MOE_TRY(check_matrix(a->dx, a->ld_dx, a->d, a->dtype));
+  if (a->rstd == nullptr || a->weight == nullptr) return MOE_ERR_INVALID;
+  if (!on_boundary(a->rstd, 4) || !on_boundary(a->weight, size_of(a->w_dtype))) return MOE_ERR_ALIGN;
+  if (sums) MOE_BUFFER(ws);
+  if (!ready()) return MOE_ERR_NOT_INIT;
+  vec = row_access(a->dy, a->ld_dy, a->rows, a->dtype, width_access(a->d));
+  vec = row_access(a->h, a->ld_h, a->rows, a->res_dtype, vec);
+  vec = row_access(a->dres, a->ld_dres, a->rows, a->res_dtype, vec);
+  vec = row_access(a->dh, a->ld_dh, a->rows, a->res_dtype, vec);
+  vec = row_access(a->dx, a->ld_dx, a->rows, a->dtype, vec);
+  vec = row_access(a->weight, 0, 1, a->w_dtype, vec);
+  p.rows = a->rows; p.d = a->d; p.inv_d = 1.0f / (float)a->d;
+  p.w_f32 = a->w_dtype == MOE_DT_F32; p.x_f16 = a->dtype == MOE_DT_F16;
+  p.dy = a->dy; p.ld_dy = a->ld_dy;
+  p.h = a->h; p.ld_h = a->ld_h;
+  p.dres = a->dres; p.ld_dres = a->ld_dres;
+  p.mean = mean; p.rstd = a->rstd; p.weight = a->weight;
+  p.dh = a->dh; p.ld_dh = a->ld_dh;
+  p.dx = a->dx; p.ld_dx = a->ld_dx;
+  p.partial = sums ? static_cast<float*>(ws) : nullptr;
+  return MOE_OK;
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" {
+
+int moe_add_norm(const moe_add_norm_args_t* a, void* stream) {
+  if (a == nullptr) return MOE_ERR_INVALID;
+  AddNormParams p = {};
+  int vec = 0;
+  MOE_TRY(add_norm_params(a, nullptr, nullptr, p, vec));
+  if (p.rows == 0) return MOE_OK;
+  return launch_add_norm(p, a->dtype, a->res_dtype, vec, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? MOE_OK
+             : MOE_ERR_CUDA;
+}
+
+int moe_add_layer_norm(const moe_add_layer_norm_args_t* a, void* stream) {
+  if (a == nullptr) return MOE_ERR_INVALID;
+  AddNormParams p = {};
+  int vec = 0;
+  MOE_TRY(add_norm_params(a, a->bias, a->mean, p, vec));
+  if (p.rows == 0) return MOE_OK;
+  return launch_add_layer_norm(p, a->dtype, a->res_dtype, vec, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MOE_OK
              : MOE_ERR_CUDA;
 }
@@ -172,33 +227,37 @@ int moe_add_norm_bwd(const moe_add_norm_bwd_args_t* a, void* ws, void* stream) {
     if (a->dw && cudaMemsetAsync(a->dw, 0, (size_t)a->d * 4, st) != cudaSuccess) return MOE_ERR_CUDA;
     return MOE_OK;
   }
-  MOE_TRY(check_matrix(a->dy, a->ld_dy, a->d, a->dtype));
-  MOE_TRY(check_matrix(a->h, a->ld_h, a->d, a->res_dtype));
-  if (a->dres) MOE_TRY(check_matrix(a->dres, a->ld_dres, a->d, a->res_dtype));
-  if (a->dh) MOE_TRY(check_matrix(a->dh, a->ld_dh, a->d, a->res_dtype));
-  if (a->dx) MOE_TRY(check_matrix(a->dx, a->ld_dx, a->d, a->dtype));
-  if (a->rstd == nullptr || a->weight == nullptr) return MOE_ERR_INVALID;
-  if (!on_boundary(a->rstd, 4) || !on_boundary(a->weight, size_of(a->w_dtype))) return MOE_ERR_ALIGN;
-  if (a->dw) MOE_BUFFER(ws);
-  if (!ready()) return MOE_ERR_NOT_INIT;
-  int vec = row_access(a->dy, a->ld_dy, a->rows, a->dtype, width_access(a->d));
-  vec = row_access(a->h, a->ld_h, a->rows, a->res_dtype, vec);
-  vec = row_access(a->dres, a->ld_dres, a->rows, a->res_dtype, vec);
-  vec = row_access(a->dh, a->ld_dh, a->rows, a->res_dtype, vec);
-  vec = row_access(a->dx, a->ld_dx, a->rows, a->dtype, vec);
-  vec = row_access(a->weight, 0, 1, a->w_dtype, vec);
-  p.rows = a->rows; p.d = a->d; p.inv_d = 1.0f / (float)a->d;
-  p.w_f32 = a->w_dtype == MOE_DT_F32; p.x_f16 = a->dtype == MOE_DT_F16;
-  p.dy = a->dy; p.ld_dy = a->ld_dy;
-  p.h = a->h; p.ld_h = a->ld_h;
-  p.dres = a->dres; p.ld_dres = a->ld_dres;
-  p.rstd = a->rstd; p.weight = a->weight;
-  p.dh = a->dh; p.ld_dh = a->ld_dh;
-  p.dx = a->dx; p.ld_dx = a->ld_dx;
-  p.partial = a->dw ? static_cast<float*>(ws) : nullptr;
-  return launch_add_norm_bwd(p, a->dtype, a->res_dtype, vec, a->dw, st) == cudaSuccess
-             ? MOE_OK
-             : MOE_ERR_CUDA;
+  int vec = 0;
+  MOE_TRY(add_norm_bwd_params(a, nullptr, a->dw != nullptr, ws, p, vec));
+  return launch_add_norm_bwd(p, a->dtype, a->res_dtype, vec, a->dw, st) == cudaSuccess ? MOE_OK : MOE_ERR_CUDA;
+}
+
+int moe_add_layer_norm_bwd_workspace_size(int64_t rows, int32_t d, size_t* ws_bytes) {
+  if (rows < 0 || d < 1 || ws_bytes == nullptr) return MOE_ERR_INVALID;
+  if (d > kNormMaxWidth || rows > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  *ws_bytes = round256((size_t)(rows < kNormPartialRows ? rows : kNormPartialRows) * d * 8);
+  return MOE_OK;
+}
+
+int moe_add_layer_norm_bwd(const moe_add_layer_norm_bwd_args_t* a, void* ws, void* stream) {
+  if (a == nullptr) return MOE_ERR_INVALID;
+  MOE_TRY(check_norm_types(a->rows, a->d, a->dtype, a->res_dtype, a->w_dtype));
+  AddNormBwdParams p = {};
+  MOE_TRY(make_rng(a->p, a->seed, a->offset, &p.rng));
+  if (!a->dh && !a->dx && !a->dw && !a->db) return MOE_ERR_INVALID;
+  if ((a->dw && !on_boundary(a->dw, 4)) || (a->db && !on_boundary(a->db, 4))) return MOE_ERR_ALIGN;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (a->rows == 0) {   // empty sums
+    for (float* sum : {a->dw, a->db})
+      if (sum && cudaMemsetAsync(sum, 0, (size_t)a->d * 4, st) != cudaSuccess) return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  if (a->mean == nullptr) return MOE_ERR_INVALID;
+  if (!on_boundary(a->mean, 4)) return MOE_ERR_ALIGN;
+  int vec = 0;
+  MOE_TRY(add_norm_bwd_params(a, a->mean, a->dw || a->db, ws, p, vec));
+  return launch_add_layer_norm_bwd(p, a->dtype, a->res_dtype, vec, a->dw, a->db, st) == cudaSuccess ? MOE_OK
+                                                                                                    : MOE_ERR_CUDA;
 }
 
 int moe_dropout(int64_t rows, int32_t cols, int32_t dtype, const void* x, int64_t ld_x, void* y,

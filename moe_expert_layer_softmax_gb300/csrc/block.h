@@ -20,10 +20,12 @@ struct AddNormParams {
   const void* residual;
   int64_t ld_residual;
   const void* weight;
+  const void* bias;         // layer norm, nullable
   void* h;
   int64_t ld_h;
   void* y;
   int64_t ld_y;
+  float* mean;              // layer norm, nullable
   float* rstd;
   uint8_t* y_q;
   uint8_t* y_scales;
@@ -44,6 +46,7 @@ struct AddNormBwdParams {
   int64_t ld_h;
   const void* dres;
   int64_t ld_dres;
+  const float* mean;   // layer norm
   const float* rstd;
   const void* weight;
   void* dh;
@@ -72,6 +75,9 @@ constexpr int kNormPartialRows = 1024;   // most blocks of the backward: rows of
 cudaError_t launch_add_norm(const AddNormParams& p, int dtype, int res_dtype, int vec, cudaStream_t s);
 cudaError_t launch_add_norm_bwd(const AddNormBwdParams& p, int dtype, int res_dtype, int vec, float* dw,
                                 cudaStream_t s);
+cudaError_t launch_add_layer_norm(const AddNormParams& p, int dtype, int res_dtype, int vec, cudaStream_t s);
+cudaError_t launch_add_layer_norm_bwd(const AddNormBwdParams& p, int dtype, int res_dtype, int vec, float* dw, float* db,
+                                      cudaStream_t s);
 cudaError_t launch_dropout(const DropoutParams& p, int dtype, int vec, cudaStream_t s);
 
 // ---------------------------------------------------------------- 4-bit weights

@@ -1,0 +1,11 @@
+// Backward of the residual addition with layer norm: norm_bwd.cuh.
+#include "norm_bwd.cuh"
+
+namespace moe {
+
+cudaError_t launch_add_layer_norm_bwd(const AddNormBwdParams& p, int dtype, int res_dtype, int vec, float* dw, float* db,
+                                      cudaStream_t s) {
+  return bwd_launch<true>(p, dtype, res_dtype, vec, dw, db, s);
+}
+
+}  // namespace moe

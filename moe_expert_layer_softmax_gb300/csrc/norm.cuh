@@ -95,6 +95,34 @@ template <bool SMALL> struct RowGroup {
     }
     return s;
   }
+  // Two sums behind one barrier.
+  MOE_DEV void sum2(float& v, float& w, float* red, float* red2) const {
+    for (int off = (!SMALL || G >= 32) ? 16 : G >> 1; off > 0; off >>= 1) {
+      v += __shfl_xor_sync(0xffffffffu, v, off);
+      w += __shfl_xor_sync(0xffffffffu, w, off);
+    }
+    if (G <= 32) return;
+    if ((threadIdx.x & 31) == 0) {
+      red[threadIdx.x >> 5] = v;
+      red2[threadIdx.x >> 5] = w;
+    }
+    bar_sync(1 + group, G);
+    const int n = G >> 5;
+    const float *from = red + group * n, *from2 = red2 + group * n;
+    v = w = 0.0f;
+    if (n & 3) {
+      for (int i = 0; i < n; ++i) {
+        v += from[i];
+        w += from2[i];
+      }
+    } else {
+      for (int i = 0; i < n; i += 4) {
+        const float4 q = *reinterpret_cast<const float4*>(from + i), u = *reinterpret_cast<const float4*>(from2 + i);
+        v += (q.x + q.y) + (q.z + q.w);
+        w += (u.x + u.y) + (u.z + u.w);
+      }
+    }
+  }
 };
 
 // 1 / sqrt(v) to about an ulp: the approximation and one Newton step.

@@ -73,6 +73,30 @@ def add_norm_bwd(dy, h, rstd, weight, dres=None, p=0.0, seed=0, offset=0):
     return dh, dropout(dh, p, seed, offset), (dy * h * r).sum(0)
 
 
+def add_layer_norm(x, residual, weight, bias, eps, p=0.0, seed=0, offset=0, rounder=lambda v: v):
+    """(h, y, mean, rstd): h is rounded by `rounder` (the stream's type) before its norm."""
+    h = dropout(x, p, seed, offset)
+    if residual is not None:
+        h = h + residual
+    h = rounder(h)
+    mean = h.mean(-1)
+    c = h - mean[:, None]
+    rstd = 1.0 / np.sqrt((c * c).mean(-1) + eps)
+    y = c * rstd[:, None] * weight
+    return h, y if bias is None else y + bias, mean, rstd
+
+
+def add_layer_norm_bwd(dy, h, mean, rstd, weight, dres=None, p=0.0, seed=0, offset=0):
+    """(dh, dx, dw, db) from the saved h, mean and rstd."""
+    r = rstd[:, None]
+    n = (h - mean[:, None]) * r
+    g = dy * weight
+    dh = r * (g - g.mean(-1, keepdims=True) - n * (g * n).mean(-1, keepdims=True))
+    if dres is not None:
+        dh = dh + dres
+    return dh, dropout(dh, p, seed, offset), (dy * n).sum(0), dy.sum(0)
+
+
 def w4_quantize(w, group, rounder):
     """codes [rows, K] 0..15 and scales [rows, K / group] (rounded by `rounder`)."""
     b = w.reshape(w.shape[0], -1, group)
