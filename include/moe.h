@@ -524,14 +524,15 @@ MOE_API int moe_layer_bwd(const moe_shape_t* shape, const moe_bwd_args_t* args, 
 
 /* ------------------------------------------------------------ around the layer
  * The operators that stand next to the layer in a transformer block: the
- * residual addition with the norm before it (and the dropout of its output),
- * and the experts on 4-bit weights for serving.  The pages have no counterpart
+ * residual addition with the norm before it (and the dropout of its output), the
+ * optimiser's step on what the backward leaves, and the experts on 4-bit weights for
+ * serving.  The pages have no counterpart
  * to these calls; their arithmetic is written out with each.  examples/block.py
  * runs them together with the layer.
  *
- * Matrices with a row stride `ld` (elements, >= the row's length), the norm's
- * weight and rstd and dw need only the alignment of their element type; every
- * other pointer (codes, scales, 8-bit outputs, workspaces, and all of
+ * Matrices with a row stride `ld` (elements, >= the row's length), the norms'
+ * weight, bias, mean, rstd, dw and db, and what moe_adamw takes need only the alignment
+ * of their element type; every other pointer (codes, scales, 8-bit outputs, workspaces, and all of
  * moe_experts_w4, topk_idx and gates among them) a 16-byte boundary, as does the x
  * of moe_matvec_w4 (its rows too).  Rows whose groups of eight columns lie on
  * 16-byte boundaries (base 16-byte aligned, row stride a multiple of 16 bytes, the
@@ -704,6 +705,67 @@ MOE_API int moe_add_layer_norm_bwd(const moe_add_layer_norm_bwd_args_t* args, vo
 MOE_API int moe_dropout(int64_t rows, int32_t cols, int32_t dtype, const void* x, int64_t ld_x,
                         void* y, int64_t ld_y, float p, uint64_t seed, uint64_t offset,
                         void* stream);
+
+/* AdamW over a list of tensors (what the layer's and the norms' backward leave in
+ * their gradient buffers), in one launch for each 224 of them.  For every value, each
+ * operation rounded to 32 bits by itself, in this order:
+ *   g = grad * grad_scale                       (grad_scale NULL: g = grad)
+ *   m = beta1 * m + (1 - beta1) * g
+ *   v = beta2 * v + (1 - beta2) * (g * g),  root = sqrt(v)
+ *   w = w * (1 - lr * weight_decay)
+ *       - (m / (root * (1 / sqrt(1 - beta2^step)) + eps)) * (lr / (1 - beta1^step))
+ * (the constants in parentheses are computed in 64 bits and rounded once.)
+ *   param   param_dtype [numel]     grad  grad_dtype [numel]: param_dtype or fp32
+ *   master  fp32 [numel]: w itself, param is its rounding; or NULL: w is param, which
+ *           is fp32, or bf16 with drawn rounding (below).  fp16 needs a master.  All
+ *           tensors of a call have one or none.
+ *   m, v    state_bits 32: fp32 [numel].  state_bits 8: E4M3 codes [numel] of m and of
+ *           root (not v), value = code * scale, with m_scale, v_scale fp32
+ *           [ceil(numel / 128)], one for 128 neighbouring values: the largest finite
+ *           magnitude among them / 448 (0, and codes 0, below 2^-100).  A magnitude
+ *           between two codes takes the upper one where the remainder, in units of
+ *           their distance, is at least 1 - number / 2^16, but a root above zero never
+ *           code 0.  An infinity or a NaN is held as a NaN.  States of zeros are zero
+ *           codes with any scale.
+ * Drawn rounding of bf16: number is added to the 32 bits of w, the lower 16 are cut.
+ * number: half-word i % 8 (low half-words first) of Philox4x32-10 (as moe_dropout) with
+ * key = seed and counter (i / 8, 4 * place of the tensor in the list + what, offset low,
+ * offset high), what = 0 for m, 1 for root, 2 for param: each step gives another offset.
+ * lr_dev (fp32) and step_dev (int64), where not NULL, are read on the device in place
+ * of lr and step: a captured step then follows them.  grad_scale: fp32 on the device.
+ * Pointers need their element's alignment (codes: none); tensors whose pointers all lie
+ * on 16-byte boundaries (codes: 8) take vector accesses.  `tensors` is a host array, read before
+ * the call returns; no two tensors may overlap.  numel may be 0.
+ * Envelope: numel <= 2^34, 0 <= beta < 1, eps, lr, weight_decay >= 0, step >= 1. */
+typedef struct {
+  void* param;
+  const void* grad;
+  float* master;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t numel;
+} moe_adamw_tensor_t;
+typedef struct {
+  const moe_adamw_tensor_t* tensors;
+  int32_t n_tensors;
+  int32_t param_dtype;
+  int32_t grad_dtype;
+  int32_t state_bits;
+  const float* grad_scale;
+  const float* lr_dev;
+  const int64_t* step_dev;
+  double lr;
+  double beta1;
+  double beta2;
+  double eps;
+  double weight_decay;
+  int64_t step;
+  uint64_t seed;
+  uint64_t offset;
+} moe_adamw_args_t;
+MOE_API int moe_adamw(const moe_adamw_args_t* args, void* stream);
 
 /* 4-bit weights with group scales along K (G = group = 32, 64 or 128, K a
  * multiple of it): W[n, k] = (code[n, k] - 8) * scale[n, k / G], codes 0..15.

@@ -51,7 +51,7 @@ EXPORTS = (
     "moe_debug_inject_stall", "moe_profile_start", "moe_profile_stop", "moe_load_balance",
     "moe_checks_read",
     "moe_add_norm", "moe_add_norm_bwd_workspace_size", "moe_add_norm_bwd", "moe_add_layer_norm",
-    "moe_add_layer_norm_bwd_workspace_size", "moe_add_layer_norm_bwd", "moe_dropout",
+    "moe_add_layer_norm_bwd_workspace_size", "moe_add_layer_norm_bwd", "moe_dropout", "moe_adamw",
     "moe_quantize_w4", "moe_dequantize_w4", "moe_matvec_w4", "moe_experts_w4_workspace_size",
     "moe_experts_w4",
 )
@@ -158,6 +158,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_add_layer_norm_bwd": [_vp, _vp, _vp],
         "moe_dropout": [i64, i32, i32, _vp, i64, _vp, i64, ctypes.c_float, ctypes.c_uint64,
                         ctypes.c_uint64, _vp],
+        "moe_adamw": [_vp, _vp],
         "moe_quantize_w4": [i64, i32, i32, i32, _vp, _vp, _vp, _vp],
         "moe_dequantize_w4": [i64, i32, i32, i32, _vp, _vp, _vp, _vp],
         "moe_matvec_w4": [i32] * 5 + [_vp, i64, _vp, _vp, _vp, i64, _vp],
@@ -416,6 +417,8 @@ _ADD_NORM = struct.Struct("@qiiii" + "Pq" * 2 + "P" + "Pq" * 2 + "PPPP" + "QQff"
 _ADD_NORM_BWD = struct.Struct("@qiiii" + "Pq" * 3 + "PP" + "Pq" * 2 + "P" + "QQf0q")
 _ADD_LAYER_NORM = struct.Struct("@qiiii" + "Pq" * 2 + "PP" + "Pq" * 2 + "PPPPP" + "QQff")
 _ADD_LAYER_NORM_BWD = struct.Struct("@qiiii" + "Pq" * 3 + "PPP" + "Pq" * 2 + "PP" + "QQf0q")
+_ADAMW_TENSOR = struct.Struct("@7Pq")
+_ADAMW = struct.Struct("@P4iPPP5dqQQ")
 _EXPERTS_W4 = struct.Struct("@7i" + "P" * 10)
 _torch = None
 _dtypes = {}
@@ -639,6 +642,100 @@ def dropout(x, y, p, seed, offset=0, stream=None):
     rc = load().moe_dropout(*args)
     if rc:
         _failed("moe_dropout", rc, *args)
+
+
+class AdamWList:
+    """The tensors of moe_adamw, checked and laid out once (adamw_list).  It holds them,
+    and a step works on the memory that they had when the list was made."""
+
+    __slots__ = ("tensors", "n", "types", "device", "held")
+
+
+ADAMW_BLOCK = 128   # values that share a scale of the 8-bit states
+
+
+def adamw_list(params, grads, exp_avg, exp_avg_sq, master=None) -> AdamWList:
+    """Contiguous CUDA tensors of one device, four (with master five) lists of the same
+    length.  An entry of exp_avg and exp_avg_sq is an fp32 tensor or, for states in 8 bits,
+    a pair (uint8 codes, fp32 scales of ADAMW_BLOCK values each); all are of one kind, as
+    are all params' types and all grads'."""
+    params, grads, exp_avg, exp_avg_sq = list(params), list(grads), list(exp_avg), list(exp_avg_sq)
+    master = None if master is None else list(master)
+    n = len(params)
+    if any(len(v) != n for v in (grads, exp_avg, exp_avg_sq)) or (master is not None and len(master) != n):
+        raise ValueError("adamw_list: lists of different lengths")
+    lst = AdamWList()
+    lst.n, lst.device = n, None
+    if n == 0:
+        lst.tensors, lst.types, lst.held = b"", (DT_F32, DT_F32, 32), ()
+        return lst
+    pt, gt, small = params[0].dtype, grads[0].dtype, isinstance(exp_avg[0], (tuple, list))
+    lst.types = (_dtype(params[0], "params"), _dtype(grads[0], "grads"), 8 if small else 32)
+    dev = params[0].get_device()
+    packed, written, held = [], [], []
+
+    def take(t, what, numel, dtype):
+        if not t.is_cuda or not t.is_contiguous():
+            raise ValueError(f"{what}: not a contiguous CUDA tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{what}: on {t.device}, the first parameter on device {dev}")
+        if t.dtype is not dtype:
+            raise TypeError(f"{what}: {t.dtype}, expected {dtype}")
+        if t.numel() != numel:
+            raise ValueError(f"{what}: {t.numel()} elements, expected {numel}")
+        held.append(t)
+        at = t.data_ptr()
+        if numel and what != "grads":
+            written.append((at, at + numel * t.element_size(), what))
+        return at
+
+    f32, u8 = _torch.float32, _torch.uint8
+    for i in range(n):
+        numel = params[i].numel()
+        states, scales = [], []
+        for s, what in ((exp_avg[i], "exp_avg"), (exp_avg_sq[i], "exp_avg_sq")):
+            if isinstance(s, (tuple, list)) != small:
+                raise TypeError(f"{what}: states in 8 and in 32 bits in one list")
+            if small:
+                states.append(take(s[0], what, numel, u8))
+                scales.append(take(s[1], what + " scales", (numel + ADAMW_BLOCK - 1) // ADAMW_BLOCK, f32))
+            else:
+                states.append(take(s, what, numel, f32))
+                scales.append(0)
+        packed.append(_ADAMW_TENSOR.pack(
+            take(params[i], "params", numel, pt), take(grads[i], "grads", numel, gt),
+            0 if master is None else take(master[i], "master", numel, f32), *states, *scales, numel))
+    written.sort()
+    for (_, end, a), (start, _, b) in zip(written, written[1:]):
+        if start < end:
+            raise ValueError(f"adamw_list: memory of {a} and {b} overlaps")
+    lst.tensors, lst.device, lst.held = b"".join(packed), dev, tuple(held)
+    return lst
+
+
+def adamw(tensors: AdamWList, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, grad_scale=None, seed=0,
+          offset=0, stream=None):
+    """moe_adamw: one step on every tensor of the list.  lr (fp32) and step (int64, from 1)
+    are numbers or CUDA tensors of one element, read when the kernel runs; grad_scale: a
+    CUDA fp32 tensor of one element that the gradients are multiplied with.  seed and
+    offset choose the numbers of drawn roundings: another offset for each step."""
+    lst = tensors
+    if lst.n == 0:
+        return
+    if _several and lst.device != _torch.cuda.current_device():
+        raise ValueError(f"adamw: tensors on device {lst.device}, not on the current device")
+    plr = pstep = 0
+    if not isinstance(lr, (int, float)):
+        plr, lr = _flat(lr, "lr", 1, _torch.float32), 0.0
+    if not isinstance(step, int):
+        pstep, step = _flat(step, "step", 1, _torch.int64), 1
+    host = ctypes.c_char_p(lst.tensors)
+    args = _ADAMW.pack(ctypes.cast(host, _vp).value, lst.n, *lst.types, _flat(grad_scale, "grad_scale", 1, _torch.float32),
+                       plr, pstep, lr, beta1, beta2, eps, weight_decay, step, seed, offset)
+    st = _stream(stream)
+    rc = load().moe_adamw(args, st)
+    if rc:
+        _failed("moe_adamw", rc, args, st)
 
 
 def _w4(q, scales, what):

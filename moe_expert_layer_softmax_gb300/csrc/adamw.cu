@@ -1,0 +1,290 @@
+// AdamW over many tensors in one launch (sm_103a).
+//
+//   g = grad * grad_scale
+//   m = b1 m + (1 - b1) g,  v = b2 v + (1 - b2) g g,  root = sqrt(v)
+//   p = p (1 - lr wd) - (lr / (1 - b1^t)) * (m / (root / sqrt(1 - b2^t) + eps))
+// Every product, sum, quotient and root is rounded to 32 bits by itself, in this
+// order (no contraction): a step can be repeated bit for bit by any program that
+// does the same.
+//
+// States in 8 bits: E4M3 codes with one fp32 scale (largest magnitude / 448) for
+// 128 neighbouring values.  The second moment is held as its root, which halves its
+// range in powers of two: 448 / 2^-9 of the codes is then 2^36 of v in a block.  A
+// state that moves by a few per cent a step (1 - b2 = 0.001) would stand still if it
+// were rounded to the nearest of steps of 6 to 12 per cent; it is rounded up with the
+// probability of its remainder instead, by 16 bits of the generator that the dropout
+// uses, so that its mean is right.  A root above zero is never held as zero: a first
+// moment beside it that was rounded up would otherwise be divided by eps alone.
+// Parameters in bf16 without an fp32 copy are rounded in the same way, for the same
+// reason: a step of lr is often less than half of theirs.
+//
+// The least that a step costs is one read of the gradient and one read and one write
+// of everything else.  A block takes 2048 neighbouring values, a thread eight, all
+// loads issued before the first is used.
+#include "block.cuh"
+#include "block.h"
+#include "kernels.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kAdamThreads = 256;
+constexpr int kAdamChunk = kAdamThreads * 8;   // values of a block: whole scale blocks
+
+template <int N> struct AdamwList {
+  AdamwTensor t[N];   // `first` ascending, behind the last one in use: the end
+  AdamwParams p;
+};
+
+// b^t in double, by squaring.
+MOE_DEV double power(double b, int64_t t) {
+  double r = 1.0;
+  for (; t > 0; t >>= 1, b *= b)
+    if (t & 1) r *= b;
+  return r;
+}
+
+// The constants of a step whose rate or number is on the device.
+MOE_DEV AdamwScalars scalars_of(const AdamwParams& p) {
+  AdamwScalars s = p.s;
+  const double lr = p.lr_dev ? (double)*p.lr_dev : p.lr;
+  double c1 = p.c1;
+  if (p.step_dev) {
+    const int64_t t = *p.step_dev;
+    c1 = 1.0 - power(p.beta1, t);
+    s.root_scale = (float)(1.0 / sqrt(1.0 - power(p.beta2, t)));
+  }
+  s.decay = (float)(1.0 - lr * p.weight_decay);
+  s.rate = (float)(lr / c1);
+  return s;
+}
+
+// Eight values from `at`; behind `n` zeros.
+template <typename T> MOE_DEV Raw8<T> fetch8(const T* p, int64_t at, int64_t n, bool vec) {
+  if (vec) return load8<T, 8>(p + at, 0, 1, 8);
+  Raw8<T> r;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) r.v[j] = at + j < n ? p[at + j] : Elem<T>::from_f(0.0f);
+  return r;
+}
+template <typename T> MOE_DEV void put8(T* p, int64_t at, int64_t n, bool vec, const Raw8<T>& r) {
+  if (vec) return store8<T, 8>(p + at, 0, 1, 8, r);
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+    if (at + j < n) p[at + j] = r.v[j];
+}
+
+// Number j (16 bits) of the eight that a counter gives.
+MOE_DEV uint32_t number_of(const uint4& r, int j) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  return j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFFu;
+}
+
+// The magnitude z in [0, 448] to one of its E4M3 neighbours: up where the remainder,
+// in units of the distance of the two, is at least 1 - r / 2^16.
+MOE_DEV float round_e4m3(float z, uint32_t r) {
+  const uint32_t e = max(__float_as_uint(z) >> 23, 121u);   // 2^-6 and below: steps of 2^-9
+  const float q = z * __uint_as_float((257u - e) << 23);
+  const float low = floorf(q);
+  const bool up = (q - low) * 65536.0f >= (float)(65536u - r);
+  return (low + (up ? 1.0f : 0.0f)) * __uint_as_float((e - 3u) << 23);
+}
+
+// Eight values to codes with the scale of the 16 lanes' 128 values; the scale is
+// returned.  An infinity or a NaN becomes a NaN and takes no part in the scale.
+// LEAST: what is above zero does not become zero.
+template <bool LEAST> MOE_DEV float quantize8(const float* x, const uint4& numbers, uint2& codes) {
+  float top = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]) < INFINITY ? fabsf(x[j]) : 0.0f);
+#pragma unroll
+  for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  const bool some = top >= 0x1p-100f;   // smaller values have no inverse in 32 bits
+  const float inv = some ? __fmul_rn(448.0f, __frcp_rn(top)) : 0.0f;
+  float c[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float z = fminf(__fmul_rn(fabsf(x[j]), inv), 448.0f);
+    float q = round_e4m3(z, number_of(numbers, j));
+    if (LEAST && z > 0.0f && q == 0.0f) q = 0x1p-9f;
+    c[j] = fabsf(x[j]) < INFINITY ? copysignf(q, x[j]) : NAN;
+  }
+  codes = e4m3x8(c);
+  return some ? __fmul_rn(top, 1.0f / 448.0f) : 0.0f;
+}
+
+MOE_DEV void widen_codes(const uint2& q, float scale, float* f) {
+  e4m3x2_to_f32(q.x, f[0], f[1]);
+  e4m3x2_to_f32(q.x >> 16, f[2], f[3]);
+  e4m3x2_to_f32(q.y, f[4], f[5]);
+  e4m3x2_to_f32(q.y >> 16, f[6], f[7]);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], scale);
+}
+
+// TP, TG: types of parameters and gradients; MASTER: the fp32 copy is what is
+// stepped, the parameter its rounding; SMALL: states in 8 bits.
+template <int N, typename TP, typename TG, bool MASTER, bool SMALL>
+__global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_constant__ AdamwList<N> list) {
+  constexpr bool DRAWN = !MASTER && sizeof(TP) == 2;   // parameters rounded by the generator
+  __shared__ AdamwScalars shared;
+  pdl_begin();
+  const AdamwParams& p = list.p;
+  AdamwScalars s = p.s;
+  if (p.lr_dev || p.step_dev) {
+    if (threadIdx.x == 0) shared = scalars_of(p);
+    __syncthreads();
+    s = shared;
+  }
+  // the tensor of this block: the last one that begins at or before it
+  int lo = 0, hi = p.n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (list.t[mid].first <= blockIdx.x) lo = mid; else hi = mid;
+  }
+  const AdamwTensor& t = list.t[lo];
+  const int64_t n = t.numel, at = (int64_t)(blockIdx.x - t.first) * kAdamChunk + threadIdx.x * 8;
+  const bool vec = t.vec && at + 8 <= n;
+  const bool live = at < n;
+  const int64_t block = at / kStateBlock;
+
+  float g[8], w[8], m[8], v[8];
+  {
+    const Raw8<TG> gr = fetch8(static_cast<const TG*>(t.grad), at, n, vec);
+    Raw8<float> wm;
+    Raw8<TP> wp;
+    if constexpr (MASTER)
+      wm = fetch8<float>(t.master, at, n, vec);
+    else
+      wp = fetch8(static_cast<const TP*>(t.param), at, n, vec);
+    if constexpr (SMALL) {
+      uint2 mq = {}, vq = {};
+      float ms = 0.0f, vs = 0.0f;
+      if (live) {
+        ms = t.m_scale[block];
+        vs = t.v_scale[block];
+      }
+      const uint8_t *mc = static_cast<const uint8_t*>(t.m), *vc = static_cast<const uint8_t*>(t.v);
+      if (vec) {
+        mq = *reinterpret_cast<const uint2*>(mc + at);
+        vq = *reinterpret_cast<const uint2*>(vc + at);
+      } else {
+        uint32_t mw[2] = {}, vw[2] = {};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (at + j < n) {
+            mw[j >> 2] |= (uint32_t)mc[at + j] << (8 * (j & 3));
+            vw[j >> 2] |= (uint32_t)vc[at + j] << (8 * (j & 3));
+          }
+        }
+        mq = make_uint2(mw[0], mw[1]);
+        vq = make_uint2(vw[0], vw[1]);
+      }
+      widen_codes(mq, ms, m);
+      widen_codes(vq, vs, v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
+    } else {
+      widen8(fetch8<float>(static_cast<const float*>(t.m), at, n, vec), m);
+      widen8(fetch8<float>(static_cast<const float*>(t.v), at, n, vec), v);
+    }
+    widen8(gr, g);
+    if constexpr (MASTER) widen8(wm, w); else widen8(wp, w);
+  }
+  if (p.grad_scale) {
+    const float scale = *p.grad_scale;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] = __fmul_rn(g[j], scale);
+  }
+  float root[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    m[j] = __fadd_rn(__fmul_rn(m[j], s.beta1), __fmul_rn(g[j], s.one_beta1));
+    v[j] = __fadd_rn(__fmul_rn(v[j], s.beta2), __fmul_rn(__fmul_rn(g[j], g[j]), s.one_beta2));
+    root[j] = __fsqrt_rn(v[j]);
+    const float d = __fadd_rn(__fmul_rn(root[j], s.root_scale), s.eps);
+    w[j] = __fadd_rn(__fmul_rn(w[j], s.decay), -__fmul_rn(__fdiv_rn(m[j], d), s.rate));
+  }
+  uint4 numbers[3];
+  if constexpr (SMALL || DRAWN) {
+    // the place's counter: its group of eight, the tensor and what is rounded
+    const uint32_t tensor = 4u * (uint32_t)(p.first_tensor + lo), group = (uint32_t)(at >> 3);
+    constexpr int from = SMALL ? 0 : 2, count = (SMALL ? 2 : 0) + (DRAWN ? 1 : 0);
+    uint4 c[count];
+#pragma unroll
+    for (int i = 0; i < count; ++i) c[i] = make_uint4(group, tensor + from + i, p.o0, p.o1);
+    philox4x32_10(c, p.k0, p.k1);
+#pragma unroll
+    for (int i = 0; i < count; ++i) numbers[from + i] = c[i];
+  }
+  if constexpr (SMALL) {
+    uint2 mq, vq;
+    const float ms = quantize8<false>(m, numbers[0], mq);
+    const float vs = quantize8<true>(root, numbers[1], vq);
+    if (live && (threadIdx.x & 15) == 0) {
+      t.m_scale[block] = ms;
+      t.v_scale[block] = vs;
+    }
+    uint8_t *mc = static_cast<uint8_t*>(t.m), *vc = static_cast<uint8_t*>(t.v);
+    if (vec) {
+      *reinterpret_cast<uint2*>(mc + at) = mq;
+      *reinterpret_cast<uint2*>(vc + at) = vq;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (at + j < n) {
+          mc[at + j] = (uint8_t)((j < 4 ? mq.x : mq.y) >> (8 * (j & 3)));
+          vc[at + j] = (uint8_t)((j < 4 ? vq.x : vq.y) >> (8 * (j & 3)));
+        }
+      }
+    }
+  } else {
+    put8(static_cast<float*>(t.m), at, n, vec, narrow8<float>(m));
+    put8(static_cast<float*>(t.v), at, n, vec, narrow8<float>(v));
+  }
+  if constexpr (MASTER) put8(t.master, at, n, vec, narrow8<float>(w));
+  if constexpr (DRAWN) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)   // the upper 16 bits are what bf16 keeps; not finite: as it is
+      if (fabsf(w[j]) < INFINITY) w[j] = __uint_as_float((__float_as_uint(w[j]) + number_of(numbers[2], j)) & 0xFFFF0000u);
+  }
+  put8(static_cast<TP*>(t.param), at, n, vec, narrow8<TP>(w));
+}
+
+template <int N, typename TP, typename TG, bool MASTER>
+cudaError_t adamw_bits(const AdamwTensor* t, const AdamwParams& p, bool small, int64_t blocks, cudaStream_t s) {
+  AdamwList<N> list;
+  for (int i = 0; i < p.n; ++i) list.t[i] = t[i];
+  list.p = p;
+  const dim3 grid((unsigned)blocks), threads(kAdamThreads);
+  return small ? launch_pdl(adamw_kernel<N, TP, TG, MASTER, true>, grid, threads, 0, s, list)
+               : launch_pdl(adamw_kernel<N, TP, TG, MASTER, false>, grid, threads, 0, s, list);
+}
+
+// A launch's table lies in its arguments: a short one where it does.
+template <typename TP, typename TG, bool MASTER>
+cudaError_t adamw_table(const AdamwTensor* t, const AdamwParams& p, bool small, int64_t blocks, cudaStream_t s) {
+  return p.n <= kAdamwFew ? adamw_bits<kAdamwFew, TP, TG, MASTER>(t, p, small, blocks, s)
+                          : adamw_bits<kAdamwMost, TP, TG, MASTER>(t, p, small, blocks, s);
+}
+
+}  // namespace
+
+int64_t adamw_blocks(int64_t numel) { return (numel + kAdamChunk - 1) / kAdamChunk; }
+
+cudaError_t launch_adamw(const AdamwTensor* t, const AdamwParams& p, int param_dtype, int grad_dtype, bool master,
+                         bool small, int64_t blocks, cudaStream_t s) {
+  const bool g32 = grad_dtype == MOE_DT_F32;
+  if (param_dtype == MOE_DT_F32) return adamw_table<float, float, false>(t, p, small, blocks, s);
+  if (param_dtype == MOE_DT_F16)
+    return g32 ? adamw_table<__half, float, true>(t, p, small, blocks, s)
+               : adamw_table<__half, __half, true>(t, p, small, blocks, s);
+  if (master)
+    return g32 ? adamw_table<__nv_bfloat16, float, true>(t, p, small, blocks, s)
+               : adamw_table<__nv_bfloat16, __nv_bfloat16, true>(t, p, small, blocks, s);
+  return g32 ? adamw_table<__nv_bfloat16, float, false>(t, p, small, blocks, s)
+             : adamw_table<__nv_bfloat16, __nv_bfloat16, false>(t, p, small, blocks, s);
+}
+
+}  // namespace moe

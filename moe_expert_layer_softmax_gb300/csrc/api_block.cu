@@ -279,6 +279,81 @@ int moe_dropout(int64_t rows, int32_t cols, int32_t dtype, const void* x, int64_
              : MOE_ERR_CUDA;
 }
 
+int moe_adamw(const moe_adamw_args_t* a, void* stream) {
+  if (a == nullptr || a->n_tensors < 0) return MOE_ERR_INVALID;
+  if (!is_dtype(a->param_dtype) || !is_dtype(a->grad_dtype)) return MOE_ERR_INVALID;
+  if (a->grad_dtype != a->param_dtype && a->grad_dtype != MOE_DT_F32) return MOE_ERR_INVALID;
+  if (a->state_bits != 32 && a->state_bits != 8) return MOE_ERR_INVALID;
+  if (!(a->beta1 >= 0.0 && a->beta1 < 1.0) || !(a->beta2 >= 0.0 && a->beta2 < 1.0)) return MOE_ERR_INVALID;
+  if (!(a->eps >= 0.0) || std::isinf(a->eps) || !(a->weight_decay >= 0.0) || std::isinf(a->weight_decay))
+    return MOE_ERR_INVALID;
+  if (!a->lr_dev && (!(a->lr >= 0.0) || std::isinf(a->lr))) return MOE_ERR_INVALID;
+  if (!a->step_dev && a->step < 1) return MOE_ERR_INVALID;
+  if (!on_boundary(a->grad_scale, 4) || !on_boundary(a->lr_dev, 4) || !on_boundary(a->step_dev, 8)) return MOE_ERR_ALIGN;
+  if (a->n_tensors == 0) return MOE_OK;
+  if (a->tensors == nullptr) return MOE_ERR_INVALID;
+  if (a->n_tensors > (1 << 24)) return MOE_ERR_UNSUPPORTED;
+  const bool small = a->state_bits == 8;
+  bool master = false;   // of the tensors that are not empty
+  for (int i = 0; i < a->n_tensors && !master; ++i) master = a->tensors[i].numel > 0 && a->tensors[i].master != nullptr;
+  const int ps = size_of(a->param_dtype), gs = size_of(a->grad_dtype);
+  int64_t total = 0;
+  for (int i = 0; i < a->n_tensors; ++i) {   // all of them before the first launch
+    const moe_adamw_tensor_t& t = a->tensors[i];
+    if (t.numel < 0) return MOE_ERR_INVALID;
+    if (t.numel > (int64_t(1) << 34)) return MOE_ERR_UNSUPPORTED;
+    if (t.numel == 0) continue;
+    if ((t.master != nullptr) != master) return MOE_ERR_INVALID;
+    if (!t.param || !t.grad || !t.m || !t.v || (small && (!t.m_scale || !t.v_scale))) return MOE_ERR_INVALID;
+    if (!on_boundary(t.param, ps) || !on_boundary(t.grad, gs) || !on_boundary(t.master, 4)) return MOE_ERR_ALIGN;
+    if (!small && (!on_boundary(t.m, 4) || !on_boundary(t.v, 4))) return MOE_ERR_ALIGN;
+    if (small && (!on_boundary(t.m_scale, 4) || !on_boundary(t.v_scale, 4))) return MOE_ERR_ALIGN;
+    total += adamw_blocks(t.numel);
+  }
+  if (total == 0) return MOE_OK;
+  // without a copy in 32 bits: fp32 itself, or bf16 with drawn rounding
+  if (master ? a->param_dtype == MOE_DT_F32 : a->param_dtype == MOE_DT_F16) return MOE_ERR_UNSUPPORTED;
+  if (total > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+  if (!ready()) return MOE_ERR_NOT_INIT;
+  AdamwParams p = {};
+  p.s.beta1 = (float)a->beta1; p.s.one_beta1 = (float)(1.0 - a->beta1);
+  p.s.beta2 = (float)a->beta2; p.s.one_beta2 = (float)(1.0 - a->beta2);
+  p.s.eps = (float)a->eps;
+  p.lr = a->lr; p.beta1 = a->beta1; p.beta2 = a->beta2; p.weight_decay = a->weight_decay;
+  if (!a->step_dev) {
+    p.c1 = 1.0 - std::pow(a->beta1, (double)a->step);
+    p.s.root_scale = (float)(1.0 / std::sqrt(1.0 - std::pow(a->beta2, (double)a->step)));
+  }
+  if (!a->step_dev && !a->lr_dev) {
+    p.s.decay = (float)(1.0 - a->lr * a->weight_decay);
+    p.s.rate = (float)(a->lr / p.c1);
+  }
+  p.grad_scale = a->grad_scale; p.lr_dev = a->lr_dev; p.step_dev = a->step_dev;
+  p.k0 = (uint32_t)a->seed; p.k1 = (uint32_t)(a->seed >> 32);
+  p.o0 = (uint32_t)a->offset; p.o1 = (uint32_t)(a->offset >> 32);
+  AdamwTensor list[kAdamwMost];
+  for (int i = 0; i < a->n_tensors;) {
+    int64_t blocks = 0;
+    p.first_tensor = i;
+    for (p.n = 0; p.n < kAdamwMost && i < a->n_tensors; ++i, ++p.n) {
+      const moe_adamw_tensor_t& t = a->tensors[i];
+      AdamwTensor& e = list[p.n];
+      e.param = t.param; e.grad = t.grad; e.master = t.master; e.m = t.m; e.v = t.v;
+      e.m_scale = t.m_scale; e.v_scale = t.v_scale;
+      e.numel = t.numel;
+      e.first = (uint32_t)blocks;
+      e.vec = on_boundary(t.param, 16) && on_boundary(t.grad, 16) && on_boundary(t.master, 16) &&
+              on_boundary(t.m, small ? 8 : 16) && on_boundary(t.v, small ? 8 : 16);
+      blocks += adamw_blocks(t.numel);
+    }
+    if (blocks == 0) continue;
+    if (launch_adamw(list, p, a->param_dtype, a->grad_dtype, master, small, blocks, static_cast<cudaStream_t>(stream)) !=
+        cudaSuccess)
+      return MOE_ERR_CUDA;
+  }
+  return MOE_OK;
+}
+
 int moe_quantize_w4(int64_t rows, int32_t K, int32_t group, int32_t dtype, const void* src,
                     uint8_t* q, void* scales, void* stream) {
   MOE_TRY(check_w4(rows, K, group, dtype));

@@ -80,6 +80,40 @@ cudaError_t launch_add_layer_norm_bwd(const AddNormBwdParams& p, int dtype, int 
                                       cudaStream_t s);
 cudaError_t launch_dropout(const DropoutParams& p, int dtype, int vec, cudaStream_t s);
 
+// ---------------------------------------------------------------- AdamW
+constexpr int kStateBlock = 128;    // values that share a scale of the 8-bit states
+constexpr int kAdamwFew = 16, kAdamwMost = 224;   // tensors of a launch's table, short and long
+
+struct AdamwTensor {
+  void* param;
+  const void* grad;
+  float* master;
+  void *m, *v;
+  float *m_scale, *v_scale;
+  int64_t numel;
+  uint32_t first;   // block that it begins with
+  uint32_t vec;     // every pointer on a 16-byte boundary
+};
+
+struct AdamwScalars {
+  float beta1, one_beta1, beta2, one_beta2, eps;
+  float root_scale, decay, rate;   // 1 / sqrt(1 - b2^t), 1 - lr wd, lr / (1 - b1^t)
+};
+
+struct AdamwParams {
+  int n, first_tensor;   // tensors of this launch, and those of the call before them
+  AdamwScalars s;
+  const float* grad_scale;
+  const float* lr_dev;
+  const int64_t* step_dev;
+  double lr, beta1, beta2, weight_decay, c1;   // c1: 1 - b1^t of the host's t
+  uint32_t k0, k1, o0, o1;
+};
+
+int64_t adamw_blocks(int64_t numel);
+cudaError_t launch_adamw(const AdamwTensor* t, const AdamwParams& p, int param_dtype, int grad_dtype, bool master,
+                         bool small, int64_t blocks, cudaStream_t s);
+
 // ---------------------------------------------------------------- 4-bit weights
 constexpr int kW4MaxColumns = 1 << 18;   // K, d and f: stages of a block's share count in 32 bits
 

@@ -97,6 +97,69 @@ def add_layer_norm_bwd(dy, h, mean, rstd, weight, dres=None, p=0.0, seed=0, offs
     return dh, dropout(dh, p, seed, offset), (dy * n).sum(0), dy.sum(0)
 
 
+def numbers16(count, high, seed, offset):
+    """The 16-bit numbers of `count` neighbouring places, counters (place / 8, high, offset)."""
+    nb = (count + 7) // 8
+    ctr = np.zeros((nb, 4), dtype=np.uint64)
+    ctr[:, 0] = np.arange(nb)
+    ctr[:, 1] = high
+    ctr[:, 2] = offset % (1 << 32)
+    ctr[:, 3] = offset >> 32
+    w = philox4x32_10(ctr, (seed % (1 << 32), seed >> 32))
+    r = np.zeros((nb, 8), dtype=np.int64)
+    for j in range(8):
+        r[:, j] = w[:, j // 2] >> np.uint64(16) if j % 2 else w[:, j // 2] % np.uint64(65536)
+    return r.reshape(-1)[:count]
+
+
+def e4m3_values(codes):
+    """E4M3 codes (uint8) to the numbers that they stand for."""
+    c = np.asarray(codes).astype(np.int64)
+    e, f = c >> 3 & 15, c & 7
+    v = np.where(e == 0, f * 2.0 ** -9, (8 + f) * np.exp2(e - 10.0))
+    v = np.where((e == 15) & (f == 7), np.nan, v)
+    return np.where(c & 128, -v, v)
+
+
+def adamw_constants(lr, beta1, beta2, weight_decay, step):
+    """(1 - b1, 1 - b2, 1 / sqrt(1 - b2^t), 1 - lr wd, lr / (1 - b1^t))"""
+    return 1 - beta1, 1 - beta2, 1 / np.sqrt(1 - beta2 ** step), 1 - lr * weight_decay, lr / (1 - beta1 ** step)
+
+
+def adamw(w, g, m, v, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, grad_scale=1.0, dtype=np.float64):
+    """(w, m, v, root), each operation in `dtype`: with float32 what the device computes,
+    operation by operation."""
+    c = [dtype(x) for x in adamw_constants(lr, beta1, beta2, weight_decay, step)]
+    w, g, m, v = (np.asarray(x, dtype=dtype) for x in (w, g, m, v))
+    g = g * dtype(grad_scale)
+    m = m * dtype(beta1) + g * c[0]
+    v = v * dtype(beta2) + (g * g) * c[1]
+    root = np.sqrt(v)
+    return w * c[3] - m / (root * c[2] + dtype(eps)) * c[4], m, v, root
+
+
+def state8(x, numbers, least):
+    """float32 values to (codes' values, scales) of 128 each, rounded by `numbers`."""
+    x = np.asarray(x, dtype=np.float32)
+    n, one = len(x), np.float32(448)
+    out, scales = np.zeros(n, dtype=np.float32), np.zeros((n + 127) // 128, dtype=np.float32)
+    for b in range(len(scales)):
+        at = slice(128 * b, min(n, 128 * b + 128))
+        v = x[at]
+        finite = np.isfinite(v)
+        top = np.abs(v[finite]).max(initial=np.float32(0))
+        inv = one * (np.float32(1) / top) if top >= np.float32(2.0 ** -100) else np.float32(0)
+        z = np.minimum(np.abs(np.where(finite, v, np.float32(0))) * inv, one)
+        step = np.exp2(np.floor(np.log2(np.maximum(z, 2.0 ** -6).astype(np.float64))) - 3)
+        low = np.floor(z / step)
+        q = (low + (z / step - low >= 1 - numbers[at] / 65536)) * step
+        if least:
+            q = np.where((z > 0) & (q == 0), 2.0 ** -9, q)
+        out[at] = np.where(finite, np.copysign(q, v), np.nan)
+        scales[b] = top * np.float32(1 / 448) if top >= np.float32(2.0 ** -100) else 0
+    return out, scales
+
+
 def w4_quantize(w, group, rounder):
     """codes [rows, K] 0..15 and scales [rows, K / group] (rounded by `rounder`)."""
     b = w.reshape(w.shape[0], -1, group)
