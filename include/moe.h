@@ -522,6 +522,41 @@ MOE_API int moe_layer_fwd(const moe_shape_t* shape, const moe_fwd_args_t* args, 
 MOE_API int moe_layer_bwd(const moe_shape_t* shape, const moe_bwd_args_t* args, const moe_saved_t* saved,
                   void* ws, void* stream);
 
+/* ------------------------------------------------------------ a few tokens
+ * moe_layer_fwd for 1 to MOE_FEW_MAX_TOKENS tokens (evaluation, generation between
+ * updates) on the bf16 weights as they are, in two kernels that read W_router and the
+ * weights of the experts with routes once: route, experts and combine, nothing saved for
+ * a backward.  Results are those of moe_layer_fwd up to the rounding of sums (a is
+ * rounded to bf16 as there, y is not).
+ *   x [T, d], w_router [E, d], w_gate, w_up [E, f, d], w_down [E, d, f], out [T, d]: bf16
+ *   with w_router:    logits [T, E] fp32 (nullable), topk_idx [T, k] int32 and gates
+ *                     [T, k] fp32 (nullable) are written, logit_bias [T, E] (nullable)
+ *                     is added; ranks, ties, gates and non-finite logits as moe_route
+ *   without (NULL):   topk_idx and gates are read (logits and logit_bias are NULL).  An
+ *                     index of -1 stands for no expert and adds nothing (a token
+ *                     without any gets zeros: unused places of a batch); any other index
+ *                     outside [0, E) adds nothing and sets MOE_DEVERR_BOUNDS.  An expert
+ *                     that a token names twice counts with the sum of its gates.
+ *   ws  moe_few_workspace_size bytes; its first word is the error word
+ * A token's results depend on its own row (and its experts' weights) alone.  The same
+ * call gives the same bits.  Envelope: that of the layer with prec MOE_BF16, T <=
+ * MOE_FEW_MAX_TOKENS (T = 0 is valid and writes nothing). */
+#define MOE_FEW_MAX_TOKENS 64
+typedef struct {
+  const void* x;
+  const void* w_router;
+  const float* logit_bias;
+  const void* w_gate;
+  const void* w_up;
+  const void* w_down;
+  float* logits;
+  int32_t* topk_idx;
+  float* gates;
+  void* out;
+} moe_few_args_t;
+MOE_API int moe_few_workspace_size(const moe_shape_t* shape, size_t* ws_bytes);
+MOE_API int moe_few_fwd(const moe_shape_t* shape, const moe_few_args_t* args, void* ws, void* stream);
+
 /* ------------------------------------------------------------ around the layer
  * The operators that stand next to the layer in a transformer block: the
  * residual addition with the norm before it (and the dropout of its output), the

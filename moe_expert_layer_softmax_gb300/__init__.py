@@ -49,7 +49,7 @@ EXPORTS = (
     "moe_combine_bwd", "moe_dispatch_bwd", "moe_router_bwd", "moe_layer_fwd", "moe_layer_bwd",
     "moe_route_noalloc", "moe_dequantize_mxfp8", "moe_build_mx_weights",
     "moe_debug_inject_stall", "moe_profile_start", "moe_profile_stop", "moe_load_balance",
-    "moe_checks_read",
+    "moe_checks_read", "moe_few_workspace_size", "moe_few_fwd",
     "moe_add_norm", "moe_add_norm_bwd_workspace_size", "moe_add_norm_bwd", "moe_add_layer_norm",
     "moe_add_layer_norm_bwd_workspace_size", "moe_add_layer_norm_bwd", "moe_dropout", "moe_adamw",
     "moe_quantize_w4", "moe_dequantize_w4", "moe_matvec_w4", "moe_experts_w4_workspace_size",
@@ -150,6 +150,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_layer_fwd": [P(Shape), P(FwdArgs), P(Saved), _vp, _vp],
         "moe_layer_bwd": [P(Shape), P(BwdArgs), P(Saved), _vp, _vp],
         "moe_checks_read": [P(i32), i32],
+        "moe_few_workspace_size": [P(Shape), P(ctypes.c_size_t)],
+        "moe_few_fwd": [P(Shape), _vp, _vp, _vp],
         "moe_add_norm": [_vp, _vp],
         "moe_add_norm_bwd_workspace_size": [i64, i32, P(ctypes.c_size_t)],
         "moe_add_norm_bwd": [_vp, _vp, _vp],
@@ -419,6 +421,7 @@ _ADD_LAYER_NORM = struct.Struct("@qiiii" + "Pq" * 2 + "PP" + "Pq" * 2 + "PPPPP" 
 _ADD_LAYER_NORM_BWD = struct.Struct("@qiiii" + "Pq" * 3 + "PPP" + "Pq" * 2 + "PP" + "QQf0q")
 _ADAMW_TENSOR = struct.Struct("@7Pq")
 _ADAMW = struct.Struct("@P4iPPP5dqQQ")
+_FEW = struct.Struct("@10P")
 _EXPERTS_W4 = struct.Struct("@7i" + "P" * 10)
 _torch = None
 _dtypes = {}
@@ -822,6 +825,38 @@ def experts_w4(x, topk_idx, gates, w: dict, out, ws, stream=None):
     rc = load().moe_experts_w4(args, pws, st)
     if rc:
         _failed("moe_experts_w4", rc, args, pws, st)
+
+
+# ------------------------------------------------------------------ a few tokens
+FEW_MAX_TOKENS = 64
+
+
+def few_workspace(s: Shape) -> int:
+    """Bytes of workspace that forward_few needs (its first word is the error word)."""
+    v = ctypes.c_size_t()
+    _check("moe_few_workspace_size", load().moe_few_workspace_size(ctypes.byref(s), ctypes.byref(v)))
+    return v.value
+
+
+def forward_few(s: Shape, x, w_router, logit_bias, w_gate, w_up, w_down, out, ws, topk_idx=None, gates=None, logits=None,
+                stream=None):
+    """moe_few_fwd: the layer's forward for at most FEW_MAX_TOKENS tokens, in two kernels.
+    With w_router topk_idx, gates and logits are outputs (or None); without, topk_idx and
+    gates are the routing (-1: no expert)."""
+    if _torch is None:
+        _dtype(x, "x")
+    T, d, E, k, f = s.T, s.d_model, s.n_experts, s.top_k, s.d_ff
+    bf, f32 = _torch.bfloat16, _torch.float32
+    args = _FEW.pack(
+        _flat(x, "x", T * d, bf), _flat(w_router, "w_router", E * d, bf), _flat(logit_bias, "logit_bias", T * E, f32),
+        _flat(w_gate, "w_gate", E * f * d, bf), _flat(w_up, "w_up", E * f * d, bf), _flat(w_down, "w_down", E * d * f, bf),
+        _flat(logits, "logits", T * E, f32), _flat(topk_idx, "topk_idx", T * k, _torch.int32),
+        _flat(gates, "gates", T * k, f32), _flat(out, "out", T * d, bf))
+    pws = _flat(ws, "ws", few_workspace(s), _torch.uint8, True)
+    st = _stream(stream)
+    rc = load().moe_few_fwd(ctypes.byref(s), args, pws, st)
+    if rc:
+        _failed("moe_few_fwd", rc, ctypes.byref(s), args, pws, st)
 
 
 # ------------------------------------------------------------------ buffers

@@ -8,11 +8,34 @@
 
 #include "moe.h"
 #include "common.cuh"
+#include "few.h"
 #include "kernels.h"
 
 namespace moe {
 
 namespace {
+
+#define MOE_TRY(expr)                   \
+  do {                                  \
+    int _rc = (expr);                   \
+    if (_rc != MOE_OK) return _rc;      \
+  } while (0)
+
+#define MOE_CUDA(expr)                              \
+  do {                                              \
+    if ((expr) != cudaSuccess) return MOE_ERR_CUDA; \
+  } while (0)
+
+#define MOE_NONNULL_ALIGNED(p)                   \
+  do {                                           \
+    if ((p) == nullptr) return MOE_ERR_INVALID;  \
+    if (!aligned16(p)) return MOE_ERR_ALIGN;     \
+  } while (0)
+
+#define MOE_ALIGNED_OR_NULL(p)                             \
+  do {                                                     \
+    if ((p) != nullptr && !aligned16(p)) return MOE_ERR_ALIGN; \
+  } while (0)
 
 DeviceInfo g_dev[kMaxDevices];
 
@@ -43,6 +66,33 @@ int64_t rows_max_of(const moe_shape_t* s) {
   const int64_t R = (int64_t)s->T * s->top_k;
   const int64_t r = R + (int64_t)s->n_experts * (kTileM - 1);
   return (r + kTileM - 1) / kTileM * kTileM;
+}
+
+// The envelope of the layer for a few tokens; *s: the shape with at least one of them.
+int check_few(const moe_shape_t* shape, moe_shape_t* s) {
+  if (shape == nullptr) return MOE_ERR_INVALID;
+  *s = *shape;
+  if (s->T == 0) s->T = 1;
+  MOE_TRY(check_shape(s));
+  if (s->prec != MOE_BF16 || s->T > MOE_FEW_MAX_TOKENS) return MOE_ERR_UNSUPPORTED;
+  if ((int64_t)s->n_experts * s->d_model > INT32_MAX || (int64_t)s->n_experts * s->d_ff > INT32_MAX)
+    return MOE_ERR_UNSUPPORTED;   // rows of weights count in 32 bits
+  return MOE_OK;
+}
+
+// Its workspace: [error word | experts and gates of the routes | their activations, whole
+// groups of eight rows]
+struct FewLayout {
+  size_t idx, gates, act, total;
+};
+FewLayout few_layout(const moe_shape_t* s) {
+  const size_t R = (size_t)s->T * s->top_k;
+  FewLayout w;
+  w.idx = 256;
+  w.gates = w.idx + align256(R * 4);
+  w.act = w.gates + align256(R * 4);
+  w.total = w.act + align256((R + 7) / 8 * 8 * s->d_ff * 2);
+  return w;
 }
 
 int n_route_blocks(const moe_shape_t* s) {
@@ -80,28 +130,6 @@ int ready_or_error() {
   if (dev < 0 || dev >= kMaxDevices || !g_dev[dev].ready) return MOE_ERR_NOT_INIT;
   return MOE_OK;
 }
-
-#define MOE_TRY(expr)                   \
-  do {                                  \
-    int _rc = (expr);                   \
-    if (_rc != MOE_OK) return _rc;      \
-  } while (0)
-
-#define MOE_CUDA(expr)                              \
-  do {                                              \
-    if ((expr) != cudaSuccess) return MOE_ERR_CUDA; \
-  } while (0)
-
-#define MOE_NONNULL_ALIGNED(p)                   \
-  do {                                           \
-    if ((p) == nullptr) return MOE_ERR_INVALID;  \
-    if (!aligned16(p)) return MOE_ERR_ALIGN;     \
-  } while (0)
-
-#define MOE_ALIGNED_OR_NULL(p)                             \
-  do {                                                     \
-    if ((p) != nullptr && !aligned16(p)) return MOE_ERR_ALIGN; \
-  } while (0)
 
 int route_impl(const moe_shape_t* s, const void* x, const void* w_router, const float* bias,
                float* logits, int32_t* topk_idx, float* gates, int32_t* counts, int32_t* offsets,
@@ -746,6 +774,47 @@ int moe_layer_bwd(const moe_shape_t* s, const moe_bwd_args_t* a, const moe_saved
                                rows_max_of(s) / kTileM, at<float>(ws, w.partial), a->dw_router,
                                st));
   }
+  return MOE_OK;
+}
+
+int moe_few_workspace_size(const moe_shape_t* shape, size_t* ws_bytes) {
+  moe_shape_t s;
+  MOE_TRY(check_few(shape, &s));
+  if (ws_bytes == nullptr) return MOE_ERR_INVALID;
+  *ws_bytes = few_layout(&s).total;
+  return MOE_OK;
+}
+
+int moe_few_fwd(const moe_shape_t* shape, const moe_few_args_t* a, void* ws, void* stream) {
+  moe_shape_t s;
+  MOE_TRY(check_few(shape, &s));
+  if (a == nullptr) return MOE_ERR_INVALID;
+  if (shape->T == 0) return MOE_OK;
+  MOE_NONNULL_ALIGNED(a->x);
+  MOE_ALIGNED_OR_NULL(a->w_router);
+  MOE_ALIGNED_OR_NULL(a->logit_bias);
+  MOE_NONNULL_ALIGNED(a->w_gate);
+  MOE_NONNULL_ALIGNED(a->w_up);
+  MOE_NONNULL_ALIGNED(a->w_down);
+  MOE_ALIGNED_OR_NULL(a->logits);
+  MOE_ALIGNED_OR_NULL(a->topk_idx);
+  MOE_ALIGNED_OR_NULL(a->gates);
+  MOE_NONNULL_ALIGNED(a->out);
+  MOE_NONNULL_ALIGNED(ws);
+  if (a->w_router == nullptr && (!a->topk_idx || !a->gates || a->logits || a->logit_bias)) return MOE_ERR_INVALID;
+  MOE_TRY(ready_or_error());
+  const FewLayout w = few_layout(&s);
+  FewParams p = {};
+  p.T = s.T; p.d = s.d_model; p.E = s.n_experts; p.k = s.top_k; p.f = s.d_ff;
+  p.bias = a->logit_bias;
+  p.logits = a->logits;
+  p.topk_idx = a->topk_idx ? a->topk_idx : at<int32_t>(ws, w.idx);
+  p.gates = a->gates ? a->gates : at<float>(ws, w.gates);
+  p.act = at<uint8_t>(ws, w.act);
+  p.out = a->out;
+  p.err = at<int32_t>(ws, 0);
+  const FewTensors t = {a->x, a->w_router, a->w_gate, a->w_up, a->w_down};
+  MOE_CUDA(launch_few(p, t, static_cast<cudaStream_t>(stream)));
   return MOE_OK;
 }
 

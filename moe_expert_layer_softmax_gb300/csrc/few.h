@@ -1,0 +1,38 @@
+// Internal launch interface of the layer for a few tokens (few.cu), called by its C
+// entry point (api.cu).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "moe.h"
+
+namespace moe {
+
+constexpr int kFewMaxRoutes = MOE_FEW_MAX_TOKENS * 32;   // top_k <= 32
+
+struct FewTensors {
+  const void *x, *w_router, *w_gate, *w_up, *w_down;
+};
+
+struct FewParams {
+  int T, d, E, k, f;
+  const float* bias;     // [T, E] or NULL
+  float* logits;         // [T, E] or NULL (written with a router)
+  int32_t* topk_idx;     // [T, k]: written with a router, else read
+  float* gates;
+  void* act;             // bf16 [T k, f]
+  void* out;
+  int32_t* err;
+  // set by the launcher
+  bool router;
+  int cluster, t_pad, stages, stage_bytes;
+};
+
+cudaError_t launch_few(const FewParams& p, const FewTensors& w, cudaStream_t s);
+
+// 2-D bf16 tensor map with 128-byte swizzle (gemm.cu): `outer` rows of `inner` elements.
+bool make_bf16_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer);
+
+}  // namespace moe

@@ -45,6 +45,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "few.h"
 
 namespace moe {
 
@@ -1890,6 +1891,10 @@ cudaError_t launch_mx_pair(Params p, const CUtensorMap& A0, const CUtensorMap& A
 }  // namespace
 
 int gemm_set_inject_stall(int mode) { return g_inject_stall.exchange(mode); }
+
+bool make_bf16_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer) {
+  return get_encoder() && make_map(m, ptr, inner, outer, box_inner, box_outer);
+}
 
 cudaError_t gemm_init_attributes() {
   if (!get_encoder()) return cudaErrorInitializationError;
