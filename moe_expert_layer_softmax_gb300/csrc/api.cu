@@ -80,17 +80,18 @@ int check_few(const moe_shape_t* shape, moe_shape_t* s) {
   return MOE_OK;
 }
 
-// Its workspace: [error word | experts and gates of the routes | their activations, whole
-// groups of eight rows]
+// Its workspace: [error word | experts and gates of the routes | their lists | their
+// activations, whole groups of eight rows]
 struct FewLayout {
-  size_t idx, gates, act, total;
+  size_t idx, gates, lists, act, total;
 };
 FewLayout few_layout(const moe_shape_t* s) {
   const size_t R = (size_t)s->T * s->top_k;
   FewLayout w;
   w.idx = 256;
   w.gates = w.idx + align256(R * 4);
-  w.act = w.gates + align256(R * 4);
+  w.lists = w.gates + align256(R * 4);
+  w.act = w.lists + align256(sizeof(FewLists));
   w.total = w.act + align256((R + 7) / 8 * 8 * s->d_ff * 2);
   return w;
 }
@@ -813,6 +814,7 @@ int moe_few_fwd(const moe_shape_t* shape, const moe_few_args_t* a, void* ws, voi
   p.act = at<uint8_t>(ws, w.act);
   p.out = a->out;
   p.err = at<int32_t>(ws, 0);
+  p.lists = at<FewLists>(ws, w.lists);
   const FewTensors t = {a->x, a->w_router, a->w_gate, a->w_up, a->w_down};
   MOE_CUDA(launch_few(p, t, static_cast<cudaStream_t>(stream)));
   return MOE_OK;

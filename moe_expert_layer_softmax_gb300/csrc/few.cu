@@ -18,8 +18,8 @@
 //          parts of the (expert, d_ff) axis, add gate * y of their parts in 32 bits and
 //          join them through distributed shared memory: sums in a fixed order.
 //
-// Tiles are built from TMA boxes of eight rows, the unit of the 128-byte swizzle, so
-// that a share may begin at any group of eight rows; an MMA row without weights holds
+// Shares begin at any group of eight rows, the unit of the 128-byte swizzle; a tile is
+// built from TMA boxes of 8 to 128 rows; an MMA row without weights holds
 // whatever the memory held, and its results are not read.  A token's rows are fetched
 // by index (gather) into the MMA's N.
 #include <atomic>
@@ -34,8 +34,10 @@ namespace {
 
 constexpr int kThreads = 192;          // TMA, MMA, four warps of the epilogue
 constexpr int kEpi = 128;
-constexpr int kWeightBytes = 128 * 128;   // of a stage: 128 rows of 64 columns
-constexpr int kMaxStages = 12;
+constexpr int kCluster = 4;
+constexpr int kMaxSteps = 8;           // times 64 columns of a stage
+constexpr int kStageBytes = 34 * 1024;   // 128 columns of 128 rows of weights and of eight tokens
+constexpr int kMaxStages = 6, kRouterStages = 12;
 constexpr int kAccCols = 64;           // of an accumulator: tokens of an expert
 constexpr int kTmem = 2 * kAccCols;
 
@@ -70,161 +72,187 @@ MOE_DEV void tma_box(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x,
 MOE_DEV void st_cluster(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
-MOE_DEV void st_cluster(uint32_t addr, int v) {
-  asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
+MOE_DEV void or_cluster(uint32_t addr, uint32_t v) {
+  asm volatile("red.relaxed.cluster.shared::cluster.or.b32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-MOE_DEV float ld_cluster(uint32_t addr) {
-  float v;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+MOE_DEV float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
 }
+MOE_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+MOE_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// Boxes of 8, 16, 32, 64 (and 128) rows: a run of groups of eight rows is as many copies
+// as its number has bits.
+struct UpMaps {
+  CUtensorMap gate[4], up[4], rows, x, router[2];
+};
+struct DownMaps {
+  CUtensorMap down[5], act[4];
+};
+// Row groups in front of the box of 2^b groups of a run of n.
+MOE_DEV int box_before(int n, int b) { return n & ~((2 << b) - 1); }
+
+// More tokens than this are all tokens' rows in one copy, not four rows a copy.
+constexpr int kGather = 16;
 
 struct Ctl {
   uint64_t full[kMaxStages], empty[kMaxStages];
+  uint64_t rfull[kRouterStages], rempty[kRouterStages];
   uint64_t tfull[2], tempty[2];
   uint64_t fin;
   uint32_t tmem;
   int abort;
-  int n_act;                            // experts with routes
-  uint32_t mask[256][2];                // tokens of an expert
-  uint16_t base[257];                   // first route of an active expert, in their order
-  uint8_t act[256], slot[256];          // active expert -> expert and back
-  uint8_t tok[kFewMaxRoutes];           // token of a route
-  int sel[kFewMaxRoutes];               // expert of (token, choice), -1: none
-  float gate[kFewMaxRoutes];            // gate of a route
+  int n_act;                  // experts with routes
+  uint16_t base[257];         // first route of an active expert, in their order
+  uint8_t act[256];           // their experts
+};
+struct UpCtl : Ctl {
+  uint32_t mask[256][2];      // tokens of an expert
+  uint8_t slot[256];          // expert -> active expert
+  uint8_t four[kGather];      // tokens of the piece that is being loaded
+  float up[64][17];           // sixteen tokens' up products
+};
+struct DownCtl : Ctl {
+  uint8_t tok[kFewMaxRoutes];   // token of a route
+  float gate[kFewMaxRoutes];    // its gate
 };
 
-// From sel: the active experts in ascending order, their routes in the tokens' order.
-// An expert that a token names twice is one route with the sum of its gates.
-MOE_DEV void build_lists(Ctl& s, const FewParams& p, const float* gates) {
-  const int R = p.T * p.k, tid = threadIdx.x;
-  for (int i = tid; i < 2 * p.E; i += kThreads) (&s.mask[0][0])[i] = 0u;
-  __syncthreads();
-  for (int r = tid; r < R; r += kThreads) {
-    const int e = s.sel[r], t = r / p.k;
-    if (e >= 0) atomicOr(&s.mask[e][t >> 5], 1u << (t & 31));
-  }
-  __syncthreads();
-  if (tid < 32) {   // eight experts a lane
+// Shared memory.  An MMA reads 16 KB from where its rows begin, whatever lies behind
+// them: of the last stage's up to 16 KB past the ring.
+constexpr int kOverread = 16 * 1024, kSumBytes = MOE_FEW_MAX_TOKENS * 512;
+constexpr int kStages = kMaxStages, kRingBytes = kStages * kStageBytes;
+constexpr int kDownStages = 5, kDownRingBytes = kDownStages * kStageBytes;
+constexpr int kUpSmem = kRingBytes + (sizeof(UpCtl) > kOverread ? (int)sizeof(UpCtl) : kOverread);
+constexpr int kDownSmem = kDownRingBytes + kSumBytes + (int)sizeof(DownCtl);
+static_assert(kUpSmem <= 227 * 1024 && kDownSmem <= 227 * 1024 && kSumBytes >= kOverread, "shared memory of a CTA");
+// the router's parts leave two stages at least: (16 + 8) KB each
+static_assert(kRingBytes - MOE_FEW_MAX_TOKENS * 256 * 4 >= 2 * 24 * 1024, "the router's stages");
+
+// From the masks (complete, behind a barrier): the active experts in ascending order and
+// where their routes begin.  Ends in a barrier.
+MOE_DEV void build_lists(UpCtl& s, const FewParams& p) {
+  const int lane = threadIdx.x;
+  if (lane < 32) {   // eight experts a lane
     int routes[8], n = 0, act = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int e = tid * 8 + i;
-      routes[i] = e < p.E ? __popc(s.mask[e][0]) + __popc(s.mask[e][1]) : 0;
+      routes[i] = __popc(s.mask[lane * 8 + i][0]) + __popc(s.mask[lane * 8 + i][1]);
       n += routes[i];
       act += routes[i] > 0;
     }
-    int n0 = n, act0 = act;
+    int both = n << 16 | act;   // at most 2048 routes, 256 experts
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int a = __shfl_up_sync(0xffffffffu, n0, off), b = __shfl_up_sync(0xffffffffu, act0, off);
-      if (tid >= off) {
-        n0 += a;
-        act0 += b;
-      }
+      const int before = __shfl_up_sync(0xffffffffu, both, off);
+      if (lane >= off) both += before;
     }
-    if (tid == 31) {
-      s.n_act = act0;
-      s.base[act0] = (uint16_t)n0;
+    int at = both >> 16, a = both & 0xFFFF;
+    if (lane == 31) {
+      s.n_act = a;
+      s.base[a] = (uint16_t)at;
     }
-    n0 -= n;
-    act0 -= act;
+    at -= n;
+    a -= act;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (routes[i]) {
-        s.act[act0] = (uint8_t)(tid * 8 + i);
-        s.slot[tid * 8 + i] = (uint8_t)act0;
-        s.base[act0] = (uint16_t)n0;
-        n0 += routes[i];
-        ++act0;
+        s.act[a] = (uint8_t)(lane * 8 + i);
+        s.slot[lane * 8 + i] = (uint8_t)a;
+        s.base[a] = (uint16_t)at;
+        at += routes[i];
+        ++a;
       }
     }
   }
   __syncthreads();
-  for (int r = tid; r < R; r += kThreads) {
-    const int e = s.sel[r], t = r / p.k;
-    if (e < 0) continue;
-    bool first = true;
-    for (int i = t * p.k; i < r; ++i) first = first && s.sel[i] != e;
-    if (!first) continue;
-    int at = s.base[s.slot[e]] + __popc(s.mask[e][t >> 5] & ((1u << (t & 31)) - 1u));
-    if (t >= 32) at += __popc(s.mask[e][0]);
-    s.tok[at] = (uint8_t)t;
-    if (gates != nullptr) {
-      float g = 0.0f;
-      for (int i = r; i < (t + 1) * p.k; ++i)
-        if (s.sel[i] == e) g += gates[i];
-      s.gate[at] = g;
-    }
-  }
-  __syncthreads();
 }
 
-// sel from indices in global memory; those outside [-1, E) are reported and left out.
-MOE_DEV void read_routes(Ctl& s, const FewParams& p) {
-  for (int r = threadIdx.x; r < p.T * p.k; r += kThreads) {
-    int e = p.topk_idx[r];
-    if (e < -1 || e >= p.E) {
-      raise_error(p.err, MOE_DEVERR_BOUNDS);
-      e = -1;
-    }
-    s.sel[r] = e;
+// One CTA, its epilogue's threads: the lists for the down kernel.  Routes of an expert
+// are in the tokens' order; one that a token names twice is one route with the sum of
+// its gates.
+MOE_DEV void write_lists(const UpCtl& s, const FewParams& p) {
+  const int tid = threadIdx.x - (kThreads - kEpi);
+  FewLists& l = *p.lists;
+  if (tid == 0) l.n_act = s.n_act;
+  for (int a = tid; a <= s.n_act; a += kEpi) {
+    l.base[a] = s.base[a];
+    if (a < s.n_act) l.act[a] = s.act[a];
   }
-  __syncthreads();
+  for (int r = tid; r < p.T * p.k; r += kEpi) {
+    const int t = r / p.k, e = p.topk_idx[r];
+    if (e == -1) continue;
+    if (e < 0 || e >= p.E) {
+      raise_error(p.err, MOE_DEVERR_BOUNDS);
+      continue;
+    }
+    bool first = true;
+    for (int i = t * p.k; i < r; ++i) first = first && p.topk_idx[i] != e;
+    if (!first) continue;
+    float g = 0.0f;
+    for (int i = r; i < (t + 1) * p.k; ++i)
+      if (p.topk_idx[i] == e) g += p.gates[i];
+    int at = s.base[s.slot[e]] + __popc(s.mask[e][t >> 5] & ((1u << (t & 31)) - 1u));
+    if (t >= 32) at += __popc(s.mask[e][0]);
+    l.tok[at] = (uint8_t)t;
+    l.gate[at] = g;
+  }
 }
+
+// Floats as unsigned numbers in the same order; 0 is below all of them.
+MOE_DEV uint32_t ordered(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+MOE_DEV float unordered(uint32_t b) { return __uint_as_float(b & 0x80000000u ? b & 0x7FFFFFFFu : ~b); }
 
 // The k largest of a token's E logits and their gates, as the layer's routing ranks
 // them: larger first, lower expert first among equals, a NaN below everything; the
-// gates' sum over 32 lanes in the butterfly's order.  `logit` gives expert e's.
-template <typename Logit, typename Sel>
-MOE_DEV void rank_token(const FewParams& p, int t, bool write, Logit logit, Sel put) {
+// gates' sum over 32 lanes in the butterfly's order.  `logit` gives expert e's; `put`
+// takes lane j's choice j.
+template <typename Logit, typename Put>
+MOE_DEV void rank_token(const FewParams& p, int t, bool write, Logit logit, Put put) {
   const int lane = threadIdx.x & 31;
-  float key[8];
-  uint32_t taken = 0;
+  uint32_t key[8];
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
+    key[i] = 0u;
     const int e = lane + 32 * i;
-    float v = 0.0f;
-    if (e < p.E) {
-      v = logit(e);
+    if (32 * i < p.E && e < p.E) {
+      const float v = logit(e);
       if (write && p.logits) p.logits[(size_t)t * p.E + e] = v;
       bad = bad || !isfinite(v);
-    } else {
-      taken |= 1u << i;
+      // both zeros are one value: the lower expert goes first among them
+      key[i] = ordered(v != v ? -INFINITY : v == 0.0f ? 0.0f : v);
     }
-    key[i] = v != v ? -INFINITY : v;
   }
   bad = __any_sync(0xffffffffu, bad);
   float mine = 0.0f, top = 0.0f;
   int id = 0;
   for (int j = 0; j < p.k; ++j) {
-    float bv = 0.0f;
-    int be = -1;
+    uint32_t best = 0u;
+    int e = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (!(taken >> i & 1u) && (be < 0 || key[i] > bv)) {
-        bv = key[i];
-        be = lane + 32 * i;
+      if (32 * i < p.E && key[i] > best) {
+        best = key[i];
+        e = lane + 32 * i;
       }
     }
+    const uint32_t max = __reduce_max_sync(0xffffffffu, best);
+    e = (int)__reduce_min_sync(0xffffffffu, best == max ? (uint32_t)e : 0xFFFFFFFFu);
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-      const float ov = __shfl_xor_sync(0xffffffffu, bv, off);
-      const int oe = __shfl_xor_sync(0xffffffffu, be, off);
-      if (oe >= 0 && (be < 0 || ov > bv || (ov == bv && oe < be))) {
-        bv = ov;
-        be = oe;
-      }
-    }
-    if ((be & 31) == lane) taken |= 1u << (be >> 5);
-    if (j == 0) top = bv;
+    for (int i = 0; i < 8; ++i)
+      if (e == lane + 32 * i) key[i] = 0u;
+    if (j == 0) top = unordered(max);
     if (lane == j) {
-      mine = bv;
-      id = be;
+      mine = unordered(max);
+      id = e;
     }
-    if (lane == 0) put(j, be);
   }
+  if (lane < p.k) put(lane, id);
   const float ex = lane < p.k ? expf(mine - top) : 0.0f;
   float sum = ex;
 #pragma unroll
@@ -240,9 +268,13 @@ MOE_DEV void rank_token(const FewParams& p, int t, bool write, Logit logit, Sel 
 MOE_DEV void begin(Ctl& s, const FewParams& p) {
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
-    for (int i = 0; i < p.stages; ++i) {
+    for (int i = 0; i < kMaxStages; ++i) {
       mbar_init(&s.full[i], 1);
       mbar_init(&s.empty[i], 1);
+    }
+    for (int i = 0; i < kRouterStages; ++i) {
+      mbar_init(&s.rfull[i], 1);
+      mbar_init(&s.rempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.tfull[i], 1);
@@ -259,56 +291,69 @@ MOE_DEV void begin(Ctl& s, const FewParams& p) {
   tc_fence_after();
 }
 
-// Where a role stands in the ring and in the accumulators.
-struct Place {
-  int stage = 0;
+// The stages and where a role stands in them.
+struct Ring {
+  uint64_t *full, *empty;
+  uint32_t base;
+  int bytes, stages, stage = 0;
   uint32_t phase = 0;
-  int it = 0;   // accumulators used so far
   long issued = 0;
-  MOE_DEV void next(const FewParams& p) {
+  MOE_DEV Ring(uint64_t* full_, uint64_t* empty_, const void* smem, int bytes_, int stages_)
+      : full(full_), empty(empty_), base(smem_u32(smem)), bytes(bytes_), stages(stages_) {}
+  MOE_DEV uint32_t at() const { return base + (uint32_t)(stage * bytes); }
+  MOE_DEV void next() {
     ++issued;
-    if (++stage == p.stages) {
+    if (++stage == stages) {
       stage = 0;
       phase ^= 1u;
     }
   }
 };
 
+// How a piece of rows fills its stages: `s` times 64 columns, the weights' rows of each
+// behind one another, then the tokens'.
+struct Fill {
+  int s;
+  uint32_t a, b;   // bytes of 64 columns
+  MOE_DEV Fill(uint32_t a_, uint32_t b_) : s(max(1, min(kMaxSteps, kStageBytes / (int)(a_ + b_)))), a(a_), b(b_) {}
+};
+
 // One warp: the next free stage, its copies announced.
-MOE_DEV bool claim(Ctl& s, const FewParams& p, const Place& at, uint32_t bytes) {
-  const bool ok = __all_sync(0xffffffffu, mbar_wait(&s.empty[at.stage], at.phase ^ 1u, &s.abort, p.err));
-  if (ok && (threadIdx.x & 31) == 0) mbar_arrive_expect_tx(&s.full[at.stage], bytes);
+MOE_DEV bool claim(Ctl& s, const FewParams& p, const Ring& r, uint32_t bytes) {
+  const bool ok = __all_sync(0xffffffffu, mbar_wait(&r.empty[r.stage], r.phase ^ 1u, &s.abort, p.err));
+  if (ok && (threadIdx.x & 31) == 0) mbar_arrive_expect_tx(&r.full[r.stage], bytes);
   __syncwarp();
   return ok;
 }
 // The producer gave up: the copies that it announced land first.
-MOE_DEV void drain(Ctl& s, const FewParams& p, const Place& at) {
-  for (long i = at.issued > p.stages ? at.issued - p.stages : 0; i < at.issued; ++i) {
-    const uint32_t bar = smem_u32(&s.full[(int)(i % p.stages)]);
+MOE_DEV void drain(const Ring& r) {
+  for (long i = r.issued > r.stages ? r.issued - r.stages : 0; i < r.issued; ++i) {
+    const uint32_t bar = smem_u32(&r.full[(int)(i % r.stages)]);
     const uint64_t t0 = globaltimer();
-    while (!mbar_try_wait(bar, (uint32_t)((i / p.stages) & 1)))
+    while (!mbar_try_wait(bar, (uint32_t)((i / r.stages) & 1)))
       if (globaltimer() - t0 > kWaitLimitNs) break;
   }
 }
 
-// One thread: `chunks` stages multiplied into the next accumulator.
-MOE_DEV bool multiply(Ctl& s, const FewParams& p, uint8_t* ring, Place& at, int chunks, int n) {
-  const int acc = at.it & 1;
-  if (!mbar_wait(&s.tempty[acc], ((uint32_t)(at.it >> 1) & 1u) ^ 1u, &s.abort, p.err)) return false;
+// One thread: `chunks` times 64 columns multiplied into accumulator `it`.
+MOE_DEV bool multiply(Ctl& s, const FewParams& p, Ring& r, int it, const Fill& fill, int chunks, int n) {
+  const int acc = it & 1;
+  if (!mbar_wait(&s.tempty[acc], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s.abort, p.err)) return false;
   tc_fence_after();
   const uint32_t d = s.tmem + acc * kAccCols, idesc = idesc_bf16_f32(128, n, 0, 0);
-  for (int c = 0; c < chunks; ++c) {
-    if (!mbar_wait(&s.full[at.stage], at.phase, &s.abort, p.err)) return false;
+  for (int c = 0; c < chunks; c += fill.s) {
+    if (!mbar_wait(&r.full[r.stage], r.phase, &s.abort, p.err)) return false;
     tc_fence_after();
-    const uint32_t a = smem_u32(ring + (size_t)at.stage * p.stage_bytes), b = a + kWeightBytes;
+    uint32_t a = r.at(), b = a + fill.s * fill.a;
+    for (int q = 0; q < fill.s && c + q < chunks; ++q, a += fill.a, b += fill.b) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-      tc_mma_bf16(d, smem_desc_sw128(a + k * 32, 16, 1024), smem_desc_sw128(b + k * 32, 16, 1024), idesc, (c | k) != 0);
-    tc_commit(&s.empty[at.stage]);
-    at.next(p);
+      for (int k = 0; k < 4; ++k)
+        tc_mma_bf16(d, smem_desc_sw128(a + k * 32, 16, 1024), smem_desc_sw128(b + k * 32, 16, 1024), idesc, (c | q | k) != 0);
+    }
+    tc_commit(&r.empty[r.stage]);
+    r.next();
   }
   tc_commit(&s.tfull[acc]);
-  ++at.it;
   return true;
 }
 // Its last word: every MMA that was issued has ended.
@@ -344,177 +389,218 @@ MOE_DEV void leave(Ctl& s) {
   }
 }
 
-MOE_DEV int share(int64_t total, int i, int n) { return (int)(total * i / n); }
+// The first of share i of n: the first total % n shares are one larger than the others.
+MOE_DEV int share(int total, int i, int n) { return total / n * i + min(i, total % n); }
 MOE_DEV int round16(int n) { return (n + 15) & ~15; }
 
 // The next rows of a share of (active expert, group of eight d_ff rows): at most eight
-// groups of one expert, a run in equal pieces.
+// groups of one expert.
 struct UpPiece {
   int a, g, n;   // active expert, first group, groups
   MOE_DEV bool next(int& from, int to, int groups) {
     if (from >= to) return false;
     a = from / groups;
     g = from - a * groups;
-    const int run = min(to, (a + 1) * groups) - from, pieces = (run + 7) / 8;
-    n = (run + pieces - 1) / pieces;
+    n = min(8, min(to, (a + 1) * groups) - from);
     from += n;
     return true;
   }
 };
 
+// Columns of the MMA for an expert of m tokens; how n groups of gate and of up rows and
+// these tokens fill a stage.
+MOE_DEV int up_columns(const FewParams& p, int m) { return m > kGather ? p.t_pad : round16(m); }
+MOE_DEV Fill up_fill(const FewParams& p, int n, int m) {
+  return Fill(n * 2048, m > kGather ? p.t_pad * 128 : (m + 7) / 8 * 1024);
+}
+
 __global__ void __launch_bounds__(kThreads, 1)
-    few_up_kernel(const __grid_constant__ CUtensorMap t_gate, const __grid_constant__ CUtensorMap t_up,
-                  const __grid_constant__ CUtensorMap t_rows, const __grid_constant__ CUtensorMap t_x,
-                  const __grid_constant__ CUtensorMap t_router, const FewParams p) {
+    few_up_kernel(const __grid_constant__ UpMaps maps, const FewParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* ring = smem;
-  Ctl& s = *reinterpret_cast<Ctl*>(smem + (size_t)p.stages * p.stage_bytes);
+  UpCtl& s = *reinterpret_cast<UpCtl*>(smem + kRingBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, row = quarter * 32 + lane;   // of the epilogue's threads
+  const bool writer = (int)blockIdx.x >= (int)gridDim.x - kCluster;   // the cluster that writes the routing
+  for (int i = threadIdx.x; i < 512; i += kThreads) (&s.mask[0][0])[i] = 0u;
   begin(s, p);
   const uint32_t tmem = s.tmem + ((uint32_t)(quarter * 32) << 16);
   const int chunks = p.d / 64;
-  Place at;
+  Ring ring(s.full, s.empty, smem, kStageBytes, kStages), first(s.rfull, s.rempty, smem, p.router_bytes, p.router_stages);
+  int it = 0;   // accumulators used so far
   bool ok = true;
   if (p.router) {
-    const int C = p.cluster, rank = (int)cluster_ctarank(), own = (p.T + C - 1) / C;
-    const int c0 = share(chunks, rank, C), c1 = share(chunks, rank + 1, C), tiles = (p.E + 127) / 128;
-    cluster_sync();   // every CTA of the cluster has begun
+    cluster_arrive();
+    const int rank = (int)cluster_ctarank(), own = (p.T + kCluster - 1) / kCluster;
+    const int c0 = share(chunks, rank, kCluster), c1 = share(chunks, rank + 1, kCluster), tiles = (p.E + 127) / 128;
+    const uint32_t a_bytes = (uint32_t)(min(p.E, 128) + 7) / 8 * 1024, b_bytes = (uint32_t)p.router_bytes - a_bytes;
     if (warp == 0) {
       for (int m = 0; m < tiles && ok; ++m) {
+        const int rows = min(p.E - m * 128, 128);
         for (int c = c0; c < c1; ++c) {
-          ok = claim(s, p, at, kWeightBytes + p.t_pad * 128);
+          ok = claim(s, p, first, (rows + p.T) * 128);
           if (!ok) break;
-          const uint32_t to = smem_u32(ring + (size_t)at.stage * p.stage_bytes);
-          if (lane == 0) {
-            tma_box(to, &t_router, &s.full[at.stage], c * 64, m * 128);
-            tma_box(to + kWeightBytes, &t_x, &s.full[at.stage], c * 64, 0);
-          }
-          at.next(p);
+          if (lane == 0) tma_box(first.at(), &maps.router[m], &first.full[first.stage], c * 64, m * 128);
+          if (lane == 1) tma_box(first.at() + a_bytes, &maps.x, &first.full[first.stage], c * 64, 0);
+          first.next();
         }
       }
-      __syncwarp();
+      if (!ok && lane == 0) drain(first);
     } else if (warp == 1) {
-      if (lane == 0)
-        for (int m = 0; m < tiles && ok; ++m) ok = multiply(s, p, ring, at, c1 - c0, p.t_pad);
-      __syncwarp();
+      if (lane == 0) {
+        Fill fill(a_bytes, b_bytes);
+        fill.s = 1;
+        for (int m = 0; m < tiles && ok; ++m) ok = multiply(s, p, first, m, fill, c1 - c0, p.t_pad);
+      }
     } else {
       for (int m = 0; m < tiles; ++m) ok = results(s, p, m) && ok;
     }
     __syncwarp();
-    cluster_sync();   // no CTA's ring is in use
+    cluster_wait();   // every CTA of the cluster has begun
     // the part of this CTA's columns to the CTA that ranks the token: [source, its
-    // token, expert] in the ring
+    // token, expert] behind the stages
     if (warp >= 2) {
-      const uint32_t mine = smem_u32(ring) + (uint32_t)(rank * own * p.E) * 4u;
+      const uint32_t mine = smem_u32(smem + p.part_at) + (uint32_t)(rank * own * p.E) * 4u;
       for (int m = 0; m < tiles; ++m) {
         const int e = m * 128 + row;
-        for (int c = 0; c < p.t_pad; c += 16) {
+        for (int c = 0; c < p.T; c += 16) {
           float v[16];
           tmem_ld16(tmem + m * kAccCols + c, v);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int t = c + i;
             if (t < p.T && e < p.E)
-              st_cluster(mapa_shared(mine + (uint32_t)((t / C) * p.E + e) * 4u, t % C), c1 > c0 ? v[i] : 0.0f);
+              st_cluster(mapa_shared(mine + (uint32_t)(t / kCluster * p.E + e) * 4u, t % kCluster), c1 > c0 ? v[i] : 0.0f);
           }
         }
         release(s, m);
       }
     }
-    at.it = tiles;
+    it = tiles;
     __syncwarp();
     cluster_sync();   // the parts are there
-    const float* part = reinterpret_cast<const float*>(ring);
-    const bool write = blockIdx.x < C;   // one cluster writes the routing
-    for (int i = warp; rank + i * C < p.T; i += kThreads / 32) {
-      const int t = rank + i * C;
+    const float* part = reinterpret_cast<const float*>(smem + p.part_at);
+    for (int i = warp; rank + i * kCluster < p.T; i += kThreads / 32) {
+      const int t = rank + i * kCluster;
       rank_token(
-          p, t, write,
+          p, t, writer,
           [&](int e) {
             float v = 0.0f;
-            for (int q = 0; q < C; ++q) v += part[(q * own + i) * p.E + e];
+#pragma unroll
+            for (int q = 0; q < kCluster; ++q) v += part[(q * own + i) * p.E + e];
             return p.bias ? v + p.bias[(size_t)t * p.E + e] : v;
           },
           [&](int j, int e) {
-            const uint32_t to = smem_u32(&s.sel[t * p.k + j]);
-            for (int q = 0; q < C; ++q) st_cluster(mapa_shared(to, q), e);
+            const uint32_t to = smem_u32(&s.mask[e][t >> 5]);
+#pragma unroll
+            for (int q = 0; q < kCluster; ++q) or_cluster(mapa_shared(to, q), 1u << (t & 31));
           });
     }
-    fence_proxy_async_smem();   // the ring was read and written by threads
+    fence_proxy_async_smem();   // the ring was written and read by threads
     __syncwarp();
     cluster_sync();   // and the routing
   } else {
-    read_routes(s, p);
+    for (int r = threadIdx.x; r < p.T * p.k; r += kThreads) {
+      const int e = p.topk_idx[r], t = r / p.k;   // others than [0, E): write_lists
+      if (e >= 0 && e < p.E) atomicOr(&s.mask[e][t >> 5], 1u << (t & 31));
+    }
+    __syncthreads();
   }
-  build_lists(s, p, nullptr);
+  build_lists(s, p);
 
   const int groups = p.f / 8;
-  const int64_t total = (int64_t)s.n_act * groups;
+  const int total = s.n_act * groups;
   int g = share(total, blockIdx.x, gridDim.x);
   const int g_end = share(total, blockIdx.x + 1, gridDim.x);
   UpPiece u;
   if (warp == 0) {
     while (ok && u.next(g, g_end, groups)) {
-      const int e = s.act[u.a], r0 = s.base[u.a], m = s.base[u.a + 1] - r0, fours = (m + 3) / 4;
-      // lanes 0-15: eight rows each, gate and up by turns (a pair of groups fills 32
-      // rows, so that one warp of the epilogue sees both products of a row); lanes
-      // 16-31: four tokens each
-      const int j = lane >> 1, side = lane & 1;
-      const uint32_t place = lane < 16 ? ((j >> 1) * 4 + (j & 1) * 2 + side) * 1024u : kWeightBytes + (lane - 16) * 512u;
-      const int y = e * p.f + (u.g + j) * 8, i = (lane - 16) * 4;
-      int y0 = 0, y1 = 0, y2 = 0, y3 = 0;
-      if (lane >= 16 && i < m) {
-        y0 = s.tok[r0 + i];
-        y1 = s.tok[r0 + min(i + 1, m - 1)];
-        y2 = s.tok[r0 + min(i + 2, m - 1)];
-        y3 = s.tok[r0 + min(i + 3, m - 1)];
+      const int e = s.act[u.a], m = s.base[u.a + 1] - s.base[u.a];
+      // lanes 0-3: gate rows, lanes 4-7: the up rows behind them; lanes 8-11: four tokens
+      // each, or lane 8: all tokens
+      const Fill fill = up_fill(p, u.n, m);
+      const bool all = m > kGather;
+      if (!all) {   // the expert's tokens in a row
+        const uint32_t m0 = s.mask[e][0], m1 = s.mask[e][1], below = (1u << lane) - 1u;
+        __syncwarp();
+        if (m0 >> lane & 1u) s.four[__popc(m0 & below)] = (uint8_t)lane;
+        if (m1 >> lane & 1u) s.four[__popc(m0) + __popc(m1 & below)] = (uint8_t)(lane + 32);
+        __syncwarp();
       }
-      for (int c = 0; c < chunks; ++c) {
-        ok = claim(s, p, at, u.n * 2048 + fours * 512);
+      const int b = lane & 3, before = box_before(u.n, b), i = (lane - 8) * 4;
+      const bool weights = lane < 8 && (u.n >> b & 1), four = !all && lane >= 8 && lane < 12 && i < m;
+      const CUtensorMap* map = lane < 4 ? &maps.gate[b] : &maps.up[b];
+      const uint32_t place = lane < 8 ? (before + (lane < 4 ? 0 : u.n)) * 1024u : fill.s * fill.a + (lane - 8) * 512u;
+      const uint32_t step = lane < 8 ? fill.a : fill.b;
+      const uint32_t bytes = u.n * 2048 + (all ? p.T * 128 : (m + 3) / 4 * 512);
+      const int y = e * p.f + (u.g + before) * 8;
+      int y0 = 0, y1 = 0, y2 = 0, y3 = 0;
+      if (four) {
+        y0 = s.four[i];
+        y1 = s.four[min(i + 1, m - 1)];
+        y2 = s.four[min(i + 2, m - 1)];
+        y3 = s.four[min(i + 3, m - 1)];
+      }
+      for (int c = 0; c < chunks; c += fill.s) {
+        const int n = min(fill.s, chunks - c);
+        ok = claim(s, p, ring, n * bytes);
         if (!ok) break;
-        const uint32_t to = smem_u32(ring + (size_t)at.stage * p.stage_bytes) + place;
-        if (lane < 2 * u.n)
-          tma_box(to, side ? &t_up : &t_gate, &s.full[at.stage], c * 64, y);
-        else if (lane >= 16 && i < m)
-          tma_gather4(to, &t_rows, &s.full[at.stage], c * 64, y0, y1, y2, y3);
-        at.next(p);
+        uint32_t to = ring.at() + place;
+        for (int q = c; q < c + n; ++q, to += step) {
+          if (weights) tma_box(to, map, &ring.full[ring.stage], q * 64, y);
+          if (four) tma_gather4(to, &maps.rows, &ring.full[ring.stage], q * 64, y0, y1, y2, y3);
+          if (all && lane == 8) tma_box(to, &maps.x, &ring.full[ring.stage], q * 64, 0);
+        }
+        ring.next();
       }
     }
-    if (!ok && lane == 0) drain(s, p, at);
+    if (!ok && lane == 0) drain(ring);
   } else if (warp == 1) {
     if (lane == 0) {
-      while (ok && u.next(g, g_end, groups))
-        ok = multiply(s, p, ring, at, chunks, round16(s.base[u.a + 1] - s.base[u.a]));
+      while (ok && u.next(g, g_end, groups)) {
+        const int m = s.base[u.a + 1] - s.base[u.a];
+        ok = multiply(s, p, ring, it++, up_fill(p, u.n, m), chunks, up_columns(p, m));
+      }
       finish(s, p);
     }
   } else {
-    // lanes 0-7 and 16-23 hold gate rows, the eight lanes after them the up rows
-    const int group = quarter * 2 + (lane >> 4), r = lane & 7;
-    const bool upper = lane & 8;
+    // the first 8 n lanes hold gate rows, the next 8 n the up rows, which change hands
+    // sixteen tokens at a time
     __nv_bfloat16* act = static_cast<__nv_bfloat16*>(p.act);
+    if (blockIdx.x == gridDim.x - 1) write_lists(s, p);
     while (ok && u.next(g, g_end, groups)) {
-      ok = results(s, p, at.it);
+      ok = bar_and(1, kEpi, results(s, p, it));
       if (!ok) break;
-      const int r0 = s.base[u.a], m = s.base[u.a + 1] - r0;
-      const size_t col = (size_t)(u.g + group) * 8 + r;
-      for (int c = 0; c < m; c += 16) {
+      const int e = s.act[u.a], r0 = s.base[u.a], m = s.base[u.a + 1] - r0, columns = m > kGather ? p.T : m;
+      const uint32_t m0 = s.mask[e][0], m1 = s.mask[e][1];
+      const int rows = u.n * 8;
+      const size_t col = (size_t)u.g * 8 + row;
+      for (int c = 0; c < columns; c += 16) {
         float v[16];
-        tmem_ld16(tmem + (at.it & 1) * kAccCols + c, v);
-        // of two neighbouring tokens each lane of the pair takes one
+        tmem_ld16(tmem + (it & 1) * kAccCols + c, v);
+        if (row >= rows && row < 2 * rows) {
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
-          const float got = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i + 1], 8);
-          const float h = upper ? got : v[i], up = upper ? v[i + 1] : got;
-          const int t = c + i + upper;
-          if (group < u.n && t < m) {
-            const float a = __fdividef(h, 1.0f + __expf(-h)) * up;
-            act[(size_t)(r0 + t) * p.f + col] = __float2bfloat16_rn(a);
+          for (int i = 0; i < 16; ++i) s.up[row - rows][i] = v[i];
+        }
+        bar_sync(1, kEpi);
+        if (row < rows) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int t = c + i;
+            int at = t;   // the route of this column
+            bool in = t < m;
+            if (m > kGather) {
+              in = (t < 32 ? m0 >> t : m1 >> (t - 32)) & 1u;
+              at = t < 32 ? __popc(m0 & ((1u << t) - 1u)) : __popc(m0) + __popc(m1 & ((1u << (t - 32)) - 1u));
+            }
+            if (in && t < columns) {
+              const float a = __fdividef(v[i], 1.0f + __expf(-v[i])) * s.up[row][i];
+              act[(size_t)(r0 + at) * p.f + col] = __float2bfloat16_rn(a);
+            }
           }
         }
+        bar_sync(1, kEpi);
       }
-      release(s, at.it);
-      ++at.it;
+      release(s, it++);
     }
   }
   leave(s);
@@ -533,61 +619,79 @@ struct DownPiece {
   }
 };
 
+// The box of 8 << b routes that holds m of them; how n groups of rows and these routes
+// fill a stage.
+MOE_DEV int route_box(int m) { return m <= 8 ? 0 : m <= 16 ? 1 : m <= 32 ? 2 : 3; }
+MOE_DEV Fill down_fill(int n, int m) { return Fill(n * 1024, 1024 << route_box(m)); }
+
 __global__ void __launch_bounds__(kThreads, 1)
-    few_down_kernel(const __grid_constant__ CUtensorMap t_down, const __grid_constant__ CUtensorMap t_act,
-                    const FewParams p) {
+    few_down_kernel(const __grid_constant__ DownMaps maps, const FewParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
-  uint8_t* ring = smem;
-  float* sums = reinterpret_cast<float*>(smem + (size_t)p.stages * p.stage_bytes);   // [T][128]
-  Ctl& s = *reinterpret_cast<Ctl*>(sums + p.T * 128);
+  float* sums = reinterpret_cast<float*>(smem + kDownRingBytes);   // [T][128]
+  DownCtl& s = *reinterpret_cast<DownCtl*>(smem + kDownRingBytes + kSumBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int quarter = warp & 3, row = quarter * 32 + lane;
   begin(s, p);
-  read_routes(s, p);
-  build_lists(s, p, p.gates);
+  {   // what the up kernel has listed, all of it at once
+    const FewLists& l = *p.lists;
+    const int R = p.T * p.k, most = min(p.E, R);
+    if (threadIdx.x == 0) s.n_act = l.n_act;
+    for (int i = threadIdx.x; i <= most; i += kThreads) s.base[i] = l.base[i];
+    for (int i = threadIdx.x; i < most; i += kThreads) s.act[i] = l.act[i];
+    for (int i = threadIdx.x; i < R; i += kThreads) {
+      s.tok[i] = l.tok[i];
+      s.gate[i] = l.gate[i];
+    }
+    for (int i = threadIdx.x; i < p.T * 32; i += kThreads) reinterpret_cast<float4*>(sums)[i] = {};
+    __syncthreads();
+  }
   const uint32_t tmem = s.tmem + ((uint32_t)(quarter * 32) << 16);
-  const int C = p.cluster, rank = (int)cluster_ctarank(), clusters = gridDim.x / C, cluster = blockIdx.x / C;
+  const int rank = (int)cluster_ctarank(), clusters = gridDim.x / kCluster, cluster = blockIdx.x / kCluster;
   const int chunks = p.f / 64, total = s.n_act * chunks;
-  const int from = share(total, rank, C), to = share(total, rank + 1, C);
+  const int from = share(total, rank, kCluster), to = share(total, rank + 1, kCluster);
   const int d0 = share(p.d / 8, cluster, clusters), d1 = share(p.d / 8, cluster + 1, clusters);
   const int tiles = (d1 - d0 + 15) / 16;
-  Place at;
+  Ring ring(s.full, s.empty, smem, kStageBytes, kDownStages);
+  int it = 0;
   bool ok = true;
   for (int tile = 0; tile < tiles; ++tile) {   // the same number in every CTA of the cluster
     const int g0 = d0 + share(d1 - d0, tile, tiles), n = d0 + share(d1 - d0, tile + 1, tiles) - g0;
-    for (int i = threadIdx.x; i < p.T * 128; i += kThreads) sums[i] = 0.0f;
-    __syncthreads();
     int c0 = from;
     DownPiece u;
     if (warp == 0) {
       while (ok && u.next(c0, to, chunks)) {
-        const int e = s.act[u.a], r0 = s.base[u.a], eights = (s.base[u.a + 1] - r0 + 7) / 8;
-        // lanes 0-15: eight rows of weights each, lanes 16-23: eight routes
-        const uint32_t place = lane < 16 ? lane * 1024u : kWeightBytes + (lane - 16) * 1024u;
-        const int y = lane < 16 ? e * p.d + (g0 + lane) * 8 : r0 + (lane - 16) * 8;
-        const bool weights = lane < n, routes = lane >= 16 && lane - 16 < eights;
-        for (int c = u.c; c < u.c + u.n; ++c) {
-          ok = claim(s, p, at, (n + eights) * 1024);
+        const int e = s.act[u.a], r0 = s.base[u.a], m = s.base[u.a + 1] - r0;
+        // lanes 0-4: rows of weights, lane 8: the routes, the smallest box that holds them
+        const Fill fill = down_fill(n, m);
+        const int b = lane < 5 ? lane : 0, before = box_before(n, b), act = route_box(m);
+        const bool weights = lane < 5 && (n >> b & 1), routes = lane == 8;
+        const uint32_t place = routes ? fill.s * fill.a : before * 1024u, step = routes ? fill.b : fill.a;
+        const CUtensorMap* map = routes ? &maps.act[act] : &maps.down[b];
+        const int y = routes ? r0 : e * p.d + (g0 + before) * 8;
+        for (int c = u.c; c < u.c + u.n; c += fill.s) {
+          const int steps = min(fill.s, u.c + u.n - c);
+          ok = claim(s, p, ring, steps * (fill.a + fill.b));
           if (!ok) break;
-          const uint32_t dst = smem_u32(ring + (size_t)at.stage * p.stage_bytes) + place;
-          if (weights || routes) tma_box(dst, routes ? &t_act : &t_down, &s.full[at.stage], c * 64, y);
-          at.next(p);
+          uint32_t dst = ring.at() + place;
+          for (int q = c; q < c + steps; ++q, dst += step)
+            if (weights || routes) tma_box(dst, map, &ring.full[ring.stage], q * 64, y);
+          ring.next();
         }
       }
-      __syncwarp();
     } else if (warp == 1) {
       if (lane == 0)
-        while (ok && u.next(c0, to, chunks))
-          ok = multiply(s, p, ring, at, u.n, round16(s.base[u.a + 1] - s.base[u.a]));
-      __syncwarp();
+        while (ok && u.next(c0, to, chunks)) {
+          const int m = s.base[u.a + 1] - s.base[u.a];
+          ok = multiply(s, p, ring, it++, down_fill(n, m), u.n, round16(m));
+        }
     } else {
       while (ok && u.next(c0, to, chunks)) {
-        ok = results(s, p, at.it);
+        ok = results(s, p, it);
         if (!ok) break;
         const int r0 = s.base[u.a], m = s.base[u.a + 1] - r0;
         for (int c = 0; c < m; c += 16) {
           float v[16];
-          tmem_ld16(tmem + (at.it & 1) * kAccCols + c, v);
+          tmem_ld16(tmem + (it & 1) * kAccCols + c, v);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             if (c + i < m) {
@@ -596,32 +700,38 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        release(s, at.it);
-        ++at.it;
+        release(s, it++);
       }
     }
     __syncwarp();
     cluster_sync();   // every CTA's sums are there
-    const int rows = (128 + C - 1) / C;
+    // this CTA's quarter of the rows, four neighbours a thread
+    constexpr int fours = 128 / kCluster / 4;
     const uint32_t mine = smem_u32(sums);
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.out);
-    for (int i = threadIdx.x; i < rows * p.T; i += kThreads) {
-      const int t = i / rows, r = i - t * rows + rank * rows;
+    for (int i = threadIdx.x; i < fours * p.T; i += kThreads) {
+      const int t = i / fours, r = (rank * fours + i % fours) * 4;
       if (r >= n * 8) continue;
-      float v = 0.0f;
-      for (int q = 0; q < C; ++q) v += ld_cluster(mapa_shared(mine + (uint32_t)(t * 128 + r) * 4u, q));
-      out[(size_t)t * p.d + g0 * 8 + r] = __float2bfloat16_rn(v);
+      float4 v[kCluster];
+#pragma unroll
+      for (int q = 0; q < kCluster; ++q) v[q] = ld_cluster4(mapa_shared(mine + (uint32_t)(t * 128 + r) * 4u, q));
+      float4 sum = v[0];
+#pragma unroll
+      for (int q = 1; q < kCluster; ++q) sum = make_float4(sum.x + v[q].x, sum.y + v[q].y, sum.z + v[q].z, sum.w + v[q].w);
+      *reinterpret_cast<uint2*>(out + (size_t)t * p.d + g0 * 8 + r) =
+          make_uint2(pack_bf16x2(sum.x, sum.y), pack_bf16x2(sum.z, sum.w));
     }
     __syncwarp();
     cluster_sync();   // and have been read
+    if (tile + 1 < tiles) {
+      for (int i = threadIdx.x; i < p.T * 32; i += kThreads) reinterpret_cast<float4*>(sums)[i] = {};
+      __syncthreads();
+    }
   }
-  if (warp == 0 && !ok && lane == 0) drain(s, p, at);
+  if (warp == 0 && !ok && lane == 0) drain(ring);
   if (warp == 1 && lane == 0) finish(s, p);
   leave(s);
 }
-
-constexpr int kCluster = 4;
-constexpr int kRingBytes = 200 * 1024;
 
 // CTAs of whole clusters that stay on the device at once.
 int resident_ctas(const void* kernel, int smem, int device) {
@@ -665,32 +775,39 @@ cudaError_t launch_clusters(void (*kernel)(KArgs...), int ctas, int smem, cudaSt
 cudaError_t launch_few(const FewParams& args, const FewTensors& w, cudaStream_t s) {
   const DeviceInfo* dev = device_info();
   FewParams p = args;
-  p.cluster = kCluster;
   p.router = w.w_router != nullptr;
-  p.t_pad = (p.T + 15) & ~15;
-  p.stage_bytes = kWeightBytes + p.t_pad * 128;
+  p.t_pad = p.T <= 16 ? 16 : p.T <= 32 ? 32 : 64;   // rows of the largest box of tokens or routes
   const uint64_t d = (uint64_t)p.d, f = (uint64_t)p.f, E = (uint64_t)p.E;
   const uint64_t routes = ((uint64_t)p.T * p.k + 7) / 8 * 8;
-  CUtensorMap gate, up, rows, x, router, down, act;
-  if (!make_bf16_map(&gate, w.w_gate, d, E * f, 64, 8) || !make_bf16_map(&up, w.w_up, d, E * f, 64, 8) ||
-      !make_bf16_map(&rows, w.x, d, (uint64_t)p.T, 64, 1) ||
-      !make_bf16_map(&x, w.x, d, (uint64_t)p.T, 64, (uint32_t)p.t_pad) ||
-      !make_bf16_map(&router, p.router ? w.w_router : w.w_gate, d, p.router ? E : E * f, 64, 128) ||
-      !make_bf16_map(&down, w.w_down, f, E * d, 64, 8) || !make_bf16_map(&act, p.act, f, routes, 64, 8))
-    return cudaErrorInvalidValue;
-  const int up_stages = kRingBytes / p.stage_bytes, down_stages = (kRingBytes - p.T * 512) / p.stage_bytes;
+  // the router's stages in front of the parts of its products
+  p.router_bytes = ((p.E < 128 ? p.E : 128) + 7) / 8 * 1024 + (p.T + 7) / 8 * 1024;
+  p.part_at = (kRingBytes - kCluster * ((p.T + kCluster - 1) / kCluster) * p.E * 4) / 1024 * 1024;
+  p.router_stages = p.part_at / p.router_bytes < kRouterStages ? p.part_at / p.router_bytes : kRouterStages;
+  UpMaps up;
+  DownMaps down;
+  const void* wr = p.router ? w.w_router : w.w_gate;   // a map that is not used is one all the same
+  bool made = make_bf16_map(&up.rows, w.x, d, (uint64_t)p.T, 64, 1) &&
+              make_bf16_map(&up.x, w.x, d, (uint64_t)p.T, 64, (uint32_t)p.T) &&
+              make_bf16_map(&up.router[0], wr, d, p.router ? E : E * f, 64, p.E < 128 ? p.E : 128) &&
+              make_bf16_map(&up.router[1], wr, d, p.router ? E : E * f, 64, p.E > 128 ? p.E - 128 : 1);
+  for (int b = 0; b < 5; ++b) {
+    const uint32_t height = 8u << b;
+    made = made && make_bf16_map(&down.down[b], w.w_down, f, E * d, 64, height);
+    if (b < 4)
+      made = made && make_bf16_map(&up.gate[b], w.w_gate, d, E * f, 64, height) &&
+             make_bf16_map(&up.up[b], w.w_up, d, E * f, 64, height) &&
+             make_bf16_map(&down.act[b], p.act, f, routes, 64, height);
+  }
+  if (!made) return cudaErrorInvalidValue;
   static SmemLimit up_limit, down_limit;
-  constexpr int most = kRingBytes + (int)sizeof(Ctl);
-  cudaError_t e = up_limit.raise(reinterpret_cast<const void*>(&few_up_kernel), most);
-  if (e == cudaSuccess) e = down_limit.raise(reinterpret_cast<const void*>(&few_down_kernel), most);
+  cudaError_t e = up_limit.raise(reinterpret_cast<const void*>(&few_up_kernel), kUpSmem);
+  if (e == cudaSuccess) e = down_limit.raise(reinterpret_cast<const void*>(&few_down_kernel), kDownSmem);
   if (e != cudaSuccess) return e;
-  const int ctas = resident_ctas(reinterpret_cast<const void*>(&few_up_kernel), most, dev->index);
+  const int ctas = resident_ctas(reinterpret_cast<const void*>(&few_up_kernel), kUpSmem, dev->index);
   if (ctas == 0) return cudaErrorInvalidConfiguration;
-  p.stages = up_stages < kMaxStages ? up_stages : kMaxStages;
-  e = launch_clusters(&few_up_kernel, ctas, p.stages * p.stage_bytes + (int)sizeof(Ctl), s, gate, up, rows, x, router, p);
+  e = launch_clusters(&few_up_kernel, ctas, kUpSmem, s, up, p);
   if (e != cudaSuccess) return e;
-  p.stages = down_stages < kMaxStages ? down_stages : kMaxStages;
-  return launch_clusters(&few_down_kernel, ctas, p.stages * p.stage_bytes + p.T * 512 + (int)sizeof(Ctl), s, down, act, p);
+  return launch_clusters(&few_down_kernel, ctas, kDownSmem, s, down, p);
 }
 
 }  // namespace moe

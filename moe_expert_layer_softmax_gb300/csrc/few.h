@@ -16,6 +16,15 @@ struct FewTensors {
   const void *x, *w_router, *w_gate, *w_up, *w_down;
 };
 
+// The routes by experts, from the up kernel to the down kernel (in the workspace).
+struct FewLists {
+  int32_t n_act;
+  uint16_t base[258];
+  uint8_t act[256];
+  uint8_t tok[kFewMaxRoutes];
+  float gate[kFewMaxRoutes];
+};
+
 struct FewParams {
   int T, d, E, k, f;
   const float* bias;     // [T, E] or NULL
@@ -25,9 +34,10 @@ struct FewParams {
   void* act;             // bf16 [T k, f]
   void* out;
   int32_t* err;
+  FewLists* lists;
   // set by the launcher
   bool router;
-  int cluster, t_pad, stages, stage_bytes;
+  int t_pad, router_bytes, router_stages, part_at;
 };
 
 cudaError_t launch_few(const FewParams& p, const FewTensors& w, cudaStream_t s);
