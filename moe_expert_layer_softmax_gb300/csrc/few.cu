@@ -36,8 +36,8 @@ constexpr int kThreads = 192;          // TMA, MMA, four warps of the epilogue
 constexpr int kEpi = 128;
 constexpr int kCluster = 4;
 constexpr int kMaxSteps = 8;           // times 64 columns of a stage
-constexpr int kStageBytes = 34 * 1024;   // 128 columns of 128 rows of weights and of eight tokens
-constexpr int kMaxStages = 6, kRouterStages = 12;
+constexpr int kStageBytes = 36 * 1024;   // 128 columns of 128 rows of weights and of 16 tokens
+constexpr int kMaxStages = 6, kRouterStages = 16;
 constexpr int kAccCols = 64;           // of an accumulator: tokens of an expert
 constexpr int kTmem = 2 * kAccCols;
 
@@ -69,6 +69,14 @@ MOE_DEV void tma_box(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x,
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y)
       : "memory");
 }
+// 64 columns of rows, several times: {column of 64, row, which 64 columns}.
+MOE_DEV void tma_box3(uint32_t dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
 MOE_DEV void st_cluster(uint32_t addr, float v) {
   asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
 }
@@ -90,6 +98,7 @@ struct UpMaps {
 };
 struct DownMaps {
   CUtensorMap down[5], act[4];
+  CUtensorMap down4, act2, act4;   // eight rows, two or four times 64 columns
 };
 // Row groups in front of the box of 2^b groups of a run of n.
 MOE_DEV int box_before(int n, int b) { return n & ~((2 << b) - 1); }
@@ -120,14 +129,19 @@ struct DownCtl : Ctl {
 };
 
 // Shared memory.  An MMA reads 16 KB from where its rows begin, whatever lies behind
-// them: of the last stage's up to 16 KB past the ring.
+// them: up to 16 KB past the last stage's weights.
 constexpr int kOverread = 16 * 1024, kSumBytes = MOE_FEW_MAX_TOKENS * 512;
 constexpr int kStages = kMaxStages, kRingBytes = kStages * kStageBytes;
 constexpr int kDownStages = 5, kDownRingBytes = kDownStages * kStageBytes;
-constexpr int kUpSmem = kRingBytes + (sizeof(UpCtl) > kOverread ? (int)sizeof(UpCtl) : kOverread);
+constexpr int kUpSmem = kRingBytes + (int)sizeof(UpCtl);
 constexpr int kDownSmem = kDownRingBytes + kSumBytes + (int)sizeof(DownCtl);
 static_assert(kUpSmem <= 227 * 1024 && kDownSmem <= 227 * 1024 && kSumBytes >= kOverread, "shared memory of a CTA");
-// the router's parts leave two stages at least: (16 + 8) KB each
+// up: s rows' parts of `a` bytes end s b bytes before the stage's end and s (a + b) <= the
+// stage, so that the last one begins 12 KB before it at least (a = 4 KB, s = 7)
+static_assert(sizeof(UpCtl) >= 4096, "what an MMA reads behind the up kernel's ring");
+// a wide stage's 16 groups are 4 KB apart
+static_assert((kDownStages - 1) * kStageBytes + 68 * 1024 <= kDownSmem, "what an MMA reads behind the down kernel's ring");
+// the router's parts (16 KB at least, for its MMAs) leave two stages of (16 + 8) KB
 static_assert(kRingBytes - MOE_FEW_MAX_TOKENS * 256 * 4 >= 2 * 24 * 1024, "the router's stages");
 
 // From the masks (complete, behind a barrier): the active experts in ascending order and
@@ -311,10 +325,12 @@ struct Ring {
 };
 
 // How a piece of rows fills its stages: `s` times 64 columns, the weights' rows of each
-// behind one another, then the tokens'.
+// behind one another, then the tokens'.  `wide`: a full stage holds s times 64 columns of
+// each group of eight rows behind one another (a copy for each group).
 struct Fill {
   int s;
   uint32_t a, b;   // bytes of 64 columns
+  bool wide = false;
   MOE_DEV Fill(uint32_t a_, uint32_t b_) : s(max(1, min(kMaxSteps, kStageBytes / (int)(a_ + b_)))), a(a_), b(b_) {}
 };
 
@@ -345,10 +361,12 @@ MOE_DEV bool multiply(Ctl& s, const FewParams& p, Ring& r, int it, const Fill& f
     if (!mbar_wait(&r.full[r.stage], r.phase, &s.abort, p.err)) return false;
     tc_fence_after();
     uint32_t a = r.at(), b = a + fill.s * fill.a;
-    for (int q = 0; q < fill.s && c + q < chunks; ++q, a += fill.a, b += fill.b) {
+    const bool wide = fill.wide && c + fill.s <= chunks;
+    const uint32_t step = wide ? 1024 : fill.a, group = wide ? fill.s * 1024 : 1024;
+    for (int q = 0; q < fill.s && c + q < chunks; ++q, a += step, b += fill.b) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
-        tc_mma_bf16(d, smem_desc_sw128(a + k * 32, 16, 1024), smem_desc_sw128(b + k * 32, 16, 1024), idesc, (c | q | k) != 0);
+        tc_mma_bf16(d, smem_desc_sw128(a + k * 32, 16, group), smem_desc_sw128(b + k * 32, 16, 1024), idesc, (c | q | k) != 0);
     }
     tc_commit(&r.empty[r.stage]);
     r.next();
@@ -406,6 +424,15 @@ struct UpPiece {
     return true;
   }
 };
+
+// Where CTA i's share begins.  Not one or two groups beside an expert's end: they would be
+// a piece of their own, of many small copies (1 token, 8 experts of 4096 x 2048: the last
+// of 144 CTAs 63 us after the start, the median 53).
+MOE_DEV int up_share(int total, int groups, int i) {
+  const int at = share(total, i, gridDim.x), r = at % groups;
+  if (total < 8 * (int)gridDim.x) return at;
+  return r <= 2 ? at - r : groups - r <= 2 ? at + groups - r : at;
+}
 
 // Columns of the MMA for an expert of m tokens; how n groups of gate and of up rows and
 // these tokens fill a stage.
@@ -509,8 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   const int groups = p.f / 8;
   const int total = s.n_act * groups;
-  int g = share(total, blockIdx.x, gridDim.x);
-  const int g_end = share(total, blockIdx.x + 1, gridDim.x);
+  int g = up_share(total, groups, blockIdx.x);
+  const int g_end = up_share(total, groups, blockIdx.x + 1);
   UpPiece u;
   if (warp == 0) {
     while (ok && u.next(g, g_end, groups)) {
@@ -622,7 +649,14 @@ struct DownPiece {
 // The box of 8 << b routes that holds m of them; how n groups of rows and these routes
 // fill a stage.
 MOE_DEV int route_box(int m) { return m <= 8 ? 0 : m <= 16 ? 1 : m <= 32 ? 2 : 3; }
-MOE_DEV Fill down_fill(int n, int m) { return Fill(n * 1024, 1024 << route_box(m)); }
+MOE_DEV Fill down_fill(int n, int m) {
+  Fill f(n * 1024, 1024 << route_box(m));
+  if (m <= 8 && n >= 4 && n <= 8) {   // fewer and larger copies
+    f.s = 4;
+    f.wide = n < 8;
+  }
+  return f;
+}
 
 __global__ void __launch_bounds__(kThreads, 1)
     few_down_kernel(const __grid_constant__ DownMaps maps, const FewParams p) {
@@ -663,18 +697,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = s.act[u.a], r0 = s.base[u.a], m = s.base[u.a + 1] - r0;
         // lanes 0-4: rows of weights, lane 8: the routes, the smallest box that holds them
         const Fill fill = down_fill(n, m);
+        // (a wide stage: lanes 0-6, a group each)
         const int b = lane < 5 ? lane : 0, before = box_before(n, b), act = route_box(m);
         const bool weights = lane < 5 && (n >> b & 1), routes = lane == 8;
+        const bool once = m <= 8 && (fill.s == 2 || fill.s == 4 || fill.s == 8);   // the routes of a full stage in one copy (eight steps: in two)
         const uint32_t place = routes ? fill.s * fill.a : before * 1024u, step = routes ? fill.b : fill.a;
         const CUtensorMap* map = routes ? &maps.act[act] : &maps.down[b];
+        const CUtensorMap* many = fill.s == 2 ? &maps.act2 : &maps.act4;
         const int y = routes ? r0 : e * p.d + (g0 + before) * 8;
         for (int c = u.c; c < u.c + u.n; c += fill.s) {
           const int steps = min(fill.s, u.c + u.n - c);
+          const bool full = steps == fill.s, wide = full && fill.wide, one = full && once;
           ok = claim(s, p, ring, steps * (fill.a + fill.b));
           if (!ok) break;
-          uint32_t dst = ring.at() + place;
-          for (int q = c; q < c + steps; ++q, dst += step)
-            if (weights || routes) tma_box(dst, map, &ring.full[ring.stage], q * 64, y);
+          const uint32_t at = ring.at();
+          uint64_t* bar = &ring.full[ring.stage];
+          if (one && routes) {
+            tma_box3(at + place, many, bar, 0, y, c);
+            if (fill.s == 8) tma_box3(at + place + 4 * step, many, bar, 0, y, c + 4);
+          }
+          if (wide && lane < n) tma_box3(at + lane * fill.s * 1024u, &maps.down4, bar, 0, e * p.d + (g0 + lane) * 8, c);
+          if ((weights && !wide) || (routes && !one)) {
+            uint32_t dst = at + place;
+            for (int q = c; q < c + steps; ++q, dst += step) tma_box(dst, map, bar, q * 64, y);
+          }
           ring.next();
         }
       }
@@ -781,7 +827,8 @@ cudaError_t launch_few(const FewParams& args, const FewTensors& w, cudaStream_t 
   const uint64_t routes = ((uint64_t)p.T * p.k + 7) / 8 * 8;
   // the router's stages in front of the parts of its products
   p.router_bytes = ((p.E < 128 ? p.E : 128) + 7) / 8 * 1024 + (p.T + 7) / 8 * 1024;
-  p.part_at = (kRingBytes - kCluster * ((p.T + kCluster - 1) / kCluster) * p.E * 4) / 1024 * 1024;
+  const int parts = kCluster * ((p.T + kCluster - 1) / kCluster) * p.E * 4;
+  p.part_at = (kRingBytes - (parts > kOverread ? parts : kOverread)) / 1024 * 1024;
   p.router_stages = p.part_at / p.router_bytes < kRouterStages ? p.part_at / p.router_bytes : kRouterStages;
   UpMaps up;
   DownMaps down;
@@ -798,6 +845,8 @@ cudaError_t launch_few(const FewParams& args, const FewTensors& w, cudaStream_t 
              make_bf16_map(&up.up[b], w.w_up, d, E * f, 64, height) &&
              make_bf16_map(&down.act[b], p.act, f, routes, 64, height);
   }
+  made = made && make_bf16_map3(&down.down4, w.w_down, f, E * d, 8, 4) && make_bf16_map3(&down.act2, p.act, f, routes, 8, 2) &&
+         make_bf16_map3(&down.act4, p.act, f, routes, 8, 4);
   if (!made) return cudaErrorInvalidValue;
   static SmemLimit up_limit, down_limit;
   cudaError_t e = up_limit.raise(reinterpret_cast<const void*>(&few_up_kernel), kUpSmem);
