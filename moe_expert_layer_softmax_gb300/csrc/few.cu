@@ -407,8 +407,11 @@ MOE_DEV void leave(Ctl& s) {
   }
 }
 
-// The first of share i of n: the first total % n shares are one larger than the others.
-MOE_DEV int share(int total, int i, int n) { return total / n * i + min(i, total % n); }
+// Where share i of n begins, floor(total i / n): whole experts where they divide the CTAs
+// evenly.  64 bits (a slow division) only where 32 do not hold the product.
+MOE_DEV int share(int total, int i, int n) {
+  return total < (1 << 23) ? (int)((uint32_t)total * (uint32_t)i / (uint32_t)n) : (int)((int64_t)total * i / n);
+}
 MOE_DEV int round16(int n) { return (n + 15) & ~15; }
 
 // The next rows of a share of (active expert, group of eight d_ff rows): at most eight
@@ -429,9 +432,8 @@ struct UpPiece {
 // a piece of their own, of many small copies (1 token, 8 experts of 4096 x 2048: the last
 // of 144 CTAs 63 us after the start, the median 53).
 MOE_DEV int up_share(int total, int groups, int i) {
-  const int at = share(total, i, gridDim.x), r = at % groups;
-  if (total < 8 * (int)gridDim.x) return at;
-  return r <= 2 ? at - r : groups - r <= 2 ? at + groups - r : at;
+  const int at = share(total, i, gridDim.x), r = at % groups, near = min(2, total / ((int)gridDim.x * 4));
+  return r <= near ? at - r : groups - r <= near ? at + groups - r : at;
 }
 
 // Columns of the MMA for an expert of m tokens; how n groups of gate and of up rows and
