@@ -351,6 +351,27 @@ MOE_DEV void drain(const Ring& r) {
   }
 }
 
+// The words of smem_desc_sw128(address, 16, group).
+MOE_DEV uint32_t desc_lo(uint32_t address) { return (address & 0x3FFFFu) >> 4 | 1u << 16; }
+MOE_DEV uint32_t desc_hi(uint32_t group) { return group >> 4 | 1u << 14 | 2u << 29; }
+
+// Four MMAs: 64 columns of K.
+MOE_DEV void mma_64(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 a0, a1, a2, a3, b0, b1, b2, b3;\n\t.reg .b32 x, y;\n\t"
+      "setp.ne.b32 p, %6, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
+      "mov.b64 a0, {%1, %2};\n\tmov.b64 b0, {%3, %4};\n\t"
+      "add.u32 x, %1, 2;\n\tadd.u32 y, %3, 2;\n\tmov.b64 a1, {x, %2};\n\tmov.b64 b1, {y, %4};\n\t"
+      "add.u32 x, %1, 4;\n\tadd.u32 y, %3, 4;\n\tmov.b64 a2, {x, %2};\n\tmov.b64 b2, {y, %4};\n\t"
+      "add.u32 x, %1, 6;\n\tadd.u32 y, %3, 6;\n\tmov.b64 a3, {x, %2};\n\tmov.b64 b3, {y, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a0, b0, %5, p;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %5, t;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %5, t;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %5, t;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
 // One thread: `chunks` times 64 columns multiplied into accumulator `it`.
 MOE_DEV bool multiply(Ctl& s, const FewParams& p, Ring& r, int it, const Fill& fill, int chunks, int n) {
   const int acc = it & 1;
@@ -360,14 +381,13 @@ MOE_DEV bool multiply(Ctl& s, const FewParams& p, Ring& r, int it, const Fill& f
   for (int c = 0; c < chunks; c += fill.s) {
     if (!mbar_wait(&r.full[r.stage], r.phase, &s.abort, p.err)) return false;
     tc_fence_after();
-    uint32_t a = r.at(), b = a + fill.s * fill.a;
+    const uint32_t a = r.at(), b = a + fill.s * fill.a;
     const bool wide = fill.wide && c + fill.s <= chunks;
     const uint32_t step = wide ? 1024 : fill.a, group = wide ? fill.s * 1024 : 1024;
-    for (int q = 0; q < fill.s && c + q < chunks; ++q, a += step, b += fill.b) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        tc_mma_bf16(d, smem_desc_sw128(a + k * 32, 16, group), smem_desc_sw128(b + k * 32, 16, 1024), idesc, (c | q | k) != 0);
-    }
+    const uint32_t a_hi = desc_hi(group), b_hi = desc_hi(1024);
+    uint32_t a_lo = desc_lo(a), b_lo = desc_lo(b);
+    for (int q = 0; q < fill.s && c + q < chunks; ++q, a_lo += step >> 4, b_lo += fill.b >> 4)
+      mma_64(d, a_lo, a_hi, b_lo, b_hi, idesc, (c | q) != 0);
     tc_commit(&r.empty[r.stage]);
     r.next();
   }
