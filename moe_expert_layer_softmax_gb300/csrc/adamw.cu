@@ -37,6 +37,58 @@ template <int N> struct AdamwList {
   AdamwParams p;
 };
 
+// Two floats whose products and fused operations take one instruction together (sm_100
+// on).  Plain sums are taken one by one: a packed product and a packed sum after it came
+// out as one fused operation (CUDA 13.0), rounded once and not twice.
+struct Two {
+  uint64_t v;
+  MOE_DEV Two() {}
+  MOE_DEV Two(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+  MOE_DEV explicit Two(float2 f) : Two(f.x, f.y) {}
+  MOE_DEV float2 get() const {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+  }
+};
+MOE_DEV Two mul(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+MOE_DEV Two fma(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+MOE_DEV float2 add(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
+
+// Correctly rounded roots and quotients of pairs from the hardware's approximations by
+// the iterations of P. Markstein ("Computation of elementary functions on the IBM RISC
+// System/6000 processor", IBM J. Res. Dev. 34, 1990): a Newton step on the reciprocal
+// (root), then the residual of the quotient (square), which is exact, decides the last
+// bit.  For v in [2^-100, 2^100], |m| in [2^-60, 2^60] and n in -[2^-60, 2^60], where
+// nothing on the way leaves the normal range.  Compared with __fsqrt_rn on every
+// mantissa of both parities, the reciprocal with __frcp_rn on every mantissa (then the
+// quotient is right by Markstein's theorem), 2.5e10 quotients with __fdiv_rn: no difference.
+MOE_DEV Two roots(float2 v) {
+  float x, y;
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(v.x));
+  asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(v.y));
+  const Two a(x, y), g = mul(Two(v), a), h = mul(a, Two(-0.5f, -0.5f)), r = fma(g, h, Two(0.5f, 0.5f));
+  const Two g1 = fma(g, r, g), h1 = fma(h, r, h);
+  const float2 q = g1.get();
+  return fma(Two(fmaf(q.x, q.x, -v.x), fmaf(q.y, q.y, -v.y)), h1, g1);
+}
+// m / -n
+MOE_DEV Two quotients(Two m, float2 n) {
+  float x, y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(-n.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(-n.y));
+  const Two a(x, y), d(n), b = fma(fma(d, a, Two(1.0f, 1.0f)), a, a), q = mul(m, b);
+  return fma(fma(d, q, m), b, q);
+}
+
 // b^t in double, by squaring.
 MOE_DEV double power(double b, int64_t t) {
   double r = 1.0;
@@ -75,52 +127,96 @@ template <typename T> MOE_DEV void put8(T* p, int64_t at, int64_t n, bool vec, c
     if (at + j < n) p[at + j] = r.v[j];
 }
 
-// Number j (16 bits) of the eight that a counter gives.
+// Number j (16 bits) of the eight that a counter gives, and the same times 16.
 MOE_DEV uint32_t number_of(const uint4& r, int j) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
   return j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFFu;
 }
+MOE_DEV uint32_t number16_of(const uint4& r, int j) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  return j & 1 ? w[j >> 1] >> 12 & 0xFFFF0u : w[j >> 1] << 4 & 0xFFFF0u;
+}
 
-// The magnitude z in [0, 448] to one of its E4M3 neighbours: up where the remainder,
-// in units of the distance of the two, is at least 1 - r / 2^16.
-MOE_DEV float round_e4m3(float z, uint32_t r) {
-  const uint32_t e = max(__float_as_uint(z) >> 23, 121u);   // 2^-6 and below: steps of 2^-9
-  const float q = z * __uint_as_float((257u - e) << 23);
-  const float low = floorf(q);
-  const bool up = (q - low) * 65536.0f >= (float)(65536u - r);
-  return (low + (up ? 1.0f : 0.0f)) * __uint_as_float((e - 3u) << 23);
+// The largest and the smallest magnitude of eight values; a NaN goes through to both.
+MOE_DEV void magnitudes(const float* x, float& most, float& least) {
+  most = least = fabsf(x[0]);
+#pragma unroll
+  for (int j = 1; j < 8; ++j) {
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(most) : "f"(most), "f"(fabsf(x[j])));
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(least) : "f"(least), "f"(fabsf(x[j])));
+  }
 }
 
 // Eight values to codes with the scale of the 16 lanes' 128 values; the scale is
-// returned.  An infinity or a NaN becomes a NaN and takes no part in the scale.
-// LEAST: what is above zero does not become zero.
-template <bool LEAST> MOE_DEV float quantize8(const float* x, const uint4& numbers, uint2& codes) {
-  float top = 0.0f;
+// returned.  `most`, `least`: the magnitudes() of the eight.  An infinity or a NaN
+// becomes a NaN and takes no part in the scale.  ROOT: nothing is below zero, and what is
+// above it does not become zero.
+//
+// A magnitude z = |x| 448 / top goes up to the next code where its remainder, in units of
+// the codes' distance, is at least 1 - r / 2^16: the upper three bits of the mantissa
+// stay, and adding r at the upper sixteen of the twenty others carries into them exactly
+// then.  (Past 448 the conversion saturates.)  Below 2^-6 the distance is 2^-9, that of
+// the values from 2^-6 on: such values are moved there and back, cut off to steps of
+// 2^-29, which leaves the comparison with multiples of 2^-25 as it is.  Few warps hold
+// one: the others take none of these steps.
+template <bool ROOT> MOE_DEV float quantize8(const float* x, float most, float least, const uint4& numbers, uint2& codes) {
+  float top = most;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]) < INFINITY ? fabsf(x[j]) : 0.0f);
+  for (int off = 8; off > 0; off >>= 1) {
+    const float other = __shfl_xor_sync(0xffffffffu, top, off);
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(top) : "f"(top), "f"(other));
+  }
+  const bool odd = __any_sync(0xffffffffu, !(top < INFINITY));
+  if (odd) {   // the largest finite one (every lane takes part)
+    top = 0.0f;
 #pragma unroll
-  for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[j]) < INFINITY ? fabsf(x[j]) : 0.0f);
+#pragma unroll
+    for (int off = 8; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  }
   const bool some = top >= 0x1p-100f;   // smaller values have no inverse in 32 bits
   const float inv = some ? __fmul_rn(448.0f, __frcp_rn(top)) : 0.0f;
-  float c[8];
+  const Two inv2(inv, inv);
+  float z[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float z = fminf(__fmul_rn(fabsf(x[j]), inv), 448.0f);
-    float q = round_e4m3(z, number_of(numbers, j));
-    if (LEAST && z > 0.0f && q == 0.0f) q = 0x1p-9f;
-    c[j] = fabsf(x[j]) < INFINITY ? copysignf(q, x[j]) : NAN;
+  for (int j = 0; j < 8; j += 2) {
+    const float2 p = mul(Two(x[j], x[j + 1]), inv2).get();
+    z[j] = p.x;
+    z[j + 1] = p.y;
   }
-  codes = e4m3x8(c);
+  if (odd || __any_sync(0xffffffffu, __fmul_rn(least, inv) < 0x1p-6f)) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float a = fabsf(z[j]), shift = a < 0x1p-6f ? 0x1p-6f : 0.0f;
+      float q = __uint_as_float((__float_as_uint(__fadd_rz(a, shift)) + number16_of(numbers, j)) & 0xFFF00000u) - shift;
+      if (ROOT && a > 0.0f) q = fmaxf(q, 0x1p-9f);
+      z[j] = fabsf(x[j]) < INFINITY ? copysignf(q, x[j]) : NAN;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t bits = __float_as_uint(z[j]), up = (bits & 0x7FFFFFFFu) + number16_of(numbers, j);
+      z[j] = __uint_as_float(ROOT ? (bits + number16_of(numbers, j)) & 0xFFF00000u : (up & 0x7FF00000u) | (bits & 0x80000000u));
+    }
+  }
+  codes = e4m3x8(z);
   return some ? __fmul_rn(top, 1.0f / 448.0f) : 0.0f;
 }
 
-MOE_DEV void widen_codes(const uint2& q, float scale, float* f) {
+// The values of eight codes, or (SQUARE) their squares.
+template <bool SQUARE> MOE_DEV void widen_codes(const uint2& q, float scale, float* f) {
   e4m3x2_to_f32(q.x, f[0], f[1]);
   e4m3x2_to_f32(q.x >> 16, f[2], f[3]);
   e4m3x2_to_f32(q.y, f[4], f[5]);
   e4m3x2_to_f32(q.y >> 16, f[6], f[7]);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], scale);
+  for (int j = 0; j < 8; j += 2) {
+    Two t = mul(Two(f[j], f[j + 1]), Two(scale, scale));
+    if (SQUARE) t = mul(t, t);
+    const float2 p = t.get();
+    f[j] = p.x;
+    f[j + 1] = p.y;
+  }
 }
 
 // TP, TG: types of parameters and gradients; MASTER: the fp32 copy is what is
@@ -181,10 +277,8 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
         mq = make_uint2(mw[0], mw[1]);
         vq = make_uint2(vw[0], vw[1]);
       }
-      widen_codes(mq, ms, m);
-      widen_codes(vq, vs, v);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(v[j], v[j]);
+      widen_codes<false>(mq, ms, m);
+      widen_codes<true>(vq, vs, v);
     } else {
       widen8(fetch8<float>(static_cast<const float*>(t.m), at, n, vec), m);
       widen8(fetch8<float>(static_cast<const float*>(t.v), at, n, vec), v);
@@ -197,14 +291,38 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
 #pragma unroll
     for (int j = 0; j < 8; ++j) g[j] = __fmul_rn(g[j], scale);
   }
-  float root[8];
+  const Two beta1(s.beta1, s.beta1), one_beta1(s.one_beta1, s.one_beta1), beta2(s.beta2, s.beta2),
+      one_beta2(s.one_beta2, s.one_beta2);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    m[j] = __fadd_rn(__fmul_rn(m[j], s.beta1), __fmul_rn(g[j], s.one_beta1));
-    v[j] = __fadd_rn(__fmul_rn(v[j], s.beta2), __fmul_rn(__fmul_rn(g[j], g[j]), s.one_beta2));
-    root[j] = __fsqrt_rn(v[j]);
-    const float d = __fadd_rn(__fmul_rn(root[j], s.root_scale), s.eps);
-    w[j] = __fadd_rn(__fmul_rn(w[j], s.decay), -__fmul_rn(__fdiv_rn(m[j], d), s.rate));
+  for (int j = 0; j < 8; j += 2) {
+    const Two gg(g[j], g[j + 1]);
+    const float2 mm = add(mul(Two(m[j], m[j + 1]), beta1).get(), mul(gg, one_beta1).get());
+    const float2 vv = add(mul(Two(v[j], v[j + 1]), beta2).get(), mul(mul(gg, gg), one_beta2).get());
+    m[j] = mm.x; m[j + 1] = mm.y;
+    v[j] = vv.x; v[j + 1] = vv.y;
+  }
+  float root[8], m_most, m_least, v_most, v_least;
+  magnitudes(m, m_most, m_least);
+  magnitudes(v, v_most, v_least);
+  // the divisor, root * root_scale + eps, below zero: what quotients() takes
+  const Two root_scale(-s.root_scale, -s.root_scale), decay(s.decay, s.decay), rate(-s.rate, -s.rate);
+  const float2 eps = make_float2(-s.eps, -s.eps);
+  if (p.narrow && v_least >= 0x1p-100f && v_most <= 0x1p100f && m_least >= 0x1p-60f && m_most <= 0x1p60f) {
+#pragma unroll
+    for (int j = 0; j < 8; j += 2) {
+      const Two rt = roots(make_float2(v[j], v[j + 1]));
+      const Two q = quotients(Two(m[j], m[j + 1]), add(mul(rt, root_scale).get(), eps));
+      const float2 ww = add(mul(Two(w[j], w[j + 1]), decay).get(), mul(q, rate).get()), rr = rt.get();
+      root[j] = rr.x; root[j + 1] = rr.y;
+      w[j] = ww.x; w[j + 1] = ww.y;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      root[j] = __fsqrt_rn(v[j]);
+      const float d = __fadd_rn(__fmul_rn(root[j], s.root_scale), s.eps);
+      w[j] = __fadd_rn(__fmul_rn(w[j], s.decay), -__fmul_rn(__fdiv_rn(m[j], d), s.rate));
+    }
   }
   uint4 numbers[3];
   if constexpr (SMALL || DRAWN) {
@@ -220,8 +338,10 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
   }
   if constexpr (SMALL) {
     uint2 mq, vq;
-    const float ms = quantize8<false>(m, numbers[0], mq);
-    const float vs = quantize8<true>(root, numbers[1], vq);
+    const float ms = quantize8<false>(m, m_most, m_least, numbers[0], mq);
+    float r_most, r_least;
+    magnitudes(root, r_most, r_least);
+    const float vs = quantize8<true>(root, r_most, r_least, numbers[1], vq);
     if (live && (threadIdx.x & 15) == 0) {
       t.m_scale[block] = ms;
       t.v_scale[block] = vs;
@@ -245,11 +365,21 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
   }
   if constexpr (MASTER) put8(t.master, at, n, vec, narrow8<float>(w));
   if constexpr (DRAWN) {
+    // the upper 16 bits are what bf16 keeps; not finite: as it is
+    uint32_t words[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)   // the upper 16 bits are what bf16 keeps; not finite: as it is
-      if (fabsf(w[j]) < INFINITY) w[j] = __uint_as_float((__float_as_uint(w[j]) + number_of(numbers[2], j)) & 0xFFFF0000u);
+    for (int j = 0; j < 8; j += 2) {
+      uint32_t lo = __float_as_uint(w[j]), hi = __float_as_uint(w[j + 1]);
+      if (fabsf(w[j]) < INFINITY) lo += number_of(numbers[2], j);
+      if (fabsf(w[j + 1]) < INFINITY) hi += number_of(numbers[2], j + 1);
+      words[j >> 1] = __byte_perm(lo, hi, 0x7632);
+    }
+    Raw8<TP> out;
+    *reinterpret_cast<uint4*>(&out) = make_uint4(words[0], words[1], words[2], words[3]);
+    put8(static_cast<TP*>(t.param), at, n, vec, out);
+  } else {
+    put8(static_cast<TP*>(t.param), at, n, vec, narrow8<TP>(w));
   }
-  put8(static_cast<TP*>(t.param), at, n, vec, narrow8<TP>(w));
 }
 
 template <int N, typename TP, typename TG, bool MASTER>

@@ -319,6 +319,8 @@ int moe_adamw(const moe_adamw_args_t* a, void* stream) {
   p.s.beta1 = (float)a->beta1; p.s.one_beta1 = (float)(1.0 - a->beta1);
   p.s.beta2 = (float)a->beta2; p.s.one_beta2 = (float)(1.0 - a->beta2);
   p.s.eps = (float)a->eps;
+  // 1 / sqrt(1 - b2^t) is at most 1 / sqrt(1 - b2), whatever t
+  p.narrow = a->eps >= 0x1p-60 && a->eps <= 1.0 && 1.0 - a->beta2 >= 0x1p-16;
   p.lr = a->lr; p.beta1 = a->beta1; p.beta2 = a->beta2; p.weight_decay = a->weight_decay;
   if (!a->step_dev) {
     p.c1 = 1.0 - std::pow(a->beta1, (double)a->step);

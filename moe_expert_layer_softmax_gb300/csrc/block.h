@@ -102,6 +102,7 @@ struct AdamwScalars {
 
 struct AdamwParams {
   int n, first_tensor;   // tensors of this launch, and those of the call before them
+  bool narrow;           // eps and 1 / sqrt(1 - b2^t) where the divisor stays within 2^-60 .. 2^60
   AdamwScalars s;
   const float* grad_scale;
   const float* lr_dev;
