@@ -37,30 +37,8 @@ template <int N> struct AdamwList {
   AdamwParams p;
 };
 
-// Two floats whose products and fused operations take one instruction together (sm_100
-// on).  Plain sums are taken one by one: a packed product and a packed sum after it came
-// out as one fused operation (CUDA 13.0), rounded once and not twice.
-struct Two {
-  uint64_t v;
-  MOE_DEV Two() {}
-  MOE_DEV Two(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
-  MOE_DEV explicit Two(float2 f) : Two(f.x, f.y) {}
-  MOE_DEV float2 get() const {
-    float2 r;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-    return r;
-  }
-};
-MOE_DEV Two mul(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-MOE_DEV Two fma(Two a, Two b, Two c) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
+// Sums of pairs, one by one: a packed product and a packed sum after it came out as one
+// fused operation (CUDA 13.0), rounded once and not twice.
 MOE_DEV float2 add(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x), __fadd_rn(a.y, b.y)); }
 
 // Correctly rounded roots and quotients of pairs from the hardware's approximations by
@@ -132,19 +110,18 @@ MOE_DEV uint32_t number_of(const uint4& r, int j) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
   return j & 1 ? w[j >> 1] >> 16 : w[j >> 1] & 0xFFFFu;
 }
-MOE_DEV uint32_t number16_of(const uint4& r, int j) {
-  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-  return j & 1 ? w[j >> 1] >> 12 & 0xFFFF0u : w[j >> 1] << 4 & 0xFFFF0u;
-}
+MOE_DEV uint32_t number16_of(const uint4& r, int j) { return number_of(r, j) << 4; }
 
 // The largest and the smallest magnitude of eight values; a NaN goes through to both.
 MOE_DEV void magnitudes(const float* x, float& most, float& least) {
   most = least = fabsf(x[0]);
 #pragma unroll
-  for (int j = 1; j < 8; ++j) {
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(most) : "f"(most), "f"(fabsf(x[j])));
-    asm("min.NaN.f32 %0, %1, %2;" : "=f"(least) : "f"(least), "f"(fabsf(x[j])));
+  for (int j = 1; j < 7; j += 2) {
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(most) : "f"(most), "f"(fabsf(x[j])), "f"(fabsf(x[j + 1])));
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(least) : "f"(least), "f"(fabsf(x[j])), "f"(fabsf(x[j + 1])));
   }
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(most) : "f"(most), "f"(fabsf(x[7])));
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(least) : "f"(least), "f"(fabsf(x[7])));
 }
 
 // Eight values to codes with the scale of the 16 lanes' 128 values; the scale is
@@ -301,7 +278,7 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
     m[j] = mm.x; m[j + 1] = mm.y;
     v[j] = vv.x; v[j + 1] = vv.y;
   }
-  float root[8], m_most, m_least, v_most, v_least;
+  float root[8], m_most, m_least, v_most, v_least, r_most, r_least;   // (roots have the order of their squares)
   magnitudes(m, m_most, m_least);
   magnitudes(v, v_most, v_least);
   // the divisor, root * root_scale + eps, below zero: what quotients() takes
@@ -316,6 +293,11 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
       root[j] = rr.x; root[j + 1] = rr.y;
       w[j] = ww.x; w[j + 1] = ww.y;
     }
+    if constexpr (SMALL) {
+      const float2 r = roots(make_float2(v_most, v_least)).get();
+      r_most = r.x;
+      r_least = r.y;
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -323,6 +305,8 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
       const float d = __fadd_rn(__fmul_rn(root[j], s.root_scale), s.eps);
       w[j] = __fadd_rn(__fmul_rn(w[j], s.decay), -__fmul_rn(__fdiv_rn(m[j], d), s.rate));
     }
+    r_most = __fsqrt_rn(v_most);
+    r_least = __fsqrt_rn(v_least);
   }
   uint4 numbers[3];
   if constexpr (SMALL || DRAWN) {
@@ -339,8 +323,6 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
   if constexpr (SMALL) {
     uint2 mq, vq;
     const float ms = quantize8<false>(m, m_most, m_least, numbers[0], mq);
-    float r_most, r_least;
-    magnitudes(root, r_most, r_least);
     const float vs = quantize8<true>(root, r_most, r_least, numbers[1], vq);
     if (live && (threadIdx.x & 15) == 0) {
       t.m_scale[block] = ms;
@@ -367,12 +349,21 @@ __global__ void __launch_bounds__(kAdamThreads) adamw_kernel(const __grid_consta
   if constexpr (DRAWN) {
     // the upper 16 bits are what bf16 keeps; not finite: as it is
     uint32_t words[4];
+    float most, least;
+    magnitudes(w, most, least);
+    if (most < INFINITY) {
 #pragma unroll
-    for (int j = 0; j < 8; j += 2) {
-      uint32_t lo = __float_as_uint(w[j]), hi = __float_as_uint(w[j + 1]);
-      if (fabsf(w[j]) < INFINITY) lo += number_of(numbers[2], j);
-      if (fabsf(w[j + 1]) < INFINITY) hi += number_of(numbers[2], j + 1);
-      words[j >> 1] = __byte_perm(lo, hi, 0x7632);
+      for (int j = 0; j < 8; j += 2)
+        words[j >> 1] = __byte_perm(__float_as_uint(w[j]) + number_of(numbers[2], j),
+                                    __float_as_uint(w[j + 1]) + number_of(numbers[2], j + 1), 0x7632);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        uint32_t lo = __float_as_uint(w[j]), hi = __float_as_uint(w[j + 1]);
+        if (fabsf(w[j]) < INFINITY) lo += number_of(numbers[2], j);
+        if (fabsf(w[j + 1]) < INFINITY) hi += number_of(numbers[2], j + 1);
+        words[j >> 1] = __byte_perm(lo, hi, 0x7632);
+      }
     }
     Raw8<TP> out;
     *reinterpret_cast<uint4*>(&out) = make_uint4(words[0], words[1], words[2], words[3]);

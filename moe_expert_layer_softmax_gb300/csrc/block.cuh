@@ -141,6 +141,36 @@ template <typename T, int V> MOE_DEV void store8_warp(T* row, int c, int G, int 
   }
 }
 
+// ------------------------------------------------------------------ pairs
+// Two floats whose products, sums and fused operations take one instruction together
+// (sm_100 on).
+struct Two {
+  uint64_t v;
+  MOE_DEV Two() {}
+  MOE_DEV Two(float x, float y) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(x), "f"(y)); }
+  MOE_DEV explicit Two(float2 f) : Two(f.x, f.y) {}
+  MOE_DEV float2 get() const {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+  }
+};
+MOE_DEV Two mul(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+MOE_DEV Two fma(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+MOE_DEV Two sum(Two a, Two b) {
+  Two r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+
 // ------------------------------------------------------------------ asynchronous copies
 MOE_DEV void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");

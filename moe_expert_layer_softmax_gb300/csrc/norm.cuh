@@ -95,6 +95,33 @@ template <bool SMALL> struct RowGroup {
     }
     return s;
   }
+  // Sum over the group's threads of this warp.
+  MOE_DEV float part(float v) const {
+    if (!SMALL || G >= 32) return warp_sum(v);
+    for (int off = G >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+  }
+  // From the warps' sums, their squares' distances from their own means and how many
+  // values they have: the mean and the squares' distances from it.
+  MOE_DEV float join(float s, float squares, float n, float inv_d, float4* red, float& mean) const {
+    if (G <= 32) {
+      mean = s * inv_d;
+      return squares;
+    }
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float4(s, squares, n, n > 0.0f ? s / n : 0.0f);
+    bar_sync(1 + group, G);
+    const int warps = G >> 5;
+    const float4* from = red + group * warps;
+    float all = 0.0f, sum = 0.0f;
+    for (int i = 0; i < warps; ++i) sum += from[i].x;
+    mean = sum * inv_d;
+    for (int i = 0; i < warps; ++i) {
+      const float4 w = from[i];
+      const float off = w.w - mean;
+      all += fmaf(w.z * off, off, w.y);
+    }
+    return all;
+  }
   // Two sums behind one barrier.
   MOE_DEV void sum2(float& v, float& w, float* red, float* red2) const {
     for (int off = (!SMALL || G >= 32) ? 16 : G >> 1; off > 0; off >>= 1) {

@@ -34,7 +34,14 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING || kNextInRegisters<TR,
   const RowGroup<NV == 1> rg(p.group);
   const int G = rg.G, lane = rg.lane, d = p.d;
   auto sync = [&]() { rg.sync(); };
-  float w[NV][8], dw[NV][8], db[LN ? NV : 1][8] = {};
+  float w[NV][8], dw[NV][8];
+  Two db[LN ? NV : 1][4], dwp[LN ? NV : 1][4];   // layer norm: in pairs
+  if constexpr (LN) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) db[i][j] = dwp[i][j] = Two(0.0f, 0.0f);
+  }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int c = first_column<V>(i, lane, G);
@@ -102,7 +109,8 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING || kNextInRegisters<TR,
       cp_async_wait<Ring::kDepth - 1>();
       __syncwarp();
     }
-    float dot = 0.0f, sum = 0.0f;
+    float dot = 0.0f;
+    Two dots(0.0f, 0.0f), sums(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = first_column<V>(i, lane, G);
@@ -123,28 +131,37 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING || kNextInRegisters<TR,
       float a[8], b[8];
       widen8(yr[i], a);
       widen8(hr[i], b);
+      if constexpr (LN) {   // sums of g = w dy and of g (h - mean)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if constexpr (LN) {
-          const float xh = (b[j] - mean) * r, g = a[j] * w[i][j];
-          dw[i][j] = fmaf(a[j], xh, dw[i][j]);
-          db[i][j] += a[j];
-          sum += g;
-          dot = fmaf(g, xh, dot);
-        } else {
+        for (int j = 0; j < 4; ++j) {
+          const Two y(a[2 * j], a[2 * j + 1]), c = sum(Two(b[2 * j], b[2 * j + 1]), Two(-mean, -mean));
+          const Two g = mul(y, Two(w[i][2 * j], w[i][2 * j + 1]));
+          dwp[i][j] = fma(mul(y, Two(r, r)), c, dwp[i][j]);
+          db[i][j] = sum(db[i][j], y);
+          sums = sum(sums, g);
+          dots = fma(g, c, dots);
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
           const float ah = a[j] * b[j];
           dw[i][j] = fmaf(ah, r, dw[i][j]);
           dot = fmaf(ah, w[i][j], dot);
         }
       }
     }
+    float k, mg = 0.0f;
     if constexpr (LN) {
-      rg.sum2(sum, dot, red[turn], red2[turn]);
-      sum *= p.inv_d;
+      const float2 s = sums.get(), t = dots.get();
+      mg = s.x + s.y;
+      dot = t.x + t.y;
+      rg.sum2(mg, dot, red[turn], red2[turn]);
+      mg *= p.inv_d;
+      k = r * (r * (dot * p.inv_d));
     } else {
       dot = rg.sum(dot, red[turn]);
+      k = r * r * (dot * p.inv_d);
     }
-    const float k = LN ? dot * p.inv_d : r * r * (dot * p.inv_d);
     uint4 numbers[NV];
     if (p.dx && p.rng.threshold)
       drop_numbers<V>(numbers, lane, G, (uint32_t)row, p.rng, xch + rg.group * G, sync);
@@ -153,11 +170,27 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING || kNextInRegisters<TR,
       const int c = first_column<V>(i, lane, G);
       const bool in = c < d && live;
       float a[8], b[8];
+      if constexpr (LN && RING) {   // again, and not in registers past the barrier
+        if (live) {
+          yr[i] = ring.template get<TX>(i * XP);
+          hr[i] = ring.template get<TR>(NV * XP + i * RP);
+        }
+      }
       widen8(yr[i], a);
       widen8(hr[i], b);
+      if constexpr (LN) {   // r (g - mean(g) - (h - mean) r^2 mean(g (h - mean)))
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        a[j] = LN ? r * ((a[j] * w[i][j] - sum) - (b[j] - mean) * r * k) : r * (a[j] * w[i][j] - b[j] * k);
+        for (int j = 0; j < 4; ++j) {
+          const Two c = sum(Two(b[2 * j], b[2 * j + 1]), Two(-mean, -mean));
+          const Two g = fma(Two(a[2 * j], a[2 * j + 1]), Two(w[i][2 * j], w[i][2 * j + 1]), Two(-mg, -mg));
+          const float2 o = mul(fma(c, Two(-k, -k), g), Two(r, r)).get();
+          a[2 * j] = o.x;
+          a[2 * j + 1] = o.y;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) a[j] = r * (a[j] * w[i][j] - b[j] * k);
+      }
       if (cd) {
         Raw8<TR> dr = {};
         if constexpr (RING)
@@ -207,8 +240,21 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING || kNextInRegisters<TR,
       }
     }
   };
-  write(dw, out);
-  if constexpr (LN) write(db, out + d);
+  if constexpr (LN) {
+    float db_[NV][8];
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 s = dwp[i][j].get(), t = db[i][j].get();
+        dw[i][2 * j] = s.x; dw[i][2 * j + 1] = s.y;
+        db_[i][2 * j] = t.x; db_[i][2 * j + 1] = t.y;
+      }
+    write(dw, out);
+    write(db_, out + d);
+  } else {
+    write(dw, out);
+  }
 }
 
 // dw[c] = sum of the partial rows, 32 columns a block: 32 warps take every

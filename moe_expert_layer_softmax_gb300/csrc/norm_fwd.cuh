@@ -41,6 +41,17 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
         load_weight8<V>(p.bias, p.w_f32, sizeof(TX) == 2 && p.x_f16, first_column<V>(i, lane, G), G, d, bias[i]);
     }
   }
+  // layer norm: columns of this warp (of a row), and what the warps tell each other
+  __shared__ float4 pairs[2][LN ? kNormMaxThreads / 32 : 1];
+  float mine = 0.0f, inv_mine = 0.0f;
+  if constexpr (LN) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) mine += column_of<V>(first_column<V>(i, lane, G), j, G) < d ? 1.0f : 0.0f;
+    mine = rg.part(mine);
+    inv_mine = mine > 0.0f ? 1.0f / mine : 0.0f;
+  }
   const int64_t step = (int64_t)gridDim.x * rg.per;
   int64_t row = (int64_t)blockIdx.x * rg.per + rg.group;
   Ring ring(smem, G);
@@ -125,21 +136,36 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
     }
     if constexpr (RING) ring.slot = ring.next(ring.slot);
     if constexpr (LN) {
-      // the deviations from the mean, then their squares: a stream that is far from
-      // zero keeps its variance; places past the row's end stay zero
-      const float mean = rg.sum(ss, red[0]) * p.inv_d;
-      if (lane == 0 && p.mean && live) p.mean[row] = mean;
-      ss = 0.0f;
+      // the deviations from the warp's mean, then their squares; the warps' are joined
+      // with the squares of their means' distances (Chan, Golub, LeVeque 1979): a stream
+      // that is far from zero keeps its variance, and one barrier is enough
+      const float part = rg.part(ss), near = part * inv_mine;
+      Two squares(0.0f, 0.0f);
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
         const int c = first_column<V>(i, lane, G);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          h[i][j] = column_of<V>(c, j, G) < d ? h[i][j] - mean : 0.0f;
-          ss = fmaf(h[i][j], h[i][j], ss);
+        for (int j = 0; j < 8; j += 2) {
+          Two t = sum(Two(h[i][j], h[i][j + 1]), Two(-near, -near));
+          if (V != 8 || c >= d) {   // places past the row's end: none
+            const float2 q = t.get();
+            t = Two(column_of<V>(c, j, G) < d ? q.x : 0.0f, column_of<V>(c, j + 1, G) < d ? q.y : 0.0f);
+          }
+          squares = fma(t, t, squares);
         }
       }
-      ss = rg.sum(ss, red[1]);
+      const float2 q = squares.get();
+      float mean;
+      ss = rg.join(part, rg.part(q.x + q.y), mine, p.inv_d, pairs[turn], mean);
+      if (lane == 0 && p.mean && live) p.mean[row] = mean;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float2 t = sum(Two(h[i][j], h[i][j + 1]), Two(-mean, -mean)).get();
+          h[i][j] = t.x;
+          h[i][j + 1] = t.y;
+        }
     } else {
       ss = rg.sum(ss, red[turn]);
     }
@@ -158,10 +184,19 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
           for (int j = 0; j < 8; ++j) b[j] = 0.0f;
         }
       }
+      if constexpr (LN) {
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+          const float* f = KEEP ? bias[KEEP ? i : 0] : b;
+          const Two n = mul(Two(h[i][j], h[i][j + 1]), Two(rstd, rstd));
+          const float2 t = fma(n, Two(w[i][j], w[i][j + 1]), Two(f[j], f[j + 1])).get();
+          h[i][j] = t.x;
+          h[i][j + 1] = t.y;
+        }
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        h[i][j] = (h[i][j] * w[i][j]) * rstd;
-        if constexpr (LN) h[i][j] += KEEP ? bias[KEEP ? i : 0][j] : b[j];
+        if constexpr (!LN) h[i][j] = (h[i][j] * w[i][j]) * rstd;
         if (MX) amax = fmaxf(amax, fabsf(h[i][j]));
       }
       if constexpr (!MX) {
