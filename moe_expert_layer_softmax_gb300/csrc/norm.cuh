@@ -101,26 +101,22 @@ template <bool SMALL> struct RowGroup {
     for (int off = G >> 1; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
     return v;
   }
-  // From the warps' sums, their squares' distances from their own means and how many
-  // values they have: the mean and the squares' distances from it.
-  MOE_DEV float join(float s, float squares, float n, float inv_d, float4* red, float& mean) const {
+  // From the warps' sums, their means, the squares of the distances from these and how
+  // many values they have: the mean and the squares of the distances from it.
+  MOE_DEV float join(float s, float near, float squares, float n, float inv_d, float4* red, float& mean) const {
     if (G <= 32) {
       mean = s * inv_d;
       return squares;
     }
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float4(s, squares, n, n > 0.0f ? s / n : 0.0f);
+    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float4(s, squares, n, near);
     bar_sync(1 + group, G);
     const int warps = G >> 5;
     const float4* from = red + group * warps;
-    float all = 0.0f, sum = 0.0f;
-    for (int i = 0; i < warps; ++i) sum += from[i].x;
-    mean = sum * inv_d;
-    for (int i = 0; i < warps; ++i) {
-      const float4 w = from[i];
-      const float off = w.w - mean;
-      all += fmaf(w.z * off, off, w.y);
-    }
-    return all;
+    const int lane = threadIdx.x & 31;   // a lane takes a warp's
+    const float4 w = lane < warps ? from[lane] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    mean = warp_sum(w.x) * inv_d;
+    const float off = w.w - mean;
+    return warp_sum(fmaf(w.z * off, off, w.y));
   }
   // Two sums behind one barrier.
   MOE_DEV void sum2(float& v, float& w, float* red, float* red2) const {

@@ -31,8 +31,11 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
     const int c = first_column<V>(i, lane, G);
     load_weight8<V>(p.weight, p.w_f32, sizeof(TX) == 2 && p.x_f16, c, G, d, w[i]);
   }
-  // the bias stays in registers where there is room, or comes from the cache for each row
-  constexpr bool KEEP = LN && NV <= 2;
+  // Layer norm.  The bias stays in registers where there is room, or comes from the cache
+  // for each row.  With up to 16 columns a thread its arithmetic goes in pairs; pairs of
+  // 24 or 32 columns need more registers than there are: 8192 columns in bf16 4.2 TB/s in
+  // pairs, 4.7 one by one, 12288 3.6 and 4.0 (but 2048 5.1 and 4.9).
+  constexpr bool KEEP = LN && NV <= 2, PAIRS = LN && NV <= 2;
   float bias[KEEP ? NV : 1][8] = {};
   if constexpr (KEEP) {
     if (p.bias) {
@@ -42,7 +45,7 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
     }
   }
   // layer norm: columns of this warp (of a row), and what the warps tell each other
-  __shared__ float4 pairs[2][LN ? kNormMaxThreads / 32 : 1];
+  __shared__ float4 parts[2][LN ? kNormMaxThreads / 32 : 1];
   float mine = 0.0f, inv_mine = 0.0f;
   if constexpr (LN) {
 #pragma unroll
@@ -140,31 +143,49 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
       // with the squares of their means' distances (Chan, Golub, LeVeque 1979): a stream
       // that is far from zero keeps its variance, and one barrier is enough
       const float part = rg.part(ss), near = part * inv_mine;
-      Two squares(0.0f, 0.0f);
+      float mean, apart = 0.0f;
+      if constexpr (PAIRS) {
+        Two squares(0.0f, 0.0f);
 #pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int c = first_column<V>(i, lane, G);
+        for (int i = 0; i < NV; ++i) {
+          const int c = first_column<V>(i, lane, G);
 #pragma unroll
-        for (int j = 0; j < 8; j += 2) {
-          Two t = sum(Two(h[i][j], h[i][j + 1]), Two(-near, -near));
-          if (V != 8 || c >= d) {   // places past the row's end: none
-            const float2 q = t.get();
-            t = Two(column_of<V>(c, j, G) < d ? q.x : 0.0f, column_of<V>(c, j + 1, G) < d ? q.y : 0.0f);
+          for (int j = 0; j < 8; j += 2) {
+            Two t = sum(Two(h[i][j], h[i][j + 1]), Two(-near, -near));
+            if (V != 8 || c >= d) {   // places past the row's end: none
+              const float2 q = t.get();
+              t = Two(column_of<V>(c, j, G) < d ? q.x : 0.0f, column_of<V>(c, j + 1, G) < d ? q.y : 0.0f);
+            }
+            squares = fma(t, t, squares);
           }
-          squares = fma(t, t, squares);
+        }
+        const float2 q = squares.get();
+        apart = q.x + q.y;
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = first_column<V>(i, lane, G);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float t = column_of<V>(c, j, G) < d ? h[i][j] - near : 0.0f;
+            apart = fmaf(t, t, apart);
+          }
         }
       }
-      const float2 q = squares.get();
-      float mean;
-      ss = rg.join(part, rg.part(q.x + q.y), mine, p.inv_d, pairs[turn], mean);
+      ss = rg.join(part, near, rg.part(apart), mine, p.inv_d, parts[turn], mean);
       if (lane == 0 && p.mean && live) p.mean[row] = mean;
 #pragma unroll
       for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
-          const float2 t = sum(Two(h[i][j], h[i][j + 1]), Two(-mean, -mean)).get();
-          h[i][j] = t.x;
-          h[i][j + 1] = t.y;
+          if constexpr (PAIRS) {
+            const float2 t = sum(Two(h[i][j], h[i][j + 1]), Two(-mean, -mean)).get();
+            h[i][j] = t.x;
+            h[i][j + 1] = t.y;
+          } else {
+            h[i][j] -= mean;
+            h[i][j + 1] -= mean;
+          }
         }
     } else {
       ss = rg.sum(ss, red[turn]);
@@ -188,10 +209,15 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
           const float* f = KEEP ? bias[KEEP ? i : 0] : b;
-          const Two n = mul(Two(h[i][j], h[i][j + 1]), Two(rstd, rstd));
-          const float2 t = fma(n, Two(w[i][j], w[i][j + 1]), Two(f[j], f[j + 1])).get();
-          h[i][j] = t.x;
-          h[i][j + 1] = t.y;
+          if constexpr (PAIRS) {
+            const Two n = mul(Two(h[i][j], h[i][j + 1]), Two(rstd, rstd));
+            const float2 t = fma(n, Two(w[i][j], w[i][j + 1]), Two(f[j], f[j + 1])).get();
+            h[i][j] = t.x;
+            h[i][j + 1] = t.y;
+          } else {
+            h[i][j] = fmaf(h[i][j] * rstd, w[i][j], f[j]);
+            h[i][j + 1] = fmaf(h[i][j + 1] * rstd, w[i][j + 1], f[j + 1]);
+          }
         }
       }
 #pragma unroll
@@ -278,7 +304,7 @@ cudaError_t fwd_types(const AddNormParams& p, cudaStream_t s) {
   constexpr bool wide = V == 8 && RowRing<8 * (sizeof(TX) + sizeof(TR)), 4>::kFits512;
   AddNormParams q = p;
   if constexpr (V == 8) {
-    RowSplit split(p.d, !MX || p.d <= 512 ? 2 : 3, 4, kNormThreads);
+    RowSplit split(p.d, LN || !MX || p.d <= 512 ? 2 : 3, 4, kNormThreads);
     q.group = split.group;
     if (split.group) {
       const int threads = split.threads();
