@@ -32,14 +32,15 @@ namespace moe {
 
 namespace {
 
-constexpr int kThreads = 192;          // TMA, MMA, four warps of the epilogue
+constexpr int kThreads = 224;          // TMA, MMA, four warps of the epilogue, MMA
 constexpr int kEpi = 128;
 constexpr int kCluster = 4;
 constexpr int kMaxSteps = 8;           // times 64 columns of a stage
 constexpr int kStageBytes = 36 * 1024;   // 128 columns of 128 rows of weights and of 16 tokens
 constexpr int kMaxStages = 6, kRouterStages = 16;
 constexpr int kAccCols = 64;           // of an accumulator: tokens of an expert
-constexpr int kTmem = 2 * kAccCols;
+constexpr int kIssuers = 2;            // threads that issue MMAs, stage by stage in turn, each with its accumulators
+constexpr int kTmem = 2 * kIssuers * kAccCols;
 
 // 32 lanes x 16 columns of tensor memory.
 MOE_DEV void tmem_ld16(uint32_t taddr, float* r) {
@@ -187,7 +188,7 @@ MOE_DEV void build_lists(UpCtl& s, const FewParams& p) {
 // are in the tokens' order; one that a token names twice is one route with the sum of
 // its gates.
 MOE_DEV void write_lists(const UpCtl& s, const FewParams& p) {
-  const int tid = threadIdx.x - (kThreads - kEpi);
+  const int tid = threadIdx.x - 64;
   FewLists& l = *p.lists;
   if (tid == 0) l.n_act = s.n_act;
   for (int a = tid; a <= s.n_act; a += kEpi) {
@@ -291,10 +292,10 @@ MOE_DEV void begin(Ctl& s, const FewParams& p) {
       mbar_init(&s.rempty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&s.tfull[i], 1);
+      mbar_init(&s.tfull[i], kIssuers);
       mbar_init(&s.tempty[i], kEpi);
     }
-    mbar_init(&s.fin, 1);
+    mbar_init(&s.fin, kIssuers);
     s.abort = 0;
     fence_barrier_init();
   }
@@ -372,13 +373,22 @@ MOE_DEV void mma_64(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uin
       : "memory");
 }
 
-// One thread: `chunks` times 64 columns multiplied into accumulator `it`.
-MOE_DEV bool multiply(Ctl& s, const FewParams& p, Ring& r, int it, const Fill& fill, int chunks, int n) {
+// One of the issuers: `chunks` times 64 columns multiplied into its columns of
+// accumulator `it`.  A stage of the ring belongs to one issuer for good, the even ones to
+// the first: its barriers' phases are waited for by one thread, none of them left out.
+// An MMA takes 57 cycles of the thread that issues it, whatever its shape up to 64
+// columns; with two threads one takes 28 (64 rows) and 39 (128).
+MOE_DEV bool multiply(Ctl& s, const FewParams& p, Ring& r, int issuer, int it, const Fill& fill, int chunks, int rows, int n) {
   const int acc = it & 1;
   if (!mbar_wait(&s.tempty[acc], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s.abort, p.err)) return false;
   tc_fence_after();
-  const uint32_t d = s.tmem + acc * kAccCols, idesc = idesc_bf16_f32(128, n, 0, 0);
+  const uint32_t d = s.tmem + (acc * kIssuers + issuer) * kAccCols, idesc = idesc_bf16_f32(rows <= 64 ? 64 : 128, n, 0, 0);
+  bool started = false;
   for (int c = 0; c < chunks; c += fill.s) {
+    if (r.stage % kIssuers != issuer) {
+      r.next();
+      continue;
+    }
     if (!mbar_wait(&r.full[r.stage], r.phase, &s.abort, p.err)) return false;
     tc_fence_after();
     const uint32_t a = r.at(), b = a + fill.s * fill.a;
@@ -386,14 +396,26 @@ MOE_DEV bool multiply(Ctl& s, const FewParams& p, Ring& r, int it, const Fill& f
     const uint32_t step = wide ? 1024 : fill.a, group = wide ? fill.s * 1024 : 1024;
     const uint32_t a_hi = desc_hi(group), b_hi = desc_hi(1024);
     uint32_t a_lo = desc_lo(a), b_lo = desc_lo(b);
-    for (int q = 0; q < fill.s && c + q < chunks; ++q, a_lo += step >> 4, b_lo += fill.b >> 4)
-      mma_64(d, a_lo, a_hi, b_lo, b_hi, idesc, (c | q) != 0);
+    for (int q = 0; q < fill.s && c + q < chunks; ++q, a_lo += step >> 4, b_lo += fill.b >> 4) {
+      mma_64(d, a_lo, a_hi, b_lo, b_hi, idesc, started);
+      started = true;
+    }
     tc_commit(&r.empty[r.stage]);
     r.next();
   }
   tc_commit(&s.tfull[acc]);
   return true;
 }
+// Which of the issuers (bits) had a stage of a piece; the ring's place moves past it.
+MOE_DEV int issuers_of(int& stage, int stages, const Fill& fill, int chunks) {
+  const int n = (chunks + fill.s - 1) / fill.s;
+  int had = 0;
+  for (int i = 0, at = stage; i < min(n, 3); ++i, at = at + 1 < stages ? at + 1 : 0) had |= 1 << at % kIssuers;
+  stage = (stage + n) % stages;
+  return had;
+}
+static_assert(kIssuers == 2, "of three stages in a row two are different issuers'");
+
 // Its last word: every MMA that was issued has ended.
 MOE_DEV void finish(Ctl& s, const FewParams& p) {
   tc_commit(&s.fin);
@@ -403,6 +425,24 @@ MOE_DEV void finish(Ctl& s, const FewParams& p) {
       raise_error(p.err, MOE_DEVERR_TIMEOUT);
       break;
     }
+  }
+}
+
+// The row that a thread of the epilogue holds of an accumulator with `rows` rows (-1:
+// none): a lane each, or of an MMA of 64 rows sixteen lanes of each warp.
+MOE_DEV int row_of(int rows) {
+  const int warp = (int)(threadIdx.x >> 5) & 3, lane = (int)(threadIdx.x & 31);
+  const int row = rows > 64 ? warp * 32 + lane : lane < 16 ? warp * 16 + lane : rows;
+  return row < rows ? row : -1;
+}
+// Sixteen columns of an accumulator: the sum of the issuers that had a part.
+MOE_DEV void sum16(uint32_t taddr, int issuers, float* v) {
+  tmem_ld16(taddr + (issuers & 1 ? 0 : kAccCols), v);
+  if (issuers == 3) {
+    float w[16];
+    tmem_ld16(taddr + kAccCols, w);
+#pragma unroll
+    for (int j = 0; j < 16; ++j) v[j] += w[j];
   }
 }
 
@@ -468,6 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   UpCtl& s = *reinterpret_cast<UpCtl*>(smem + kRingBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int issuer = warp == 1 ? 0 : warp == 6 ? 1 : -1;
   const int quarter = warp & 3, row = quarter * 32 + lane;   // of the epilogue's threads
   const bool writer = (int)blockIdx.x >= (int)gridDim.x - kCluster;   // the cluster that writes the routing
   for (int i = threadIdx.x; i < 512; i += kThreads) (&s.mask[0][0])[i] = 0u;
@@ -482,6 +523,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int rank = (int)cluster_ctarank(), own = (p.T + kCluster - 1) / kCluster;
     const int c0 = share(chunks, rank, kCluster), c1 = share(chunks, rank + 1, kCluster), tiles = (p.E + 127) / 128;
     const uint32_t a_bytes = (uint32_t)(min(p.E, 128) + 7) / 8 * 1024, b_bytes = (uint32_t)p.router_bytes - a_bytes;
+    Fill fill(a_bytes, b_bytes);
+    fill.s = 1;
     if (warp == 0) {
       for (int m = 0; m < tiles && ok; ++m) {
         const int rows = min(p.E - m * 128, 128);
@@ -494,12 +537,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok && lane == 0) drain(first);
-    } else if (warp == 1) {
-      if (lane == 0) {
-        Fill fill(a_bytes, b_bytes);
-        fill.s = 1;
-        for (int m = 0; m < tiles && ok; ++m) ok = multiply(s, p, first, m, fill, c1 - c0, p.t_pad);
-      }
+    } else if (issuer >= 0) {
+      if (lane == 0)
+        for (int m = 0; m < tiles && ok; ++m) ok = multiply(s, p, first, issuer, m, fill, c1 - c0, 128, p.t_pad);
     } else {
       for (int m = 0; m < tiles; ++m) ok = results(s, p, m) && ok;
     }
@@ -507,13 +547,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     cluster_wait();   // every CTA of the cluster has begun
     // the part of this CTA's columns to the CTA that ranks the token: [source, its
     // token, expert] behind the stages
-    if (warp >= 2) {
+    if (warp >= 2 && issuer < 0) {
       const uint32_t mine = smem_u32(smem + p.part_at) + (uint32_t)(rank * own * p.E) * 4u;
-      for (int m = 0; m < tiles; ++m) {
-        const int e = m * 128 + row;
+      for (int m = 0, at = 0; m < tiles; ++m) {
+        const int e = m * 128 + row, issuers = issuers_of(at, p.router_stages, fill, c1 - c0);
         for (int c = 0; c < p.T; c += 16) {
           float v[16];
-          tmem_ld16(tmem + m * kAccCols + c, v);
+          if (c1 > c0) sum16(tmem + m * kIssuers * kAccCols + c, issuers, v);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int t = c + i;
@@ -603,11 +643,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!ok && lane == 0) drain(ring);
-  } else if (warp == 1) {
+  } else if (issuer >= 0) {
     if (lane == 0) {
       while (ok && u.next(g, g_end, groups)) {
         const int m = s.base[u.a + 1] - s.base[u.a];
-        ok = multiply(s, p, ring, it++, up_fill(p, u.n, m), chunks, up_columns(p, m));
+        ok = multiply(s, p, ring, issuer, it++, up_fill(p, u.n, m), chunks, u.n * 16, up_columns(p, m));
       }
       finish(s, p);
     }
@@ -615,23 +655,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the first 8 n lanes hold gate rows, the next 8 n the up rows, which change hands
     // sixteen tokens at a time
     __nv_bfloat16* act = static_cast<__nv_bfloat16*>(p.act);
+    int at_stage = 0;
     if (blockIdx.x == gridDim.x - 1) write_lists(s, p);
     while (ok && u.next(g, g_end, groups)) {
       ok = bar_and(1, kEpi, results(s, p, it));
       if (!ok) break;
       const int e = s.act[u.a], r0 = s.base[u.a], m = s.base[u.a + 1] - r0, columns = m > kGather ? p.T : m;
       const uint32_t m0 = s.mask[e][0], m1 = s.mask[e][1];
-      const int rows = u.n * 8;
+      const int rows = u.n * 8, row = row_of(2 * rows), issuers = issuers_of(at_stage, kStages, up_fill(p, u.n, m), chunks);
       const size_t col = (size_t)u.g * 8 + row;
       for (int c = 0; c < columns; c += 16) {
         float v[16];
-        tmem_ld16(tmem + (it & 1) * kAccCols + c, v);
-        if (row >= rows && row < 2 * rows) {
+        sum16(tmem + (it & 1) * kIssuers * kAccCols + c, issuers, v);
+        if (row >= rows) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) s.up[row - rows][i] = v[i];
         }
         bar_sync(1, kEpi);
-        if (row < rows) {
+        if (row >= 0 && row < rows) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int t = c + i;
@@ -686,7 +727,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* sums = reinterpret_cast<float*>(smem + kDownRingBytes);   // [T][128]
   DownCtl& s = *reinterpret_cast<DownCtl*>(smem + kDownRingBytes + kSumBytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int quarter = warp & 3, row = quarter * 32 + lane;
+  const int issuer = warp == 1 ? 0 : warp == 6 ? 1 : -1;
+  const int quarter = warp & 3;
   begin(s, p);
   {   // what the up kernel has listed, all of it at once
     const FewLists& l = *p.lists;
@@ -708,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int d0 = share(p.d / 8, cluster, clusters), d1 = share(p.d / 8, cluster + 1, clusters);
   const int tiles = (d1 - d0 + 15) / 16;
   Ring ring(s.full, s.empty, smem, kStageBytes, kDownStages);
-  int it = 0;
+  int it = 0, at_stage = 0;
   bool ok = true;
   for (int tile = 0; tile < tiles; ++tile) {   // the same number in every CTA of the cluster
     const int g0 = d0 + share(d1 - d0, tile, tiles), n = d0 + share(d1 - d0, tile + 1, tiles) - g0;
@@ -746,23 +788,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           ring.next();
         }
       }
-    } else if (warp == 1) {
+    } else if (issuer >= 0) {
       if (lane == 0)
         while (ok && u.next(c0, to, chunks)) {
           const int m = s.base[u.a + 1] - s.base[u.a];
-          ok = multiply(s, p, ring, it++, down_fill(n, m), u.n, round16(m));
+          ok = multiply(s, p, ring, issuer, it++, down_fill(n, m), u.n, n * 8, round16(m));
         }
     } else {
       while (ok && u.next(c0, to, chunks)) {
         ok = results(s, p, it);
         if (!ok) break;
-        const int r0 = s.base[u.a], m = s.base[u.a + 1] - r0;
+        const int r0 = s.base[u.a], m = s.base[u.a + 1] - r0, row = row_of(n * 8), issuers = issuers_of(at_stage, kDownStages, down_fill(n, m), u.n);
         for (int c = 0; c < m; c += 16) {
           float v[16];
-          tmem_ld16(tmem + (it & 1) * kAccCols + c, v);
+          sum16(tmem + (it & 1) * kIssuers * kAccCols + c, issuers, v);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
-            if (c + i < m) {
+            if (c + i < m && row >= 0) {
               float& sum = sums[s.tok[r0 + c + i] * 128 + row];
               sum = fmaf(s.gate[r0 + c + i], v[i], sum);
             }
@@ -797,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   if (warp == 0 && !ok && lane == 0) drain(ring);
-  if (warp == 1 && lane == 0) finish(s, p);
+  if (issuer >= 0 && lane == 0) finish(s, p);
   leave(s);
 }
 
