@@ -941,6 +941,40 @@ def allocate(s: Shape, device=None, with_grads: bool = True,
     return LayerBuffers(s, n, ws, saved, grads, mxw, mxb)
 
 
+def adamw_states(params, bits=32):
+    """(exp_avg, exp_avg_sq) for adamw_list: zeros for each parameter, fp32 or (bits=8)
+    pairs of codes and scales."""
+    import torch
+    if bits not in (8, 32):
+        raise ValueError(f"adamw_states: states of {bits} bits")
+
+    def state(p):
+        n, dev = p.numel(), p.device
+        if bits == 32:
+            return _alloc((n,), torch.float32, dev, zero=True)
+        return (_alloc((n,), torch.uint8, dev, zero=True),
+                _alloc(((n + ADAMW_BLOCK - 1) // ADAMW_BLOCK,), torch.float32, dev, zero=True))
+    return [state(p) for p in params], [state(p) for p in params]
+
+
+def layer_adamw(buf: LayerBuffers, w_router, w_gate, w_up, w_down, bits=32, master=True) -> AdamWList:
+    """What adamw() steps after backward(buf, ...): the layer's weights (w_router may be
+    None) with the gradients that the backward leaves in buf.grads, new states of `bits`
+    bits and, with `master`, fp32 copies of the weights as they are now.  (With MXFP8
+    shapes build_mx_weights follows each step.)"""
+    g = buf.grads
+    pairs = [(w_router, g["dw_router"])] if w_router is not None else []
+    pairs += [(w_gate, g["dw_gate"]), (w_up, g["dw_up"]), (w_down, g["dw_down"])]
+    params, grads = [p for p, _ in pairs], [v for _, v in pairs]
+    copies = None
+    if master:
+        import torch
+        copies = [_alloc((p.numel(),), torch.float32, p.device) for p in params]
+        for c, p in zip(copies, params):
+            c.copy_(p.view(-1))
+    return adamw_list(params, grads, *adamw_states(params, bits), master=copies)
+
+
 def forward(buf: LayerBuffers, x, w_router, logit_bias, w_gate, w_up, w_down, out, stream=None):
     """moe_layer_fwd.  MXFP8 shapes use buf.mx_weights (fill them with
     build_mx_weights whenever the bf16 weights change)."""
