@@ -308,7 +308,7 @@ int moe_adamw(const moe_adamw_args_t* a, void* stream) {
     if (!on_boundary(t.param, ps) || !on_boundary(t.grad, gs) || !on_boundary(t.master, 4)) return MOE_ERR_ALIGN;
     if (!small && (!on_boundary(t.m, 4) || !on_boundary(t.v, 4))) return MOE_ERR_ALIGN;
     if (small && (!on_boundary(t.m_scale, 4) || !on_boundary(t.v_scale, 4))) return MOE_ERR_ALIGN;
-    total += adamw_blocks(t.numel);
+    total += adamw_blocks(t.numel, 1);
   }
   if (total == 0) return MOE_OK;
   // without a copy in 32 bits: fp32 itself, or bf16 with drawn rounding
@@ -335,8 +335,10 @@ int moe_adamw(const moe_adamw_args_t* a, void* stream) {
   p.o0 = (uint32_t)a->offset; p.o1 = (uint32_t)(a->offset >> 32);
   AdamwTensor list[kAdamwMost];
   for (int i = 0; i < a->n_tensors;) {
-    int64_t blocks = 0;
+    int64_t blocks = 0, chunks = 0;
     p.first_tensor = i;
+    for (int j = i; j < a->n_tensors && j < i + kAdamwMost; ++j) chunks += adamw_blocks(a->tensors[j].numel, 1);
+    p.turns = adamw_turns(chunks, small);
     for (p.n = 0; p.n < kAdamwMost && i < a->n_tensors; ++i, ++p.n) {
       const moe_adamw_tensor_t& t = a->tensors[i];
       AdamwTensor& e = list[p.n];
@@ -346,7 +348,7 @@ int moe_adamw(const moe_adamw_args_t* a, void* stream) {
       e.first = (uint32_t)blocks;
       e.vec = on_boundary(t.param, 16) && on_boundary(t.grad, 16) && on_boundary(t.master, 16) &&
               on_boundary(t.m, small ? 8 : 16) && on_boundary(t.v, small ? 8 : 16);
-      blocks += adamw_blocks(t.numel);
+      blocks += adamw_blocks(t.numel, p.turns);
     }
     if (blocks == 0) continue;
     if (launch_adamw(list, p, a->param_dtype, a->grad_dtype, master, small, blocks, static_cast<cudaStream_t>(stream)) !=

@@ -102,6 +102,7 @@ struct AdamwScalars {
 
 struct AdamwParams {
   int n, first_tensor;   // tensors of this launch, and those of the call before them
+  int turns;             // chunks that a block takes one after the other
   bool narrow;           // eps and 1 / sqrt(1 - b2^t) where the divisor stays within 2^-60 .. 2^60
   AdamwScalars s;
   const float* grad_scale;
@@ -111,7 +112,8 @@ struct AdamwParams {
   uint32_t k0, k1, o0, o1;
 };
 
-int64_t adamw_blocks(int64_t numel);
+int64_t adamw_blocks(int64_t numel, int turns);   // blocks of a tensor, each of so many chunks
+int adamw_turns(int64_t chunks, bool small);               // of a block of a launch of so many chunks
 cudaError_t launch_adamw(const AdamwTensor* t, const AdamwParams& p, int param_dtype, int grad_dtype, bool master,
                          bool small, int64_t blocks, cudaStream_t s);
 
