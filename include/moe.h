@@ -526,8 +526,8 @@ MOE_API int moe_layer_bwd(const moe_shape_t* shape, const moe_bwd_args_t* args, 
  * moe_layer_fwd for 1 to MOE_FEW_MAX_TOKENS tokens (evaluation, generation between
  * updates) on the bf16 weights as they are, in two kernels that read W_router and the
  * weights of the experts with routes once: route, experts and combine, nothing saved for
- * a backward.  Results are those of moe_layer_fwd up to the rounding of sums (a is
- * rounded to bf16 as there, y is not).
+ * a backward.  Results are those of moe_layer_fwd but for roundings: sums are taken in
+ * another order, a keeps 16 bits or more (two bf16 parts), y is not rounded.
  *   x [T, d], w_router [E, d], w_gate, w_up [E, f, d], w_down [E, d, f], out [T, d]: bf16
  *   with w_router:    logits [T, E] fp32 (nullable), topk_idx [T, k] int32 and gates
  *                     [T, k] fp32 (nullable) are written, logit_bias [T, E] (nullable)
@@ -538,8 +538,9 @@ MOE_API int moe_layer_bwd(const moe_shape_t* shape, const moe_bwd_args_t* args, 
  *                     outside [0, E) adds nothing and sets MOE_DEVERR_BOUNDS.  An expert
  *                     that a token names twice counts with the sum of its gates.
  *   ws  moe_few_workspace_size bytes; its first word is the error word
- * A token's results depend on its own row (and its experts' weights) alone.  The same
- * call gives the same bits.  Envelope: that of the layer with prec MOE_BF16, T <=
+ * A token's results depend on its own row and its experts' weights alone, but for the
+ * order of sums, which goes by how many experts and routes a call has.  The same call
+ * gives the same bits.  out may be x.  Envelope: that of the layer with prec MOE_BF16, T <=
  * MOE_FEW_MAX_TOKENS (T = 0 is valid and writes nothing). */
 #define MOE_FEW_MAX_TOKENS 64
 typedef struct {

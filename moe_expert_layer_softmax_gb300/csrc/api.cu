@@ -92,7 +92,7 @@ FewLayout few_layout(const moe_shape_t* s) {
   w.gates = w.idx + align256(R * 4);
   w.lists = w.gates + align256(R * 4);
   w.act = w.lists + align256(sizeof(FewLists));
-  w.total = w.act + align256((R + 7) / 8 * 8 * s->d_ff * 2);
+  w.total = w.act + align256((2 * R + 7) / 8 * 8 * s->d_ff * 2);
   return w;
 }
 

@@ -13,7 +13,9 @@
 //          each CTA ranks some of the tokens for its cluster (every cluster does this
 //          for itself: no wait on the grid).  Then the active experts' gate and up rows
 //          are dealt out in groups of eight, equal shares for all CTAs; the epilogue
-//          leaves a = silu(h) u of every route in the workspace (bf16, as the layer).
+//          leaves a = silu(h) u of every route in the workspace, as two bf16 numbers (a
+//          and what its rounding leaves over): they are two columns of the down MMA's N,
+//          whose 16 at least are there anyway, and cost the result no second rounding.
 //   down   a cluster owns some of d_model's rows for all experts; its CTAs take equal
 //          parts of the (expert, d_ff) axis, add gate * y of their parts in 32 bits and
 //          join them through distributed shared memory: sums in a fixed order.
@@ -38,9 +40,11 @@ constexpr int kCluster = 4;
 constexpr int kMaxSteps = 8;           // times 64 columns of a stage
 constexpr int kStageBytes = 36 * 1024;   // 128 columns of 128 rows of weights and of 16 tokens
 constexpr int kMaxStages = 6, kRouterStages = 16;
-constexpr int kAccCols = 64;           // of an accumulator: tokens of an expert
+// Columns of an accumulator: tokens of an expert, in the down kernel two for each.
+constexpr int kUpCols = MOE_FEW_MAX_TOKENS, kDownCols = 2 * MOE_FEW_MAX_TOKENS;
 constexpr int kIssuers = 2;            // threads that issue MMAs, stage by stage in turn, each with its accumulators
-constexpr int kTmem = 2 * kIssuers * kAccCols;
+constexpr int kAccs = 2;               // accumulators: one is multiplied into while the other is read
+static_assert(kAccs * kIssuers * kDownCols <= 512, "tensor memory");
 
 // 32 lanes x 16 columns of tensor memory.
 MOE_DEV void tmem_ld16(uint32_t taddr, float* r) {
@@ -98,8 +102,8 @@ struct UpMaps {
   CUtensorMap gate[4], up[4], rows, x, router[2];
 };
 struct DownMaps {
-  CUtensorMap down[5], act[4];
-  CUtensorMap down4, act2, act4;   // eight rows, two or four times 64 columns
+  CUtensorMap down[5], act[5];
+  CUtensorMap down4, act2[2], act4[2];   // eight rows (act: or 16), two or four times 64 columns
 };
 // Row groups in front of the box of 2^b groups of a run of n.
 MOE_DEV int box_before(int n, int b) { return n & ~((2 << b) - 1); }
@@ -114,6 +118,7 @@ struct Ctl {
   uint64_t fin;
   uint32_t tmem;
   int abort;
+  int cols;                   // of an accumulator
   int n_act;                  // experts with routes
   uint16_t base[257];         // first route of an active expert, in their order
   uint8_t act[256];           // their experts
@@ -280,7 +285,7 @@ MOE_DEV void rank_token(const FewParams& p, int t, bool write, Logit logit, Put 
 }
 
 // Barriers, tensor memory; the previous kernel's outputs are visible from here on.
-MOE_DEV void begin(Ctl& s, const FewParams& p) {
+MOE_DEV void begin(Ctl& s, const FewParams& p, int cols) {
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMaxStages; ++i) {
@@ -297,10 +302,11 @@ MOE_DEV void begin(Ctl& s, const FewParams& p) {
     }
     mbar_init(&s.fin, kIssuers);
     s.abort = 0;
+    s.cols = cols;
     fence_barrier_init();
   }
   pdl_wait();
-  if (threadIdx.x / 32 == 1) tmem_alloc(&s.tmem, kTmem);
+  if (threadIdx.x / 32 == 1) tmem_alloc(&s.tmem, kAccs * kIssuers * cols);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -382,7 +388,7 @@ MOE_DEV bool multiply(Ctl& s, const FewParams& p, Ring& r, int issuer, int it, c
   const int acc = it & 1;
   if (!mbar_wait(&s.tempty[acc], ((uint32_t)(it >> 1) & 1u) ^ 1u, &s.abort, p.err)) return false;
   tc_fence_after();
-  const uint32_t d = s.tmem + (acc * kIssuers + issuer) * kAccCols, idesc = idesc_bf16_f32(rows <= 64 ? 64 : 128, n, 0, 0);
+  const uint32_t d = s.tmem + (acc * kIssuers + issuer) * s.cols, idesc = idesc_bf16_f32(rows <= 64 ? 64 : 128, n, 0, 0);
   bool started = false;
   for (int c = 0; c < chunks; c += fill.s) {
     if (r.stage % kIssuers != issuer) {
@@ -435,12 +441,12 @@ MOE_DEV int row_of(int rows) {
   const int row = rows > 64 ? warp * 32 + lane : lane < 16 ? warp * 16 + lane : rows;
   return row < rows ? row : -1;
 }
-// Sixteen columns of an accumulator: the sum of the issuers that had a part.
-MOE_DEV void sum16(uint32_t taddr, int issuers, float* v) {
-  tmem_ld16(taddr + (issuers & 1 ? 0 : kAccCols), v);
+// Sixteen columns of an accumulator of `cols`: the sum of the issuers that had a part.
+MOE_DEV void sum16(uint32_t taddr, int cols, int issuers, float* v) {
+  tmem_ld16(taddr + (issuers & 1 ? 0 : cols), v);
   if (issuers == 3) {
     float w[16];
-    tmem_ld16(taddr + kAccCols, w);
+    tmem_ld16(taddr + cols, w);
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] += w[j];
   }
@@ -463,7 +469,7 @@ MOE_DEV void leave(Ctl& s) {
   tc_fence_after();
   if (threadIdx.x / 32 == 1) {
     __syncwarp();
-    tmem_dealloc(s.tmem, kTmem);
+    tmem_dealloc(s.tmem, kAccs * kIssuers * s.cols);
   }
 }
 
@@ -512,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int quarter = warp & 3, row = quarter * 32 + lane;   // of the epilogue's threads
   const bool writer = (int)blockIdx.x >= (int)gridDim.x - kCluster;   // the cluster that writes the routing
   for (int i = threadIdx.x; i < 512; i += kThreads) (&s.mask[0][0])[i] = 0u;
-  begin(s, p);
+  begin(s, p, kUpCols);
   const uint32_t tmem = s.tmem + ((uint32_t)(quarter * 32) << 16);
   const int chunks = p.d / 64;
   Ring ring(s.full, s.empty, smem, kStageBytes, kStages), first(s.rfull, s.rempty, smem, p.router_bytes, p.router_stages);
@@ -553,7 +559,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int e = m * 128 + row, issuers = issuers_of(at, p.router_stages, fill, c1 - c0);
         for (int c = 0; c < p.T; c += 16) {
           float v[16];
-          if (c1 > c0) sum16(tmem + m * kIssuers * kAccCols + c, issuers, v);
+          if (c1 > c0) sum16(tmem + m * kIssuers * kUpCols + c, kUpCols, issuers, v);
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             const int t = c + i;
@@ -666,7 +672,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const size_t col = (size_t)u.g * 8 + row;
       for (int c = 0; c < columns; c += 16) {
         float v[16];
-        sum16(tmem + (it & 1) * kIssuers * kAccCols + c, issuers, v);
+        sum16(tmem + (it & 1) * kIssuers * kUpCols + c, kUpCols, issuers, v);
         if (row >= rows) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) s.up[row - rows][i] = v[i];
@@ -684,7 +690,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (in && t < columns) {
               const float a = __fdividef(v[i], 1.0f + __expf(-v[i])) * s.up[row][i];
-              act[(size_t)(r0 + at) * p.f + col] = __float2bfloat16_rn(a);
+              const __nv_bfloat16 high = __float2bfloat16_rn(a);
+              const float rest = a - __bfloat162float(high);
+              __nv_bfloat16* to = act + (size_t)(r0 + at) * 2 * p.f + col;
+              to[0] = high;
+              to[p.f] = __float2bfloat16_rn(fabsf(rest) < INFINITY ? rest : 0.0f);
             }
           }
         }
@@ -709,12 +719,12 @@ struct DownPiece {
   }
 };
 
-// The box of 8 << b routes that holds m of them; how n groups of rows and these routes
-// fill a stage.
-MOE_DEV int route_box(int m) { return m <= 8 ? 0 : m <= 16 ? 1 : m <= 32 ? 2 : 3; }
+// The box of 8 << b rows that holds the activations of m routes, two rows each; how n
+// groups of rows of weights and these fill a stage.
+MOE_DEV int route_box(int m) { return m <= 4 ? 0 : m <= 8 ? 1 : m <= 16 ? 2 : m <= 32 ? 3 : 4; }
 MOE_DEV Fill down_fill(int n, int m) {
   Fill f(n * 1024, 1024 << route_box(m));
-  if (m <= 8 && n >= 4 && n <= 8) {   // fewer and larger copies
+  if (m <= 8 && n >= 4 && n <= 8 && 4 * (f.a + f.b) <= kStageBytes) {   // fewer and larger copies
     f.s = 4;
     f.wide = n < 8;
   }
@@ -729,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int issuer = warp == 1 ? 0 : warp == 6 ? 1 : -1;
   const int quarter = warp & 3;
-  begin(s, p);
+  begin(s, p, kDownCols);
   {   // what the up kernel has listed, all of it at once
     const FewLists& l = *p.lists;
     const int R = p.T * p.k, most = min(p.E, R);
@@ -767,8 +777,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool once = m <= 8 && (fill.s == 2 || fill.s == 4 || fill.s == 8);   // the routes of a full stage in one copy (eight steps: in two)
         const uint32_t place = routes ? fill.s * fill.a : before * 1024u, step = routes ? fill.b : fill.a;
         const CUtensorMap* map = routes ? &maps.act[act] : &maps.down[b];
-        const CUtensorMap* many = fill.s == 2 ? &maps.act2 : &maps.act4;
-        const int y = routes ? r0 : e * p.d + (g0 + before) * 8;
+        const CUtensorMap* many = fill.s == 2 ? &maps.act2[act & 1] : &maps.act4[act & 1];
+        const int y = routes ? 2 * r0 : e * p.d + (g0 + before) * 8;
         for (int c = u.c; c < u.c + u.n; c += fill.s) {
           const int steps = min(fill.s, u.c + u.n - c);
           const bool full = steps == fill.s, wide = full && fill.wide, one = full && once;
@@ -792,21 +802,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0)
         while (ok && u.next(c0, to, chunks)) {
           const int m = s.base[u.a + 1] - s.base[u.a];
-          ok = multiply(s, p, ring, issuer, it++, down_fill(n, m), u.n, n * 8, round16(m));
+          ok = multiply(s, p, ring, issuer, it++, down_fill(n, m), u.n, n * 8, round16(2 * m));
         }
     } else {
       while (ok && u.next(c0, to, chunks)) {
         ok = results(s, p, it);
         if (!ok) break;
         const int r0 = s.base[u.a], m = s.base[u.a + 1] - r0, row = row_of(n * 8), issuers = issuers_of(at_stage, kDownStages, down_fill(n, m), u.n);
-        for (int c = 0; c < m; c += 16) {
+        for (int c = 0; c < m; c += 8) {   // eight routes: sixteen columns
           float v[16];
-          sum16(tmem + (it & 1) * kIssuers * kAccCols + c, issuers, v);
+          sum16(tmem + (it & 1) * kIssuers * kDownCols + 2 * c, kDownCols, issuers, v);
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < 8; ++i) {
             if (c + i < m && row >= 0) {
               float& sum = sums[s.tok[r0 + c + i] * 128 + row];
-              sum = fmaf(s.gate[r0 + c + i], v[i], sum);
+              sum = fmaf(s.gate[r0 + c + i], v[2 * i] + v[2 * i + 1], sum);
             }
           }
         }
@@ -888,7 +898,7 @@ cudaError_t launch_few(const FewParams& args, const FewTensors& w, cudaStream_t 
   p.router = w.w_router != nullptr;
   p.t_pad = p.T <= 16 ? 16 : p.T <= 32 ? 32 : 64;   // rows of the largest box of tokens or routes
   const uint64_t d = (uint64_t)p.d, f = (uint64_t)p.f, E = (uint64_t)p.E;
-  const uint64_t routes = ((uint64_t)p.T * p.k + 7) / 8 * 8;
+  const uint64_t routes = ((uint64_t)p.T * p.k * 2 + 7) / 8 * 8;   // rows of activations
   // the router's stages in front of the parts of its products
   p.router_bytes = ((p.E < 128 ? p.E : 128) + 7) / 8 * 1024 + (p.T + 7) / 8 * 1024;
   const int parts = kCluster * ((p.T + kCluster - 1) / kCluster) * p.E * 4;
@@ -903,14 +913,16 @@ cudaError_t launch_few(const FewParams& args, const FewTensors& w, cudaStream_t 
               make_bf16_map(&up.router[1], wr, d, p.router ? E : E * f, 64, p.E > 128 ? p.E - 128 : 1);
   for (int b = 0; b < 5; ++b) {
     const uint32_t height = 8u << b;
-    made = made && make_bf16_map(&down.down[b], w.w_down, f, E * d, 64, height);
+    made = made && make_bf16_map(&down.down[b], w.w_down, f, E * d, 64, height) &&
+           make_bf16_map(&down.act[b], p.act, f, routes, 64, height);
     if (b < 4)
       made = made && make_bf16_map(&up.gate[b], w.w_gate, d, E * f, 64, height) &&
-             make_bf16_map(&up.up[b], w.w_up, d, E * f, 64, height) &&
-             make_bf16_map(&down.act[b], p.act, f, routes, 64, height);
+             make_bf16_map(&up.up[b], w.w_up, d, E * f, 64, height);
+    if (b < 2)
+      made = made && make_bf16_map3(&down.act2[b], p.act, f, routes, height, 2) &&
+             make_bf16_map3(&down.act4[b], p.act, f, routes, height, 4);
   }
-  made = made && make_bf16_map3(&down.down4, w.w_down, f, E * d, 8, 4) && make_bf16_map3(&down.act2, p.act, f, routes, 8, 2) &&
-         make_bf16_map3(&down.act4, p.act, f, routes, 8, 4);
+  made = made && make_bf16_map3(&down.down4, w.w_down, f, E * d, 8, 4);
   if (!made) return cudaErrorInvalidValue;
   static SmemLimit up_limit, down_limit;
   cudaError_t e = up_limit.raise(reinterpret_cast<const void*>(&few_up_kernel), kUpSmem);

@@ -31,7 +31,7 @@ struct FewParams {
   float* logits;         // [T, E] or NULL (written with a router)
   int32_t* topk_idx;     // [T, k]: written with a router, else read
   float* gates;
-  void* act;             // bf16 [T k, f]
+  void* act;             // bf16 [T k, 2, f]: a rounded, and the rest
   void* out;
   int32_t* err;
   FewLists* lists;
