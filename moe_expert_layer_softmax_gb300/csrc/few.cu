@@ -24,7 +24,19 @@
 // built from TMA boxes of 8 to 128 rows; an MMA row without weights holds
 // whatever the memory held, and its results are not read.  A token's rows are fetched
 // by index (gather) into the MMA's N.
+//
+// Bound by HBM, behind a fixed cost.  Measured (floor at a copy's 6.78 TB/s), bf16:
+//   1 token,   8 of 64 experts, 4096 x 2048   83.8 us (59.5): up 6.6, down 6.1 TB/s while
+//              weights stream, 62 us; routing 9; the kernels' starts and joins 12
+//   16 tokens, 4 of 32, 2048 x 1024           75 us (52.5): 7.0 and 5.6 TB/s; routing 7
+//   64 tokens, 4 of 64, 2048 x 1408           191 us (161); routing 16, sixteen tokens a CTA
+// A TMA copy costs about as much as 2 to 4 KB of data, whatever its size: with boxes of
+// eight rows alone the first took 148 us.  Clusters of two instead of four fill all 152
+// multiprocessors (four: 144) but read W_router twice as often: 16 to 30 % slower.
+#include <cudaTypedefs.h>
+
 #include <atomic>
+#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -134,8 +146,8 @@ struct DownCtl : Ctl {
   float gate[kFewMaxRoutes];    // its gate
 };
 
-// Shared memory.  An MMA reads 16 KB from where its rows begin, whatever lies behind
-// them: up to 16 KB past the last stage's weights.
+// Shared memory.  An MMA reads 64 or 128 rows (8 or 16 KB) from where its rows begin,
+// however few of them are weights: what lies behind the last stage has to be the CTA's.
 constexpr int kOverread = 16 * 1024, kSumBytes = MOE_FEW_MAX_TOKENS * 512;
 constexpr int kStages = kMaxStages, kRingBytes = kStages * kStageBytes;
 constexpr int kDownStages = 5, kDownRingBytes = kDownStages * kStageBytes;
@@ -145,8 +157,9 @@ static_assert(kUpSmem <= 227 * 1024 && kDownSmem <= 227 * 1024 && kSumBytes >= k
 // up: s rows' parts of `a` bytes end s b bytes before the stage's end and s (a + b) <= the
 // stage, so that the last one begins 12 KB before it at least (a = 4 KB, s = 7)
 static_assert(sizeof(UpCtl) >= 4096, "what an MMA reads behind the up kernel's ring");
-// a wide stage's 16 groups are 4 KB apart
-static_assert((kDownStages - 1) * kStageBytes + 68 * 1024 <= kDownSmem, "what an MMA reads behind the down kernel's ring");
+// a wide stage has at most seven groups, 4 KB apart, and its MMAs read eight: from the
+// fourth step of the last stage on, (3 + 29) KB
+static_assert((kDownStages - 1) * kStageBytes + 32 * 1024 <= kDownSmem, "what an MMA reads behind the down kernel's ring");
 // the router's parts (16 KB at least, for its MMAs) leave two stages of (16 + 8) KB
 static_assert(kRingBytes - MOE_FEW_MAX_TOKENS * 256 * 4 >= 2 * 24 * 1024, "the router's stages");
 
@@ -853,6 +866,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   leave(s);
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
+std::once_flag g_encode_once;
+
+// Tensor map of `outer` rows of `inner` bf16 elements with 128-byte swizzle: boxes of 64
+// columns of `box_rows` rows, zeros behind the last row.  `steps` > 0: the rows as
+// [inner / 64][outer][64], `steps` times 64 columns in a box, one step behind the other.
+bool make_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_rows, uint32_t steps = 0) {
+  std::call_once(g_encode_once, [] {
+    void* fn = nullptr;
+    cudaDriverEntryPointQueryResult found;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &found) == cudaSuccess &&
+        found == cudaDriverEntryPointSuccess)
+      g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+  });
+  if (!g_encode) return false;
+  const cuuint64_t dims[3] = {steps ? 64 : inner, outer, inner / 64}, strides[2] = {inner * 2, 128};
+  const cuuint32_t box[3] = {64, box_rows, steps}, ones[3] = {1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, steps ? 3 : 2, const_cast<void*>(ptr), dims, strides, box, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // CTAs of whole clusters that stay on the device at once.
 int resident_ctas(const void* kernel, int smem, int device) {
   static std::atomic<int> known[kMaxDevices];
@@ -907,22 +942,22 @@ cudaError_t launch_few(const FewParams& args, const FewTensors& w, cudaStream_t 
   UpMaps up;
   DownMaps down;
   const void* wr = p.router ? w.w_router : w.w_gate;   // a map that is not used is one all the same
-  bool made = make_bf16_map(&up.rows, w.x, d, (uint64_t)p.T, 64, 1) &&
-              make_bf16_map(&up.x, w.x, d, (uint64_t)p.T, 64, (uint32_t)p.T) &&
-              make_bf16_map(&up.router[0], wr, d, p.router ? E : E * f, 64, p.E < 128 ? p.E : 128) &&
-              make_bf16_map(&up.router[1], wr, d, p.router ? E : E * f, 64, p.E > 128 ? p.E - 128 : 1);
+  bool made = make_map(&up.rows, w.x, d, (uint64_t)p.T, 1) &&
+              make_map(&up.x, w.x, d, (uint64_t)p.T, (uint32_t)p.T) &&
+              make_map(&up.router[0], wr, d, p.router ? E : E * f, p.E < 128 ? p.E : 128) &&
+              make_map(&up.router[1], wr, d, p.router ? E : E * f, p.E > 128 ? p.E - 128 : 1);
   for (int b = 0; b < 5; ++b) {
     const uint32_t height = 8u << b;
-    made = made && make_bf16_map(&down.down[b], w.w_down, f, E * d, 64, height) &&
-           make_bf16_map(&down.act[b], p.act, f, routes, 64, height);
+    made = made && make_map(&down.down[b], w.w_down, f, E * d, height) &&
+           make_map(&down.act[b], p.act, f, routes, height);
     if (b < 4)
-      made = made && make_bf16_map(&up.gate[b], w.w_gate, d, E * f, 64, height) &&
-             make_bf16_map(&up.up[b], w.w_up, d, E * f, 64, height);
+      made = made && make_map(&up.gate[b], w.w_gate, d, E * f, height) &&
+             make_map(&up.up[b], w.w_up, d, E * f, height);
     if (b < 2)
-      made = made && make_bf16_map3(&down.act2[b], p.act, f, routes, height, 2) &&
-             make_bf16_map3(&down.act4[b], p.act, f, routes, height, 4);
+      made = made && make_map(&down.act2[b], p.act, f, routes, height, 2) &&
+             make_map(&down.act4[b], p.act, f, routes, height, 4);
   }
-  made = made && make_bf16_map3(&down.down4, w.w_down, f, E * d, 8, 4);
+  made = made && make_map(&down.down4, w.w_down, f, E * d, 8, 4);
   if (!made) return cudaErrorInvalidValue;
   static SmemLimit up_limit, down_limit;
   cudaError_t e = up_limit.raise(reinterpret_cast<const void*>(&few_up_kernel), kUpSmem);

@@ -42,11 +42,4 @@ struct FewParams {
 
 cudaError_t launch_few(const FewParams& p, const FewTensors& w, cudaStream_t s);
 
-// 2-D bf16 tensor map with 128-byte swizzle (gemm.cu): `outer` rows of `inner` elements.
-bool make_bf16_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer);
-
-// The same rows as [inner / 64][outer][64]: a box of `box_steps` times 64 columns of
-// `box_outer` rows, one step behind the other.
-bool make_bf16_map3(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_outer, uint32_t box_steps);
-
 }  // namespace moe

@@ -45,7 +45,6 @@
 
 #include "common.cuh"
 #include "kernels.h"
-#include "few.h"
 
 namespace moe {
 
@@ -1891,19 +1890,6 @@ cudaError_t launch_mx_pair(Params p, const CUtensorMap& A0, const CUtensorMap& A
 }  // namespace
 
 int gemm_set_inject_stall(int mode) { return g_inject_stall.exchange(mode); }
-
-bool make_bf16_map(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_inner, uint32_t box_outer) {
-  return get_encoder() && make_map(m, ptr, inner, outer, box_inner, box_outer);
-}
-
-bool make_bf16_map3(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t box_outer, uint32_t box_steps) {
-  if (!get_encoder()) return false;
-  const cuuint64_t dims[3] = {64, outer, inner / 64}, strides[2] = {inner * 2, 128};
-  const cuuint32_t box[3] = {64, box_outer, box_steps}, ones[3] = {1, 1, 1};
-  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, ones,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
 
 cudaError_t gemm_init_attributes() {
   if (!get_encoder()) return cudaErrorInitializationError;

@@ -1,5 +1,5 @@
-// Residual addition with the root-mean-square norm, its backward, and dropout
-// (sm_103a).
+// Residual addition with the root-mean-square norm or the layer norm, their backward,
+// and dropout (sm_103a).
 //
 //   u = dropout(x)                      (u = x without dropout)
 //   h = residual + u, rounded to the stream's type
@@ -9,6 +9,12 @@
 // E4M3 codes with one E8M0 scale per 32 columns (rounded once, from the 32-bit
 // y), optionally with the values the codes stand for.  With g = w dy:
 //   dh = dres + r (g - h r^2 mean(g h)),  dx = dropout'(dh),  dw = sum dy h r.
+// The layer norm takes the row's mean out first:
+//   m = mean(h),  r = (mean((h - m)^2) + eps)^(-1/2),  n = (h - m) r,  y = n w + b
+//   dh = dres + r (g - mean(g) - n mean(g n)),  dw = sum dy n,  db = sum dy.
+// Squares are of differences from a mean, never a difference of two large sums: each
+// warp takes the mean and the squares of its own part, and behind one barrier the parts
+// are joined (Chan, Golub and LeVeque).
 //
 // The least a call costs is one read and one write of each matrix.  A row stays in
 // registers between the pass that sums it and the pass that writes it.  A fixed
@@ -36,6 +42,11 @@
 // in bf16 2.1-3.2, on an fp32 stream 3.3-5.2, in fp32 4.7-6.8, up to 8192 1.7-3.0,
 // 2.6-4.3 and 3.2-5.8 (with 1024 threads; 512 with twice the columns spilled: 4999
 // columns in fp32 3.2 and 4.1 forward, 2.3 and 3.2 backward).
+//
+// Layer norm: forward 8192 x 2048 26.3 us (5.1 TB/s; bound by issue, 65 % of the slots),
+// 32768 x 4096 with dropout and 8-bit output 280 us, 8192 and 12288 columns 4.7 and
+// 4.0; backward 8192 x 2048 35.0 us (4.8), 32768 x 4096 on an fp32 stream with dropout
+// 342 us (6.3), other sizes 4.8-6.3.
 #pragma once
 
 #include "block.cuh"
