@@ -771,7 +771,8 @@ MOE_API int moe_dropout(int64_t rows, int32_t cols, int32_t dtype, const void* x
  * of lr and step: a captured step then follows them.  grad_scale: fp32 on the device.
  * Pointers need their element's alignment (codes: none); tensors whose pointers all lie
  * on 16-byte boundaries (codes: 8) take vector accesses.  `tensors` is a host array, read before
- * the call returns; no two tensors may overlap.  numel may be 0.
+ * the call returns; what is written (all but the gradients) may overlap nothing else.
+ * numel may be 0.
  * Envelope: numel <= 2^34, 0 <= beta < 1, eps, lr, weight_decay >= 0, step >= 1. */
 typedef struct {
   void* param;

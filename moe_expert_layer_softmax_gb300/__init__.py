@@ -11,6 +11,7 @@ Shapes follow include/moe.h: x [T, d] bf16, W_r [E, d] bf16, W_gate/W_up
 """
 from __future__ import annotations
 
+import bisect
 import ctypes
 import os
 import struct
@@ -675,7 +676,7 @@ def adamw_list(params, grads, exp_avg, exp_avg_sq, master=None) -> AdamWList:
     pt, gt, small = params[0].dtype, grads[0].dtype, isinstance(exp_avg[0], (tuple, list))
     lst.types = (_dtype(params[0], "params"), _dtype(grads[0], "grads"), 8 if small else 32)
     dev = params[0].get_device()
-    packed, written, held = [], [], []
+    packed, written, read, held = [], [], [], []
 
     def take(t, what, numel, dtype):
         if not t.is_cuda or not t.is_contiguous():
@@ -688,8 +689,8 @@ def adamw_list(params, grads, exp_avg, exp_avg_sq, master=None) -> AdamWList:
             raise ValueError(f"{what}: {t.numel()} elements, expected {numel}")
         held.append(t)
         at = t.data_ptr()
-        if numel and what != "grads":
-            written.append((at, at + numel * t.element_size(), what))
+        if numel:
+            (read if what == "grads" else written).append((at, at + numel * t.element_size(), what))
         return at
 
     f32, u8 = _torch.float32, _torch.uint8
@@ -712,6 +713,11 @@ def adamw_list(params, grads, exp_avg, exp_avg_sq, master=None) -> AdamWList:
     for (_, end, a), (start, _, b) in zip(written, written[1:]):
         if start < end:
             raise ValueError(f"adamw_list: memory of {a} and {b} overlaps")
+    starts = [start for start, _, _ in written]
+    for start, end, _ in read:   # the last range that begins before its end
+        at = bisect.bisect_left(starts, end) - 1
+        if at >= 0 and written[at][1] > start:
+            raise ValueError(f"adamw_list: memory of grads and {written[at][2]} overlaps")
     lst.tensors, lst.device, lst.held = b"".join(packed), dev, tuple(held)
     return lst
 

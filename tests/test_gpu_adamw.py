@@ -347,3 +347,25 @@ def test_refused_lists(moe_gpu):
     assert (p == 0).all()
     m.adamw(m.adamw_list([], [], [], []), lr=1e-3, step=1)
     m.adamw(m.adamw_list([f(0)], [f(0)], [f(0)], [f(0)]), lr=1e-3, step=1)
+
+
+def test_gradients_that_overlap(moe_gpu):
+    """A gradient may serve two tensors, but not lie in what the step writes: a block
+    would read there what another has written."""
+    m, dev = moe_gpu
+    f = lambda n=64: torch.zeros(n, dtype=torch.float32, device=dev)   # noqa: E731
+    p, a, b, more = f(), f(), f(), f(256)
+    for g in (p, a, b):
+        with pytest.raises(ValueError):
+            m.adamw_list([p], [g], [a], [b])
+    for at in (129, 191, 64):   # its end and its beginning in what is written, all of it
+        with pytest.raises(ValueError):
+            m.adamw_list([f(64 if at > 64 else 192)], [more[at:at + 64] if at > 64 else more[64:256]],
+                         [more[128:192] if at > 64 else f(192)], [f(64 if at > 64 else 192)] if at > 64 else [more[:192]])
+    g = more[64:128]
+    g.fill_(1.0)
+    q = f()
+    m.adamw(m.adamw_list([p, q], [g, g], [more[:64], more[128:192]], [f(), f()]), lr=0.5, step=1, eps=0.0, weight_decay=0.0)
+    # about eight roundings of 2^-24 each
+    assert torch.allclose(p, torch.full_like(p, -0.5), rtol=1e-6) and torch.equal(p, q) and (g == 1).all()
+    assert (more[192:] == 0).all()
