@@ -766,7 +766,10 @@ MOE_API int moe_dropout(int64_t rows, int32_t cols, int32_t dtype, const void* x
  * Drawn rounding of bf16: number is added to the 32 bits of w, the lower 16 are cut.
  * number: half-word i % 8 (low half-words first) of Philox4x32-10 (as moe_dropout) with
  * key = seed and counter (i / 8, 4 * place of the tensor in the list + what, offset low,
- * offset high), what = 0 for m, 1 for root, 2 for param: each step gives another offset.
+ * offset high), what = 0 for m, 1 for root, 2 for param.  Each step that rounds by numbers
+ * needs another offset: with the same numbers every time a place's rounding would go by a
+ * fixed border, and its mean would not be that of the values.  A captured step has to
+ * take its offset from the device for that (moe_adamw_at).
  * lr_dev (fp32) and step_dev (int64), where not NULL, are read on the device in place
  * of lr and step: a captured step then follows them.  grad_scale: fp32 on the device.
  * Pointers need their element's alignment (codes: none); tensors whose pointers all lie
@@ -803,6 +806,10 @@ typedef struct {
   uint64_t offset;
 } moe_adamw_args_t;
 MOE_API int moe_adamw(const moe_adamw_args_t* args, void* stream);
+/* The same with offset + *offset_dev (modulo 2^64, read when the kernel runs) in place of
+ * offset: replays of a captured step whose counter goes on draw numbers of their own.
+ * The step's number will do (offset_dev = step_dev).  NULL: moe_adamw. */
+MOE_API int moe_adamw_at(const moe_adamw_args_t* args, const uint64_t* offset_dev, void* stream);
 
 /* 4-bit weights with group scales along K (G = group = 32, 64 or 128, K a
  * multiple of it): W[n, k] = (code[n, k] - 8) * scale[n, k / G], codes 0..15.

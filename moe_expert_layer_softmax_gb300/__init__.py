@@ -52,7 +52,7 @@ EXPORTS = (
     "moe_debug_inject_stall", "moe_profile_start", "moe_profile_stop", "moe_load_balance",
     "moe_checks_read", "moe_few_workspace_size", "moe_few_fwd",
     "moe_add_norm", "moe_add_norm_bwd_workspace_size", "moe_add_norm_bwd", "moe_add_layer_norm",
-    "moe_add_layer_norm_bwd_workspace_size", "moe_add_layer_norm_bwd", "moe_dropout", "moe_adamw",
+    "moe_add_layer_norm_bwd_workspace_size", "moe_add_layer_norm_bwd", "moe_dropout", "moe_adamw", "moe_adamw_at",
     "moe_quantize_w4", "moe_dequantize_w4", "moe_matvec_w4", "moe_experts_w4_workspace_size",
     "moe_experts_w4",
 )
@@ -162,6 +162,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_dropout": [i64, i32, i32, _vp, i64, _vp, i64, ctypes.c_float, ctypes.c_uint64,
                         ctypes.c_uint64, _vp],
         "moe_adamw": [_vp, _vp],
+        "moe_adamw_at": [_vp, _vp, _vp],
         "moe_quantize_w4": [i64, i32, i32, i32, _vp, _vp, _vp, _vp],
         "moe_dequantize_w4": [i64, i32, i32, i32, _vp, _vp, _vp, _vp],
         "moe_matvec_w4": [i32] * 5 + [_vp, i64, _vp, _vp, _vp, i64, _vp],
@@ -462,6 +463,17 @@ def _failed(fn, rc, *args):
     _check(fn, rc)
 
 
+def _call(fn, *args):
+    """A call whose argument before the stream is the address of the offset's part on the
+    device, or 0: then the form without it."""
+    *args, at, st = args
+    if at:
+        fn, args = fn + "_at", (*args, at)
+    rc = getattr(load(), fn)(*args, st)
+    if rc:
+        _failed(fn, rc, *args, st)
+
+
 def _shape(x):
     """(rows, columns) of a tensor whose axes before the last are rows."""
     d = x.size(-1)
@@ -723,11 +735,13 @@ def adamw_list(params, grads, exp_avg, exp_avg_sq, master=None) -> AdamWList:
 
 
 def adamw(tensors: AdamWList, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01, grad_scale=None, seed=0,
-          offset=0, stream=None):
+          offset=0, stream=None, offset_dev=None):
     """moe_adamw: one step on every tensor of the list.  lr (fp32) and step (int64, from 1)
     are numbers or CUDA tensors of one element, read when the kernel runs; grad_scale: a
     CUDA fp32 tensor of one element that the gradients are multiplied with.  seed and
-    offset choose the numbers of drawn roundings: another offset for each step."""
+    offset choose the numbers of drawn roundings: another offset for each step.  A captured
+    step gets it from offset_dev, a CUDA int64 tensor of one element (the step's own will
+    do) that is added to offset when the kernel runs."""
     lst = tensors
     if lst.n == 0:
         return
@@ -738,13 +752,12 @@ def adamw(tensors: AdamWList, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight
         plr, lr = _flat(lr, "lr", 1, _torch.float32), 0.0
     if not isinstance(step, int):
         pstep, step = _flat(step, "step", 1, _torch.int64), 1
+    poffset = _flat(offset_dev, "offset_dev", 1, _torch.int64)
     host = ctypes.c_char_p(lst.tensors)
     args = _ADAMW.pack(ctypes.cast(host, _vp).value, lst.n, *lst.types, _flat(grad_scale, "grad_scale", 1, _torch.float32),
                        plr, pstep, lr, beta1, beta2, eps, weight_decay, step, seed, offset)
     st = _stream(stream)
-    rc = load().moe_adamw(args, st)
-    if rc:
-        _failed("moe_adamw", rc, args, st)
+    _call("moe_adamw", args, poffset, st)
 
 
 def _w4(q, scales, what):

@@ -203,8 +203,10 @@ template <bool SQUARE> MOE_DEV void widen_codes(const uint2& q, float scale, flo
 }
 
 // TP, TG: types of parameters and gradients; MASTER: the fp32 copy is what is
-// stepped, the parameter its rounding; SMALL: states in 8 bits.
-template <int N, typename TP, typename TG, bool MASTER, bool SMALL>
+// stepped, the parameter its rounding; SMALL: states in 8 bits.  AT: part of the numbers'
+// offset lies on the device (a kernel of its own: as a branch it cost every call with
+// 8-bit states 1 %, 627 and 633 us).
+template <int N, typename TP, typename TG, bool MASTER, bool SMALL, bool AT>
 __global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_constant__ AdamwList<N> list) {
   constexpr bool DRAWN = !MASTER && sizeof(TP) == 2;   // parameters rounded by the generator
   __shared__ AdamwScalars shared;
@@ -217,6 +219,12 @@ __global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_con
     s.decay = shared.decay;
     s.rate = shared.rate;
     s.root_scale = shared.root_scale;
+  }
+  uint32_t o0 = p.o0, o1 = p.o1;
+  if constexpr (AT) {
+    const uint64_t offset = ((uint64_t)o1 << 32 | o0) + *p.offset_dev;
+    o0 = (uint32_t)offset;
+    o1 = (uint32_t)(offset >> 32);
   }
   // the tensor of this block: the last one that begins at or before it
   int lo = 0, hi = p.n;
@@ -326,7 +334,7 @@ __global__ void __launch_bounds__(kAdamThreads, 4) adamw_kernel(const __grid_con
       constexpr int from = SMALL ? 0 : 2, count = (SMALL ? 2 : 0) + (DRAWN ? 1 : 0);
       uint4 c[count];
 #pragma unroll
-      for (int i = 0; i < count; ++i) c[i] = make_uint4(group, tensor + from + i, p.o0, p.o1);
+      for (int i = 0; i < count; ++i) c[i] = make_uint4(group, tensor + from + i, o0, o1);
       philox4x32_10(c, p.k0, p.k1);
 #pragma unroll
       for (int i = 0; i < count; ++i) numbers[from + i] = c[i];
@@ -391,8 +399,13 @@ cudaError_t adamw_bits(const AdamwTensor* t, const AdamwParams& p, bool small, i
   for (int i = 0; i < p.n; ++i) list.t[i] = t[i];
   list.p = p;
   const dim3 grid((unsigned)blocks), threads(kAdamThreads);
-  return small ? launch_pdl(adamw_kernel<N, TP, TG, MASTER, true>, grid, threads, 0, s, list)
-               : launch_pdl(adamw_kernel<N, TP, TG, MASTER, false>, grid, threads, 0, s, list);
+  if (small)
+    return p.offset_dev ? launch_pdl(adamw_kernel<N, TP, TG, MASTER, true, true>, grid, threads, 0, s, list)
+                        : launch_pdl(adamw_kernel<N, TP, TG, MASTER, true, false>, grid, threads, 0, s, list);
+  if constexpr (!MASTER && sizeof(TP) == 2) {   // bf16 alone: its rounding draws numbers
+    if (p.offset_dev) return launch_pdl(adamw_kernel<N, TP, TG, MASTER, false, true>, grid, threads, 0, s, list);
+  }
+  return launch_pdl(adamw_kernel<N, TP, TG, MASTER, false, false>, grid, threads, 0, s, list);
 }
 
 // A launch's table lies in its arguments: a short one where it does.

@@ -279,7 +279,9 @@ int moe_dropout(int64_t rows, int32_t cols, int32_t dtype, const void* x, int64_
              : MOE_ERR_CUDA;
 }
 
-int moe_adamw(const moe_adamw_args_t* a, void* stream) {
+int moe_adamw(const moe_adamw_args_t* a, void* stream) { return moe_adamw_at(a, nullptr, stream); }
+
+int moe_adamw_at(const moe_adamw_args_t* a, const uint64_t* offset_dev, void* stream) {
   if (a == nullptr || a->n_tensors < 0) return MOE_ERR_INVALID;
   if (!is_dtype(a->param_dtype) || !is_dtype(a->grad_dtype)) return MOE_ERR_INVALID;
   if (a->grad_dtype != a->param_dtype && a->grad_dtype != MOE_DT_F32) return MOE_ERR_INVALID;
@@ -290,6 +292,7 @@ int moe_adamw(const moe_adamw_args_t* a, void* stream) {
   if (!a->lr_dev && (!(a->lr >= 0.0) || std::isinf(a->lr))) return MOE_ERR_INVALID;
   if (!a->step_dev && a->step < 1) return MOE_ERR_INVALID;
   if (!on_boundary(a->grad_scale, 4) || !on_boundary(a->lr_dev, 4) || !on_boundary(a->step_dev, 8)) return MOE_ERR_ALIGN;
+  if (!on_boundary(offset_dev, 8)) return MOE_ERR_ALIGN;
   if (a->n_tensors == 0) return MOE_OK;
   if (a->tensors == nullptr) return MOE_ERR_INVALID;
   if (a->n_tensors > (1 << 24)) return MOE_ERR_UNSUPPORTED;
@@ -330,7 +333,7 @@ int moe_adamw(const moe_adamw_args_t* a, void* stream) {
     p.s.decay = (float)(1.0 - a->lr * a->weight_decay);
     p.s.rate = (float)(a->lr / p.c1);
   }
-  p.grad_scale = a->grad_scale; p.lr_dev = a->lr_dev; p.step_dev = a->step_dev;
+  p.grad_scale = a->grad_scale; p.lr_dev = a->lr_dev; p.step_dev = a->step_dev; p.offset_dev = offset_dev;
   p.k0 = (uint32_t)a->seed; p.k1 = (uint32_t)(a->seed >> 32);
   p.o0 = (uint32_t)a->offset; p.o1 = (uint32_t)(a->offset >> 32);
   AdamwTensor list[kAdamwMost];

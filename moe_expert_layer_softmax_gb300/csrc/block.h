@@ -108,6 +108,7 @@ struct AdamwParams {
   const float* grad_scale;
   const float* lr_dev;
   const int64_t* step_dev;
+  const uint64_t* offset_dev;   // nullable: added to the offset o1 : o0
   double lr, beta1, beta2, weight_decay, c1;   // c1: 1 - b1^t of the host's t
   uint32_t k0, k1, o0, o1;
 };

@@ -1,0 +1,82 @@
+"""Calls whose offset of the drawn numbers lies on the device: refusals of the C entries
+and of the binding, and which entry the binding takes.  Host only."""
+import ctypes
+import os
+import shutil
+
+import pytest
+import torch
+
+import moe_expert_layer_softmax_gb300 as m
+from moe_expert_layer_softmax_gb300 import _build
+from test_adamw_host import ARGS, P, TENSOR, placed
+
+INVALID, ALIGN = -1, -3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    if shutil.which("nvcc") is None and not os.path.exists("/usr/local/cuda/bin/nvcc"):
+        pytest.skip("nvcc not available")
+    _build.build()
+    return m.load()
+
+
+def test_adamw_refusals(lib):
+    t = ctypes.create_string_buffer(m._ADAMW_TENSOR.pack(*TENSOR.values()))
+
+    def pack(**change):
+        return m._ADAMW.pack(ctypes.addressof(t), *{**ARGS, **change}.values())
+    assert lib.moe_adamw_at(None, P, None) == INVALID
+    assert lib.moe_adamw_at(pack(), P + 4, None) == ALIGN
+    assert lib.moe_adamw_at(pack(b1=1.0), P, None) == INVALID
+    assert lib.moe_adamw_at(pack(n_tensors=0), P, None) == 0
+
+
+class Library:
+    """Takes the calls down; every entry answers 0."""
+
+    def __init__(self):
+        self.calls = []
+
+    def __getattr__(self, name):
+        return lambda *args: self.calls.append((name, args)) or 0
+
+
+@pytest.fixture
+def fake(monkeypatch):
+    m._dtype(torch.zeros(1), "x")
+    lib = Library()
+    monkeypatch.setattr(m, "load", lambda: lib)
+    monkeypatch.setattr(m, "_stream", lambda stream: 77)
+    monkeypatch.setattr(m, "_several", False)
+    return lib
+
+
+def counter(n=1, dtype=torch.int64):
+    return placed(n, 0, dtype)
+
+
+def calls():
+    lst = m.adamw_list(*([placed(8, 0)] for _ in range(4)))
+    return {"adamw": lambda **kw: m.adamw(lst, lr=0.1, step=1, **kw)}
+
+
+@pytest.mark.parametrize("name", ["adamw"])
+def test_the_entry_that_is_called(fake, name):
+    call, at = calls()[name], counter()
+    call()
+    call(offset_dev=at)
+    (plain, a), (other, b) = fake.calls
+    assert plain == "moe_" + name and other == plain + "_at"
+    assert len(b) == len(a) + 1 and a[-1] == b[-1] == 77 and b[-2] == at.data_ptr()
+
+
+@pytest.mark.parametrize("name", ["adamw"])
+def test_counters_that_are_refused(fake, name):
+    call = calls()[name]
+    for bad, error in ((counter(2), ValueError), (counter(0), ValueError), (counter(1, torch.int32), TypeError),
+                       (counter(1, torch.float32), TypeError), (torch.zeros(1, dtype=torch.int64), ValueError)):
+        with pytest.raises(error):
+            call(offset_dev=bad)
+    assert not fake.calls

@@ -1,0 +1,114 @@
+"""Calls that draw numbers, captured into a graph: each replay has numbers of its own when
+the offset comes from the device.
+
+Replays are compared bit for bit with eager calls that are given the sum of the two offsets,
+which other tests compare with the oracle.  How far many roundings stray is compared with
+the binomial distribution.  GPU only."""
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_adamw import HYPER, SEED, Tensors
+
+pytestmark = pytest.mark.gpu
+
+
+def captured(fn):
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        fn()
+    return graph
+
+
+# ------------------------------------------------------------------ AdamW
+@pytest.mark.parametrize("kind,bits", [(("bf16", "f32", False), 32), (("bf16", "bf16", False), 8), (("bf16", "f32", True), 8),
+                                       (("f32", "f32", False), 8), (("f16", "f16", True), 8)], ids=str)
+@pytest.mark.parametrize("offset", [0, (1 << 32) - 2, (1 << 64) - 2], ids=hex)
+def test_replays_equal_steps_with_offsets_of_their_own(moe_gpu, kind, bits, offset):
+    """The sum carries into the upper word and past 64 bits."""
+    m, dev = moe_gpu
+    t, u = (Tensors(m, dev, [5000, 17, 0, 129], kind, bits) for _ in range(2))
+    step = torch.zeros(1, dtype=torch.int64, device=dev)
+
+    def one():
+        step.add_(1)
+        m.adamw(t.list, step=step, seed=SEED, offset=offset, offset_dev=step, **HYPER)
+    graph = captured(one)
+    for k in (1, 2, 3):
+        graph.replay()
+        m.adamw(u.list, step=k, seed=SEED, offset=(offset + k) % (1 << 64), **HYPER)
+        torch.cuda.synchronize()
+        for a, b in zip(t.list.held, u.list.held):
+            assert torch.equal(a, b)
+
+
+def test_the_counter_is_no_part_of_steps_without_drawn_numbers(moe_gpu):
+    m, dev = moe_gpu
+    for kind in (("f32", "f32", False), ("bf16", "f32", True)):
+        t, u = (Tensors(m, dev, [300], kind, 32) for _ in range(2))
+        m.adamw(t.list, step=1, offset_dev=torch.tensor([5], device=dev), **HYPER)
+        m.adamw(u.list, step=1, **HYPER)
+        for a, b in zip(t.list.held, u.list.held):
+            assert torch.equal(a, b)
+
+
+def test_captured_steps_of_bf16_parameters_follow_their_mean(moe_gpu):
+    """A hundred replayed steps of -1e-4 from 1, where bf16 steps by 2^-8: each goes down
+    with the probability 1e-4 * 2^8 (16 bits of it: 2^-16 off at most), so that a place has
+    taken a binomial number of steps.  The mean of n places strays by five standard errors
+    at most, the spread by five of its own (sigma / sqrt(2 n) for a normal distribution; the
+    binomial one's fourth moment is below 3.4 sigma^4: 1.1 times that)."""
+    m, dev = moe_gpu
+    n, steps, lr = 1 << 18, 100, 1e-4
+    p = torch.ones(n, dtype=torch.bfloat16, device=dev)
+    g = torch.full((n,), 0.25, device=dev)
+    lst = m.adamw_list([p], [g], *m.adamw_states([p]))
+    step = torch.zeros(1, dtype=torch.int64, device=dev)
+
+    def one():
+        step.add_(1)
+        m.adamw(lst, lr, step, eps=0.0, weight_decay=0.0, seed=SEED, offset_dev=step)
+    graph = captured(one)
+    for _ in range(steps):
+        graph.replay()
+    torch.cuda.synchronize()
+    down = lr * 256
+    sigma = 2.0 ** -8 * np.sqrt(steps * down * (1 - down))
+    got = p.double()
+    assert step.item() == steps
+    assert abs(got.mean().item() - (1 - steps * lr)) <= 5 * sigma / np.sqrt(n) + 2 * steps * 2.0 ** -24
+    assert abs(got.std().item() / sigma - 1) <= 1.1 * 5 / np.sqrt(2 * n) + steps * 2.0 ** -16
+    assert got.max().item() <= 1 and (got == 1).double().mean().item() < 0.1   # (1 - down)^100 = 0.075 never moved
+
+
+def test_captured_steps_of_8_bit_states_follow_their_mean(moe_gpu):
+    """A gradient of 0.4 beside one of 1 each 128, a hundred steps from zeros: the first
+    moment is 0.4 (1 - b^100).  A step adds 1 - b of the distance, and a rounding that is
+    right in the mean (16 bits of the probability: off by 2^-16 of a code's step at most) and
+    strays by at most half of that step, 32 / 448 below the code of 512; each rounding counts
+    b of the one before it in the next step.  With the same numbers at every replay a place
+    would stand still where its distance no longer reaches its border."""
+    m, dev = moe_gpu
+    n, steps, beta = 1 << 16, 100, 0.9
+    p = torch.zeros(n, device=dev)
+    g = torch.full((n,), 0.4, device=dev)
+    g[::128] = 1.0
+    states = m.adamw_states([p], 8)
+    lst = m.adamw_list([p], [g], *states)
+    step = torch.zeros(1, dtype=torch.int64, device=dev)
+
+    def one():
+        step.add_(1)
+        m.adamw(lst, 1e-3, step, beta1=beta, beta2=beta, seed=SEED, offset=3 << 40, offset_dev=step)
+    graph = captured(one)
+    for _ in range(steps):
+        graph.replay()
+    torch.cuda.synchronize()
+    few = torch.arange(n, device=dev) % 128 != 0
+    code, scale = states[0][0]
+    v = (code.view(torch.float8_e4m3fn).double() * scale.double().repeat_interleave(128))[few]
+    want, unit = 0.4 * (1 - beta ** steps), 32 / 448
+    sigma = unit / 2 / np.sqrt(1 - beta ** 2)
+    off = 5 * sigma / np.sqrt(len(v)) + 2.0 ** -16 * unit / (1 - beta) + 2.0 ** -20
+    assert abs(v.mean().item() - want) <= off and v.std().item() <= sigma
