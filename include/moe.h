@@ -736,11 +736,28 @@ MOE_API int moe_add_layer_norm_bwd(const moe_add_layer_norm_bwd_args_t* args, vo
  * Philox4x32-10 (Salmon et al., SC 2011) with key = seed and counter
  * (col / 8, row, offset low 32 bits, offset high 32 bits): a function of the
  * element's place alone, not of types, strides or the launch.  A step that
- * drops several matrices gives each its own offset.  The backward is the same
- * call on dy.  y may be x (same stride).  cols <= 2^30, rows < 2^31. */
+ * drops several matrices gives each its own offset, and so does each step (captured ones:
+ * the calls below).  The backward is the same call on dy.  y may be x (same stride).
+ * cols <= 2^30, rows < 2^31. */
 MOE_API int moe_dropout(int64_t rows, int32_t cols, int32_t dtype, const void* x, int64_t ld_x,
                         void* y, int64_t ld_y, float p, uint64_t seed, uint64_t offset,
                         void* stream);
+
+/* The calls above with offset + *offset_dev (modulo 2^64, read when the kernel runs) in
+ * place of offset.  An offset that is an argument is frozen in a captured graph: each
+ * replay would drop the same places.  With a counter on the device that goes on between
+ * the replays, after the backward that needs the forward's, each has masks of its own.
+ * Matrices of a step keep theirs apart by offsets that the counter does not pass from one
+ * to the other: it goes on by their number, or they lie far apart (i << 32).
+ * offset_dev: 8-byte aligned; NULL: the call without. */
+MOE_API int moe_add_norm_at(const moe_add_norm_args_t* args, const uint64_t* offset_dev, void* stream);
+MOE_API int moe_add_norm_bwd_at(const moe_add_norm_bwd_args_t* args, void* ws, const uint64_t* offset_dev, void* stream);
+MOE_API int moe_add_layer_norm_at(const moe_add_layer_norm_args_t* args, const uint64_t* offset_dev, void* stream);
+MOE_API int moe_add_layer_norm_bwd_at(const moe_add_layer_norm_bwd_args_t* args, void* ws, const uint64_t* offset_dev,
+                                      void* stream);
+MOE_API int moe_dropout_at(int64_t rows, int32_t cols, int32_t dtype, const void* x, int64_t ld_x,
+                           void* y, int64_t ld_y, float p, uint64_t seed, uint64_t offset,
+                           const uint64_t* offset_dev, void* stream);
 
 /* AdamW over a list of tensors (what the layer's and the norms' backward leave in
  * their gradient buffers), in one launch for each 224 of them.  For every value, each

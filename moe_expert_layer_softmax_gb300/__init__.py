@@ -53,6 +53,7 @@ EXPORTS = (
     "moe_checks_read", "moe_few_workspace_size", "moe_few_fwd",
     "moe_add_norm", "moe_add_norm_bwd_workspace_size", "moe_add_norm_bwd", "moe_add_layer_norm",
     "moe_add_layer_norm_bwd_workspace_size", "moe_add_layer_norm_bwd", "moe_dropout", "moe_adamw", "moe_adamw_at",
+    "moe_add_norm_at", "moe_add_norm_bwd_at", "moe_add_layer_norm_at", "moe_add_layer_norm_bwd_at", "moe_dropout_at",
     "moe_quantize_w4", "moe_dequantize_w4", "moe_matvec_w4", "moe_experts_w4_workspace_size",
     "moe_experts_w4",
 )
@@ -161,6 +162,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_add_layer_norm_bwd": [_vp, _vp, _vp],
         "moe_dropout": [i64, i32, i32, _vp, i64, _vp, i64, ctypes.c_float, ctypes.c_uint64,
                         ctypes.c_uint64, _vp],
+        "moe_add_norm_at": [_vp, _vp, _vp],
+        "moe_add_norm_bwd_at": [_vp, _vp, _vp, _vp],
+        "moe_add_layer_norm_at": [_vp, _vp, _vp],
+        "moe_add_layer_norm_bwd_at": [_vp, _vp, _vp, _vp],
+        "moe_dropout_at": [i64, i32, i32, _vp, i64, _vp, i64, ctypes.c_float, ctypes.c_uint64,
+                           ctypes.c_uint64, _vp, _vp],
         "moe_adamw": [_vp, _vp],
         "moe_adamw_at": [_vp, _vp, _vp],
         "moe_quantize_w4": [i64, i32, i32, i32, _vp, _vp, _vp, _vp],
@@ -463,17 +470,6 @@ def _failed(fn, rc, *args):
     _check(fn, rc)
 
 
-def _call(fn, *args):
-    """A call whose argument before the stream is the address of the offset's part on the
-    device, or 0: then the form without it."""
-    *args, at, st = args
-    if at:
-        fn, args = fn + "_at", (*args, at)
-    rc = getattr(load(), fn)(*args, st)
-    if rc:
-        _failed(fn, rc, *args, st)
-
-
 def _shape(x):
     """(rows, columns) of a tensor whose axes before the last are rows."""
     d = x.size(-1)
@@ -521,10 +517,21 @@ def _flat(t, what, numel, dtype, at_least=False):
     return t.data_ptr()
 
 
+def _call_at(fn, offset_dev, *args):
+    """The form of a call (its arguments, the stream last) that adds `offset_dev`, an int64
+    tensor of one element, to the offset."""
+    fn, args = fn + "_at", (*args[:-1], _flat(offset_dev, "offset_dev", 1, _torch.int64), args[-1])
+    rc = getattr(load(), fn)(*args)
+    if rc:
+        _failed(fn, rc, *args)
+
+
 def add_norm(x, weight, y, residual=None, h=None, rstd=None, eps=1e-5, p=0.0, seed=0, offset=0,
-             y_q=None, y_scales=None, y_dq=None, stream=None):
+             y_q=None, y_scales=None, y_dq=None, stream=None, offset_dev=None):
     """moe_add_norm: h = residual + dropout(x), y = h * rstd * weight.  y=None with
-    y_q, y_scales (and y_dq): the MXFP8 output, buffers of roundup(rows, 128) rows."""
+    y_q, y_scales (and y_dq): the MXFP8 output, buffers of roundup(rows, 128) rows.
+    offset_dev, here and below: a CUDA int64 tensor of one element that is added to offset
+    when the kernel runs (captured graphs whose replays draw masks of their own)."""
     xt = x.dtype
     dt = _dtype(x, "x")
     rows, d = _shape(x)
@@ -545,6 +552,8 @@ def add_norm(x, weight, y, residual=None, h=None, rstd=None, eps=1e-5, p=0.0, se
         px, ld_x, pr, ld_r, _flat(weight, "weight", d, weight.dtype), ph, ld_h, py, ld_y,
         _flat(rstd, "rstd", rows, _torch.float32), pq, ps, pd, seed, offset, eps, p)
     st = _stream(stream)
+    if offset_dev is not None:
+        return _call_at("moe_add_norm", offset_dev, args, st)
     rc = load().moe_add_norm(args, st)
     if rc:
         _failed("moe_add_norm", rc, args, st)
@@ -559,7 +568,7 @@ def add_norm_bwd_workspace(rows, d) -> int:
 
 
 def add_norm_bwd(dy, h, rstd, weight, dres=None, dh=None, dx=None, dw=None, ws=None, p=0.0, seed=0,
-                 offset=0, stream=None):
+                 offset=0, stream=None, offset_dev=None):
     """moe_add_norm_bwd: dh (gradient of the stream), dx (of the dropped input), dw."""
     xt, ht = dy.dtype, h.dtype
     dt = _dtype(dy, "dy")
@@ -577,13 +586,15 @@ def add_norm_bwd(dy, h, rstd, weight, dres=None, dh=None, dx=None, dw=None, ws=N
         _flat(rstd, "rstd", rows, _torch.float32), _flat(weight, "weight", d, weight.dtype),
         pdh, ld_dh, pdx, ld_dx, _flat(dw, "dw", d, _torch.float32), seed, offset, p)
     st = _stream(stream)
+    if offset_dev is not None:
+        return _call_at("moe_add_norm_bwd", offset_dev, args, pws, st)
     rc = load().moe_add_norm_bwd(args, pws, st)
     if rc:
         _failed("moe_add_norm_bwd", rc, args, pws, st)
 
 
 def add_layer_norm(x, weight, bias, y, residual=None, h=None, mean=None, rstd=None, eps=1e-5, p=0.0, seed=0, offset=0,
-                   y_q=None, y_scales=None, y_dq=None, stream=None):
+                   y_q=None, y_scales=None, y_dq=None, stream=None, offset_dev=None):
     """moe_add_layer_norm: h = residual + dropout(x), y = (h - mean) * rstd * weight + bias
     (bias=None: none).  y=None with y_q, y_scales (and y_dq): the MXFP8 output, buffers
     of roundup(rows, 128) rows."""
@@ -608,6 +619,8 @@ def add_layer_norm(x, weight, bias, y, residual=None, h=None, mean=None, rstd=No
         px, ld_x, pr, ld_r, _flat(weight, "weight", d, weight.dtype), _flat(bias, "bias", d, weight.dtype), ph, ld_h,
         py, ld_y, _flat(mean, "mean", rows, f32), _flat(rstd, "rstd", rows, f32), pq, ps, pd, seed, offset, eps, p)
     st = _stream(stream)
+    if offset_dev is not None:
+        return _call_at("moe_add_layer_norm", offset_dev, args, st)
     rc = load().moe_add_layer_norm(args, st)
     if rc:
         _failed("moe_add_layer_norm", rc, args, st)
@@ -622,7 +635,7 @@ def add_layer_norm_bwd_workspace(rows, d) -> int:
 
 
 def add_layer_norm_bwd(dy, h, mean, rstd, weight, dres=None, dh=None, dx=None, dw=None, db=None, ws=None, p=0.0, seed=0,
-                       offset=0, stream=None):
+                       offset=0, stream=None, offset_dev=None):
     """moe_add_layer_norm_bwd: dh (gradient of the stream), dx (of the dropped input),
     dw and db."""
     xt, ht = dy.dtype, h.dtype
@@ -642,12 +655,14 @@ def add_layer_norm_bwd(dy, h, mean, rstd, weight, dres=None, dh=None, dx=None, d
         _flat(mean, "mean", rows, f32), _flat(rstd, "rstd", rows, f32), _flat(weight, "weight", d, weight.dtype),
         pdh, ld_dh, pdx, ld_dx, _flat(dw, "dw", d, f32), _flat(db, "db", d, f32), seed, offset, p)
     st = _stream(stream)
+    if offset_dev is not None:
+        return _call_at("moe_add_layer_norm_bwd", offset_dev, args, pws, st)
     rc = load().moe_add_layer_norm_bwd(args, pws, st)
     if rc:
         _failed("moe_add_layer_norm_bwd", rc, args, pws, st)
 
 
-def dropout(x, y, p, seed, offset=0, stream=None):
+def dropout(x, y, p, seed, offset=0, stream=None, offset_dev=None):
     """moe_dropout: y = dropout(x), the mask a function of (seed, offset, row,
     column); the backward is the same call on the gradient."""
     dt = _dtype(x, "x")
@@ -655,6 +670,8 @@ def dropout(x, y, p, seed, offset=0, stream=None):
     px, ld_x = _matrix(x, "x", rows, d, x.dtype)
     py, ld_y = _matrix(y, "y", rows, d, x.dtype)
     args = (rows, d, dt, px, ld_x, py, ld_y, p, seed, offset, _stream(stream))
+    if offset_dev is not None:
+        return _call_at("moe_dropout", offset_dev, *args)
     rc = load().moe_dropout(*args)
     if rc:
         _failed("moe_dropout", rc, *args)
@@ -752,12 +769,15 @@ def adamw(tensors: AdamWList, lr, step, beta1=0.9, beta2=0.999, eps=1e-8, weight
         plr, lr = _flat(lr, "lr", 1, _torch.float32), 0.0
     if not isinstance(step, int):
         pstep, step = _flat(step, "step", 1, _torch.int64), 1
-    poffset = _flat(offset_dev, "offset_dev", 1, _torch.int64)
     host = ctypes.c_char_p(lst.tensors)
     args = _ADAMW.pack(ctypes.cast(host, _vp).value, lst.n, *lst.types, _flat(grad_scale, "grad_scale", 1, _torch.float32),
                        plr, pstep, lr, beta1, beta2, eps, weight_decay, step, seed, offset)
     st = _stream(stream)
-    _call("moe_adamw", args, poffset, st)
+    if offset_dev is not None:
+        return _call_at("moe_adamw", offset_dev, args, st)
+    rc = load().moe_adamw(args, st)
+    if rc:
+        _failed("moe_adamw", rc, args, st)
 
 
 def _w4(q, scales, what):

@@ -41,12 +41,14 @@ int row_access(const void* p, int64_t ld, int64_t rows, int dtype, int most = 8)
 int width_access(int32_t d) { return d % 8 == 0 ? 8 : d % 2 == 0 ? 2 : 1; }
 
 // p in [0, 1]; the keep probability is a multiple of 2^-16.
-int make_rng(float p, uint64_t seed, uint64_t offset, DropRng* g) {
+int make_rng(float p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev, DropRng* g) {
   if (!(p >= 0.0f && p <= 1.0f)) return MOE_ERR_INVALID;
   g->k0 = (uint32_t)seed;
   g->k1 = (uint32_t)(seed >> 32);
   g->o0 = (uint32_t)offset;
   g->o1 = (uint32_t)(offset >> 32);
+  g->offset_dev = offset_dev;
+  if (!on_boundary(offset_dev, 8)) return MOE_ERR_ALIGN;
   g->threshold = (uint32_t)std::floor((double)p * 65536.0 + 0.5);
   g->scale = g->threshold < 65536u ? (float)(65536.0 / (65536.0 - g->threshold)) : 0.0f;
   return MOE_OK;
@@ -95,9 +97,9 @@ int check_experts(int32_t T, int32_t d, int32_t E, int32_t k, int32_t f, int32_t
 // Checks and parameters of either norm's forward; without rows p.rows
 // stays zero and nothing is launched.  The layer norm's bias and mean may be NULL.
 template <typename Args>
-int add_norm_params(const Args* a, const void* bias, float* mean, AddNormParams& p, int& vec) {
+int add_norm_params(const Args* a, const uint64_t* offset_dev, const void* bias, float* mean, AddNormParams& p, int& vec) {
   MOE_TRY(check_norm_types(a->rows, a->d, a->dtype, a->res_dtype, a->w_dtype));
-  MOE_TRY(make_rng(a->p, a->seed, a->offset, &p.rng));
+  MOE_TRY(make_rng(a->p, a->seed, a->offset, offset_dev, &p.rng));
   if (!(a->eps >= 0.0f) || std::isinf(a->eps)) return MOE_ERR_INVALID;
   if (a->rows == 0) return MOE_OK;
   MOE_TRY(check_matrix(a->x, a->ld_x, a->d, a->dtype));
@@ -186,11 +188,13 @@ using namespace moe;
 
 extern "C" {
 
-int moe_add_norm(const moe_add_norm_args_t* a, void* stream) {
+int moe_add_norm(const moe_add_norm_args_t* a, void* stream) { return moe_add_norm_at(a, nullptr, stream); }
+
+int moe_add_norm_at(const moe_add_norm_args_t* a, const uint64_t* offset_dev, void* stream) {
   if (a == nullptr) return MOE_ERR_INVALID;
   AddNormParams p = {};
   int vec = 0;
-  MOE_TRY(add_norm_params(a, nullptr, nullptr, p, vec));
+  MOE_TRY(add_norm_params(a, offset_dev, nullptr, nullptr, p, vec));
   if (p.rows == 0) return MOE_OK;
   return launch_add_norm(p, a->dtype, a->res_dtype, vec, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MOE_OK
@@ -198,10 +202,14 @@ int moe_add_norm(const moe_add_norm_args_t* a, void* stream) {
 }
 
 int moe_add_layer_norm(const moe_add_layer_norm_args_t* a, void* stream) {
+  return moe_add_layer_norm_at(a, nullptr, stream);
+}
+
+int moe_add_layer_norm_at(const moe_add_layer_norm_args_t* a, const uint64_t* offset_dev, void* stream) {
   if (a == nullptr) return MOE_ERR_INVALID;
   AddNormParams p = {};
   int vec = 0;
-  MOE_TRY(add_norm_params(a, a->bias, a->mean, p, vec));
+  MOE_TRY(add_norm_params(a, offset_dev, a->bias, a->mean, p, vec));
   if (p.rows == 0) return MOE_OK;
   return launch_add_layer_norm(p, a->dtype, a->res_dtype, vec, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? MOE_OK
@@ -216,10 +224,14 @@ int moe_add_norm_bwd_workspace_size(int64_t rows, int32_t d, size_t* ws_bytes) {
 }
 
 int moe_add_norm_bwd(const moe_add_norm_bwd_args_t* a, void* ws, void* stream) {
+  return moe_add_norm_bwd_at(a, ws, nullptr, stream);
+}
+
+int moe_add_norm_bwd_at(const moe_add_norm_bwd_args_t* a, void* ws, const uint64_t* offset_dev, void* stream) {
   if (a == nullptr) return MOE_ERR_INVALID;
   MOE_TRY(check_norm_types(a->rows, a->d, a->dtype, a->res_dtype, a->w_dtype));
   AddNormBwdParams p = {};
-  MOE_TRY(make_rng(a->p, a->seed, a->offset, &p.rng));
+  MOE_TRY(make_rng(a->p, a->seed, a->offset, offset_dev, &p.rng));
   if (!a->dh && !a->dx && !a->dw) return MOE_ERR_INVALID;
   if (a->dw && !on_boundary(a->dw, 4)) return MOE_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -240,10 +252,14 @@ int moe_add_layer_norm_bwd_workspace_size(int64_t rows, int32_t d, size_t* ws_by
 }
 
 int moe_add_layer_norm_bwd(const moe_add_layer_norm_bwd_args_t* a, void* ws, void* stream) {
+  return moe_add_layer_norm_bwd_at(a, ws, nullptr, stream);
+}
+
+int moe_add_layer_norm_bwd_at(const moe_add_layer_norm_bwd_args_t* a, void* ws, const uint64_t* offset_dev, void* stream) {
   if (a == nullptr) return MOE_ERR_INVALID;
   MOE_TRY(check_norm_types(a->rows, a->d, a->dtype, a->res_dtype, a->w_dtype));
   AddNormBwdParams p = {};
-  MOE_TRY(make_rng(a->p, a->seed, a->offset, &p.rng));
+  MOE_TRY(make_rng(a->p, a->seed, a->offset, offset_dev, &p.rng));
   if (!a->dh && !a->dx && !a->dw && !a->db) return MOE_ERR_INVALID;
   if ((a->dw && !on_boundary(a->dw, 4)) || (a->db && !on_boundary(a->db, 4))) return MOE_ERR_ALIGN;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -262,10 +278,15 @@ int moe_add_layer_norm_bwd(const moe_add_layer_norm_bwd_args_t* a, void* ws, voi
 
 int moe_dropout(int64_t rows, int32_t cols, int32_t dtype, const void* x, int64_t ld_x, void* y,
                 int64_t ld_y, float prob, uint64_t seed, uint64_t offset, void* stream) {
+  return moe_dropout_at(rows, cols, dtype, x, ld_x, y, ld_y, prob, seed, offset, nullptr, stream);
+}
+
+int moe_dropout_at(int64_t rows, int32_t cols, int32_t dtype, const void* x, int64_t ld_x, void* y, int64_t ld_y,
+                   float prob, uint64_t seed, uint64_t offset, const uint64_t* offset_dev, void* stream) {
   if (rows < 0 || cols < 1 || !is_dtype(dtype)) return MOE_ERR_INVALID;
   if (rows > INT32_MAX || cols > (1 << 30)) return MOE_ERR_UNSUPPORTED;
   DropoutParams p = {};
-  MOE_TRY(make_rng(prob, seed, offset, &p.rng));
+  MOE_TRY(make_rng(prob, seed, offset, offset_dev, &p.rng));
   if (rows == 0) return MOE_OK;
   MOE_TRY(check_matrix(x, ld_x, cols, dtype));
   MOE_TRY(check_matrix(y, ld_y, cols, dtype));

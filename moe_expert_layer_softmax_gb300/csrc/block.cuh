@@ -198,6 +198,7 @@ struct DropRng {
   uint32_t k0, k1, o0, o1;
   uint32_t threshold;   // 0: keep everything
   float scale;
+  const uint64_t* offset_dev;   // nullable: added to the offset o1 : o0
 };
 
 // Philox of N counters at once: the rounds' keys are made once.
@@ -214,6 +215,22 @@ template <int N> MOE_DEV void philox4x32_10(uint4 (&c)[N], uint32_t k0, uint32_t
     k0 += 0x9E3779B9u;
     k1 += 0xBB67AE85u;
   }
+}
+
+// The numbers of N counters (x, y, offset).  AT: a part of the offset lies on the device and
+// is read where it is used; two registers through a whole kernel would spill.
+template <bool AT, int N> MOE_DEV void draw(uint4 (&c)[N], const DropRng& g) {
+  uint32_t low = g.o0, high = g.o1;
+  if constexpr (AT) {
+    uint64_t offset;
+    asm volatile("ld.global.u64 %0, [%1];" : "=l"(offset) : "l"(g.offset_dev));
+    offset += (uint64_t)high << 32 | low;
+    low = (uint32_t)offset;
+    high = (uint32_t)(offset >> 32);
+  }
+#pragma unroll
+  for (int n = 0; n < N; ++n) c[n] = make_uint4(c[n].x, c[n].y, low, high);
+  philox4x32_10(c, g.k0, g.k1);
 }
 
 // Drop and scale eight values by their numbers.  Dropped places become zero
@@ -253,11 +270,11 @@ MOE_DEV void exchange_numbers(uint4& r, int lane, int G, uint4* xch, Sync sync) 
 
 // The numbers of a thread's N times eight values of a row: groups lane, lane +
 // G, ... of neighbouring columns (V = 8), or the columns first_column() says.
-template <int V, int N, typename Sync>
+template <int V, bool AT, int N, typename Sync>
 MOE_DEV void drop_numbers(uint4 (&r)[N], int lane, int G, uint32_t row, const DropRng& g, uint4* xch, Sync sync) {
 #pragma unroll
-  for (int n = 0; n < N; ++n) r[n] = make_uint4((uint32_t)(lane + n * G), row, g.o0, g.o1);
-  philox4x32_10(r, g.k0, g.k1);
+  for (int n = 0; n < N; ++n) r[n] = make_uint4((uint32_t)(lane + n * G), row, 0, 0);
+  draw<AT>(r, g);
   if constexpr (V != 8) {
 #pragma unroll
     for (int n = 0; n < N; ++n) exchange_numbers<V>(r[n], lane, G, xch, sync);

@@ -78,6 +78,12 @@ cudaError_t launch_add_norm_bwd(const AddNormBwdParams& p, int dtype, int res_dt
 cudaError_t launch_add_layer_norm(const AddNormParams& p, int dtype, int res_dtype, int vec, cudaStream_t s);
 cudaError_t launch_add_layer_norm_bwd(const AddNormBwdParams& p, int dtype, int res_dtype, int vec, float* dw, float* db,
                                       cudaStream_t s);
+// The same with dropout whose offset has a part on the device.
+cudaError_t launch_add_norm_at(const AddNormParams& p, int dtype, int res_dtype, int vec, cudaStream_t s);
+cudaError_t launch_add_norm_bwd_at(const AddNormBwdParams& p, int dtype, int res_dtype, int vec, float* dw, cudaStream_t s);
+cudaError_t launch_add_layer_norm_at(const AddNormParams& p, int dtype, int res_dtype, int vec, cudaStream_t s);
+cudaError_t launch_add_layer_norm_bwd_at(const AddNormBwdParams& p, int dtype, int res_dtype, int vec, float* dw, float* db,
+                                         cudaStream_t s);
 cudaError_t launch_dropout(const DropoutParams& p, int dtype, int vec, cudaStream_t s);
 
 // ---------------------------------------------------------------- AdamW

@@ -4,7 +4,8 @@
 namespace moe {
 
 cudaError_t launch_add_layer_norm(const AddNormParams& p, int dtype, int res_dtype, int vec, cudaStream_t s) {
-  return fwd_launch<true>(p, dtype, res_dtype, vec, s);
+  return drawn_at(p) ? launch_add_layer_norm_at(p, dtype, res_dtype, vec, s)
+                     : fwd_launch<true, false>(p, dtype, res_dtype, vec, s);
 }
 
 }  // namespace moe

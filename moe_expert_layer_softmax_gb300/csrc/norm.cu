@@ -8,9 +8,9 @@ namespace {
 
 // y = dropout(x): a warp, or (SMALL, rows up to 64 and 128 columns) 8 or 16 lanes,
 // takes eight columns a lane of two rows at a time.  Bound by the generator (16-bit
-// types) and HBM (fp32): 16384 x 2048 bf16 26.6 us, 5.0 TB/s; fp32 5.7 TB/s.  Four
-// blocks a multiprocessor leave 64 registers: with vector loads 12 to 40 bytes a thread
-// spill (fp32 12, fp16 20, bf16 40; without them at most 12).
+// types) and HBM (fp32): 16384 x 2048 bf16 25.9 us, 5.2 TB/s; fp32 42.7 us, 6.3 TB/s.  Four
+// blocks a multiprocessor leave 64 registers: at most 12 bytes a thread spill.  The branch
+// for an offset on the device costs nothing (with and without it 25.9 and 26.0 us).
 template <typename T, int V, bool SMALL>
 __global__ void __launch_bounds__(256, 4) dropout_kernel(DropoutParams p) {
   __shared__ uint4 xch[V == 8 ? 1 : 256];
@@ -34,8 +34,8 @@ __global__ void __launch_bounds__(256, 4) dropout_kernel(DropoutParams p) {
       if (p.rng.threshold) {
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-          numbers[u] = make_uint4((uint32_t)(lane + L * i), (uint32_t)(row + u), p.rng.o0, p.rng.o1);
-        philox4x32_10(numbers, p.rng.k0, p.rng.k1);
+          numbers[u] = make_uint4((uint32_t)(lane + L * i), (uint32_t)(row + u), 0, 0);
+        if (p.rng.offset_dev) draw<true>(numbers, p.rng); else draw<false>(numbers, p.rng);
         if constexpr (V != 8) {
 #pragma unroll
           for (int u = 0; u < 2; ++u) exchange_numbers<V>(numbers[u], lane, L, xch + group * L, sync);
@@ -55,7 +55,8 @@ __global__ void __launch_bounds__(256, 4) dropout_kernel(DropoutParams p) {
 }  // namespace
 
 cudaError_t launch_add_norm(const AddNormParams& p, int dtype, int res_dtype, int vec, cudaStream_t s) {
-  return fwd_launch<false>(p, dtype, res_dtype, vec, s);
+  return drawn_at(p) ? launch_add_norm_at(p, dtype, res_dtype, vec, s)
+                     : fwd_launch<false, false>(p, dtype, res_dtype, vec, s);
 }
 
 template <typename T> static cudaError_t dropout_types(const DropoutParams& p, int vec, dim3 grid, cudaStream_t s) {

@@ -1,0 +1,11 @@
+// Residual addition with the root-mean-square norm, forward, dropout's offset with a part on the
+// device: norm_fwd.cuh.
+#include "norm_fwd.cuh"
+
+namespace moe {
+
+cudaError_t launch_add_norm_at(const AddNormParams& p, int dtype, int res_dtype, int vec, cudaStream_t s) {
+  return fwd_launch<false, true>(p, dtype, res_dtype, vec, s);
+}
+
+}  // namespace moe

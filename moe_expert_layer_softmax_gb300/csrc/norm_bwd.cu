@@ -5,7 +5,8 @@ namespace moe {
 
 cudaError_t launch_add_norm_bwd(const AddNormBwdParams& p, int dtype, int res_dtype, int vec, float* dw,
                                 cudaStream_t s) {
-  return bwd_launch<false>(p, dtype, res_dtype, vec, dw, nullptr, s);
+  return drawn_at(p) ? launch_add_norm_bwd_at(p, dtype, res_dtype, vec, dw, s)
+                     : bwd_launch<false, false>(p, dtype, res_dtype, vec, dw, nullptr, s);
 }
 
 }  // namespace moe

@@ -20,7 +20,7 @@ constexpr bool kNextInRegisters = !RING && NV == 1 && MAXT < kNormMaxThreads && 
 // partial sums a block goes to `partial` [gridDim.x, d].  Measured: 8192 x 2048
 // bf16 33.2 us (5.05 TB/s; 4 us of it the sum of the partial rows), 32768 x 4096 on
 // an fp32 stream with dropout 317 us (6.8 TB/s, a plain copy's rate).
-template <bool LN, typename TX, typename TR, int V, bool RING, int NV, int MAXT>
+template <bool LN, bool AT, typename TX, typename TR, int V, bool RING, int NV, int MAXT>
 __global__ void __launch_bounds__(MAXT, norm_blocks(RING || kNextInRegisters<TR, V, RING, NV, MAXT>, NV, MAXT)) add_norm_bwd_kernel(AddNormBwdParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float red[2][kNormMaxThreads / 32], red2[2][LN ? kNormMaxThreads / 32 : 4];
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING || kNextInRegisters<TR,
     }
     uint4 numbers[NV];
     if (p.dx && p.rng.threshold)
-      drop_numbers<V>(numbers, lane, G, (uint32_t)row, p.rng, xch + rg.group * G, sync);
+      drop_numbers<V, AT>(numbers, lane, G, (uint32_t)row, p.rng, xch + rg.group * G, sync);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = first_column<V>(i, lane, G);
@@ -284,9 +284,9 @@ __global__ void __launch_bounds__(1024) add_norm_dw_kernel(const float* __restri
   }
 }
 
-template <bool LN, typename TX, typename TR, int V, bool RING, int NV, int MAXT>
+template <bool LN, bool AT, typename TX, typename TR, int V, bool RING, int NV, int MAXT>
 cudaError_t bwd_run(const AddNormBwdParams& p, int threads, int* blocks, cudaStream_t s) {
-  auto* kernel = &add_norm_bwd_kernel<LN, TX, TR, V, RING, NV, MAXT>;
+  auto* kernel = &add_norm_bwd_kernel<LN, AT, TX, TR, V, RING, NV, MAXT>;
   constexpr int ring = RING ? RowRing<8 * (sizeof(TX) + 2 * sizeof(TR)), NV>::kBytes : 0;
   if constexpr (RING) {
     static SmemLimit limit;
@@ -301,7 +301,7 @@ cudaError_t bwd_run(const AddNormBwdParams& p, int threads, int* blocks, cudaStr
 
 // Rows up to 8192 columns (512 threads; 16384 where both matrices are 16 bits)
 // come through the ring; wider ones are read as they are needed.
-template <bool LN, typename TX, typename TR, int V>
+template <bool LN, bool AT, typename TX, typename TR, int V>
 cudaError_t bwd_types(const AddNormBwdParams& p, int* blocks, cudaStream_t s) {
   constexpr bool wide = V == 8 && RowRing<8 * (sizeof(TX) + 2 * sizeof(TR)), 4>::kFits512;
   AddNormBwdParams q = p;
@@ -310,49 +310,49 @@ cudaError_t bwd_types(const AddNormBwdParams& p, int* blocks, cudaStream_t s) {
   if (split.group) {
     const int threads = split.threads();
     if constexpr (wide) {
-      if (split.nv == 3) return bwd_run<LN, TX, TR, V, true, 3, 512>(q, threads, blocks, s);
-      if (split.nv == 4) return bwd_run<LN, TX, TR, V, true, 4, 512>(q, threads, blocks, s);
+      if (split.nv == 3) return bwd_run<LN, AT, TX, TR, V, true, 3, 512>(q, threads, blocks, s);
+      if (split.nv == 4) return bwd_run<LN, AT, TX, TR, V, true, 4, 512>(q, threads, blocks, s);
     }
     if constexpr (V == 8) {
       if (split.nv == 2 && split.group <= kNormThreads)
-        return bwd_run<LN, TX, TR, V, true, 2, kNormThreads>(q, threads, blocks, s);
-      return split.nv == 1 ? bwd_run<LN, TX, TR, V, true, 1, kNormThreads>(q, threads, blocks, s)
-                           : bwd_run<LN, TX, TR, V, true, 2, 512>(q, threads, blocks, s);
+        return bwd_run<LN, AT, TX, TR, V, true, 2, kNormThreads>(q, threads, blocks, s);
+      return split.nv == 1 ? bwd_run<LN, AT, TX, TR, V, true, 1, kNormThreads>(q, threads, blocks, s)
+                           : bwd_run<LN, AT, TX, TR, V, true, 2, 512>(q, threads, blocks, s);
     } else {
-      if (split.group > 512) return bwd_run<LN, TX, TR, V, false, 1, kNormMaxThreads>(q, threads, blocks, s);
-      return split.group <= kNormThreads ? bwd_run<LN, TX, TR, V, false, 1, kNormThreads>(q, threads, blocks, s)
-                                         : bwd_run<LN, TX, TR, V, false, 1, 512>(q, threads, blocks, s);
+      if (split.group > 512) return bwd_run<LN, AT, TX, TR, V, false, 1, kNormMaxThreads>(q, threads, blocks, s);
+      return split.group <= kNormThreads ? bwd_run<LN, AT, TX, TR, V, false, 1, kNormThreads>(q, threads, blocks, s)
+                                         : bwd_run<LN, AT, TX, TR, V, false, 1, 512>(q, threads, blocks, s);
     }
   }
   split = RowSplit(p.d, wide ? 3 : 2, 4, kNormMaxThreads);
   q.group = split.group;
   if constexpr (!wide)
-    if (split.nv == 2) return bwd_run<LN, TX, TR, V, false, 2, kNormMaxThreads>(q, q.group, blocks, s);
-  return split.nv == 3 ? bwd_run<LN, TX, TR, V, false, 3, kNormMaxThreads>(q, q.group, blocks, s)
-                       : bwd_run<LN, TX, TR, V, false, 4, kNormMaxThreads>(q, q.group, blocks, s);
+    if (split.nv == 2) return bwd_run<LN, AT, TX, TR, V, false, 2, kNormMaxThreads>(q, q.group, blocks, s);
+  return split.nv == 3 ? bwd_run<LN, AT, TX, TR, V, false, 3, kNormMaxThreads>(q, q.group, blocks, s)
+                       : bwd_run<LN, AT, TX, TR, V, false, 4, kNormMaxThreads>(q, q.group, blocks, s);
 }
 
-template <bool LN, typename TX, typename TR>
+template <bool LN, bool AT, typename TX, typename TR>
 cudaError_t bwd_vec(const AddNormBwdParams& p, int vec, int* blocks, cudaStream_t s) {
-  return vec == 8   ? bwd_types<LN, TX, TR, 8>(p, blocks, s)
-         : vec == 2 ? bwd_types<LN, TX, TR, 2>(p, blocks, s)
-                    : bwd_types<LN, TX, TR, 1>(p, blocks, s);
+  return vec == 8   ? bwd_types<LN, AT, TX, TR, 8>(p, blocks, s)
+         : vec == 2 ? bwd_types<LN, AT, TX, TR, 2>(p, blocks, s)
+                    : bwd_types<LN, AT, TX, TR, 1>(p, blocks, s);
 }
 
 // The entry of either norm: a kernel for the types and the access, and the sum of
 // the blocks' weight (and bias) gradients.
-template <bool LN>
+template <bool LN, bool AT>
 cudaError_t bwd_launch(const AddNormBwdParams& p, int dtype, int res_dtype, int vec, float* dw, float* db, cudaStream_t s) {
   const bool same = dtype == res_dtype;
   int blocks = 0;
   cudaError_t e;
   if (dtype == MOE_DT_BF16)
-    e = same ? bwd_vec<LN, __nv_bfloat16, __nv_bfloat16>(p, vec, &blocks, s)
-             : bwd_vec<LN, __nv_bfloat16, float>(p, vec, &blocks, s);
+    e = same ? bwd_vec<LN, AT, __nv_bfloat16, __nv_bfloat16>(p, vec, &blocks, s)
+             : bwd_vec<LN, AT, __nv_bfloat16, float>(p, vec, &blocks, s);
   else if (dtype == MOE_DT_F16)
-    e = same ? bwd_vec<LN, __half, __half>(p, vec, &blocks, s) : bwd_vec<LN, __half, float>(p, vec, &blocks, s);
+    e = same ? bwd_vec<LN, AT, __half, __half>(p, vec, &blocks, s) : bwd_vec<LN, AT, __half, float>(p, vec, &blocks, s);
   else
-    e = bwd_vec<LN, float, float>(p, vec, &blocks, s);
+    e = bwd_vec<LN, AT, float, float>(p, vec, &blocks, s);
   if (e != cudaSuccess || p.partial == nullptr) return e;
   const int width = LN ? 2 * p.d : p.d;
   return launch_pdl(add_norm_dw_kernel, dim3((unsigned)((width + 31) / 32)), dim3(1024), 0, s,

@@ -14,7 +14,7 @@ namespace {
 // padding of the last 128-row tile.  Measured: 8192 x 2048 bf16 23.7 us (5.7 TB/s),
 // bound by HBM and, at 60% of the issue slots, by waits between instructions; 8
 // bits, dropout, 32768 x 4096 238 us (5.1 TB/s), 65% of the issue slots.
-template <bool LN, typename TX, typename TR, bool MX, int V, bool RING, int NV, int MAXT>
+template <bool LN, bool AT, typename TX, typename TR, bool MX, int V, bool RING, int NV, int MAXT>
 __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_kernel(AddNormParams p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ __align__(16) float red[2][kNormMaxThreads / 32];
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
       __syncwarp();
     }
     uint4 numbers[NV];
-    if (p.rng.threshold) drop_numbers<V>(numbers, lane, G, (uint32_t)row, p.rng, xch + rg.group * G, sync);
+    if (p.rng.threshold) drop_numbers<V, AT>(numbers, lane, G, (uint32_t)row, p.rng, xch + rg.group * G, sync);
     float ss = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -272,9 +272,9 @@ __global__ void __launch_bounds__(MAXT, norm_blocks(RING, NV, MAXT)) add_norm_ke
   }
 }
 
-template <bool LN, typename TX, typename TR, bool MX, int V, bool RING, int NV, int MAXT>
+template <bool LN, bool AT, typename TX, typename TR, bool MX, int V, bool RING, int NV, int MAXT>
 cudaError_t fwd_run(const AddNormParams& p, int threads, cudaStream_t s) {
-  auto* kernel = &add_norm_kernel<LN, TX, TR, MX, V, RING, NV, MAXT>;
+  auto* kernel = &add_norm_kernel<LN, AT, TX, TR, MX, V, RING, NV, MAXT>;
   constexpr int ring = RING ? RowRing<8 * (sizeof(TX) + sizeof(TR)), NV>::kBytes : 0;
   if constexpr (RING) {
     static SmemLimit limit;
@@ -299,7 +299,7 @@ cudaError_t fwd_run(const AddNormParams& p, int threads, cudaStream_t s) {
 // without vector loads: one), for the 8-bit output three or four.  Measured at 32768
 // x 4096 (8-bit, dropout) 243 us with four, 266 with two; at 8192 x 2048 (bf16) 26
 // with four, 24 with two.
-template <bool LN, typename TX, typename TR, bool MX, int V>
+template <bool LN, bool AT, typename TX, typename TR, bool MX, int V>
 cudaError_t fwd_types(const AddNormParams& p, cudaStream_t s) {
   constexpr bool wide = V == 8 && RowRing<8 * (sizeof(TX) + sizeof(TR)), 4>::kFits512;
   AddNormParams q = p;
@@ -308,55 +308,55 @@ cudaError_t fwd_types(const AddNormParams& p, cudaStream_t s) {
     q.group = split.group;
     if (split.group) {
       const int threads = split.threads();
-      if (split.nv == 1) return fwd_run<LN, TX, TR, MX, 8, true, 1, kNormThreads>(q, threads, s);
-      if (split.nv == 2) return fwd_run<LN, TX, TR, MX, 8, true, 2, kNormThreads>(q, threads, s);
-      if (split.nv == 3) return fwd_run<LN, TX, TR, MX, 8, true, 3, kNormThreads>(q, threads, s);
-      return fwd_run<LN, TX, TR, MX, 8, true, 4, kNormThreads>(q, threads, s);
+      if (split.nv == 1) return fwd_run<LN, AT, TX, TR, MX, 8, true, 1, kNormThreads>(q, threads, s);
+      if (split.nv == 2) return fwd_run<LN, AT, TX, TR, MX, 8, true, 2, kNormThreads>(q, threads, s);
+      if (split.nv == 3) return fwd_run<LN, AT, TX, TR, MX, 8, true, 3, kNormThreads>(q, threads, s);
+      return fwd_run<LN, AT, TX, TR, MX, 8, true, 4, kNormThreads>(q, threads, s);
     }
     if constexpr (wide) {
       split = RowSplit(p.d, 3, 4, 512);
       q.group = split.group;
       if (split.group)
-        return split.nv == 3 ? fwd_run<LN, TX, TR, MX, 8, true, 3, 512>(q, q.group, s)
-                             : fwd_run<LN, TX, TR, MX, 8, true, 4, 512>(q, q.group, s);
+        return split.nv == 3 ? fwd_run<LN, AT, TX, TR, MX, 8, true, 3, 512>(q, q.group, s)
+                             : fwd_run<LN, AT, TX, TR, MX, 8, true, 4, 512>(q, q.group, s);
     }
   } else {
     const RowSplit split(p.d, 1, 1, kNormMaxThreads);
     q.group = split.group;
     if (split.group) {
       const int threads = split.threads();
-      if (split.group > 512) return fwd_run<LN, TX, TR, MX, V, false, 1, kNormMaxThreads>(q, threads, s);
-      return split.group <= kNormThreads ? fwd_run<LN, TX, TR, MX, V, false, 1, kNormThreads>(q, threads, s)
-                                         : fwd_run<LN, TX, TR, MX, V, false, 1, 512>(q, threads, s);
+      if (split.group > 512) return fwd_run<LN, AT, TX, TR, MX, V, false, 1, kNormMaxThreads>(q, threads, s);
+      return split.group <= kNormThreads ? fwd_run<LN, AT, TX, TR, MX, V, false, 1, kNormThreads>(q, threads, s)
+                                         : fwd_run<LN, AT, TX, TR, MX, V, false, 1, 512>(q, threads, s);
     }
   }
   const RowSplit split(p.d, wide ? 3 : 2, 4, kNormMaxThreads);
   q.group = split.group;
   if constexpr (!wide)
-    if (split.nv == 2) return fwd_run<LN, TX, TR, MX, V, false, 2, kNormMaxThreads>(q, q.group, s);
-  return split.nv == 3 ? fwd_run<LN, TX, TR, MX, V, false, 3, kNormMaxThreads>(q, q.group, s)
-                       : fwd_run<LN, TX, TR, MX, V, false, 4, kNormMaxThreads>(q, q.group, s);
+    if (split.nv == 2) return fwd_run<LN, AT, TX, TR, MX, V, false, 2, kNormMaxThreads>(q, q.group, s);
+  return split.nv == 3 ? fwd_run<LN, AT, TX, TR, MX, V, false, 3, kNormMaxThreads>(q, q.group, s)
+                       : fwd_run<LN, AT, TX, TR, MX, V, false, 4, kNormMaxThreads>(q, q.group, s);
 }
 
-template <bool LN, typename TX, typename TR>
+template <bool LN, bool AT, typename TX, typename TR>
 cudaError_t fwd_vec(const AddNormParams& p, int vec, cudaStream_t s) {
-  return vec == 8   ? fwd_types<LN, TX, TR, false, 8>(p, s)
-         : vec == 2 ? fwd_types<LN, TX, TR, false, 2>(p, s)
-                    : fwd_types<LN, TX, TR, false, 1>(p, s);
+  return vec == 8   ? fwd_types<LN, AT, TX, TR, false, 8>(p, s)
+         : vec == 2 ? fwd_types<LN, AT, TX, TR, false, 2>(p, s)
+                    : fwd_types<LN, AT, TX, TR, false, 1>(p, s);
 }
 
 // The entry of either norm: a kernel for the types and the access.
-template <bool LN> cudaError_t fwd_launch(const AddNormParams& p, int dtype, int res_dtype, int vec, cudaStream_t s) {
+template <bool LN, bool AT> cudaError_t fwd_launch(const AddNormParams& p, int dtype, int res_dtype, int vec, cudaStream_t s) {
   const bool same = dtype == res_dtype;
   if (p.y_q)
-    return same ? fwd_types<LN, __nv_bfloat16, __nv_bfloat16, true, 8>(p, s)
-                : fwd_types<LN, __nv_bfloat16, float, true, 8>(p, s);
+    return same ? fwd_types<LN, AT, __nv_bfloat16, __nv_bfloat16, true, 8>(p, s)
+                : fwd_types<LN, AT, __nv_bfloat16, float, true, 8>(p, s);
   if (dtype == MOE_DT_BF16)
-    return same ? fwd_vec<LN, __nv_bfloat16, __nv_bfloat16>(p, vec, s)
-                : fwd_vec<LN, __nv_bfloat16, float>(p, vec, s);
+    return same ? fwd_vec<LN, AT, __nv_bfloat16, __nv_bfloat16>(p, vec, s)
+                : fwd_vec<LN, AT, __nv_bfloat16, float>(p, vec, s);
   if (dtype == MOE_DT_F16)
-    return same ? fwd_vec<LN, __half, __half>(p, vec, s) : fwd_vec<LN, __half, float>(p, vec, s);
-  return fwd_vec<LN, float, float>(p, vec, s);
+    return same ? fwd_vec<LN, AT, __half, __half>(p, vec, s) : fwd_vec<LN, AT, __half, float>(p, vec, s);
+  return fwd_vec<LN, AT, float, float>(p, vec, s);
 }
 
 }  // namespace

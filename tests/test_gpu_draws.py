@@ -112,3 +112,90 @@ def test_captured_steps_of_8_bit_states_follow_their_mean(moe_gpu):
     sigma = unit / 2 / np.sqrt(1 - beta ** 2)
     off = 5 * sigma / np.sqrt(len(v)) + 2.0 ** -16 * unit / (1 - beta) + 2.0 ** -20
     assert abs(v.mean().item() - want) <= off and v.std().item() <= sigma
+
+
+# ------------------------------------------------------------------ norms and dropout
+def normal(gen, shape, dtype, dev):
+    return torch.randn(shape, generator=gen, device=dev).to(dtype)
+
+
+def norm_calls(m, dev, rows, d, xt, rt, layer):
+    """(call(offset, offset_dev), its outputs): forward, 8-bit forward where there is one, and
+    backward of one norm, and the dropout, each on outputs of its own."""
+    gen = torch.Generator(device=dev).manual_seed(rows + d)
+    x, dy = normal(gen, (rows, d), xt, dev), normal(gen, (rows, d), xt, dev)
+    res, w = normal(gen, (rows, d), rt, dev), normal(gen, (d,), xt, dev)
+    f = lambda *s, dtype=torch.float32: torch.zeros(*s, dtype=dtype, device=dev)   # noqa: E731
+    out = dict(h=f(rows, d, dtype=rt), y=f(rows, d, dtype=xt), rstd=f(rows), dh=f(rows, d, dtype=rt), dx=f(rows, d, dtype=xt),
+               dw=f(d), dropped=f(rows, d, dtype=xt), h8=f(rows, d, dtype=rt))
+    mean, rstd = normal(gen, (rows,), torch.float32, dev), torch.rand(rows, generator=gen, device=dev)
+    size = m.add_layer_norm_bwd_workspace(rows, d)
+    ws = torch.empty(size, dtype=torch.uint8, device=dev)
+    pad = (rows + 127) // 128 * 128
+    if xt is torch.bfloat16 and d % 128 == 0:
+        out.update(q=f(pad, d, dtype=torch.uint8), s=f(pad * d // 32, dtype=torch.uint8))
+
+    def call(offset, at=None):
+        kw = dict(p=0.3, seed=SEED, offset=offset, offset_dev=at)
+        if layer:
+            fwd = lambda y, h, **k: m.add_layer_norm(x, w, w, y, res, h, None, out["rstd"], **k)   # noqa: E731
+            m.add_layer_norm_bwd(dy, res, mean, rstd, w, None, out["dh"], out["dx"], out["dw"], None, ws, **kw)
+        else:
+            fwd = lambda y, h, **k: m.add_norm(x, w, y, res, h, out["rstd"], **k)   # noqa: E731
+            m.add_norm_bwd(dy, res, rstd, w, None, out["dh"], out["dx"], out["dw"], ws, **kw)
+        fwd(out["y"], out["h"], **kw)
+        if "q" in out:
+            fwd(None, out["h8"], y_q=out["q"], y_scales=out["s"], **kw)
+        m.dropout(x, out["dropped"], 0.3, SEED, offset, offset_dev=at)
+    return call, out
+
+
+@pytest.mark.parametrize("d", [64, 77, 250, 2048, 9000])
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32")], ids="-".join)
+@pytest.mark.parametrize("layer", [False, True], ids=["rms", "layer"])
+def test_replayed_masks_are_those_of_the_summed_offsets(moe_gpu, d, types, layer):
+    m, dev = moe_gpu
+    xt, rt = ({"bf16": torch.bfloat16, "f32": torch.float32}[t] for t in types)
+    rows, first = 37, (1 << 64) - 2
+    call, out = norm_calls(m, dev, rows, d, xt, rt, layer)
+    at = torch.zeros(1, dtype=torch.int64, device=dev)
+    call(first)   # shared memory limits are raised before the capture
+
+    def one():
+        at.add_(1)
+        call(first, at)
+    graph, seen = captured(one), []
+    for k in (1, 2, 3):
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {n: t.clone() for n, t in out.items()}
+        call((first + k) % (1 << 64))
+        for n, t in out.items():
+            assert torch.equal(got[n], t), n
+        seen.append(got["dropped"])
+    assert not torch.equal(seen[0], seen[1]) and not torch.equal(seen[1], seen[2])
+
+
+def test_a_counter_without_dropout(moe_gpu):
+    """p = 0: the counter is not needed and changes nothing."""
+    m, dev = moe_gpu
+    x, w = torch.randn(9, 256, device=dev), torch.ones(256, device=dev)
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    at = torch.tensor([3], device=dev)
+    m.add_layer_norm(x, w, None, a, offset_dev=at)
+    m.add_layer_norm(x, w, None, b)
+    assert torch.equal(a, b)
+    m.dropout(x, a, 0.0, 1, offset_dev=at)
+    assert torch.equal(a, x)
+
+
+def test_counters_of_a_wrong_kind_are_refused(moe_gpu):
+    m, dev = moe_gpu
+    x, w = torch.randn(4, 64, device=dev), torch.ones(64, device=dev)
+    y = torch.zeros_like(x)
+    for bad in (torch.zeros(1, device=dev), torch.zeros(2, dtype=torch.int64, device=dev), torch.zeros(1, dtype=torch.int64)):
+        with pytest.raises((TypeError, ValueError)):
+            m.dropout(x, y, 0.5, 1, offset_dev=bad)
+        with pytest.raises((TypeError, ValueError)):
+            m.add_norm(x, w, y, h=y, p=0.5, offset_dev=bad)
+    assert (y == 0).all()
