@@ -5,7 +5,9 @@
 TrainBlock   layer norm with residual and dropout, the MoE layer, layer norm; forward,
              backward, and AdamW on all weights (norms in fp32, the layer's in bf16 with
              states in 8 bits or with fp32 copies and 32-bit states).  A step is
-             captured into one CUDA graph that reads rate and step number from the device.
+             captured into one CUDA graph that reads rate and step number from the device,
+             and counters for the numbers that it draws: each replay has its own masks and
+             roundings.
 few()        the same block for a few tokens, on the weights that the last step has
              written: no conversion, no buffers of the training batch.
 
@@ -44,9 +46,11 @@ class TrainBlock:
         self.layer = moe.layer_adamw(self.buf, self.w_router, self.w_gate, self.w_up, self.w_down, bits, master=bits == 32)
         self.norm_list = moe.adamw_list(self.norms, self.d_norms, *moe.adamw_states(self.norms))
         self.lr, self.step = torch.full((1,), lr, **F32), torch.zeros(1, dtype=torch.int64, device="cuda")
+        self.drawn = torch.zeros_like(self.step)   # masks of the steps so far, two each
 
     def _norm(self, i, x, stream, y, h, mean=None, rstd=None, p=0.0):
-        moe.add_layer_norm(x, self.norms[2 * i], self.norms[2 * i + 1], y, stream, h, mean, rstd, self.eps, p, self.seed, i)
+        moe.add_layer_norm(x, self.norms[2 * i], self.norms[2 * i + 1], y, stream, h, mean, rstd, self.eps, p, self.seed, i,
+                           offset_dev=self.drawn)
 
     def forward(self, x, stream):
         """x [T, d] bf16, stream [T, d] fp32 -> y2."""
@@ -57,19 +61,22 @@ class TrainBlock:
 
     def _norm_bwd(self, i, dy, dres, dh, dx):
         moe.add_layer_norm_bwd(dy, self.h[i], self.mean[i], self.rstd[i], self.norms[2 * i], dres, dh, dx,
-                               self.d_norms[2 * i], self.d_norms[2 * i + 1], self.ws, self.p, self.seed, i)
+                               self.d_norms[2 * i], self.d_norms[2 * i + 1], self.ws, self.p, self.seed, i, offset_dev=self.drawn)
 
     def backward(self, dy2, dh2=None):
         """dy2 [T, d] bf16, dh2: what comes back through the stream (or None)."""
         self._norm_bwd(1, dy2, dh2, self.dh, self.d_out)
         moe.backward(self.buf, self.d_out, self.y[0], self.w_router, self.w_gate, self.w_up, self.w_down)
         self._norm_bwd(0, self.buf.grads["dx"], self.dh, self.dstream, self.dx)
+        self.drawn.add_(2)   # the next forward's masks are others
         return self.dx, self.dstream
 
-    def update(self, offset=0):
-        """One step on all weights; `offset` chooses the numbers of the drawn roundings."""
+    def update(self, offset=None):
+        """One step on all weights.  The numbers of the drawn roundings go with the step's, far
+        from those of the masks; with `offset` they are this offset's (at every replay)."""
         self.step.add_(1)
-        moe.adamw(self.layer, self.lr, self.step, weight_decay=0.01, seed=self.seed, offset=offset)
+        draws = dict(offset=1 << 32, offset_dev=self.step) if offset is None else dict(offset=offset)
+        moe.adamw(self.layer, self.lr, self.step, weight_decay=0.01, seed=self.seed, **draws)
         moe.adamw(self.norm_list, self.lr, self.step, weight_decay=0.0)
 
     def few(self, x, stream):

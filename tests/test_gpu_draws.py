@@ -8,7 +8,9 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import block_oracle as B
 from test_gpu_adamw import HYPER, SEED, Tensors
+from test_gpu_updates_example import example, inputs, new_block   # noqa: F401 (a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -199,3 +201,52 @@ def test_counters_of_a_wrong_kind_are_refused(moe_gpu):
         with pytest.raises((TypeError, ValueError)):
             m.add_norm(x, w, y, h=y, p=0.5, offset_dev=bad)
     assert (y == 0).all()
+
+
+# ------------------------------------------------------------------ the example
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_captured_training_step(example, bits):   # noqa: F811
+    """Replays of the example's step: each with the oracle's masks of its own offsets, and the
+    weights that eager steps leave."""
+    x, stream, dy, _ = inputs(300)
+    blocks = []
+    for _ in range(2):
+        b = new_block(example, bits)
+        b.forward(x, stream)
+        b.backward(dy)
+        blocks.append(b)
+
+    def step(b):
+        b.forward(x, stream)
+        b.backward(dy)
+        b.update()
+    graph = captured(lambda: step(blocks[0]))
+    kept = []
+    for k in (1, 2, 3):
+        graph.replay()
+        step(blocks[1])
+        torch.cuda.synchronize()
+        for n in ("w_router", "w_gate", "w_up", "w_down"):
+            assert torch.equal(getattr(blocks[0], n), getattr(blocks[1], n)), (k, n)
+        for i in range(2):
+            assert torch.equal(blocks[0].h[i], blocks[1].h[i])
+        got = (blocks[0].h[0] != stream).cpu().numpy()   # places that were kept
+        want = B.keep_mask(*x.shape, blocks[0].p, blocks[0].seed, 2 * k)
+        # a kept x of zero, or one that is lost beside the stream's value, looks dropped
+        assert not (got & ~want).any() and (want & ~got).mean() < 0.02
+        kept.append(got)
+    assert (kept[0] != kept[1]).any() and (kept[1] != kept[2]).any()
+
+
+def test_steps_of_the_example_draw_other_roundings(example):   # noqa: F811
+    """The same gradients and weights, stepped as step 1 and as step 2 of 8-bit states whose
+    constants are the same: the codes differ."""
+    blocks = [new_block(example, 8) for _ in range(2)]
+    for s, b in enumerate(blocks):
+        gen = torch.Generator(device="cuda").manual_seed(7)
+        for g in ("dw_router", "dw_gate", "dw_up", "dw_down"):
+            b.buf.grads[g].normal_(generator=gen)
+        b.step.fill_(1 + s)
+        b.update()
+    codes = [b.layer.held[0] for b in blocks]   # of the first tensor's first moment
+    assert codes[0].dtype == torch.uint8 and not torch.equal(codes[0], codes[1])
