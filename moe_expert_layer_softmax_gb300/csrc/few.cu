@@ -702,6 +702,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               at = t < 32 ? __popc(m0 & ((1u << t) - 1u)) : __popc(m0) + __popc(m1 & ((1u << (t - 32)) - 1u));
             }
             if (in && t < columns) {
+              // the fast exponential and quotient, as the layer's own: off by 2 + 1.2 |h| and
+              // two last places, less than what the sum before them was cut off by
               const float a = __fdividef(v[i], 1.0f + __expf(-v[i])) * s.up[row][i];
               const __nv_bfloat16 high = __float2bfloat16_rn(a);
               const float rest = a - __bfloat162float(high);
