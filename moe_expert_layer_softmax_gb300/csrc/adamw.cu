@@ -55,6 +55,7 @@ MOE_DEV float2 add(float2 a, float2 b) { return make_float2(__fadd_rn(a.x, b.x),
 // nothing on the way leaves the normal range.  Compared with __fsqrt_rn on every
 // mantissa of both parities, the reciprocal with __frcp_rn on every mantissa (then the
 // quotient is right by Markstein's theorem), 2.5e10 quotients with __fdiv_rn: no difference.
+// tests/test_gpu_adamw_ranges.py repeats the roots, the reciprocals and 7e7 quotients.
 MOE_DEV Two roots(float2 v) {
   float x, y;
   asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(v.x));
