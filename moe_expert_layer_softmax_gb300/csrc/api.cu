@@ -362,7 +362,7 @@ int moe_checks_read(int32_t* flags, int32_t reset) {
   if (flags == nullptr) return MOE_ERR_INVALID;
   *flags = 0;
   int32_t* words[] = {check_word_move(), check_word_quant(), check_word_balance(),
-                      check_word_gemm(), check_word_route()};
+                      check_word_gemm(), check_word_route(), check_word_few()};
   bool any = false;
   for (int32_t* w : words) {
     if (w == nullptr) continue;

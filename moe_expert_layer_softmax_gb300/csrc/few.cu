@@ -746,6 +746,23 @@ MOE_DEV Fill down_fill(int n, int m) {
   return f;
 }
 
+#ifdef MOE_CHECKS
+// What the up kernel has listed, before it becomes rows of copies and places of sums; a list
+// with a wrong entry is taken as empty.
+MOE_DEV void check_lists(DownCtl& s, const FewParams& p) {
+  if (threadIdx.x == 0) {
+    const int R = p.T * p.k;
+    bool ok = MOE_CHECK_OK(s.n_act, min(p.E, R) + 1);
+    for (int a = 0; ok && a < s.n_act; ++a)
+      ok = MOE_CHECK_OK(s.act[a], p.E) && MOE_CHECK_OK(s.base[a + 1], R + 1) &&
+           MOE_CHECK_OK(s.base[a + 1] - s.base[a] - 1, p.T);
+    for (int r = 0; ok && r < (s.n_act ? s.base[s.n_act] : 0); ++r) ok = MOE_CHECK_OK(s.tok[r], p.T);
+    if (!ok) s.n_act = 0;
+  }
+  __syncthreads();
+}
+#endif
+
 __global__ void __launch_bounds__(kThreads, 1)
     few_down_kernel(const __grid_constant__ DownMaps maps, const FewParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -767,6 +784,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = threadIdx.x; i < p.T * 32; i += kThreads) reinterpret_cast<float4*>(sums)[i] = {};
     __syncthreads();
+#ifdef MOE_CHECKS
+    check_lists(s, p);
+#endif
   }
   const uint32_t tmem = s.tmem + ((uint32_t)(quarter * 32) << 16);
   const int rank = (int)cluster_ctarank(), clusters = gridDim.x / kCluster, cluster = blockIdx.x / kCluster;
@@ -971,5 +991,7 @@ cudaError_t launch_few(const FewParams& args, const FewTensors& w, cudaStream_t 
   if (e != cudaSuccess) return e;
   return launch_clusters(&few_down_kernel, ctas, kDownSmem, s, down, p);
 }
+
+MOE_CHECK_WORD_ACCESSOR(few)
 
 }  // namespace moe

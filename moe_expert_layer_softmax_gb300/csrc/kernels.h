@@ -199,6 +199,7 @@ int32_t* check_word_quant();
 int32_t* check_word_balance();
 int32_t* check_word_gemm();
 int32_t* check_word_route();
+int32_t* check_word_few();
 void noalloc_forget_device(int dev);   // moe_route_noalloc's cached scratch address
 int gemm_set_inject_stall(int mode);   // returns the previous mode
 
