@@ -785,7 +785,7 @@ MOE_API int moe_dropout_at(int64_t rows, int32_t cols, int32_t dtype, const void
  *           between two codes takes the upper one where the remainder, in units of
  *           their distance, is at least 1 - number / 2^16, but a root above zero never
  *           code 0.  An infinity or a NaN is held as a NaN.  States of zeros are zero
- *           codes with any scale.
+ *           codes with any finite scale.
  * Drawn rounding of bf16: number is added to the 32 bits of w, the lower 16 are cut.
  * number: half-word i % 8 (low half-words first) of Philox4x32-10 (as moe_dropout) with
  * key = seed and counter (i / 8, 4 * place of the tensor in the list + what, offset low,

@@ -22,11 +22,15 @@
 // of everything else.  A block takes 2048 neighbouring values at a time, a thread eight,
 // all loads issued before the first is used.  Measured on 201 M values, fp32 gradients:
 // bf16 with fp32 copies and 32-bit states (30 bytes a value) 847 us, 7.1 TB/s, HBM; bf16
-// alone with 8-bit states (12 bytes) 621 us, 3.9 TB/s, bound by issue: 85 instructions a
-// value, a fifth of them the generator's (without it 512 us with one chunk a block, when
-// the whole took 666).  Scalar products and roots took 753 us there, the compiler's
-// division and root and a rounding by conversions 908; fetching the next chunk into
-// registers ahead gave nothing (three blocks a multiprocessor instead of four).
+// alone with 8-bit states (12 bytes) 621 us, 3.9 TB/s: 85 instructions a value, a fifth of
+// them the generator's (without it 512 us with one chunk a block, when the whole took 666),
+// fill 67 % of the issue slots; in the rest the warps wait for loads, which a thread issues
+// for its next chunk only when it is done with this one (registers for both cost a block of
+// four and gave nothing).  Scalar products and roots took 753 us there, the compiler's
+// division and root and a rounding by conversions 908.
+// Values whose moments are zero (a gradient that has always been zero: experts that never
+// had a token) take the roots and quotients one by one: an eighth of the values 671 us, all
+// of them 1029; gradients of zero beside moments that are not 628.
 #include "block.cuh"
 #include "block.h"
 #include "kernels.h"

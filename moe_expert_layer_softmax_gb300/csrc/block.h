@@ -98,7 +98,7 @@ struct AdamwTensor {
   float *m_scale, *v_scale;
   int64_t numel;
   uint32_t first;   // block that it begins with
-  uint32_t vec;     // every pointer on a 16-byte boundary
+  uint32_t vec;     // vector accesses: pointers on 16-byte boundaries, codes on 8 (scales: any)
 };
 
 struct AdamwScalars {

@@ -26,10 +26,15 @@
 // by index (gather) into the MMA's N.
 //
 // Bound by HBM, behind a fixed cost.  Measured (floor at a copy's 6.78 TB/s), bf16:
-//   1 token,   8 of 64 experts, 4096 x 2048   83.8 us (59.5): up 6.6, down 6.1 TB/s while
+//   1 token,   8 of 64 experts, 4096 x 2048   84 us (59.5): up 6.6, down 6.1 TB/s while
 //              weights stream, 62 us; routing 9; the kernels' starts and joins 12
-//   16 tokens, 4 of 32, 2048 x 1024           75 us (52.5): 7.0 and 5.6 TB/s; routing 7
-//   64 tokens, 4 of 64, 2048 x 1408           191 us (161); routing 16, sixteen tokens a CTA
+//   16 tokens, 4 of 32, 2048 x 1024           78 us (52.5): 7.0 and 5.6 TB/s; routing 7
+//   64 tokens, 4 of 64, 2048 x 1408           192 us (161); routing 16, sixteen tokens a CTA
+// The fixed cost shows most on small layers: 1 token, 4 of 64 experts of 2048 x 1408 31 us
+// (10.2), 8 of 64 of 2048 x 1024 36 us (14.9), 4 tokens, 2 of 8 of 512 x 128 20 us (under 1);
+// 64 tokens, 8 of 128 of 1024 x 512 115 us (58.5), pieces of four tokens.  Neither kernel
+// starts before the other has ended: each takes all of the shared memory, the second all
+// of the tensor memory.
 // A TMA copy costs about as much as 2 to 4 KB of data, whatever its size: with boxes of
 // eight rows alone the first took 148 us.  Clusters of two instead of four fill all 152
 // multiprocessors (four: 144) but read W_router twice as often: 16 to 30 % slower.

@@ -22,7 +22,7 @@
 // way into shared memory, each thread copying and reading its own pieces, so that
 // the pipeline needs no barrier and no registers: 512 threads a multiprocessor
 // keep 50 to 130 KB in flight.  A thread holds 16 columns (rows up to 256: 8; the
-// 8-bit output and wide rows: up to 32), so that what a row costs beside its
+// RMS norm's 8-bit output and wide rows: up to 32), so that what a row costs beside its
 // elements (the sums over threads, the square root, addresses) is shared: with
 // eight columns a thread the 8192 x 2048 forward took 294 instructions per eight
 // columns and 28.5 us, bound by issue.  A row has a group of 8, 16 or any multiple
@@ -43,10 +43,17 @@
 // 2.6-4.3 and 3.2-5.8 (with 1024 threads; 512 with twice the columns spilled: 4999
 // columns in fp32 3.2 and 4.1 forward, 2.3 and 3.2 backward).
 //
-// Layer norm: forward 8192 x 2048 26.3 us (5.1 TB/s; bound by issue, 65 % of the slots),
-// 32768 x 4096 with dropout and 8-bit output 280 us, 8192 and 12288 columns 4.7 and
-// 4.0; backward 8192 x 2048 35.0 us (4.8), 32768 x 4096 on an fp32 stream with dropout
-// 342 us (6.3), other sizes 4.8-6.3.
+// Layer norm (TB/s, bf16 stream / fp32 stream, without dropout): forward 8192 x 2048 26.2
+// us, 5.1 / 5.2; 64 to 4096 columns 4.2-6.3 / 5.2-6.5; 8192 4.7 / 5.0 (fp32 throughout 3.8),
+// 12288 and 16384 4.0-4.2 / 4.4-4.5; with dropout 3.3-5.0 / 4.6-6.5.  8-bit output, 4096
+// columns: 5.2 / 6.5, with dropout 4.3 / 5.7 (32768 rows 280 / 308 us).  Widths without
+// vector loads: 257 columns 1.6 / 2.5, 1001 2.9 / 4.3, 4999 2.1 / 3.1.  Backward 8192 x 2048
+// 35.0 us, 4.8 / 5.5; 64 to 8192 columns 4.4-6.3 / 4.7-6.6, with dropout 3.5-5.2 / 4.2-6.4
+// (32768 x 4096 342 us, 6.3); 12288 4.1 / 2.2, 16384 3.2 / 2.1 (24 and 32 columns a thread
+// from the ring spill 184 and 708 bytes, the kernels beyond 0.9 to 3 KB); 257 1.5 / 2.6,
+// 1001 2.7 / 4.4, 4999 1.7 / 2.5.
+// What bounds the bf16 forward at 2048 columns is neither HBM nor issue (62 % of the slots)
+// but four reductions after one another in each row, at 16 warps a multiprocessor.
 #pragma once
 
 #include "block.cuh"
