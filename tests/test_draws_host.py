@@ -110,3 +110,15 @@ def test_counters_that_are_refused(fake, name):
         with pytest.raises(error):
             call(offset_dev=bad)
     assert not fake.calls
+
+
+def test_a_device_that_is_not_set_up(fake, monkeypatch):
+    """The call with a counter sets the device up and is made again, itself and not the form
+    without."""
+    answers, made = [m.ERR_NOT_INIT, 0], []
+    monkeypatch.setattr(m, "load", lambda: type("L", (), {"__getattr__": lambda s, n: lambda *a: made.append((n, a)) or answers.pop(0)})())
+    monkeypatch.setattr(m, "_capturing", lambda handle: False)
+    monkeypatch.setattr(m, "init", lambda: made.append("init"))
+    calls()["dropout"](offset_dev=counter())
+    (first, a), init, (second, b) = made
+    assert first == second == "moe_dropout_at" and init == "init" and a == b
